@@ -29,7 +29,10 @@ import threading
 __all__ = ["prepare", "scan", "forward", "forward_states", "forward_varlen", "rescan_dq",
            "workspace_bytes", "wait_timeouts",
            "load_library",
-           "GdnError", "LIB_PATH", "POISON_LIB_PATH", "STATUS"]
+           "GdnError", "LIB_PATH", "POISON_LIB_PATH", "STATUS",
+           # the layer's other operators (layer.py)
+           "norm_forward", "norm_backward", "conv_forward", "conv_backward", "conv_step",
+           "ssm_forward", "ssm_step"]
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(_HERE, "libgdn.so")
@@ -52,7 +55,22 @@ EXPORTS = ["gdn_prepare", "gdn_scan", "gdn_forward", "gdn_forward_states",
            "gdn_workspace_bytes_split", "gdn_backward", "gdn_workspace_bytes_backward",
            "gdn_forward_split_point"]
 NOALLOC_SCRATCH_BYTES = 32 << 20
-ABI_VERSION = 10
+ABI_VERSION = 11
+
+
+_LAYER = ("norm_forward", "norm_backward", "conv_forward", "conv_backward", "conv_step",
+          "ssm_forward", "ssm_step")
+
+
+def __getattr__(name):
+    # the layer's operators live in a module that imports torch; this one
+    # imports it only where it is used
+    if name in _LAYER:
+        from . import layer
+        for n in _LAYER:
+            globals()[n] = getattr(layer, n)
+        return globals()[name]
+    raise AttributeError("module %r has no attribute %r" % (__name__, name))
 
 
 class GdnError(RuntimeError):
@@ -117,6 +135,8 @@ def load_library(path: str | None = None):
         lib.gdn_abi_version.restype = ctypes.c_int
         lib.gdn_wait_timeouts.argtypes = [ctypes.POINTER(ctypes.c_uint32), ctypes.c_int]
         lib.gdn_wait_timeouts.restype = ctypes.c_int
+        from . import layer
+        layer.declare(lib)
         if lib.gdn_abi_version() != ABI_VERSION:
             raise RuntimeError("libgdn ABI %d, binding expects %d"
                                % (lib.gdn_abi_version(), ABI_VERSION))

@@ -55,6 +55,9 @@ UNITS = {
     "gdn_split.hip": [],
     "gdn_backward.hip": [],
     "gdn_backward_kda.hip": [],
+    "gdn_norm.hip": [],
+    "gdn_conv.hip": [],
+    "gdn_ssm.hip": [],
 }
 
 

@@ -80,7 +80,7 @@
 extern "C" {
 #endif
 
-#define GDN_ABI_VERSION 10
+#define GDN_ABI_VERSION 11
 
 typedef enum gdn_status {
     GDN_OK = 0,
