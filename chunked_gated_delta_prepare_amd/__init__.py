@@ -32,7 +32,7 @@ __all__ = ["prepare", "scan", "forward", "forward_states", "forward_varlen", "re
            "GdnError", "LIB_PATH", "POISON_LIB_PATH", "STATUS",
            # the layer's other operators (layer.py)
            "norm_forward", "norm_backward", "conv_forward", "conv_backward", "conv_step",
-           "ssm_forward", "ssm_step"]
+           "ssm_forward", "ssm_backward", "ssm_step"]
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(_HERE, "libgdn.so")
@@ -59,7 +59,7 @@ ABI_VERSION = 11
 
 
 _LAYER = ("norm_forward", "norm_backward", "conv_forward", "conv_backward", "conv_step",
-          "ssm_forward", "ssm_step")
+          "ssm_forward", "ssm_backward", "ssm_step")
 
 
 def __getattr__(name):

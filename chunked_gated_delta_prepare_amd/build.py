@@ -58,6 +58,7 @@ UNITS = {
     "gdn_norm.hip": [],
     "gdn_conv.hip": [],
     "gdn_ssm.hip": [],
+    "gdn_ssm_backward.hip": [],
 }
 
 

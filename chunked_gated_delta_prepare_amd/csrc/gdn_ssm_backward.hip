@@ -1,0 +1,644 @@
+// Selective state space scan, backward: dx by the reverse scan of
+// ssm_scan_kernel, dC and dB by ssm_key_kernel in either direction, and the
+// gates' gradients from the sums the two leave (see gdn_ssm.h).
+#include "gdn_ssm.h"
+
+namespace gdn {
+
+// ---------------------------------------------------------------------------
+// out2 (dC forward, dB in reverse), and per head and row the sum
+// q_i . out2_i.  Here a wave keeps N / 4 rows of the state, all columns of
+// them: S q2 sums over columns.  Per chunk:
+//   1  the lower triangles of q k^T and q2 v^T; the products of both, times
+//      decays and weights, sum up to the rows' part inside the chunk; those
+//      of q2 v^T alone, summed over the heads here, go to LDS as M
+//   2  out2 = e^cum S q2 + M k, transposed, so that a lane holds four of the
+//      N values of a row
+//   3  S' = e^total S + (w k)^T v
+// S enters its product in three bf16 parts and (w k) in three (relative error
+// 2^-27): the sums feed dt's and A's gradients, which are fp32.  M is rounded once to out2's own type.
+// ---------------------------------------------------------------------------
+template <typename IO, int N, int NCB, bool REV>
+__global__ void __launch_bounds__(256) ssm_key_kernel(SsmParams p) {
+    typedef SOp<IO> O;
+    typedef typename O::elem E;
+    constexpr int C = kSsmChunk, COLS = 64 * NCB, LX = COLS + O::kPad, LN = N + O::kPad, LM = C + O::kPad;
+    constexpr int NH = NCB, NB = N / 64, PB = COLS / 16;      // this wave's blocks of N; blocks of columns
+    constexpr int kP = O::template kParts<3>;
+    __shared__ E sv[C * LX], sz[C * LX], sk[C * LN], sq[C * LN], sm[C * LM];
+    __shared__ Gates gates[NH];
+    __shared__ float inner[NH][4][C], outer[NH][4][C], diag[NH][2][C];
+    __shared__ float dots[NH][4];
+    int item, hb;
+    place(p, item, hb);
+    if (item >= p.n_items) return;
+    const Segment seg = find_segment(p, item);
+    if (!seg.live) return;
+    const int w = wave_id(), l = lane_id(), q = l >> 4, j = l & 15;
+    const int col0 = hb * COLS, head0 = col0 / p.P, nh = p.P == 64 ? NCB : 1, grp = head0 / p.heads_per_group;
+    const int wn = w * (N / 4);                   // this wave's first of N
+    const bool gater = w < nh;
+    const float A = gater ? p.A[head0 + w] : 0.f, bias = gater && p.bias ? p.bias[head0 + w] : 0.f;
+
+    // h[nb * PB + pb][e] = S[n = wn + 16 nb + j][column 16 pb + 4 q + e]
+    float4v h[NB * PB];
+#pragma unroll
+    for (int i = 0; i < NB * PB; ++i) h[i] = float4v{0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+    for (int hh = 0; hh < NH; ++hh)
+        if (hh < nh) {
+            const float d = segments_before<REV>(p, seg, hb, NH, hh, [&](int64_t at, float f) {
+                const float *e0 = p.ends + at * (N * COLS) + (wn + j) * COLS + 4 * q;
+#pragma unroll
+                for (int nb = 0; nb < NB; ++nb)
+#pragma unroll
+                    for (int pb = 0; pb < PB; ++pb)
+                        if (nh == 1 || pb / (PB / NH) == hh) h[nb * PB + pb] += f * *(const float4v *)(e0 + 16 * nb * COLS + 16 * pb);
+            });
+            if (p.s0) {
+#pragma unroll
+                for (int nb = 0; nb < NB; ++nb)
+#pragma unroll
+                    for (int pb = 0; pb < PB; ++pb)
+                        if (nh == 1 || pb / (PB / NH) == hh) {
+                            const int col = col0 + 16 * pb + 4 * q;
+                            const float *s = p.s0 + (((int64_t)seg.seq * p.H + col / p.P) * N + wn + 16 * nb + j) * p.P + col % p.P;
+#pragma unroll
+                            for (int e = 0; e < 4; ++e) h[nb * PB + pb][e] += d * s[e];
+                        }
+            }
+        }
+    for (int i = threadIdx.x; i < 2 * 16 * 16; i += 256) {
+        const int blk = i >> 8, r = (i >> 4) & 15, c = i & 15;
+        sm[(32 * blk + r) * LM + 32 * blk + 16 + c] = E(0);
+    }
+
+    TileRegs<IO, COLS, REV> tv, tz;
+    TileRegs<IO, N, REV> tk, tq;
+    float raw = 0.f;
+    const int64_t voff = seg.batch * p.vb + col0, zoff = seg.batch * p.q2b + col0, koff = seg.batch * p.qkb + (int64_t)grp * N;
+    auto fetch = [&](int c) {
+        int lo;
+        const int rows = chunk_of<REV>(seg, c, lo);
+        tv.load(p.v, voff + lo * p.vt, (uint32_t)p.vt, rows);
+        tz.load(p.q2, zoff + lo * p.q2t, (uint32_t)p.q2t, rows);
+        tk.load(p.k, koff + lo * p.qkt, (uint32_t)p.qkt, rows);
+        tq.load(p.q, koff + lo * p.qkt, (uint32_t)p.qkt, rows);
+        if (gater) raw = raw_dt<IO, REV>(p, seg.batch, head0 + w, lo, rows);
+    };
+    const int nc = chunks_of(seg);
+    if (nc > 0) fetch(0);
+    for (int c = 0; c < nc; ++c) {
+        int lo;
+        const int rows = chunk_of<REV>(seg, c, lo);
+        __syncthreads();                          // the last chunk's tiles and sums are done with
+        tv.put(sv, LX);
+        tz.put(sz, LX);
+        tk.put(sk, LN);
+        tq.put(sq, LN);
+        if (gater) make_gates<REV>(gates[w], dt_of(p, raw, bias, l < rows), A);
+        if (c + 1 < nc) fetch(c + 1);
+        const int mark = mark_slot(p, seg, REV ? nc - 1 - c : c);
+        if constexpr (REV) {
+            // behind this chunk h meets the state's gradient
+            if (mark >= 0) {
+                const float2 *m = (const float2 *)p.marks + ((int64_t)mark * p.n_hb + hb) * (N * COLS / 2) + threadIdx.x;
+                float dot[NH];
+#pragma unroll
+                for (int hh = 0; hh < NH; ++hh) dot[hh] = 0.f;
+#pragma unroll
+                for (int i = 0; i < NB * PB; ++i) {
+                    const float2 a = m[(2 * i) * 256], b = m[(2 * i + 1) * 256];
+                    const float d = a.x * h[i][0] + a.y * h[i][1] + b.x * h[i][2] + b.y * h[i][3];
+                    if (nh == 1 || NH == 1 || (i % PB) / (PB / NH) == 0)
+                        dot[0] += d;
+                    else
+                        dot[NH - 1] += d;
+                }
+#pragma unroll
+                for (int hh = 0; hh < NH; ++hh) {
+                    const float d = wave_sum(dot[hh]);
+                    if (l == 0) dots[hh][w] = d;
+                }
+            }
+        }
+        __syncthreads();
+        if constexpr (REV) {
+            if (mark >= 0 && w < nh && l == 0)
+                p.X[((int64_t)mark * p.n_hb + hb) * NH + w] =
+                    ((double)dots[w][0] + (double)dots[w][1]) + ((double)dots[w][2] + (double)dots[w][3]);
+        }
+        // 1
+#pragma unroll
+        for (int r = 0; r < 3; ++r) {
+            const int idx = w + 4 * r;
+            if (idx < 10) {
+                const int bi = idx < 1 ? 0 : idx < 3 ? 1 : idx < 6 ? 2 : 3, bk = idx - bi * (bi + 1) / 2;
+                const int ii = 16 * bi + j;
+                float4v s = float4v{0.f, 0.f, 0.f, 0.f}, m = s;
+#pragma unroll
+                for (int n0 = 0; n0 < N; n0 += 32) O::mma(s, O::row(sk, LN, 16 * bk, n0), O::row(sq, LN, 16 * bi, n0));
+#pragma unroll
+                for (int hh = 0; hh < NH; ++hh)
+                    if (hh < nh) {
+                        float4v x = float4v{0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+                        for (int k = 0; k < COLS / 32; ++k)
+                            if (nh == 1 || k / (COLS / 32 / NH) == hh) O::mma(x, O::row(sv, LX, 16 * bk, 32 * k), O::row(sz, LX, 16 * bi, 32 * k));
+                        const float2 ci = gates[hh].cum[ii];
+                        const float post = REV ? gates[hh].dt[ii] : 1.f;
+                        float sum = 0.f;
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) {
+                            const int kk = 16 * bk + 4 * q + e;
+                            const float d = kk <= ii ? x[e] * decay_between(ci, gates[hh].cum[kk]) * gates[hh].w[kk] : 0.f;
+                            m[e] += d * post;
+                            if (kk < ii) sum += d * s[e];
+                            if (!REV && kk == ii) {
+                                diag[hh][0][ii] = x[e];
+                                diag[hh][1][ii] = x[e] * s[e];
+                            }
+                        }
+                        sum += __shfl_xor(sum, 16, 64);
+                        sum += __shfl_xor(sum, 32, 64);
+                        if (q == 0) inner[hh][bk][ii] = sum;
+                    }
+                O::put4(&sm[ii * LM + 16 * bk + 4 * q], m);
+            }
+        }
+        // 2, the state's part: z = S q2 of every head, its sum with q, and
+        // times e^cum the start of out2
+        float4v z[NB * 4];
+#pragma unroll
+        for (int i = 0; i < NB * 4; ++i) z[i] = float4v{0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+        for (int hh = 0; hh < NH; ++hh)
+            if (hh < nh) {
+                float4v a[NB * 4];
+#pragma unroll
+                for (int i = 0; i < NB * 4; ++i) a[i] = float4v{0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+                for (int pb = 0; pb < PB; pb += 2)
+                    if (nh == 1 || pb / (PB / NH) == hh) {
+                        typename O::frag hf[NB][kP];
+#pragma unroll
+                        for (int nb = 0; nb < NB; ++nb) O::acc_split(h[nb * PB + pb], h[nb * PB + pb + 1], hf[nb]);
+#pragma unroll
+                        for (int bi = 0; bi < 4; ++bi) {
+                            const typename O::frag zf = O::row_split(sz, LX, 16 * bi, 16 * pb);
+#pragma unroll
+                            for (int nb = 0; nb < NB; ++nb)
+#pragma unroll
+                                for (int k = 0; k < kP; ++k) O::mma(a[nb * 4 + bi], hf[nb][k], zf);
+                        }
+                    }
+#pragma unroll
+                for (int bi = 0; bi < 4; ++bi) {
+                    const int ii = 16 * bi + j;
+                    const float ec = gates[hh].ecum[ii], post = REV ? gates[hh].dt[ii] : 1.f;
+                    float sum = 0.f;
+#pragma unroll
+                    for (int nb = 0; nb < NB; ++nb) {
+                        float x[4];
+                        O::get4(&sq[ii * LN + wn + 16 * nb + 4 * q], x);
+                        a[nb * 4 + bi] *= ec;
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) sum += a[nb * 4 + bi][e] * x[e];
+                        z[nb * 4 + bi] += a[nb * 4 + bi] * post;
+                    }
+                    sum += __shfl_xor(sum, 16, 64);
+                    sum += __shfl_xor(sum, 32, 64);
+                    if (q == 0) outer[hh][w][ii] = sum;
+                }
+            }
+        __syncthreads();                          // M and the sums are whole
+        if (w < nh && l < rows) {
+            // row l's sums, to the token's place
+            const int t = lo + (REV ? rows - 1 - l : l);
+            const int64_t at = ((int64_t)hb * NH + w) * p.rows + (int64_t)seg.batch * p.T + t;
+            float sum = 0.f;
+#pragma unroll
+            for (int b = 0; b < 4; ++b)
+                if (b <= l >> 4) sum += inner[w][b][l];
+            p.inside[at] = sum;
+            p.across[at] = outer[w][0][l] + outer[w][1][l] + outer[w][2][l] + outer[w][3][l];
+            if constexpr (!REV) {
+                p.dyx[at] = diag[w][0][l];
+                p.wtt[at] = diag[w][1][l];
+            }
+        }
+        // 2 and 3: both take k by its N values
+#pragma unroll
+        for (int hh = 0; hh < NH; ++hh)
+            if (hh < nh) {
+                const float et = fast_exp2((float)gates[hh].total);
+#pragma unroll
+                for (int i = 0; i < NB * PB; ++i)
+                    if (nh == 1 || (i % PB) / (PB / NH) == hh) h[i] *= et;
+            }
+#pragma unroll
+        for (int s0 = 0; s0 < C; s0 += 32) {
+            typename O::frag kf[NB], kw[NH][NB][kP];
+#pragma unroll
+            for (int nb = 0; nb < NB; ++nb) kf[nb] = O::col(sk, LN, wn + 16 * nb, s0);
+#pragma unroll
+            for (int hh = 0; hh < NH; ++hh)
+                if (hh < nh) {
+                    float wt[8];
+#pragma unroll
+                    for (int e = 0; e < 8; ++e) wt[e] = gates[hh].end[s0 + 8 * q + e];
+#pragma unroll
+                    for (int nb = 0; nb < NB; ++nb) O::scaled(kf[nb], wt, kw[hh][nb]);
+                }
+#pragma unroll
+            for (int bi = s0 / 16; bi < 4; ++bi) {
+                const typename O::frag mf = O::row(sm, LM, 16 * bi, s0);
+#pragma unroll
+                for (int nb = 0; nb < NB; ++nb) O::mma(z[nb * 4 + bi], kf[nb], mf);
+            }
+#pragma unroll
+            for (int pb = 0; pb < PB; ++pb) {
+                const typename O::frag vf = O::col(sv, LX, 16 * pb, s0);
+#pragma unroll
+                for (int nb = 0; nb < NB; ++nb) {
+#pragma unroll
+                    for (int hh = 0; hh < NH; ++hh)
+                        if (hh < nh && (nh == 1 || pb / (PB / NH) == hh)) {
+#pragma unroll
+                            for (int k = 0; k < kP; ++k) O::mma(h[nb * PB + pb], vf, kw[hh][nb][k]);
+                        }
+                }
+            }
+        }
+        if constexpr (!REV) {
+            if (mark >= 0) {
+                float2 *m = (float2 *)p.marks + ((int64_t)mark * p.n_hb + hb) * (N * COLS / 2) + threadIdx.x;
+#pragma unroll
+                for (int i = 0; i < NB * PB; ++i) {
+                    m[(2 * i) * 256] = make_float2(h[i][0], h[i][1]);
+                    m[(2 * i + 1) * 256] = make_float2(h[i][2], h[i][3]);
+                }
+            }
+        }
+        // (the sum over the blocks of columns of a group follows in ssm_sum_kernel)
+        const int slot = chunk_slot(p, seg, c);
+        if (slot < p.n_slots) {
+            float2 *part = (float2 *)p.part + ((int64_t)slot * p.n_hb + hb) * (NB * 8 * 256) + threadIdx.x;
+#pragma unroll
+            for (int i = 0; i < NB * 4; ++i) {
+                part[(2 * i) * 256] = make_float2(z[i][0], z[i][1]);
+                part[(2 * i + 1) * 256] = make_float2(z[i][2], z[i][3]);
+            }
+        }
+    }
+}
+
+// out2 of a chunk and group: the sum over the group's blocks of columns, in
+// the lanes' own layout.
+template <typename IO, int N, bool REV>
+__global__ void __launch_bounds__(256) ssm_sum_kernel(SsmParams p) {
+    constexpr int NB = N / 64;
+    const int cps = p.seg_tokens / kSsmChunk, G = p.H / p.heads_per_group;
+    const int g = blockIdx.x % G, c = blockIdx.x / G % cps, item = blockIdx.x / G / cps;
+    const Segment seg = find_segment(p, item);
+    if (!seg.live || c >= chunks_of(seg)) return;
+    const int slot = chunk_slot(p, seg, c);
+    if (slot >= p.n_slots) return;
+    const int w = wave_id(), l = lane_id(), q = l >> 4, j = l & 15, per = p.n_hb / G;
+    float4v z[NB * 4];
+#pragma unroll
+    for (int i = 0; i < NB * 4; ++i) z[i] = float4v{0.f, 0.f, 0.f, 0.f};
+    const float2 *part = (const float2 *)p.part + ((int64_t)slot * p.n_hb + g * per) * (NB * 8 * 256) + threadIdx.x;
+    for (int k = 0; k < per; ++k, part += NB * 8 * 256) {
+#pragma unroll
+        for (int i = 0; i < NB * 4; ++i) {
+            const float2 a = part[(2 * i) * 256], b = part[(2 * i + 1) * 256];
+            z[i] += float4v{a.x, a.y, b.x, b.y};
+        }
+    }
+    int lo;
+    const int rows = chunk_of<REV>(seg, c, lo);
+    const rsrc_t r = make_rsrc((IO *)p.out + seg.batch * p.ob + lo * p.ot + (int64_t)g * N, 0x7fffffffu);
+#pragma unroll
+    for (int nb = 0; nb < NB; ++nb)
+#pragma unroll
+        for (int bi = 0; bi < 4; ++bi) {
+            const int ii = 16 * bi + j, t = REV ? rows - 1 - ii : ii;
+            const uint32_t e = (uint32_t)t * (uint32_t)p.ot + w * (N / 4) + 16 * nb + 4 * q;
+            store_row4<IO>(r, ii < rows ? e * (uint32_t)sizeof(IO) : 0xfffffff0u, z[nb * 4 + bi]);
+        }
+}
+
+// The gradients of a segment's gates, one head a workgroup, a chunk a wave
+// (see gdn_ssm.h): ddt_t = c_t + A dg_t, through softplus; dA += dt_t dg_t.
+struct GateParams {
+    SsmParams s;                          // the forward scan's
+    const float *c_inside, *c_across;     // the reverse scan's sums
+    void *ddt;
+    double *grads;                        // [item][H][3]: dA, d(dt_bias), dD
+    float *dA, *dD, *dbias;
+    int ncb;
+};
+
+__device__ __forceinline__ double block_sum(double v, double *red) {
+#pragma unroll
+    for (int m = 1; m < 64; m <<= 1) v += __shfl_xor(v, m, 64);
+    __syncthreads();
+    if (lane_id() == 0) red[wave_id()] = v;
+    __syncthreads();
+    return red[0] + red[1] + red[2] + red[3];
+}
+
+template <typename IO>
+__global__ void __launch_bounds__(256) ssm_gate_kernel(GateParams gp) {
+    const SsmParams &p = gp.s;
+    __shared__ double red[4], wsum[4][5];
+    const int head = blockIdx.x % p.H, item = blockIdx.x / p.H, tid = threadIdx.x;
+    const Segment seg = find_segment(p, item);
+    if (!seg.live) {
+        // a place that no segment has
+        if (tid < 3) gp.grads[((int64_t)item * p.H + head) * 3 + tid] = 0.0;
+        return;
+    }
+    const int cols = 64 * gp.ncb, per_hb = cols / p.P;          // heads of a block of columns (0: a part of one)
+    const int hb0 = head * p.P / cols, tiles = per_hb ? 1 : p.P / cols, hh = per_hb ? head % per_hb : 0;
+    const float A = p.A[head], bias = p.bias ? p.bias[head] : 0.f;
+    double dA = 0.0, dD = 0.0, db = 0.0;
+    double x = 0.0;                           // X at the end of the chunk at hand
+    const int w = wave_id(), l = lane_id();
+    for (int c0 = chunks_of(seg) - 1; c0 >= 0; c0 -= 4) {
+        // wave w takes chunk c0 - w
+        const int t = seg.begin + (c0 - w) * kSsmChunk + l;
+        const bool on = c0 >= w && t < seg.end;
+        float ri = 0.f, ra = 0.f, ci = 0.f, ca = 0.f, dd = 0.f, wtt = 0.f, raw = 0.f;
+        if (on) {
+            for (int k = 0; k < tiles; ++k) {
+                const int64_t at = ((int64_t)(hb0 + k) * gp.ncb + hh) * p.rows + (int64_t)seg.batch * p.T + t;
+                ri += p.inside[at];
+                ra += p.across[at];
+                ci += gp.c_inside[at];
+                ca += gp.c_across[at];
+                dd += p.dyx[at];
+                wtt += p.wtt[at];
+            }
+            const int64_t at = seg.batch * p.db + t * p.dt_ + head;
+            raw = (p.dt_f32 ? ((const float *)p.dt)[at] : io_traits<IO>::load((const IO *)p.dt + at)) + bias;
+        }
+        const float dt = on ? (p.softplus ? softplus(raw) : raw) : 0.f;
+        const double dca = (double)dt * (double)ca, in = (double)ri - (double)dt * (double)ci + (double)ra;
+        const double pre_in = wave_scan(in), pre_ca = wave_scan(dca), pre_ra = wave_scan((double)ra);
+        const double all_in = __shfl(pre_in, 63, 64), all_ca = __shfl(pre_ca, 63, 64), all_ra = __shfl(pre_ra, 63, 64);
+        // nothing of weight crosses a chunk whose decay is below fp32's step
+        const bool cut = (float)__shfl(wave_scan((double)dt * (double)A), 63, 64) < -16.6f;
+        __syncthreads();
+        if (l == 0) {
+            const int mark = c0 >= w ? mark_slot(p, seg, c0 - w) : -1;
+            wsum[w][0] = all_ca;
+            wsum[w][1] = all_ra;
+            wsum[w][2] = cut ? 0.0 : 1.0;
+            wsum[w][3] = mark >= 0 ? 1.0 : 0.0;
+            double m = 0.0;
+            for (int k = 0; mark >= 0 && k < tiles; ++k) m += p.X[((int64_t)mark * p.n_hb + hb0 + k) * gp.ncb + hh];
+            wsum[w][4] = m;
+        }
+        __syncthreads();
+        double Q = 0.0;
+        for (int k = 0; k < 4; ++k) {
+            if (wsum[k][3] != 0.0) x = wsum[k][4];
+            const double qk = wsum[k][2] * (x - wsum[k][0]);
+            if (k == w) Q = qk;
+            x = qk + wsum[k][1];
+        }
+        if (on) {
+            const double dg = (all_in - pre_in + in) + (pre_ca - dca) + Q;
+            double g = (double)ci + (double)ca + (double)wtt + (double)A * dg;
+            if (p.softplus) g /= 1.0 + (double)expf(-raw);
+            const int64_t at = ((int64_t)seg.batch * p.T + t) * p.H + head;
+            if (p.dt_f32)
+                ((float *)gp.ddt)[at] = (float)g;
+            else
+                io_traits<IO>::store((IO *)gp.ddt + at, (float)g);
+            dA += (double)dt * dg;
+            db += g;
+            dD += (double)dd;
+        }
+    }
+    dA = block_sum(dA, red);
+    db = block_sum(db, red);
+    dD = block_sum(dD, red);
+    if (tid == 0) {
+        double *o = gp.grads + ((int64_t)item * p.H + head) * 3;
+        o[0] = dA;
+        o[1] = db;
+        o[2] = dD;
+    }
+}
+
+// dA, d(dt_bias) and dD of a head: the sums over the segments, a head a wave.
+__global__ void __launch_bounds__(64) ssm_head_kernel(GateParams gp) {
+    const SsmParams &p = gp.s;
+    const int head = blockIdx.x;
+    double a[3] = {0.0, 0.0, 0.0};
+    for (int i0 = 0; i0 < p.n_items; i0 += 64) {
+        const int i = i0 + lane_id();
+        if (i < p.n_items)
+            for (int k = 0; k < 3; ++k) a[k] += gp.grads[((int64_t)i * p.H + head) * 3 + k];
+    }
+#pragma unroll
+    for (int k = 0; k < 3; ++k)
+#pragma unroll
+        for (int m = 1; m < 64; m <<= 1) a[k] += __shfl_xor(a[k], m, 64);
+    if (lane_id() == 0) {
+        gp.dA[head] = (float)a[0];
+        if (gp.dbias) gp.dbias[head] = (float)a[1];
+        if (gp.dD) gp.dD[head] = (float)a[2];
+    }
+}
+
+namespace {
+
+struct BwdPlan {
+    SsmPlan s;
+    int64_t slots, marks, rows;
+    size_t total, ends, ends_rev, sums[6], mark, X, part, grads, bytes;      // offsets
+};
+
+BwdPlan bwd_plan(const gdn_ssm_problem *pr, bool packed) {
+    BwdPlan b;
+    b.s = ssm_plan(pr, packed);
+    b.rows = pr->B * pr->T;
+    b.slots = packed ? pr->T / kSsmChunk + pr->n_seqs + 1 : pr->B * ((pr->T + kSsmChunk - 1) / kSsmChunk);
+    const int64_t per = 4 * kSsmChunk;
+    b.marks = packed ? pr->T / per + pr->n_seqs + 1 : pr->B * ((pr->T + per - 1) / per);
+    const size_t blocks = (size_t)b.s.n_items * b.s.n_hb;
+    size_t at = 0;
+    auto take = [&](size_t n) {
+        const size_t was = at;
+        at += (n + 15) / 16 * 16;
+        return was;
+    };
+    b.total = take(blocks * b.s.ncb * 8);
+    b.ends = take(blocks * pr->N * 64 * b.s.ncb * 4);
+    b.ends_rev = take(blocks * pr->N * 64 * b.s.ncb * 4);
+    for (size_t &o : b.sums) o = take((size_t)b.s.n_hb * b.s.ncb * b.rows * 4);
+    b.mark = take((size_t)b.marks * b.s.n_hb * pr->N * 64 * b.s.ncb * 4);
+    b.X = take((size_t)b.marks * b.s.n_hb * b.s.ncb * 8);
+    b.part = take((size_t)b.slots * b.s.n_hb * kSsmChunk * pr->N * 4);
+    b.grads = take((size_t)b.s.n_items * pr->H * 3 * 8);
+    b.bytes = at;
+    return b;
+}
+
+template <typename IO, int N, int NCB>
+struct BwdFns {
+    static const void *ends(bool rev) {
+        return rev ? (const void *)&ssm_scan_kernel<IO, N, NCB, true, true, 3> : (const void *)&ssm_scan_kernel<IO, N, NCB, true, false, 3>;
+    }
+    static const void *dx() { return (const void *)&ssm_scan_kernel<IO, N, NCB, false, true, 2>; }
+    static const void *key(bool rev) {
+        return rev ? (const void *)&ssm_key_kernel<IO, N, NCB, true> : (const void *)&ssm_key_kernel<IO, N, NCB, false>;
+    }
+    static const void *sum(bool rev) {
+        return rev ? (const void *)&ssm_sum_kernel<IO, N, true> : (const void *)&ssm_sum_kernel<IO, N, false>;
+    }
+};
+
+template <typename F>
+gdn_status bwd_launches(const gdn_ssm_problem *pr, const BwdPlan &b, const SsmParams &fwd, const SsmParams &rev, GateParams &gp,
+                        void *dx, void *dB, void *dC, float *dh0, hipStream_t s) {
+    const bool one = b.s.n_items == b.s.seqs;      // one segment each
+    SsmParams f = fwd, r = rev;
+    const int grid = ssm_grid(f, b.s);
+    ssm_grid(r, b.s);
+    gdn_status st = GDN_OK;
+    auto go = [&](const void *fn, int g, SsmParams &sp) {
+        if (st == GDN_OK) st = launch_kernel(fn, g, &sp, s);
+    };
+    if (!one) {
+        go(F::ends(false), grid, f);
+        go(F::ends(true), grid, r);
+    }
+    SsmParams d = r;
+    d.out = dx;
+    d.sT = dh0;
+    go(F::dx(), grid, d);
+    const int sgrid = b.s.n_items * (b.s.seg_tokens / kSsmChunk) * (int)pr->G;
+    f.out = dC;
+    go(F::key(false), grid, f);
+    go(F::sum(false), sgrid, f);
+    r.out = dB;
+    go(F::key(true), grid, r);
+    go(F::sum(true), sgrid, r);
+    if (st != GDN_OK) return st;
+    gp.s = f;
+    return GDN_OK;
+}
+
+}  // namespace
+}  // namespace gdn
+
+using namespace gdn;
+
+extern "C" {
+
+size_t gdn_workspace_bytes_ssm_backward(const gdn_ssm_problem *pr) {
+    const bool packed = pr && pr->n_seqs > 0;
+    if (check_ssm(pr, packed) != GDN_OK) return 0;
+    return bwd_plan(pr, packed).bytes;
+}
+
+gdn_status gdn_ssm_backward(const gdn_ssm_problem *pr, const void *dy, const void *x, const void *dt, const float *A,
+                            const void *Bm, const void *Cm, const float *D, const float *dt_bias, const float *h0,
+                            const int32_t *cu_seqlens, const float *dhT, void *dx, void *ddt, float *dA, void *dB,
+                            void *dC, float *dD, float *ddt_bias, float *dh0, void *workspace, size_t workspace_bytes,
+                            void *stream) {
+    gdn_status st = check_ssm(pr, cu_seqlens != nullptr);
+    if (st != GDN_OK) return st;
+    if (!A || !dA) return GDN_ERR_NULL_ARG;
+    const int64_t eb = dtype_bytes(pr->io_dtype);
+    if (pr->T > 0) {
+        st = check_ssm_pointers(pr, x, dt, A, Bm, Cm, D, dt_bias, true);
+        if (st != GDN_OK) return st;
+        if (!dy || !dx || !ddt || !dB || !dC) return GDN_ERR_NULL_ARG;
+        if (pr->dxbc_stride_b * eb % 16 || pr->dxbc_stride_t * eb % 16) return GDN_ERR_ALIGNMENT;
+    }
+    for (const void *q : {dy, (const void *)dx, (const void *)dB, (const void *)dC, (const void *)workspace})
+        if (!aligned_to(q, 16)) return GDN_ERR_ALIGNMENT;
+    for (const void *q : {(const void *)A, (const void *)D, (const void *)dt_bias, (const void *)h0, (const void *)dhT, (const void *)dA,
+                          (const void *)dD, (const void *)ddt_bias, (const void *)dh0, (const void *)cu_seqlens})
+        if (!aligned_to(q, 4)) return GDN_ERR_ALIGNMENT;
+    if (!aligned_to(ddt, dtype_bytes(pr->dt_dtype))) return GDN_ERR_ALIGNMENT;
+    const BwdPlan b = bwd_plan(pr, cu_seqlens != nullptr);
+    if (!workspace || workspace_bytes < b.bytes) return GDN_ERR_WORKSPACE;
+    char *ws = (char *)workspace;
+    SsmParams f;
+    fill_ssm(pr, f);
+    f.dt = dt;
+    f.A = A;
+    f.D = D;
+    f.bias = dt_bias;
+    f.cu = cu_seqlens;
+    f.total = (double *)(ws + b.total);
+    f.part = (float *)(ws + b.part);
+    f.n_slots = (int)b.slots;
+    f.marks = (float *)(ws + b.mark);
+    f.X = (double *)(ws + b.X);
+    f.n_marks = (int)b.marks;
+    f.rows = b.rows;
+    f.ob = pr->dxbc_stride_b;
+    f.ot = pr->dxbc_stride_t;
+    SsmParams r = f;
+    const int64_t yt = pr->H * pr->P, yb = yt * pr->T;
+    f.q = Cm;
+    f.k = Bm;
+    f.v = x;
+    f.vb = pr->x_stride_b;
+    f.vt = pr->x_stride_t;
+    f.q2 = dy;
+    f.q2b = yb;
+    f.q2t = yt;
+    f.s0 = h0;
+    f.ends = (float *)(ws + b.ends);
+    f.inside = (float *)(ws + b.sums[0]);
+    f.across = (float *)(ws + b.sums[1]);
+    f.dyx = (float *)(ws + b.sums[2]);
+    f.wtt = (float *)(ws + b.sums[3]);
+    r.q = Bm;
+    r.k = Cm;
+    r.v = dy;
+    r.vb = yb;
+    r.vt = yt;
+    r.q2 = x;
+    r.q2b = pr->x_stride_b;
+    r.q2t = pr->x_stride_t;
+    r.s0 = dhT;
+    r.ends = (float *)(ws + b.ends_rev);
+    r.inside = (float *)(ws + b.sums[4]);
+    r.across = (float *)(ws + b.sums[5]);
+    GateParams gp{};
+    gp.c_inside = r.inside;
+    gp.c_across = r.across;
+    gp.ddt = ddt;
+    gp.grads = (double *)(ws + b.grads);
+    gp.dA = dA;
+    gp.dD = dD;
+    gp.dbias = ddt_bias;
+    gp.ncb = b.s.ncb;
+    hipStream_t s = (hipStream_t)stream;
+    if (pr->io_dtype == GDN_F32)
+        st = pr->N == 64 ? bwd_launches<BwdFns<float, 64, 1>>(pr, b, f, r, gp, dx, dB, dC, dh0, s)
+                         : bwd_launches<BwdFns<float, 128, 1>>(pr, b, f, r, gp, dx, dB, dC, dh0, s);
+    else if (b.s.ncb == 1)
+        st = pr->N == 64 ? bwd_launches<BwdFns<bf16_t, 64, 1>>(pr, b, f, r, gp, dx, dB, dC, dh0, s)
+                         : bwd_launches<BwdFns<bf16_t, 128, 1>>(pr, b, f, r, gp, dx, dB, dC, dh0, s);
+    else
+        st = pr->N == 64 ? bwd_launches<BwdFns<bf16_t, 64, 2>>(pr, b, f, r, gp, dx, dB, dC, dh0, s)
+                         : bwd_launches<BwdFns<bf16_t, 128, 2>>(pr, b, f, r, gp, dx, dB, dC, dh0, s);
+    if (st != GDN_OK) return st;
+    const void *fn = pr->io_dtype == GDN_F32 ? (const void *)&ssm_gate_kernel<float> : (const void *)&ssm_gate_kernel<bf16_t>;
+    st = launch_kernel(fn, b.s.n_items * (int)pr->H, &gp, s);
+    if (st != GDN_OK) return st;
+    return launch_kernel((const void *)&ssm_head_kernel, (int)pr->H, &gp, s, 64);
+}
+
+}  // extern "C"

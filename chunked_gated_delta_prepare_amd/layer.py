@@ -27,7 +27,8 @@ import torch
 GDN_E4M3 = 2
 LAYER_EXPORTS = ["gdn_norm_forward", "gdn_norm_backward", "gdn_workspace_bytes_norm_backward",
                  "gdn_conv_forward", "gdn_conv_backward", "gdn_workspace_bytes_conv_backward",
-                 "gdn_conv_step", "gdn_ssm_forward", "gdn_workspace_bytes_ssm", "gdn_ssm_step"]
+                 "gdn_conv_step", "gdn_ssm_forward", "gdn_workspace_bytes_ssm", "gdn_ssm_backward",
+                 "gdn_workspace_bytes_ssm_backward", "gdn_ssm_step"]
 
 _I64, _I32, _F32 = ctypes.c_int64, ctypes.c_int32, ctypes.c_float
 
@@ -65,8 +66,9 @@ def declare(lib):
     lib.gdn_conv_backward.argtypes = [c] + [vp] * 12 + [sz, vp]
     lib.gdn_conv_step.argtypes = [c] + [vp] * 5 + [i64, vp, vp]
     lib.gdn_ssm_forward.argtypes = [s] + [vp] * 12 + [sz, vp]
+    lib.gdn_ssm_backward.argtypes = [s] + [vp] * 20 + [sz, vp]
     lib.gdn_ssm_step.argtypes = [s] + [vp] * 9 + [i64, vp, vp]
-    for name, arg in (("norm_backward", n), ("conv_backward", c), ("ssm", s)):
+    for name, arg in (("norm_backward", n), ("conv_backward", c), ("ssm", s), ("ssm_backward", s)):
         f = getattr(lib, "gdn_workspace_bytes_" + name)
         f.argtypes, f.restype = [arg], sz
     for name in LAYER_EXPORTS:
@@ -483,6 +485,65 @@ def ssm_forward(x, dt, A, B, C, D=None, dt_bias=None, h0=None, *, dt_softplus=Tr
         _call("gdn_ssm_forward", ctypes.byref(pr), _ptr(x), _ptr(dt), _ptr(A), _ptr(B), _ptr(C), _ptr(D),
               _ptr(dt_bias), _ptr(h0), _ptr(cu_seqlens), _ptr(y), _ptr(hT), _ptr(workspace), size, handle)
     return y, hT
+
+
+def ssm_backward(dy, x, dt, A, B, C, D=None, dt_bias=None, h0=None, dhT=None, *, dt_softplus=True,
+                 cu_seqlens=None, dx=None, ddt=None, dA=None, dB=None, dC=None, dD=None, ddt_bias=None, dh0=None,
+                 workspace=None, stream=None):
+    """The scan's gradients for dy [b, T, H, P] and dhT (of the final states,
+    or None); the states are formed again from the inputs.  Returns (dx, ddt,
+    dA, dB, dC, dD, ddt_bias, dh0): dx, dB and dC in x's type, ddt in dt's, the
+    others fp32; dD, ddt_bias and dh0 are None where D, dt_bias and h0 are.
+    dx, dB and dC may be given as parts of one buffer (with the same strides
+    between tokens), as the gradient of a convolution's output."""
+    dev, code, H, P, G, N = _ssm_checks(x, dt, A, B, C, D, dt_bias, 2)
+    b, T = x.shape[:2]
+    n = _packed(cu_seqlens, dev, b)
+    st = (n or b, H, N, P)
+    _check(dy, "dy", dev, x.shape, x.dtype)
+    for t, name in ((h0, "h0"), (dhT, "dhT")):
+        if t is not None:
+            _check(t, name, dev, st, torch.float32)
+    lib = _library()
+    ins = (dy, x, dt, A, B, C, D, dt_bias, h0, dhT, cu_seqlens)
+    with _On(dev, stream) as handle:
+        given = [t is not None for t in (dx, dB, dC)]
+        if any(given):
+            if not all(given):
+                raise ValueError("dx, dB and dC are given together or not at all")
+            for t, name, like in ((dx, "dx", x), (dB, "dB", B), (dC, "dC", C)):
+                _check(t, name, dev, like.shape, x.dtype, dense=False)
+            grads = _strides(dx, "dx")
+            if any(_strides(t, name) != grads for t, name in ((dB, "dB"), (dC, "dC"))):
+                raise ValueError("dx, dB and dC must have the same strides between batches and tokens")
+            lo = min(t.data_ptr() for t in (dx, dB, dC))
+            for t in ins:
+                if t is not None and t.numel() and T and lo < t.data_ptr() + t.numel() * t.element_size():
+                    for o, name in ((dx, "dx"), (dB, "dB"), (dC, "dC")):
+                        _apart(o, name, t)
+        else:
+            # side by side, as the convolution that feeds the scan laid them out
+            both = torch.empty(b, T, H * P + 2 * G * N, device=dev, dtype=x.dtype)
+            dx = both[..., :H * P].unflatten(-1, (H, P))
+            dB = both[..., H * P:H * P + G * N].unflatten(-1, (G, N))
+            dC = both[..., H * P + G * N:].unflatten(-1, (G, N))
+            grads = _strides(dx, "dx")
+        ddt = _out(ddt, "ddt", dev, (b, T, H), dt.dtype, ins)
+        dA = _out(dA, "dA", dev, (H,), torch.float32, ins)
+        if D is not None:
+            dD = _out(dD, "dD", dev, (H,), torch.float32, ins)
+        if dt_bias is not None:
+            ddt_bias = _out(ddt_bias, "ddt_bias", dev, (H,), torch.float32, ins)
+        if h0 is not None:
+            dh0 = _out(dh0, "dh0", dev, st, torch.float32, ins)
+        pr = _ssm_problem(x, dt, B, C, code, dt_softplus, n, grads)
+        workspace, size = _workspace(int(lib.gdn_workspace_bytes_ssm_backward(ctypes.byref(pr))), dev, workspace)
+        _call("gdn_ssm_backward", ctypes.byref(pr), _ptr(dy), _ptr(x), _ptr(dt), _ptr(A), _ptr(B), _ptr(C), _ptr(D),
+              _ptr(dt_bias), _ptr(h0), _ptr(cu_seqlens), _ptr(dhT), _ptr(dx), _ptr(ddt), _ptr(dA), _ptr(dB), _ptr(dC),
+              _ptr(dD) if D is not None else None, _ptr(ddt_bias) if dt_bias is not None else None,
+              _ptr(dh0) if h0 is not None else None, _ptr(workspace), size, handle)
+    return (dx, ddt, dA, dB, dC, dD if D is not None else None, ddt_bias if dt_bias is not None else None,
+            dh0 if h0 is not None else None)
 
 
 def ssm_step(x, dt, A, B, C, state, D=None, dt_bias=None, *, dt_softplus=True, slots=None, y=None, stream=None):

@@ -175,7 +175,7 @@ typedef struct gdn_ssm_problem {
 /*
  * gdn_ssm_forward -- y [B, T, H, P] (dense) and the final states.
  *   A [H] fp32; D, dt_bias [H] fp32 or NULL (zero); h0, hT [B, H, N, P] fp32
- *   ([n_seqs, H, N, P] with cu_seqlens) or NULL; hT may alias h0.
+ *   ([n_seqs, H, N, P] with cu_seqlens) or NULL.
  *   cu_seqlens as in gdn_conv_forward; rows of y that belong to no sequence
  *   are left as they were.
  * Workspace: gdn_workspace_bytes_ssm(problem) bytes (may be 0), 16-byte
@@ -187,6 +187,23 @@ gdn_status gdn_ssm_forward(const gdn_ssm_problem *problem, const void *x, const 
                            void *y, float *hT, void *workspace, size_t workspace_bytes,
                            void *stream);
 size_t gdn_workspace_bytes_ssm(const gdn_ssm_problem *problem);
+
+/*
+ * gdn_ssm_backward -- the gradients for dy [B, T, H, P] (dense) and dhT (the
+ * final states' gradient, or NULL): dx, dB, dC in the io type (strides
+ * dxbc_stride_*), ddt [B, T, H] dense in dt's type, dA, dD, ddt_bias [H] fp32
+ * (dD, ddt_bias may be NULL), dh0 fp32 like h0 (or NULL).  With cu_seqlens,
+ * dx, dB, dC and ddt of rows that belong to no sequence are left as they
+ * were.  Workspace: gdn_workspace_bytes_ssm_backward(problem) bytes, 16-byte
+ * aligned.
+ */
+gdn_status gdn_ssm_backward(const gdn_ssm_problem *problem, const void *dy, const void *x,
+                            const void *dt, const float *A, const void *Bm, const void *Cm,
+                            const float *D, const float *dt_bias, const float *h0,
+                            const int32_t *cu_seqlens, const float *dhT, void *dx, void *ddt,
+                            float *dA, void *dB, void *dC, float *dD, float *ddt_bias,
+                            float *dh0, void *workspace, size_t workspace_bytes, void *stream);
+size_t gdn_workspace_bytes_ssm_backward(const gdn_ssm_problem *problem);
 
 /*
  * gdn_ssm_step -- one token for each of B sequences (T = 1): y [B, H, P], and
