@@ -40,8 +40,11 @@ __device__ __forceinline__ void row_load(rsrc_t r, uint32_t e, float (&x)[VEC]) 
     }
 }
 
+// two floats as bf16, in one instruction
 __device__ __forceinline__ uint32_t pack_bf16(float a, float b) {
-    return (uint32_t)f32_to_bf16_bits(a) | ((uint32_t)f32_to_bf16_bits(b) << 16);
+    typedef float float2v __attribute__((ext_vector_type(2)));
+    typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
+    return __builtin_bit_cast(uint32_t, __builtin_convertvector(float2v{a, b}, bf16x2));
 }
 
 __device__ __forceinline__ float swap_pair(float x) {      // the value of lane ^ 1
@@ -75,6 +78,15 @@ __device__ __forceinline__ void row_load_either(rsrc_t r, bool f32, uint32_t e, 
         row_load<float, VEC>(r, e, x);
     else
         row_load<T, VEC>(r, e, x);
+}
+
+// A workgroup barrier that orders LDS only: global loads in flight (the next
+// chunk's rows) and stores stay in flight, which __syncthreads would wait for.
+__device__ __forceinline__ void lds_barrier() {
+    asm volatile("" ::: "memory");
+    __builtin_amdgcn_s_waitcnt(kWaitLgkm0);
+    __builtin_amdgcn_s_barrier();
+    asm volatile("" ::: "memory");
 }
 
 // ---------------------------------------------------------------------------

@@ -89,61 +89,129 @@ struct SsmParams {
     int softplus, swizzle, dt_f32;
 };
 
+// x, unknown to the compiler: what is computed from it inside a loop stays
+// there.  Addresses of swizzled tiles, taken out of the chunk loop, would hold
+// some forty registers a lane.
+__device__ __forceinline__ int again(int x) {
+    asm volatile("" : "+v"(x));
+    return x;
+}
+
+// Element (row, col) of a row-major tile of LD elements in LDS: 16-byte chunk c
+// of row r sits at chunk c ^ s(r), s linear over r mod 16's bits.  Of the 2^16
+// such maps, timed with eight waves reading at once, these cost a fragment
+// read of 16 bytes a lane and transposed reads of two and of four chunks the
+// least there is (4.3, 4.3 and 3.4 cycles a wave's read; r's bits in order
+// cost 4.3, 8.2 and 4.3, and no map at all 32, 16 and 16).
+template <int CHUNKS>
+__device__ __forceinline__ constexpr int swizzle(int r) {
+    if (CHUNKS == 8) return ((r & 1) ? 7 : 0) ^ ((r & 2) ? 6 : 0) ^ ((r & 8) ? 2 : 0);
+    return ((r & 1) ? 4 : 0) ^ ((r & 2) ? 2 : 0) ^ ((r & 4) ? 9 : 0) ^ ((r & 8) ? 8 : 0);
+}
+template <typename E, int LD>
+__device__ __forceinline__ int at(int row, int col) {
+    constexpr int kPer = 16 / sizeof(E);
+    return row * LD + (((col / kPer) ^ swizzle<LD / kPer>(row)) * kPer) + col % kPer;
+}
+
+// A lane's byte offsets into tiles of LD elements, from which a fragment's
+// are an xor with its first column and an addition of its first row (see at:
+// rows come in multiples of 16, and a column's high bits do not meet the
+// lane's low ones).  Kept out of the compiler's sight once a chunk, so that it
+// does not keep every fragment's offset in a register of its own.
+template <typename E, int LD> struct Lane {
+    int row, tr2, tr4;
+};
+template <int LD> struct Lane<uint16_t, LD> {
+    static constexpr int kFour = swizzle<LD / 8>(4) << 4;      // what four rows on changes
+    int row, tr2, tr4;         // fragments of rows; transposed reads of two and of four chunks
+    __device__ explicit Lane(int l) {
+        const int q = l >> 4, j = l & 15, r = 8 * q + (j >> 2), s = swizzle<LD / 8>(r), c = j & 3;
+        row = again(j * LD * 2 + ((q ^ swizzle<LD / 8>(j)) << 4));
+        tr2 = again(r * LD * 2 + (((c >> 1) ^ s) << 4) + (c & 1) * 8);
+        tr4 = again(r * LD * 2 + ((c ^ s) << 4));
+    }
+};
+template <int LD> struct Lane<float, LD> {
+    int l;
+    __device__ explicit Lane(int lane) : l(again(lane)) {}
+};
+
 // Operands of the matrix cores by io type: bf16 products for bf16 io, fp32
 // products for fp32 io.  Both take eight k slots a lane.
+//
+// row: lane (q, j) gets S[m0 + j][k0 + 8 q .. +7].
+// col: S[k0 + 8 q + e][m0 + j], e = 0..7: rows of the transpose.
+// pair: as col, but for the 16 columns that half `hf` of a block of 32 takes
+// in accumulators: lane j gets column m0 + 8 (j / 4) + 4 hf + j % 4, so that
+// accumulators of both halves hold, in lane group q, rows m0 + 8 q .. +7 of
+// their product, which are the slots of a row fragment.
 template <typename IO> struct SOp;
 
 template <> struct SOp<bf16_t> {
     typedef uint16_t elem;
     typedef bf16x8 frag;
-    static constexpr int kPad = 8;
     template <int PARTS> static constexpr int kParts = PARTS;
-    __device__ static frag bits(u32x2 a, u32x2 b) { return __builtin_bit_cast(frag, u32x4{a[0], a[1], b[0], b[1]}); }
     __device__ static void mma(float4v &acc, const frag &a, const frag &b) {
         acc = __builtin_amdgcn_mfma_f32_16x16x32_bf16(a, b, acc, 0, 0, 0);
     }
-    // S[row][k0 + 8 q ..] of a row-major S
-    __device__ static frag row(const elem *S, int ld, int m0, int k0) {
-        const int l = lane_id();
-        return __builtin_bit_cast(frag, *(const u32x4 *)(S + (m0 + (l & 15)) * ld + k0 + 8 * (l >> 4)));
+    template <int LD>
+    __device__ static frag row(const elem *S, const Lane<elem, LD> &a, int m0, int k0) {
+        return __builtin_bit_cast(frag, *(const u32x4 *)((const char *)S + (a.row ^ (k0 * 2)) + m0 * LD * 2));
     }
-    // S[k0 + 8 q + e][m0 + j] of a row-major S (its transpose's rows)
-    __device__ static frag col(const elem *S, int ld, int m0, int k0) {
-        const int l = lane_id(), q = l >> 4;
-        // (read_T4 takes rows 4 q ..; slots 8 q .. need rows 8 q ..)
-        return bits(read_T4(S + (k0 + 4 * q) * ld, ld, m0), read_T4(S + (k0 + 4 * q + 4) * ld, ld, m0));
+    // two transposed reads of four rows each; lane L of a group of 16 fetches
+    // row L / 4, and columns c(L % 4) .. +3, which lanes 4 (L % 4) .. +3 get
+    template <int LD>
+    __device__ static frag tr(const elem *S, int off, int plus) {
+        typedef __fp16 v4fp16 __attribute__((vector_size(8)));
+        typedef __attribute__((address_space(3))) v4fp16 lds_v4fp16;
+        const char *p = (const char *)S + off + plus, *r = (const char *)S + (off ^ Lane<elem, LD>::kFour) + plus + 4 * LD * 2;
+        const u32x2 a = __builtin_bit_cast(u32x2, __builtin_amdgcn_ds_read_tr16_b64_v4f16((lds_v4fp16 *)p));
+        const u32x2 b = __builtin_bit_cast(u32x2, __builtin_amdgcn_ds_read_tr16_b64_v4f16((lds_v4fp16 *)r));
+        return __builtin_bit_cast(frag, u32x4{a[0], a[1], b[0], b[1]});
     }
-    // split slots: S[m0 + j][k0 + 4 q ..] and S[..][k0 + 16 + 4 q ..]
-    __device__ static frag row_split(const elem *S, int ld, int m0, int k0) {
-        const int l = lane_id();
-        const elem *p = S + (m0 + (l & 15)) * ld + k0 + 4 * (l >> 4);
-        return bits(*(const u32x2 *)p, *(const u32x2 *)(p + 16));
+    template <int LD>
+    __device__ static frag col(const elem *S, const Lane<elem, LD> &a, int m0, int k0) {
+        return tr<LD>(S, a.tr2 ^ (m0 * 2), k0 * LD * 2);
+    }
+    template <int LD>
+    __device__ static frag pair(const elem *S, const Lane<elem, LD> &a, int m0, int hf, int k0) {
+        return tr<LD>(S, a.tr4 ^ (m0 * 2), k0 * LD * 2 + 8 * hf);
     }
     // an fp32 operand in PARTS bf16 ones, each holding what rounding left over
     // of those before: a relative error of 2^-9, 2^-18 or 2^-27 at most
     template <int PARTS>
     __device__ static void parts_of(const float (&v)[8], frag (&f)[PARTS]) {
+        u32x4 u[PARTS];
 #pragma unroll
-        for (int e = 0; e < 8; ++e) {
-            float x = v[e];
+        for (int i = 0; i < 4; ++i) {
+            float a = v[2 * i], b = v[2 * i + 1];
 #pragma unroll
             for (int k = 0; k < PARTS; ++k) {
-                f[k][e] = (__bf16)x;
-                x -= (float)f[k][e];
+                u[k][i] = pack_bf16(a, b);
+                a -= __uint_as_float(u[k][i] << 16);
+                b -= __uint_as_float(u[k][i] & 0xffff0000u);
             }
         }
+#pragma unroll
+        for (int k = 0; k < PARTS; ++k) f[k] = __builtin_bit_cast(frag, u[k]);
     }
+    // the accumulators of both halves of a block
     template <int PARTS>
-    __device__ static void acc_split(const float4v &lo, const float4v &hi, frag (&f)[PARTS]) {
+    __device__ static void acc(const float4v &lo, const float4v &hi, frag (&f)[PARTS]) {
         const float v[8] = {lo[0], lo[1], lo[2], lo[3], hi[0], hi[1], hi[2], hi[3]};
         parts_of(v, f);
     }
     // w .* a
     template <int PARTS>
     __device__ static void scaled(const frag &a, const float (&w)[8], frag (&f)[PARTS]) {
+        const u32x4 u = __builtin_bit_cast(u32x4, a);
         float v[8];
 #pragma unroll
-        for (int e = 0; e < 8; ++e) v[e] = (float)a[e] * w[e];
+        for (int i = 0; i < 4; ++i) {
+            v[2 * i] = __uint_as_float(u[i] << 16) * w[2 * i];
+            v[2 * i + 1] = __uint_as_float(u[i] & 0xffff0000u) * w[2 * i + 1];
+        }
         parts_of(v, f);
     }
     __device__ static void put4(elem *p, const float4v &v) {
@@ -161,14 +229,34 @@ template <> struct SOp<bf16_t> {
 template <> struct SOp<float> {
     typedef float elem;
     typedef Mma<float>::frag frag;
-    static constexpr int kPad = 4;
     template <int PARTS> static constexpr int kParts = 1;
     __device__ static void mma(float4v &acc, const frag &a, const frag &b) { Mma<float>::mma(acc, a, b); }
-    __device__ static frag row(const elem *S, int ld, int m0, int k0) { return Mma<float>::load(frag_ptr(S + m0 * ld, ld, k0)); }
-    __device__ static frag col(const elem *S, int ld, int m0, int k0) { return frag_T(S, ld, m0, k0); }
-    __device__ static frag row_split(const elem *S, int ld, int m0, int k0) { return fragA_split(S, ld, m0, k0); }
+    template <int LD>
+    __device__ static frag row(const elem *S, const Lane<elem, LD> &a, int m0, int k0) {
+        const int l = a.l, r = m0 + (l & 15), c = k0 + 8 * (l >> 4);
+        return frag{*(const float4v *)(S + at<elem, LD>(r, c)), *(const float4v *)(S + at<elem, LD>(r, c + 4))};
+    }
+    template <int LD>
+    __device__ static frag col_at(const elem *S, int c, int r) {
+        frag f;
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+            f.lo[e] = S[at<elem, LD>(r + e, c)];
+            f.hi[e] = S[at<elem, LD>(r + 4 + e, c)];
+        }
+        return f;
+    }
+    template <int LD>
+    __device__ static frag col(const elem *S, const Lane<elem, LD> &a, int m0, int k0) {
+        return col_at<LD>(S, m0 + (a.l & 15), k0 + 8 * (a.l >> 4));
+    }
+    template <int LD>
+    __device__ static frag pair(const elem *S, const Lane<elem, LD> &a, int m0, int hf, int k0) {
+        const int j = a.l & 15;
+        return col_at<LD>(S, m0 + 8 * (j >> 2) + 4 * hf + (j & 3), k0 + 8 * (a.l >> 4));
+    }
     template <int PARTS>
-    __device__ static void acc_split(const float4v &lo, const float4v &hi, frag (&f)[PARTS]) { f[0] = frag{lo, hi}; }
+    __device__ static void acc(const float4v &lo, const float4v &hi, frag (&f)[PARTS]) { f[0] = frag{lo, hi}; }
     template <int PARTS>
     __device__ static void scaled(const frag &a, const float (&w)[8], frag (&f)[PARTS]) {
 #pragma unroll
@@ -212,18 +300,26 @@ __device__ __forceinline__ double wave_scan(double v) {
     return v;
 }
 
-// A chunk's gates of one head, a lane a row.
-struct Gates {
+// A chunk's gates of one head, a lane a row.  (w is dt forward, 1 in reverse.)
+struct __align__(16) Gates {
     float2 cum[kSsmChunk];      // log2 of the decay from the chunk's start to the row
     float ecum[kSsmChunk];      // that decay
     float end[kSsmChunk];       // w times the decay from the row to the chunk's end
-    float w[kSsmChunk];
     float dt[kSsmChunk];
     double total;               // log2 of the whole chunk's decay
 };
 
-__device__ __forceinline__ float decay_between(const float2 &t, const float2 &s) {
-    return fast_exp2((t.x - s.x) + (t.y - s.y));
+// The decays from rows k .. k + 3 (k a multiple of 4) to row i, times the
+// weights w; 0 for rows behind i.
+template <bool REV>
+__device__ __forceinline__ float4v decays(const Gates &g, int i, int k) {
+    const float2 ci = g.cum[i];
+    const float4v a = *(const float4v *)&g.cum[k], b = *(const float4v *)&g.cum[k + 2];
+    float4v d = {(ci.x - a[0]) + (ci.y - a[1]), (ci.x - a[2]) + (ci.y - a[3]), (ci.x - b[0]) + (ci.y - b[1]), (ci.x - b[2]) + (ci.y - b[3])};
+#pragma unroll
+    for (int e = 0; e < 4; ++e) d[e] = k + e <= i ? fast_exp2(d[e]) : 0.f;
+    if constexpr (!REV) d *= *(const float4v *)&g.dt[k];
+    return d;
 }
 
 // dt of a token from its raw value (0 where there is no token).
@@ -234,14 +330,14 @@ __device__ __forceinline__ float dt_of(const SsmParams &p, float raw, float bias
 
 template <bool REV>
 __device__ __forceinline__ void make_gates(Gates &g, float dt, float A) {
-    const int l = lane_id();
+    const int l = again(lane_id());
+    asm volatile("" : "+s"(A));                // (its double is not kept in registers either)
     const double own = (double)dt * (double)A * 1.4426950408889634074, upto = wave_scan(own);
     const double total = __shfl(upto, 63, 64), cum = REV ? upto - own : upto;
     const float hi = (float)cum, w = REV ? 1.f : dt;
     g.cum[l] = make_float2(hi, (float)(cum - (double)hi));
     g.ecum[l] = fast_exp2(hi);
     g.end[l] = w * fast_exp2((float)(total - cum));
-    g.w[l] = w;
     g.dt[l] = dt;
     if (l == 63) g.total = total;
 }
@@ -324,27 +420,37 @@ __device__ __forceinline__ void place(const SsmParams &p, int &item, int &hb) {
     }
 }
 
+__device__ __forceinline__ float uniform(float x) {
+    return __int_as_float(__builtin_amdgcn_readfirstlane(__float_as_int(x)));
+}
+
 // 64 rows of COLS elements from HBM through registers into LDS, 16 bytes a
-// lane and step, in scan order (REV: from the last of `rows` to the first);
-// rows at or past `rows` as zeros.
-template <typename IO, int COLS, bool REV>
+// lane and step: rows at or past `rows` as zeros (they lie behind the
+// descriptor's end).  LDS has them in scan order (REV: the last row first).
+template <typename IO, int COLS, bool REV, int THREADS>
 struct TileRegs {
-    static constexpr int kPer = 16 / sizeof(IO), kLine = COLS / kPer, kN = kSsmChunk * kLine / 256;
+    typedef typename SOp<IO>::elem E;
+    static constexpr int kPer = 16 / sizeof(IO), kLine = COLS / kPer, kN = kSsmChunk * kLine / THREADS, kStep = THREADS / kLine;
     u32x4 v[kN];
-    __device__ __forceinline__ void load(const void *base, int64_t elems, uint32_t stride, int rows) {
-        const rsrc_t r = make_rsrc((const IO *)base + elems, 0x7fffffffu);
+    __device__ __forceinline__ void load(int tid, const void *base, int64_t elems, uint32_t stride, int rows) {
+        const rsrc_t r = make_rsrc((const IO *)base + elems, ((uint32_t)(rows - 1) * stride + COLS) * (uint32_t)sizeof(IO));
+        const uint32_t off = ((uint32_t)(tid / kLine) * stride + tid % kLine * kPer) * (uint32_t)sizeof(IO);
 #pragma unroll
-        for (int i = 0; i < kN; ++i) {
-            const int k = i * 256 + threadIdx.x, t = k / kLine, c = k % kLine * kPer;
-            const uint32_t off = ((REV ? rows - 1 - t : t) * stride + c) * (uint32_t)sizeof(IO);
-            v[i] = bload128(r, t < rows ? off : 0xfffffff0u, 0);
-        }
+        for (int i = 0; i < kN; ++i) v[i] = bload128(r, off + i * (kStep * stride * (uint32_t)sizeof(IO)), 0);
     }
-    __device__ __forceinline__ void put(typename SOp<IO>::elem *S, int ld) const {
+    __device__ __forceinline__ void put(int tid, E *S, int rows) const {
+        // a step of 16 rows or more keeps the swizzle
+        const int t = tid / kLine, c = tid % kLine * kPer;
+        if (kStep % 16 == 0 && (!REV || rows == kSsmChunk)) {
+            E *p = S + at<E, COLS>(REV ? kSsmChunk - 1 - t : t, c);
 #pragma unroll
-        for (int i = 0; i < kN; ++i) {
-            const int k = i * 256 + threadIdx.x, t = k / kLine, c = k % kLine * kPer;
-            *(u32x4 *)(S + t * ld + c) = v[i];
+            for (int i = 0; i < kN; ++i) *(u32x4 *)(p + (REV ? -i : i) * kStep * COLS) = v[i];
+        } else {
+#pragma unroll
+            for (int i = 0; i < kN; ++i) {
+                const int k = t + i * kStep;
+                *(u32x4 *)(S + at<E, COLS>(REV && k < rows ? rows - 1 - k : k, c)) = v[i];
+            }
         }
     }
 };
@@ -375,13 +481,19 @@ __device__ __forceinline__ int mark_slot(const SsmParams &p, const Segment &s, i
     return m < p.n_marks ? m : -1;
 }
 
-// The raw dt of row l of a chunk.
+// The raw dt of row l of a chunk, as its bits: turned into a number only where
+// it is used, since a conversion here would wait for every load in flight.
 template <typename IO, bool REV>
-__device__ __forceinline__ float raw_dt(const SsmParams &p, int batch, int head, int lo, int rows) {
-    const int l = lane_id();
-    if (l >= rows) return 0.f;
-    const int64_t at = batch * p.db + (lo + (REV ? rows - 1 - l : l)) * p.dt_ + head;
-    return p.dt_f32 ? ((const float *)p.dt)[at] : io_traits<IO>::load((const IO *)p.dt + at);
+__device__ __forceinline__ uint32_t raw_dt(const SsmParams &p, int batch, int head, int lo, int rows) {
+    const int l = again(lane_id());
+    const int64_t at = batch * p.db + lo * p.dt_ + head;
+    const uint32_t e = (uint32_t)((REV ? rows - 1 - l : l) * (int)p.dt_);
+    if (sizeof(IO) == 4 || p.dt_f32) return bload32(make_rsrc((const float *)p.dt + at, 0x7fffffffu), l < rows ? e * 4 : 0xfffffff0u, 0);
+    return bload16(make_rsrc((const uint16_t *)p.dt + at, 0x7fffffffu), l < rows ? e * 2 : 0xfffffff0u, 0);
+}
+template <typename IO>
+__device__ __forceinline__ float raw_value(const SsmParams &p, uint32_t bits) {
+    return __uint_as_float(sizeof(IO) == 4 || p.dt_f32 ? bits : bits << 16);
 }
 
 // For every segment that the scan passes before this one, nearest first:
@@ -401,9 +513,10 @@ __device__ __forceinline__ float segments_before(const SsmParams &p, const Segme
 }
 
 // ---------------------------------------------------------------------------
-// out1, the state, or both.  A wave keeps the state of its columns, all N
-// rows of them, in accumulators, and uses them as operands without a trip
-// through LDS.  Per chunk:
+// out1, the state, or both, for COLS columns of one head or (NH = 2) of two.
+// Wave w keeps the state of columns 16 w .. +15, all N rows of them, in
+// accumulators, and uses them as operands without a trip through LDS.  Per
+// chunk:
 //   1  the lower triangle of q k^T, times decays and weights, to LDS (16 x 16
 //      blocks, dealt to the waves); S^T q on the way
 //   2  out1 = M v + e^cum S^T q, transposed, so that a lane stores four columns
@@ -411,19 +524,25 @@ __device__ __forceinline__ float segments_before(const SsmParams &p, const Segme
 // The state's products take w v in PARTS bf16 parts: two (relative error 2^-18)
 // for a state that is an output and is read on by every later chunk, three
 // where it goes into dA, a sum over all tokens of both signs in which two
-// left errors of up to 5e-5.  out1's operands are rounded once to bf16,
-// its own type.  The next chunk's rows are in flight while one is worked on.
+// left errors of up to 5e-5.  out1's operands are rounded once to bf16, its
+// own type.  The next chunk's rows are in flight while one is worked on, and
+// its gates are formed by the waves with the fewest blocks.
 // ENDS: only the state, from a zero start, to the workspace.
+//
+// Sixteen columns a wave, eight waves for 128 columns: with 32 columns a wave
+// and four waves the kernel read a third less from LDS but held 375
+// registers a lane, one wave per SIMD (1.8 ms at 65536 tokens, 64 heads).
 // ---------------------------------------------------------------------------
-template <typename IO, int N, int NCB, bool ENDS, bool REV, int PARTS>
-__global__ void __launch_bounds__(256) ssm_scan_kernel(SsmParams p) {
+template <typename IO, int N, int COLS, int NH, bool ENDS, bool REV, int PARTS>
+__global__ void __launch_bounds__(4 * COLS, sizeof(IO) == 4 ? 1 : COLS == 64 && N == 128 ? 3 : 4) ssm_scan_kernel(SsmParams p) {
     typedef SOp<IO> O;
     typedef typename O::elem E;
-    constexpr int C = kSsmChunk, COLS = 64 * NCB, LX = COLS + O::kPad, LN = N + O::kPad, LM = C + O::kPad;
-    constexpr int NH = NCB, NB = N / 16;          // heads at most; row blocks of the state
+    constexpr int C = kSsmChunk, NW = COLS / 16, NB = N / 16, kThreads = 4 * COLS, P = COLS / NH;
     constexpr int kP = O::template kParts<PARTS>;
-    __shared__ E sv[C * LX], sk[C * LN], sq[ENDS ? 1 : C * LN], sm[ENDS ? 1 : NH][ENDS ? 1 : C * LM];
-    __shared__ Gates gates[NH];
+    __shared__ __align__(16) E sv[C * COLS], sk[C * N], sq[ENDS ? 8 : C * N], sm[ENDS ? 1 : NH][ENDS ? 8 : C * C];
+    // chunks whose gates are formed at once, one chunk and head a wave
+    constexpr int GC = NW / NH;
+    __shared__ Gates gates[GC][NH];
     int item, hb;
     place(p, item, hb);
     if (item >= p.n_items) return;
@@ -431,156 +550,147 @@ __global__ void __launch_bounds__(256) ssm_scan_kernel(SsmParams p) {
     if (!seg.live) return;
     if (ENDS && (REV ? seg.begin == seg.seq_begin : seg.end == seg.seq_end)) return;
     const int w = wave_id(), l = lane_id(), q = l >> 4, j = l & 15;
-    const int col0 = hb * COLS, head0 = col0 / p.P, nh = p.P == 64 ? NCB : 1;
-    const int mine = nh == 2 ? w >> 1 : 0, head = head0 + mine, grp = head0 / p.heads_per_group;
-    const int wc = w * 16 * NCB;                  // this wave's first column
-    const bool gater = w < nh;                    // waves that form the gates of head0 + w
-    const float A = gater ? p.A[head0 + w] : 0.f, bias = gater && p.bias ? p.bias[head0 + w] : 0.f;
-    const float Dh = p.D ? p.D[head] : 0.f;
+    const int col0 = hb * COLS, head0 = col0 / p.P, mine = w * 16 / P, head = head0 + mine, grp = head0 / p.heads_per_group;
+    const int wc = w * 16;                        // this wave's first column
+    const int gh = w % NH, gc = w / NH;           // the head and the chunk of a group whose gates it forms
+    const bool gater = gc < GC;
+    const float A = uniform(p.A[head0 + gh]), bias = p.bias ? uniform(p.bias[head0 + gh]) : 0.f;
+    const float Dh = p.D ? uniform(p.D[head]) : 0.f;
 
-    // h[cb * NB + nb][e] = S[16 nb + 4 q + e][column wc + 16 cb + j]
-    float4v h[NCB * NB];
+    // h[nb][e] = S[row_of(nb, e)][column wc + j]
+    float4v h[NB];
 #pragma unroll
-    for (int i = 0; i < NCB * NB; ++i) h[i] = float4v{0.f, 0.f, 0.f, 0.f};
-    const int64_t hoff = ((int64_t)seg.seq * p.H * N) * p.P;
-    auto hidx = [&](int cb, int nb, int e) {
-        const int col = col0 + wc + 16 * cb + j;
-        return hoff + ((int64_t)(col / p.P) * N + 16 * nb + 4 * q + e) * p.P + col % p.P;
+    for (int i = 0; i < NB; ++i) h[i] = float4v{0.f, 0.f, 0.f, 0.f};
+    auto row_of = [&](int nb, int e) { return 32 * (nb >> 1) + 8 * q + 4 * (nb & 1) + e; };
+    auto state_at = [&](const int l) {            // of h[0][0] in s0 and sT, less 8 q rows
+        const int col = col0 + wc + (l & 15);
+        return ((int64_t)seg.seq * p.H + col / p.P) * N * p.P + col % p.P;
     };
-    const int ends_at = 4 * q * COLS + wc + j;    // of h[0][0] in a segment's [N][COLS]
     if constexpr (!ENDS) {
         const float d = segments_before<REV>(p, seg, hb, NH, mine, [&](int64_t at, float f) {
-            const float *e0 = p.ends + at * (N * COLS) + ends_at;
+            const float *e0 = p.ends + at * (N * COLS) + wc + j;
 #pragma unroll
-            for (int cb = 0; cb < NCB; ++cb)
+            for (int nb = 0; nb < NB; ++nb)
 #pragma unroll
-                for (int nb = 0; nb < NB; ++nb)
-#pragma unroll
-                    for (int e = 0; e < 4; ++e) h[cb * NB + nb][e] += f * e0[(16 * nb + e) * COLS + 16 * cb];
+                for (int e = 0; e < 4; ++e) h[nb][e] += f * e0[row_of(nb, e) * COLS];
         });
         if (p.s0) {
 #pragma unroll
-            for (int cb = 0; cb < NCB; ++cb)
+            for (int nb = 0; nb < NB; ++nb)
 #pragma unroll
-                for (int nb = 0; nb < NB; ++nb)
-#pragma unroll
-                    for (int e = 0; e < 4; ++e) h[cb * NB + nb][e] += d * p.s0[hidx(cb, nb, e)];
+                for (int e = 0; e < 4; ++e) h[nb][e] += d * p.s0[state_at(l) + row_of(nb, e) * p.P];
         }
         // the blocks of M right of the diagonal that a 32-wide step touches
-        for (int i = threadIdx.x; i < NH * 2 * 16 * 16; i += 256) {
+        for (int i = threadIdx.x; i < NH * 2 * 16 * 16; i += kThreads) {
             const int hh = i >> 9, blk = (i >> 8) & 1, r = (i >> 4) & 15, c = i & 15;
-            sm[hh][(32 * blk + r) * LM + 32 * blk + 16 + c] = E(0);
+            sm[hh][at<E, C>(32 * blk + r, 32 * blk + 16 + c)] = E(0);
         }
     }
 
-    TileRegs<IO, COLS, REV> tv;
-    TileRegs<IO, N, REV> tk, tq;
-    float raw = 0.f;
+    TileRegs<IO, COLS, REV, kThreads> tv;
+    TileRegs<IO, N, REV, kThreads> tk, tq;
     const int64_t voff = seg.batch * p.vb + col0, koff = seg.batch * p.qkb + (int64_t)grp * N;
+    const int nc = chunks_of(seg);
     auto fetch = [&](int c) {
         int lo;
-        const int rows = chunk_of<REV>(seg, c, lo);
-        tv.load(p.v, voff + lo * p.vt, (uint32_t)p.vt, rows);
-        tk.load(p.k, koff + lo * p.qkt, (uint32_t)p.qkt, rows);
-        if constexpr (!ENDS) tq.load(p.q, koff + lo * p.qkt, (uint32_t)p.qkt, rows);
-        if (gater) raw = raw_dt<IO, REV>(p, seg.batch, head0 + w, lo, rows);
+        const int rows = chunk_of<REV>(seg, c, lo), tid = again(threadIdx.x);
+        tv.load(tid, p.v, voff + lo * p.vt, (uint32_t)p.vt, rows);
+        tk.load(tid, p.k, koff + lo * p.qkt, (uint32_t)p.qkt, rows);
+        if constexpr (!ENDS) tq.load(tid, p.q, koff + lo * p.qkt, (uint32_t)p.qkt, rows);
+    };
+    uint32_t raw = 0;
+    auto fetch_dt = [&](int c) {                  // of this wave's chunk of the group at c
+        if (gater && c + gc < nc) {
+            int lo;
+            const int rows = chunk_of<REV>(seg, c + gc, lo);
+            raw = raw_dt<IO, REV>(p, seg.batch, head0 + gh, lo, rows);
+        }
+    };
+    auto form_gates = [&](int c) {
+        if (gater && c + gc < nc) {
+            int lo;
+            const int rows = chunk_of<REV>(seg, c + gc, lo);
+            make_gates<REV>(gates[gc][gh], dt_of(p, raw_value<IO>(p, raw), bias, again(lane_id()) < rows), A);
+        }
     };
     double total = 0.0;
-    const int nc = chunks_of(seg);
-    if (nc > 0) fetch(0);
+    if (nc > 0) {
+        fetch_dt(0);
+        fetch(0);
+    }
     for (int c = 0; c < nc; ++c) {
         int lo;
-        const int rows = chunk_of<REV>(seg, c, lo);
-        __syncthreads();                          // the last chunk's tiles are done with
-        tv.put(sv, LX);
-        tk.put(sk, LN);
-        if constexpr (!ENDS) tq.put(sq, LN);
-        if (gater) make_gates<REV>(gates[w], dt_of(p, raw, bias, l < rows), A);
+        const int rows = chunk_of<REV>(seg, c, lo), tid = again(threadIdx.x), l = tid & 63, q = l >> 4, j = l & 15;
+        const Lane<E, N> aN(l);
+        const Lane<E, COLS> aP(l);
+        const Lane<E, C> aM(l);
+        lds_barrier();                            // the last chunk's tiles are done with
+        if (c % GC == 0) {
+            form_gates(c);
+            fetch_dt(c + GC);
+        }
+        tv.put(tid, sv, rows);
+        tk.put(tid, sk, rows);
+        if constexpr (!ENDS) tq.put(tid, sq, rows);
         if (c + 1 < nc) fetch(c + 1);
-        __syncthreads();
-        const Gates &g = gates[mine];
-        float4v y[ENDS ? 1 : NCB * 4];
+        lds_barrier();
+        const Gates *gs = gates[c % GC], &g = gs[mine];
+        float4v y[ENDS ? 1 : 4];
         if constexpr (!ENDS) {
             // 1: M[i][k] = (q_i . k_k) e^(cum_i - cum_k) w_k, k <= i
 #pragma unroll
-            for (int r = 0; r < 3; ++r) {
-                const int idx = w + 4 * r;
+            for (int r = 0; r < (10 + NW - 1) / NW; ++r) {
+                const int idx = w + NW * r;
                 if (idx < 10) {
                     const int bi = idx < 1 ? 0 : idx < 3 ? 1 : idx < 6 ? 2 : 3, bk = idx - bi * (bi + 1) / 2;
                     float4v s = float4v{0.f, 0.f, 0.f, 0.f};
 #pragma unroll
                     for (int n0 = 0; n0 < N; n0 += 32)
-                        O::mma(s, O::row(sk, LN, 16 * bk, n0), O::row(sq, LN, 16 * bi, n0));
+                        O::mma(s, O::template row<N>(sk, aN, 16 * bk, n0), O::template row<N>(sq, aN, 16 * bi, n0));
                     const int ii = 16 * bi + j;
 #pragma unroll
-                    for (int hh = 0; hh < NH; ++hh)
-                        if (hh < nh) {
-                            float4v m;
-                            const float2 ci = gates[hh].cum[ii];
-#pragma unroll
-                            for (int e = 0; e < 4; ++e) {
-                                const int kk = 16 * bk + 4 * q + e;
-                                m[e] = kk <= ii ? s[e] * decay_between(ci, gates[hh].cum[kk]) * gates[hh].w[kk] : 0.f;
-                            }
-                            O::put4(&sm[hh][ii * LM + 16 * bk + 4 * q], m);
-                        }
+                    for (int hh = 0; hh < NH; ++hh) {
+                        O::put4(&sm[hh][at<E, C>(ii, 16 * bk + 4 * q)], s * decays<REV>(gs[hh], ii, 16 * bk + 4 * q));
+                    }
                 }
             }
             // out1^T = S^T q^T, then times e^cum
 #pragma unroll
-            for (int i = 0; i < NCB * 4; ++i) y[i] = float4v{0.f, 0.f, 0.f, 0.f};
+            for (int i = 0; i < 4; ++i) y[i] = float4v{0.f, 0.f, 0.f, 0.f};
 #pragma unroll
             for (int n0 = 0; n0 < N; n0 += 32) {
-                typename O::frag hf[NCB][1];
+                typename O::frag hf[1];
+                O::acc(h[n0 / 16], h[n0 / 16 + 1], hf);
 #pragma unroll
-                for (int cb = 0; cb < NCB; ++cb) O::acc_split(h[cb * NB + n0 / 16], h[cb * NB + n0 / 16 + 1], hf[cb]);
-#pragma unroll
-                for (int bi = 0; bi < 4; ++bi) {
-                    const typename O::frag qf = O::row_split(sq, LN, 16 * bi, n0);
-#pragma unroll
-                    for (int cb = 0; cb < NCB; ++cb) O::mma(y[cb * 4 + bi], hf[cb][0], qf);
-                }
+                for (int bi = 0; bi < 4; ++bi) O::mma(y[bi], hf[0], O::template row<N>(sq, aN, 16 * bi, n0));
             }
 #pragma unroll
-            for (int bi = 0; bi < 4; ++bi) {
-                const float ec = g.ecum[16 * bi + j];
-#pragma unroll
-                for (int cb = 0; cb < NCB; ++cb) y[cb * 4 + bi] *= ec;
-            }
-            __syncthreads();                      // M is whole
+            for (int bi = 0; bi < 4; ++bi) y[bi] *= g.ecum[16 * bi + j];
         }
+        if constexpr (!ENDS) lds_barrier();       // M is whole
         // 2 and 3: both take v by columns
         const double tot = g.total;
-        total += tot;
+        if constexpr (ENDS) total += tot;
         const float et = fast_exp2((float)tot);
 #pragma unroll
-        for (int i = 0; i < NCB * NB; ++i) h[i] *= et;
+        for (int i = 0; i < NB; ++i) h[i] *= et;
 #pragma unroll
         for (int s0 = 0; s0 < C; s0 += 32) {
             float wt[8];
 #pragma unroll
             for (int e = 0; e < 8; ++e) wt[e] = g.end[s0 + 8 * q + e];
-            typename O::frag vf[NCB], vw[NCB][kP];
-#pragma unroll
-            for (int cb = 0; cb < NCB; ++cb) {
-                vf[cb] = O::col(sv, LX, wc + 16 * cb, s0);
-                O::scaled(vf[cb], wt, vw[cb]);
-            }
+            const typename O::frag vf = O::template col<COLS>(sv, aP, wc, s0);
+            typename O::frag vw[kP];
+            O::scaled(vf, wt, vw);
             if constexpr (!ENDS) {
 #pragma unroll
-                for (int bi = s0 / 16; bi < 4; ++bi) {
-                    const typename O::frag mf = O::row(sm[mine], LM, 16 * bi, s0);
-#pragma unroll
-                    for (int cb = 0; cb < NCB; ++cb) O::mma(y[cb * 4 + bi], vf[cb], mf);
-                }
+                for (int bi = s0 / 16; bi < 4; ++bi) O::mma(y[bi], vf, O::template row<C>(sm[mine], aM, 16 * bi, s0));
             }
 #pragma unroll
             for (int nb = 0; nb < NB; ++nb) {
-                const typename O::frag kf = O::col(sk, LN, 16 * nb, s0);
+                const typename O::frag kf = O::template pair<N>(sk, aN, 32 * (nb >> 1), nb & 1, s0);
 #pragma unroll
-                for (int cb = 0; cb < NCB; ++cb)
-#pragma unroll
-                    for (int k = 0; k < kP; ++k) O::mma(h[cb * NB + nb], kf, vw[cb][k]);
+                for (int k = 0; k < kP; ++k) O::mma(h[nb], kf, vw[k]);
             }
         }
         if constexpr (!ENDS) {
@@ -588,44 +698,37 @@ __global__ void __launch_bounds__(256) ssm_scan_kernel(SsmParams p) {
             const rsrc_t ry = make_rsrc((IO *)p.out + seg.batch * p.ob + lo * p.ot + col0, 0x7fffffffu);
 #pragma unroll
             for (int bi = 0; bi < 4; ++bi) {
-                const int ii = 16 * bi + j, t = REV ? rows - 1 - ii : ii;
+                const int ii = 16 * bi + j, t = REV ? rows - 1 - ii : ii, cc = wc + 4 * q;
                 const float post = REV ? g.dt[ii] : 1.f;
+                float x[4];
+                O::get4(&sv[at<E, COLS>(ii, cc)], x);
+                float4v o;
 #pragma unroll
-                for (int cb = 0; cb < NCB; ++cb) {
-                    const int cc = wc + 16 * cb + 4 * q;
-                    float x[4];
-                    O::get4(&sv[ii * LX + cc], x);
-                    float4v o;
-#pragma unroll
-                    for (int e = 0; e < 4; ++e) o[e] = post * y[cb * 4 + bi][e] + Dh * x[e];
-                    const uint32_t off = ii < rows ? (uint32_t)(t * (uint32_t)p.ot + cc) * (uint32_t)sizeof(IO) : 0xfffffff0u;
-                    store_row4<IO>(ry, off, o);
-                }
+                for (int e = 0; e < 4; ++e) o[e] = post * y[bi][e] + Dh * x[e];
+                store_row4<IO>(ry, ii < rows ? (uint32_t)(t * (uint32_t)p.ot + cc) * (uint32_t)sizeof(IO) : 0xfffffff0u, o);
             }
         }
     }
     if constexpr (ENDS) {
-        const int64_t at = (int64_t)item * p.n_hb + hb;
-        float *e0 = p.ends + at * (N * COLS) + ends_at;
+        const int64_t place_at = (int64_t)item * p.n_hb + hb;
+        float *e0 = p.ends + place_at * (N * COLS) + wc + j;
 #pragma unroll
-        for (int cb = 0; cb < NCB; ++cb)
+        for (int nb = 0; nb < NB; ++nb)
 #pragma unroll
-            for (int nb = 0; nb < NB; ++nb)
-#pragma unroll
-                for (int e = 0; e < 4; ++e) e0[(16 * nb + e) * COLS + 16 * cb] = h[cb * NB + nb][e];
-        if (!REV && l == 0 && (nh == 1 ? w == 0 : (w & 1) == 0)) p.total[at * NH + mine] = total;
+            for (int e = 0; e < 4; ++e) e0[row_of(nb, e) * COLS] = h[nb][e];
+        if (!REV && l == 0 && w == mine * (NW / NH)) p.total[place_at * NH + mine] = total;
     } else if (p.sT && (REV ? seg.begin == seg.seq_begin : seg.end == seg.seq_end)) {
+        const int l = again(lane_id()), q = l >> 4;
+        float *sT = p.sT + state_at(l) + 8 * q * p.P;
 #pragma unroll
-        for (int cb = 0; cb < NCB; ++cb)
+        for (int nb = 0; nb < NB; ++nb)
 #pragma unroll
-            for (int nb = 0; nb < NB; ++nb)
-#pragma unroll
-                for (int e = 0; e < 4; ++e) p.sT[hidx(cb, nb, e)] = h[cb * NB + nb][e];
+            for (int e = 0; e < 4; ++e) sT[(32 * (nb >> 1) + 4 * (nb & 1) + e) * p.P] = h[nb][e];
     }
 }
 
 struct SsmPlan {
-    int ncb, n_hb, n_items, seg_tokens, seqs;
+    int ncb, nh, n_hb, n_items, seg_tokens, seqs;
 };
 
 gdn_status check_ssm(const gdn_ssm_problem *pr, bool packed);

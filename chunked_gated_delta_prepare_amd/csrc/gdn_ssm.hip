@@ -1,8 +1,8 @@
 // Selective state space scan, forward (see gdn_ssm.h for the mathematics).
 //
-// A workgroup of four waves walks one segment of one stream, a stream being
-// 64 NCB columns of the state: one head's, or with P = 64 and NCB = 2 two
-// heads' of a group, which then share B, C and the products C . B.
+// A workgroup walks one segment of one stream, a stream being 64 or 128
+// columns of the state: one head's, or two heads' of a group, which then share
+// B, C and the products C . B.
 #include "gdn_ssm.h"
 
 namespace gdn {
@@ -81,9 +81,9 @@ __global__ void __launch_bounds__(256) ssm_step_kernel(StepParams p) {
     io_traits<IO>::store(y + c + 1, o.y + D * x1);
 }
 
-// Two blocks of 16 columns a wave where the columns of a head, or of two
-// heads of one group, fill them: every fragment of B, C and M then feeds two
-// products.  fp32 io has one (its tiles fill LDS).
+// 128 columns a workgroup where a head, or two heads of one group, fill them
+// (every row of B and C then serves twice the columns), else 64.  fp32 io has
+// 64 (its tiles fill LDS).
 static int columns(const gdn_ssm_problem *pr) {
     if (pr->io_dtype == GDN_F32) return 1;
     return pr->P == 128 || (pr->H / pr->G) % 2 == 0 ? 2 : 1;
@@ -92,6 +92,7 @@ static int columns(const gdn_ssm_problem *pr) {
 SsmPlan ssm_plan(const gdn_ssm_problem *pr, bool packed) {
     SsmPlan s;
     s.ncb = columns(pr);
+    s.nh = s.ncb == 2 && pr->P == 64 ? 2 : 1;
     s.n_hb = (int)(pr->H * pr->P / (64 * s.ncb));
     s.seqs = (int)(packed ? pr->n_seqs : pr->B);
     const int64_t chunks = (pr->T + kSsmChunk - 1) / kSsmChunk;
@@ -119,7 +120,7 @@ int ssm_grid(SsmParams &sp, const SsmPlan &s) {
 
 static size_t forward_ws(const gdn_ssm_problem *pr, const SsmPlan &s) {
     if (s.n_items == s.seqs) return 0;            // one segment each
-    return (size_t)s.n_items * s.n_hb * (8 * s.ncb + 4 * pr->N * 64 * s.ncb);
+    return (size_t)s.n_items * s.n_hb * (8 * 2 + 4 * pr->N * 64 * s.ncb);
 }
 
 gdn_status check_ssm(const gdn_ssm_problem *pr, bool packed) {
@@ -170,16 +171,18 @@ void fill_ssm(const gdn_ssm_problem *pr, SsmParams &sp) {
 
 namespace {
 
-template <typename IO, int NCB>
+template <typename IO, int COLS, int NH>
 const void *ssm_fn(int N, bool ends) {
-    if (N == 64) return ends ? (const void *)&ssm_scan_kernel<IO, 64, NCB, true, false, 2> : (const void *)&ssm_scan_kernel<IO, 64, NCB, false, false, 2>;
-    return ends ? (const void *)&ssm_scan_kernel<IO, 128, NCB, true, false, 2> : (const void *)&ssm_scan_kernel<IO, 128, NCB, false, false, 2>;
+    if (N == 64)
+        return ends ? (const void *)&ssm_scan_kernel<IO, 64, COLS, NH, true, false, 2> : (const void *)&ssm_scan_kernel<IO, 64, COLS, NH, false, false, 2>;
+    return ends ? (const void *)&ssm_scan_kernel<IO, 128, COLS, NH, true, false, 2> : (const void *)&ssm_scan_kernel<IO, 128, COLS, NH, false, false, 2>;
 }
 
-const void *ssm_pick(const gdn_ssm_problem *pr, int ncb, bool ends) {
+const void *ssm_pick(const gdn_ssm_problem *pr, const SsmPlan &s, bool ends) {
     const int N = (int)pr->N;
-    if (pr->io_dtype == GDN_F32) return ssm_fn<float, 1>(N, ends);
-    return ncb == 2 ? ssm_fn<bf16_t, 2>(N, ends) : ssm_fn<bf16_t, 1>(N, ends);
+    if (pr->io_dtype == GDN_F32) return ssm_fn<float, 64, 1>(N, ends);
+    if (s.ncb == 1) return ssm_fn<bf16_t, 64, 1>(N, ends);
+    return s.nh == 2 ? ssm_fn<bf16_t, 128, 2>(N, ends) : ssm_fn<bf16_t, 128, 1>(N, ends);
 }
 
 template <typename IO>
@@ -236,13 +239,13 @@ gdn_status gdn_ssm_forward(const gdn_ssm_problem *pr, const void *x, const void 
     sp.ob = sp.ot * pr->T;
     sp.sT = hT;
     sp.total = (double *)workspace;
-    sp.ends = (float *)workspace + (int64_t)s.n_items * s.n_hb * s.ncb * 2;
+    sp.ends = (float *)workspace + (int64_t)s.n_items * s.n_hb * 4;
     const int grid = ssm_grid(sp, s);
     if (need) {
-        st = launch_kernel(ssm_pick(pr, s.ncb, true), grid, &sp, (hipStream_t)stream);
+        st = launch_kernel(ssm_pick(pr, s, true), grid, &sp, (hipStream_t)stream, 256 * s.ncb);
         if (st != GDN_OK) return st;
     }
-    return launch_kernel(ssm_pick(pr, s.ncb, false), grid, &sp, (hipStream_t)stream);
+    return launch_kernel(ssm_pick(pr, s, false), grid, &sp, (hipStream_t)stream, 256 * s.ncb);
 }
 
 gdn_status gdn_ssm_step(const gdn_ssm_problem *pr, const void *x, const void *dt, const float *A, const void *Bm,

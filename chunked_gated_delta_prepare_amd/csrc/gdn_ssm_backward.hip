@@ -7,7 +7,7 @@ namespace gdn {
 
 // ---------------------------------------------------------------------------
 // out2 (dC forward, dB in reverse), and per head and row the sum
-// q_i . out2_i.  Here a wave keeps N / 4 rows of the state, all columns of
+// q_i . out2_i.  Here wave w keeps rows 16 w .. +15 of the state, all columns of
 // them: S q2 sums over columns.  Per chunk:
 //   1  the lower triangles of q k^T and q2 v^T; the products of both, times
 //      decays and weights, sum up to the rows' part inside the chunk; those
@@ -16,278 +16,263 @@ namespace gdn {
 //      N values of a row
 //   3  S' = e^total S + (w k)^T v
 // S enters its product in three bf16 parts and (w k) in three (relative error
-// 2^-27): the sums feed dt's and A's gradients, which are fp32.  M is rounded once to out2's own type.
+// 2^-27): the sums feed dt's and A's gradients, which are fp32.  M is rounded
+// once to out2's own type.
 // ---------------------------------------------------------------------------
-template <typename IO, int N, int NCB, bool REV>
-__global__ void __launch_bounds__(256) ssm_key_kernel(SsmParams p) {
+template <typename IO, int N, int COLS, int NH, bool REV>
+__global__ void __launch_bounds__(4 * N, sizeof(IO) == 2 ? 2 : 1) ssm_key_kernel(SsmParams p) {
     typedef SOp<IO> O;
     typedef typename O::elem E;
-    constexpr int C = kSsmChunk, COLS = 64 * NCB, LX = COLS + O::kPad, LN = N + O::kPad, LM = C + O::kPad;
-    constexpr int NH = NCB, NB = N / 64, PB = COLS / 16;      // this wave's blocks of N; blocks of columns
+    constexpr int C = kSsmChunk, NW = N / 16, PB = COLS / 16, kThreads = 4 * N;      // PB: blocks of columns
     constexpr int kP = O::template kParts<3>;
-    __shared__ E sv[C * LX], sz[C * LX], sk[C * LN], sq[C * LN], sm[C * LM];
-    __shared__ Gates gates[NH];
-    __shared__ float inner[NH][4][C], outer[NH][4][C], diag[NH][2][C];
-    __shared__ float dots[NH][4];
+    __shared__ __align__(16) E sv[C * COLS], sz[C * COLS], sk[C * N], sq[C * N], sm[C * C];
+    // chunks whose gates are formed at once, one chunk and head a wave
+    constexpr int GC = 2;
+    __shared__ Gates gates[GC][NH];
+    __shared__ float inner[NH][4][C], outer[NH][NW][C], dots[NH][NW];
     int item, hb;
     place(p, item, hb);
     if (item >= p.n_items) return;
     const Segment seg = find_segment(p, item);
     if (!seg.live) return;
     const int w = wave_id(), l = lane_id(), q = l >> 4, j = l & 15;
-    const int col0 = hb * COLS, head0 = col0 / p.P, nh = p.P == 64 ? NCB : 1, grp = head0 / p.heads_per_group;
-    const int wn = w * (N / 4);                   // this wave's first of N
-    const bool gater = w < nh;
-    const float A = gater ? p.A[head0 + w] : 0.f, bias = gater && p.bias ? p.bias[head0 + w] : 0.f;
+    const int col0 = hb * COLS, head0 = col0 / p.P, grp = head0 / p.heads_per_group;
+    const int wn = 16 * w;                        // this wave's first row of the state
+    const int gh = w % NH, gc = w / NH;           // the head and the chunk of a group whose gates it forms
+    const bool gater = gc < GC;
+    const float A = uniform(p.A[head0 + gh]), bias = p.bias ? uniform(p.bias[head0 + gh]) : 0.f;
 
-    // h[nb * PB + pb][e] = S[n = wn + 16 nb + j][column 16 pb + 4 q + e]
-    float4v h[NB * PB];
+    // h[pb][e] = S[n = wn + j][column col_of(pb, e)]
+    float4v h[PB];
 #pragma unroll
-    for (int i = 0; i < NB * PB; ++i) h[i] = float4v{0.f, 0.f, 0.f, 0.f};
+    for (int i = 0; i < PB; ++i) h[i] = float4v{0.f, 0.f, 0.f, 0.f};
+    auto col_of = [&](int pb) { return 32 * (pb >> 1) + 8 * q + 4 * (pb & 1); };      // of e = 0
 #pragma unroll
-    for (int hh = 0; hh < NH; ++hh)
-        if (hh < nh) {
-            const float d = segments_before<REV>(p, seg, hb, NH, hh, [&](int64_t at, float f) {
-                const float *e0 = p.ends + at * (N * COLS) + (wn + j) * COLS + 4 * q;
+    for (int hh = 0; hh < NH; ++hh) {
+        const float d = segments_before<REV>(p, seg, hb, NH, hh, [&](int64_t at, float f) {
+            const float *e0 = p.ends + at * (N * COLS) + (wn + j) * COLS;
 #pragma unroll
-                for (int nb = 0; nb < NB; ++nb)
+            for (int pb = hh * (PB / NH); pb < (hh + 1) * (PB / NH); ++pb) h[pb] += f * *(const float4v *)(e0 + col_of(pb));
+        });
+        if (p.s0) {
 #pragma unroll
-                    for (int pb = 0; pb < PB; ++pb)
-                        if (nh == 1 || pb / (PB / NH) == hh) h[nb * PB + pb] += f * *(const float4v *)(e0 + 16 * nb * COLS + 16 * pb);
-            });
-            if (p.s0) {
+            for (int pb = hh * (PB / NH); pb < (hh + 1) * (PB / NH); ++pb) {
+                const int col = col0 + col_of(pb);
+                const float *s = p.s0 + (((int64_t)seg.seq * p.H + col / p.P) * N + wn + j) * p.P + col % p.P;
 #pragma unroll
-                for (int nb = 0; nb < NB; ++nb)
-#pragma unroll
-                    for (int pb = 0; pb < PB; ++pb)
-                        if (nh == 1 || pb / (PB / NH) == hh) {
-                            const int col = col0 + 16 * pb + 4 * q;
-                            const float *s = p.s0 + (((int64_t)seg.seq * p.H + col / p.P) * N + wn + 16 * nb + j) * p.P + col % p.P;
-#pragma unroll
-                            for (int e = 0; e < 4; ++e) h[nb * PB + pb][e] += d * s[e];
-                        }
+                for (int e = 0; e < 4; ++e) h[pb][e] += d * s[e];
             }
         }
-    for (int i = threadIdx.x; i < 2 * 16 * 16; i += 256) {
+    }
+    for (int i = threadIdx.x; i < 2 * 16 * 16; i += kThreads) {
         const int blk = i >> 8, r = (i >> 4) & 15, c = i & 15;
-        sm[(32 * blk + r) * LM + 32 * blk + 16 + c] = E(0);
+        sm[at<E, C>(32 * blk + r, 32 * blk + 16 + c)] = E(0);
     }
 
-    TileRegs<IO, COLS, REV> tv, tz;
-    TileRegs<IO, N, REV> tk, tq;
-    float raw = 0.f;
+    TileRegs<IO, COLS, REV, kThreads> tv, tz;
+    TileRegs<IO, N, REV, kThreads> tk, tq;
     const int64_t voff = seg.batch * p.vb + col0, zoff = seg.batch * p.q2b + col0, koff = seg.batch * p.qkb + (int64_t)grp * N;
+    const int nc = chunks_of(seg);
     auto fetch = [&](int c) {
         int lo;
-        const int rows = chunk_of<REV>(seg, c, lo);
-        tv.load(p.v, voff + lo * p.vt, (uint32_t)p.vt, rows);
-        tz.load(p.q2, zoff + lo * p.q2t, (uint32_t)p.q2t, rows);
-        tk.load(p.k, koff + lo * p.qkt, (uint32_t)p.qkt, rows);
-        tq.load(p.q, koff + lo * p.qkt, (uint32_t)p.qkt, rows);
-        if (gater) raw = raw_dt<IO, REV>(p, seg.batch, head0 + w, lo, rows);
+        const int rows = chunk_of<REV>(seg, c, lo), tid = again(threadIdx.x);
+        tv.load(tid, p.v, voff + lo * p.vt, (uint32_t)p.vt, rows);
+        tz.load(tid, p.q2, zoff + lo * p.q2t, (uint32_t)p.q2t, rows);
+        tk.load(tid, p.k, koff + lo * p.qkt, (uint32_t)p.qkt, rows);
+        tq.load(tid, p.q, koff + lo * p.qkt, (uint32_t)p.qkt, rows);
     };
-    const int nc = chunks_of(seg);
-    if (nc > 0) fetch(0);
+    uint32_t raw = 0;
+    auto fetch_dt = [&](int c) {                  // of this wave's chunk of the group at c
+        if (gater && c + gc < nc) {
+            int lo;
+            const int rows = chunk_of<REV>(seg, c + gc, lo);
+            raw = raw_dt<IO, REV>(p, seg.batch, head0 + gh, lo, rows);
+        }
+    };
+    auto form_gates = [&](int c) {
+        if (gater && c + gc < nc) {
+            int lo;
+            const int rows = chunk_of<REV>(seg, c + gc, lo);
+            make_gates<REV>(gates[gc][gh], dt_of(p, raw_value<IO>(p, raw), bias, again(lane_id()) < rows), A);
+        }
+    };
+    if (nc > 0) {
+        fetch_dt(0);
+        fetch(0);
+    }
     for (int c = 0; c < nc; ++c) {
         int lo;
-        const int rows = chunk_of<REV>(seg, c, lo);
-        __syncthreads();                          // the last chunk's tiles and sums are done with
-        tv.put(sv, LX);
-        tz.put(sz, LX);
-        tk.put(sk, LN);
-        tq.put(sq, LN);
-        if (gater) make_gates<REV>(gates[w], dt_of(p, raw, bias, l < rows), A);
+        const int rows = chunk_of<REV>(seg, c, lo), tid = again(threadIdx.x), l = tid & 63, q = l >> 4, j = l & 15;
+        const Lane<E, N> aN(l);
+        const Lane<E, COLS> aP(l);
+        const Lane<E, C> aM(l);
+        lds_barrier();                            // the last chunk's tiles and sums are done with
+        if (c % GC == 0) {
+            form_gates(c);
+            fetch_dt(c + GC);
+        }
+        tv.put(tid, sv, rows);
+        tz.put(tid, sz, rows);
+        tk.put(tid, sk, rows);
+        tq.put(tid, sq, rows);
         if (c + 1 < nc) fetch(c + 1);
         const int mark = mark_slot(p, seg, REV ? nc - 1 - c : c);
         if constexpr (REV) {
             // behind this chunk h meets the state's gradient
             if (mark >= 0) {
-                const float2 *m = (const float2 *)p.marks + ((int64_t)mark * p.n_hb + hb) * (N * COLS / 2) + threadIdx.x;
-                float dot[NH];
-#pragma unroll
-                for (int hh = 0; hh < NH; ++hh) dot[hh] = 0.f;
-#pragma unroll
-                for (int i = 0; i < NB * PB; ++i) {
-                    const float2 a = m[(2 * i) * 256], b = m[(2 * i + 1) * 256];
-                    const float d = a.x * h[i][0] + a.y * h[i][1] + b.x * h[i][2] + b.y * h[i][3];
-                    if (nh == 1 || NH == 1 || (i % PB) / (PB / NH) == 0)
-                        dot[0] += d;
-                    else
-                        dot[NH - 1] += d;
-                }
+                const float2 *m = (const float2 *)p.marks + ((int64_t)mark * p.n_hb + hb) * (N * COLS / 2) + tid;
 #pragma unroll
                 for (int hh = 0; hh < NH; ++hh) {
-                    const float d = wave_sum(dot[hh]);
+                    float d = 0.f;
+#pragma unroll
+                    for (int pb = hh * (PB / NH); pb < (hh + 1) * (PB / NH); ++pb) {
+                        const float2 a = m[(2 * pb) * kThreads], b = m[(2 * pb + 1) * kThreads];
+                        d += a.x * h[pb][0] + a.y * h[pb][1] + b.x * h[pb][2] + b.y * h[pb][3];
+                    }
+                    d = wave_sum(d);
                     if (l == 0) dots[hh][w] = d;
                 }
             }
         }
-        __syncthreads();
+        lds_barrier();
+        const Gates *gs = gates[c % GC];
         if constexpr (REV) {
-            if (mark >= 0 && w < nh && l == 0)
-                p.X[((int64_t)mark * p.n_hb + hb) * NH + w] =
-                    ((double)dots[w][0] + (double)dots[w][1]) + ((double)dots[w][2] + (double)dots[w][3]);
+            if (mark >= 0 && w < NH && l == 0) {
+                double d = 0.0;
+#pragma unroll
+                for (int k = 0; k < NW; ++k) d += (double)dots[w][k];
+                p.X[((int64_t)mark * p.n_hb + hb) * NH + w] = d;
+            }
         }
         // 1
+        const int64_t row0 = (int64_t)seg.batch * p.T + lo;
 #pragma unroll
-        for (int r = 0; r < 3; ++r) {
-            const int idx = w + 4 * r;
+        for (int r = 0; r < (10 + NW - 1) / NW; ++r) {
+            const int idx = w + NW * r;
             if (idx < 10) {
                 const int bi = idx < 1 ? 0 : idx < 3 ? 1 : idx < 6 ? 2 : 3, bk = idx - bi * (bi + 1) / 2;
-                const int ii = 16 * bi + j;
+                const int ii = 16 * bi + j, k0 = 16 * bk + 4 * q;
                 float4v s = float4v{0.f, 0.f, 0.f, 0.f}, m = s;
 #pragma unroll
-                for (int n0 = 0; n0 < N; n0 += 32) O::mma(s, O::row(sk, LN, 16 * bk, n0), O::row(sq, LN, 16 * bi, n0));
+                for (int n0 = 0; n0 < N; n0 += 32) O::mma(s, O::template row<N>(sk, aN, 16 * bk, n0), O::template row<N>(sq, aN, 16 * bi, n0));
 #pragma unroll
-                for (int hh = 0; hh < NH; ++hh)
-                    if (hh < nh) {
-                        float4v x = float4v{0.f, 0.f, 0.f, 0.f};
+                for (int hh = 0; hh < NH; ++hh) {
+                    float4v x = float4v{0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-                        for (int k = 0; k < COLS / 32; ++k)
-                            if (nh == 1 || k / (COLS / 32 / NH) == hh) O::mma(x, O::row(sv, LX, 16 * bk, 32 * k), O::row(sz, LX, 16 * bi, 32 * k));
-                        const float2 ci = gates[hh].cum[ii];
-                        const float post = REV ? gates[hh].dt[ii] : 1.f;
-                        float sum = 0.f;
+                    for (int k = hh * (COLS / NH); k < (hh + 1) * (COLS / NH); k += 32)
+                        O::mma(x, O::template row<COLS>(sv, aP, 16 * bk, k), O::template row<COLS>(sz, aP, 16 * bi, k));
+                    const float4v d = x * decays<REV>(gs[hh], ii, k0);
+                    m += d * (REV ? gs[hh].dt[ii] : 1.f);
+                    float sum = 0.f;
 #pragma unroll
-                        for (int e = 0; e < 4; ++e) {
-                            const int kk = 16 * bk + 4 * q + e;
-                            const float d = kk <= ii ? x[e] * decay_between(ci, gates[hh].cum[kk]) * gates[hh].w[kk] : 0.f;
-                            m[e] += d * post;
-                            if (kk < ii) sum += d * s[e];
-                            if (!REV && kk == ii) {
-                                diag[hh][0][ii] = x[e];
-                                diag[hh][1][ii] = x[e] * s[e];
-                            }
+                    for (int e = 0; e < 4; ++e) {
+                        sum += k0 + e < ii ? d[e] * s[e] : 0.f;
+                        if (!REV && k0 + e == ii && ii < rows) {
+                            const int64_t to = ((int64_t)hb * NH + hh) * p.rows + row0 + ii;
+                            p.dyx[to] = x[e];
+                            p.wtt[to] = x[e] * s[e];
                         }
-                        sum += __shfl_xor(sum, 16, 64);
-                        sum += __shfl_xor(sum, 32, 64);
-                        if (q == 0) inner[hh][bk][ii] = sum;
                     }
-                O::put4(&sm[ii * LM + 16 * bk + 4 * q], m);
+                    sum += __shfl_xor(sum, 16, 64);
+                    sum += __shfl_xor(sum, 32, 64);
+                    if (q == 0) inner[hh][bk][ii] = sum;
+                }
+                O::put4(&sm[at<E, C>(ii, k0)], m);
             }
         }
         // 2, the state's part: z = S q2 of every head, its sum with q, and
         // times e^cum the start of out2
-        float4v z[NB * 4];
+        float4v z[4];
 #pragma unroll
-        for (int i = 0; i < NB * 4; ++i) z[i] = float4v{0.f, 0.f, 0.f, 0.f};
+        for (int i = 0; i < 4; ++i) z[i] = float4v{0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-        for (int hh = 0; hh < NH; ++hh)
-            if (hh < nh) {
-                float4v a[NB * 4];
+        for (int hh = 0; hh < NH; ++hh) {
+            float4v a[4];
 #pragma unroll
-                for (int i = 0; i < NB * 4; ++i) a[i] = float4v{0.f, 0.f, 0.f, 0.f};
+            for (int i = 0; i < 4; ++i) a[i] = float4v{0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-                for (int pb = 0; pb < PB; pb += 2)
-                    if (nh == 1 || pb / (PB / NH) == hh) {
-                        typename O::frag hf[NB][kP];
-#pragma unroll
-                        for (int nb = 0; nb < NB; ++nb) O::acc_split(h[nb * PB + pb], h[nb * PB + pb + 1], hf[nb]);
-#pragma unroll
-                        for (int bi = 0; bi < 4; ++bi) {
-                            const typename O::frag zf = O::row_split(sz, LX, 16 * bi, 16 * pb);
-#pragma unroll
-                            for (int nb = 0; nb < NB; ++nb)
-#pragma unroll
-                                for (int k = 0; k < kP; ++k) O::mma(a[nb * 4 + bi], hf[nb][k], zf);
-                        }
-                    }
+            for (int pb = hh * (PB / NH); pb < (hh + 1) * (PB / NH); pb += 2) {
+                typename O::frag hf[kP];
+                O::acc(h[pb], h[pb + 1], hf);
 #pragma unroll
                 for (int bi = 0; bi < 4; ++bi) {
-                    const int ii = 16 * bi + j;
-                    const float ec = gates[hh].ecum[ii], post = REV ? gates[hh].dt[ii] : 1.f;
-                    float sum = 0.f;
+                    const typename O::frag zf = O::template row<COLS>(sz, aP, 16 * bi, 16 * pb);
 #pragma unroll
-                    for (int nb = 0; nb < NB; ++nb) {
-                        float x[4];
-                        O::get4(&sq[ii * LN + wn + 16 * nb + 4 * q], x);
-                        a[nb * 4 + bi] *= ec;
-#pragma unroll
-                        for (int e = 0; e < 4; ++e) sum += a[nb * 4 + bi][e] * x[e];
-                        z[nb * 4 + bi] += a[nb * 4 + bi] * post;
-                    }
-                    sum += __shfl_xor(sum, 16, 64);
-                    sum += __shfl_xor(sum, 32, 64);
-                    if (q == 0) outer[hh][w][ii] = sum;
+                    for (int k = 0; k < kP; ++k) O::mma(a[bi], hf[k], zf);
                 }
             }
-        __syncthreads();                          // M and the sums are whole
-        if (w < nh && l < rows) {
+#pragma unroll
+            for (int bi = 0; bi < 4; ++bi) {
+                const int ii = 16 * bi + j;
+                float x[4], sum = 0.f;
+                O::get4(&sq[at<E, N>(ii, wn + 4 * q)], x);
+                a[bi] *= gs[hh].ecum[ii];
+#pragma unroll
+                for (int e = 0; e < 4; ++e) sum += a[bi][e] * x[e];
+                z[bi] += a[bi] * (REV ? gs[hh].dt[ii] : 1.f);
+                sum += __shfl_xor(sum, 16, 64);
+                sum += __shfl_xor(sum, 32, 64);
+                if (q == 0) outer[hh][w][ii] = sum;
+            }
+        }
+        lds_barrier();                            // M and the sums are whole
+        if (w < NH && l < rows) {
             // row l's sums, to the token's place
-            const int t = lo + (REV ? rows - 1 - l : l);
-            const int64_t at = ((int64_t)hb * NH + w) * p.rows + (int64_t)seg.batch * p.T + t;
-            float sum = 0.f;
+            const int64_t to = ((int64_t)hb * NH + w) * p.rows + row0 + (REV ? rows - 1 - l : l);
+            float sum = 0.f, out = 0.f;
 #pragma unroll
             for (int b = 0; b < 4; ++b)
                 if (b <= l >> 4) sum += inner[w][b][l];
-            p.inside[at] = sum;
-            p.across[at] = outer[w][0][l] + outer[w][1][l] + outer[w][2][l] + outer[w][3][l];
-            if constexpr (!REV) {
-                p.dyx[at] = diag[w][0][l];
-                p.wtt[at] = diag[w][1][l];
-            }
+#pragma unroll
+            for (int b = 0; b < NW; ++b) out += outer[w][b][l];
+            p.inside[to] = sum;
+            p.across[to] = out;
         }
         // 2 and 3: both take k by its N values
 #pragma unroll
-        for (int hh = 0; hh < NH; ++hh)
-            if (hh < nh) {
-                const float et = fast_exp2((float)gates[hh].total);
+        for (int hh = 0; hh < NH; ++hh) {
+            const float et = fast_exp2((float)gs[hh].total);
 #pragma unroll
-                for (int i = 0; i < NB * PB; ++i)
-                    if (nh == 1 || (i % PB) / (PB / NH) == hh) h[i] *= et;
-            }
+            for (int pb = hh * (PB / NH); pb < (hh + 1) * (PB / NH); ++pb) h[pb] *= et;
+        }
 #pragma unroll
         for (int s0 = 0; s0 < C; s0 += 32) {
-            typename O::frag kf[NB], kw[NH][NB][kP];
+            const typename O::frag kf = O::template col<N>(sk, aN, wn, s0);
 #pragma unroll
-            for (int nb = 0; nb < NB; ++nb) kf[nb] = O::col(sk, LN, wn + 16 * nb, s0);
+            for (int bi = s0 / 16; bi < 4; ++bi) O::mma(z[bi], kf, O::template row<C>(sm, aM, 16 * bi, s0));
 #pragma unroll
-            for (int hh = 0; hh < NH; ++hh)
-                if (hh < nh) {
-                    float wt[8];
+            for (int hh = 0; hh < NH; ++hh) {
+                typename O::frag kw[kP];
+                float wt[8];
 #pragma unroll
-                    for (int e = 0; e < 8; ++e) wt[e] = gates[hh].end[s0 + 8 * q + e];
+                for (int e = 0; e < 8; ++e) wt[e] = gs[hh].end[s0 + 8 * q + e];
+                O::scaled(kf, wt, kw);
 #pragma unroll
-                    for (int nb = 0; nb < NB; ++nb) O::scaled(kf[nb], wt, kw[hh][nb]);
-                }
+                for (int pb = hh * (PB / NH); pb < (hh + 1) * (PB / NH); ++pb) {
+                    const typename O::frag vf = O::template pair<COLS>(sv, aP, 32 * (pb >> 1), pb & 1, s0);
 #pragma unroll
-            for (int bi = s0 / 16; bi < 4; ++bi) {
-                const typename O::frag mf = O::row(sm, LM, 16 * bi, s0);
-#pragma unroll
-                for (int nb = 0; nb < NB; ++nb) O::mma(z[nb * 4 + bi], kf[nb], mf);
-            }
-#pragma unroll
-            for (int pb = 0; pb < PB; ++pb) {
-                const typename O::frag vf = O::col(sv, LX, 16 * pb, s0);
-#pragma unroll
-                for (int nb = 0; nb < NB; ++nb) {
-#pragma unroll
-                    for (int hh = 0; hh < NH; ++hh)
-                        if (hh < nh && (nh == 1 || pb / (PB / NH) == hh)) {
-#pragma unroll
-                            for (int k = 0; k < kP; ++k) O::mma(h[nb * PB + pb], vf, kw[hh][nb][k]);
-                        }
+                    for (int k = 0; k < kP; ++k) O::mma(h[pb], vf, kw[k]);
                 }
             }
         }
         if constexpr (!REV) {
             if (mark >= 0) {
-                float2 *m = (float2 *)p.marks + ((int64_t)mark * p.n_hb + hb) * (N * COLS / 2) + threadIdx.x;
+                float2 *m = (float2 *)p.marks + ((int64_t)mark * p.n_hb + hb) * (N * COLS / 2) + tid;
 #pragma unroll
-                for (int i = 0; i < NB * PB; ++i) {
-                    m[(2 * i) * 256] = make_float2(h[i][0], h[i][1]);
-                    m[(2 * i + 1) * 256] = make_float2(h[i][2], h[i][3]);
+                for (int pb = 0; pb < PB; ++pb) {
+                    m[(2 * pb) * kThreads] = make_float2(h[pb][0], h[pb][1]);
+                    m[(2 * pb + 1) * kThreads] = make_float2(h[pb][2], h[pb][3]);
                 }
             }
         }
         // (the sum over the blocks of columns of a group follows in ssm_sum_kernel)
-        const int slot = chunk_slot(p, seg, c);
+        const int slot = chunk_slot(p, seg, REV ? nc - 1 - c : c);
         if (slot < p.n_slots) {
-            float2 *part = (float2 *)p.part + ((int64_t)slot * p.n_hb + hb) * (NB * 8 * 256) + threadIdx.x;
+            float2 *part = (float2 *)p.part + ((int64_t)slot * p.n_hb + hb) * (8 * kThreads) + tid;
 #pragma unroll
-            for (int i = 0; i < NB * 4; ++i) {
-                part[(2 * i) * 256] = make_float2(z[i][0], z[i][1]);
-                part[(2 * i + 1) * 256] = make_float2(z[i][2], z[i][3]);
+            for (int i = 0; i < 4; ++i) {
+                part[(2 * i) * kThreads] = make_float2(z[i][0], z[i][1]);
+                part[(2 * i + 1) * kThreads] = make_float2(z[i][2], z[i][3]);
             }
         }
     }
@@ -296,23 +281,24 @@ __global__ void __launch_bounds__(256) ssm_key_kernel(SsmParams p) {
 // out2 of a chunk and group: the sum over the group's blocks of columns, in
 // the lanes' own layout.
 template <typename IO, int N, bool REV>
-__global__ void __launch_bounds__(256) ssm_sum_kernel(SsmParams p) {
-    constexpr int NB = N / 64;
+__global__ void __launch_bounds__(4 * N) ssm_sum_kernel(SsmParams p) {
+    constexpr int kThreads = 4 * N;
     const int cps = p.seg_tokens / kSsmChunk, G = p.H / p.heads_per_group;
     const int g = blockIdx.x % G, c = blockIdx.x / G % cps, item = blockIdx.x / G / cps;
     const Segment seg = find_segment(p, item);
-    if (!seg.live || c >= chunks_of(seg)) return;
-    const int slot = chunk_slot(p, seg, c);
+    const int nc = chunks_of(seg);
+    if (!seg.live || c >= nc) return;
+    const int slot = chunk_slot(p, seg, REV ? nc - 1 - c : c);
     if (slot >= p.n_slots) return;
     const int w = wave_id(), l = lane_id(), q = l >> 4, j = l & 15, per = p.n_hb / G;
-    float4v z[NB * 4];
+    float4v z[4];
 #pragma unroll
-    for (int i = 0; i < NB * 4; ++i) z[i] = float4v{0.f, 0.f, 0.f, 0.f};
-    const float2 *part = (const float2 *)p.part + ((int64_t)slot * p.n_hb + g * per) * (NB * 8 * 256) + threadIdx.x;
-    for (int k = 0; k < per; ++k, part += NB * 8 * 256) {
+    for (int i = 0; i < 4; ++i) z[i] = float4v{0.f, 0.f, 0.f, 0.f};
+    const float2 *part = (const float2 *)p.part + ((int64_t)slot * p.n_hb + g * per) * (8 * kThreads) + threadIdx.x;
+    for (int k = 0; k < per; ++k, part += 8 * kThreads) {
 #pragma unroll
-        for (int i = 0; i < NB * 4; ++i) {
-            const float2 a = part[(2 * i) * 256], b = part[(2 * i + 1) * 256];
+        for (int i = 0; i < 4; ++i) {
+            const float2 a = part[(2 * i) * kThreads], b = part[(2 * i + 1) * kThreads];
             z[i] += float4v{a.x, a.y, b.x, b.y};
         }
     }
@@ -320,13 +306,11 @@ __global__ void __launch_bounds__(256) ssm_sum_kernel(SsmParams p) {
     const int rows = chunk_of<REV>(seg, c, lo);
     const rsrc_t r = make_rsrc((IO *)p.out + seg.batch * p.ob + lo * p.ot + (int64_t)g * N, 0x7fffffffu);
 #pragma unroll
-    for (int nb = 0; nb < NB; ++nb)
-#pragma unroll
-        for (int bi = 0; bi < 4; ++bi) {
-            const int ii = 16 * bi + j, t = REV ? rows - 1 - ii : ii;
-            const uint32_t e = (uint32_t)t * (uint32_t)p.ot + w * (N / 4) + 16 * nb + 4 * q;
-            store_row4<IO>(r, ii < rows ? e * (uint32_t)sizeof(IO) : 0xfffffff0u, z[nb * 4 + bi]);
-        }
+    for (int bi = 0; bi < 4; ++bi) {
+        const int ii = 16 * bi + j, t = REV ? rows - 1 - ii : ii;
+        const uint32_t e = (uint32_t)t * (uint32_t)p.ot + 16 * w + 4 * q;
+        store_row4<IO>(r, ii < rows ? e * (uint32_t)sizeof(IO) : 0xfffffff0u, z[bi]);
+    }
 }
 
 // The gradients of a segment's gates, one head a workgroup, a chunk a wave
@@ -361,6 +345,7 @@ __global__ void __launch_bounds__(256) ssm_gate_kernel(GateParams gp) {
         return;
     }
     const int cols = 64 * gp.ncb, per_hb = cols / p.P;          // heads of a block of columns (0: a part of one)
+    const int nh = per_hb > 1 ? per_hb : 1;
     const int hb0 = head * p.P / cols, tiles = per_hb ? 1 : p.P / cols, hh = per_hb ? head % per_hb : 0;
     const float A = p.A[head], bias = p.bias ? p.bias[head] : 0.f;
     double dA = 0.0, dD = 0.0, db = 0.0;
@@ -373,7 +358,7 @@ __global__ void __launch_bounds__(256) ssm_gate_kernel(GateParams gp) {
         float ri = 0.f, ra = 0.f, ci = 0.f, ca = 0.f, dd = 0.f, wtt = 0.f, raw = 0.f;
         if (on) {
             for (int k = 0; k < tiles; ++k) {
-                const int64_t at = ((int64_t)(hb0 + k) * gp.ncb + hh) * p.rows + (int64_t)seg.batch * p.T + t;
+                const int64_t at = ((int64_t)(hb0 + k) * nh + hh) * p.rows + (int64_t)seg.batch * p.T + t;
                 ri += p.inside[at];
                 ra += p.across[at];
                 ci += gp.c_inside[at];
@@ -398,7 +383,7 @@ __global__ void __launch_bounds__(256) ssm_gate_kernel(GateParams gp) {
             wsum[w][2] = cut ? 0.0 : 1.0;
             wsum[w][3] = mark >= 0 ? 1.0 : 0.0;
             double m = 0.0;
-            for (int k = 0; mark >= 0 && k < tiles; ++k) m += p.X[((int64_t)mark * p.n_hb + hb0 + k) * gp.ncb + hh];
+            for (int k = 0; mark >= 0 && k < tiles; ++k) m += p.X[((int64_t)mark * p.n_hb + hb0 + k) * nh + hh];
             wsum[w][4] = m;
         }
         __syncthreads();
@@ -477,26 +462,27 @@ BwdPlan bwd_plan(const gdn_ssm_problem *pr, bool packed) {
         at += (n + 15) / 16 * 16;
         return was;
     };
-    b.total = take(blocks * b.s.ncb * 8);
+    b.total = take(blocks * b.s.nh * 8);
     b.ends = take(blocks * pr->N * 64 * b.s.ncb * 4);
     b.ends_rev = take(blocks * pr->N * 64 * b.s.ncb * 4);
-    for (size_t &o : b.sums) o = take((size_t)b.s.n_hb * b.s.ncb * b.rows * 4);
+    for (size_t &o : b.sums) o = take((size_t)b.s.n_hb * b.s.nh * b.rows * 4);
     b.mark = take((size_t)b.marks * b.s.n_hb * pr->N * 64 * b.s.ncb * 4);
-    b.X = take((size_t)b.marks * b.s.n_hb * b.s.ncb * 8);
+    b.X = take((size_t)b.marks * b.s.n_hb * b.s.nh * 8);
     b.part = take((size_t)b.slots * b.s.n_hb * kSsmChunk * pr->N * 4);
     b.grads = take((size_t)b.s.n_items * pr->H * 3 * 8);
     b.bytes = at;
     return b;
 }
 
-template <typename IO, int N, int NCB>
+template <typename IO, int N, int COLS, int NH>
 struct BwdFns {
+    static constexpr int kScanThreads = 4 * COLS, kKeyThreads = 4 * N;
     static const void *ends(bool rev) {
-        return rev ? (const void *)&ssm_scan_kernel<IO, N, NCB, true, true, 3> : (const void *)&ssm_scan_kernel<IO, N, NCB, true, false, 3>;
+        return rev ? (const void *)&ssm_scan_kernel<IO, N, COLS, NH, true, true, 3> : (const void *)&ssm_scan_kernel<IO, N, COLS, NH, true, false, 3>;
     }
-    static const void *dx() { return (const void *)&ssm_scan_kernel<IO, N, NCB, false, true, 2>; }
+    static const void *dx() { return (const void *)&ssm_scan_kernel<IO, N, COLS, NH, false, true, 2>; }
     static const void *key(bool rev) {
-        return rev ? (const void *)&ssm_key_kernel<IO, N, NCB, true> : (const void *)&ssm_key_kernel<IO, N, NCB, false>;
+        return rev ? (const void *)&ssm_key_kernel<IO, N, COLS, NH, true> : (const void *)&ssm_key_kernel<IO, N, COLS, NH, false>;
     }
     static const void *sum(bool rev) {
         return rev ? (const void *)&ssm_sum_kernel<IO, N, true> : (const void *)&ssm_sum_kernel<IO, N, false>;
@@ -511,24 +497,24 @@ gdn_status bwd_launches(const gdn_ssm_problem *pr, const BwdPlan &b, const SsmPa
     const int grid = ssm_grid(f, b.s);
     ssm_grid(r, b.s);
     gdn_status st = GDN_OK;
-    auto go = [&](const void *fn, int g, SsmParams &sp) {
-        if (st == GDN_OK) st = launch_kernel(fn, g, &sp, s);
+    auto go = [&](const void *fn, int g, SsmParams &sp, int threads) {
+        if (st == GDN_OK) st = launch_kernel(fn, g, &sp, s, threads);
     };
     if (!one) {
-        go(F::ends(false), grid, f);
-        go(F::ends(true), grid, r);
+        go(F::ends(false), grid, f, F::kScanThreads);
+        go(F::ends(true), grid, r, F::kScanThreads);
     }
     SsmParams d = r;
     d.out = dx;
     d.sT = dh0;
-    go(F::dx(), grid, d);
+    go(F::dx(), grid, d, F::kScanThreads);
     const int sgrid = b.s.n_items * (b.s.seg_tokens / kSsmChunk) * (int)pr->G;
     f.out = dC;
-    go(F::key(false), grid, f);
-    go(F::sum(false), sgrid, f);
+    go(F::key(false), grid, f, F::kKeyThreads);
+    go(F::sum(false), sgrid, f, F::kKeyThreads);
     r.out = dB;
-    go(F::key(true), grid, r);
-    go(F::sum(true), sgrid, r);
+    go(F::key(true), grid, r, F::kKeyThreads);
+    go(F::sum(true), sgrid, r, F::kKeyThreads);
     if (st != GDN_OK) return st;
     gp.s = f;
     return GDN_OK;
@@ -625,15 +611,18 @@ gdn_status gdn_ssm_backward(const gdn_ssm_problem *pr, const void *dy, const voi
     gp.dbias = ddt_bias;
     gp.ncb = b.s.ncb;
     hipStream_t s = (hipStream_t)stream;
+    auto run = [&](auto n64, auto n128) {
+        return pr->N == 64 ? bwd_launches<decltype(n64)>(pr, b, f, r, gp, dx, dB, dC, dh0, s)
+                           : bwd_launches<decltype(n128)>(pr, b, f, r, gp, dx, dB, dC, dh0, s);
+    };
     if (pr->io_dtype == GDN_F32)
-        st = pr->N == 64 ? bwd_launches<BwdFns<float, 64, 1>>(pr, b, f, r, gp, dx, dB, dC, dh0, s)
-                         : bwd_launches<BwdFns<float, 128, 1>>(pr, b, f, r, gp, dx, dB, dC, dh0, s);
+        st = run(BwdFns<float, 64, 64, 1>(), BwdFns<float, 128, 64, 1>());
     else if (b.s.ncb == 1)
-        st = pr->N == 64 ? bwd_launches<BwdFns<bf16_t, 64, 1>>(pr, b, f, r, gp, dx, dB, dC, dh0, s)
-                         : bwd_launches<BwdFns<bf16_t, 128, 1>>(pr, b, f, r, gp, dx, dB, dC, dh0, s);
+        st = run(BwdFns<bf16_t, 64, 64, 1>(), BwdFns<bf16_t, 128, 64, 1>());
+    else if (b.s.nh == 2)
+        st = run(BwdFns<bf16_t, 64, 128, 2>(), BwdFns<bf16_t, 128, 128, 2>());
     else
-        st = pr->N == 64 ? bwd_launches<BwdFns<bf16_t, 64, 2>>(pr, b, f, r, gp, dx, dB, dC, dh0, s)
-                         : bwd_launches<BwdFns<bf16_t, 128, 2>>(pr, b, f, r, gp, dx, dB, dC, dh0, s);
+        st = run(BwdFns<bf16_t, 64, 128, 1>(), BwdFns<bf16_t, 128, 128, 1>());
     if (st != GDN_OK) return st;
     const void *fn = pr->io_dtype == GDN_F32 ? (const void *)&ssm_gate_kernel<float> : (const void *)&ssm_gate_kernel<bf16_t>;
     st = launch_kernel(fn, b.s.n_items * (int)pr->H, &gp, s);
