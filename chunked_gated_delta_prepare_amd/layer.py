@@ -19,8 +19,8 @@ outputs and workspaces are allocated on that stream.
 """
 from __future__ import annotations
 
-import contextlib
 import ctypes
+import functools
 
 import torch
 
@@ -76,33 +76,48 @@ def declare(lib):
             getattr(lib, name).restype = ctypes.c_int
 
 
-def _library():
-    from . import load_library
-    return load_library()
+_functions = {}
+
+
+def _function(name):
+    f = _functions.get(name)
+    if f is None:
+        from . import load_library
+        f = _functions[name] = getattr(load_library(), name)
+    return f
 
 
 def _call(name, *args):
-    lib = _library()
-    rc = getattr(lib, name)(*args)
+    rc = _function(name)(*args)
     if rc != 0:
-        from . import GdnError
-        raise GdnError(name, rc, lib.gdn_status_str(rc).decode())
+        from . import GdnError, load_library
+        raise GdnError(name, rc, load_library().gdn_status_str(rc).decode())
+
+
+# What a problem's sizes, strides and types alone decide: its structure and
+# the bytes of workspace it needs.
+@functools.lru_cache(maxsize=4096)
+def _problem(kind, size_of, *fields):
+    ref = ctypes.byref(kind(*fields))
+    return ref, int(_function(size_of)(ref)) if size_of else 0
 
 
 def _io_code(t, name):
-    if t.dtype not in (torch.bfloat16, torch.float32):
+    code = _CODE.get(t.dtype)
+    if code is None or code == GDN_E4M3:
         raise TypeError("%s must be bfloat16 or float32, got %s" % (name, t.dtype))
-    return _CODE[t.dtype]
+    return code
 
 
-def _check(t, name, device, shape, dtype=None, dense=True):
+def _check(t, name, device, shape, dtype=None, other=None, dense=True):
+    """A tensor on the device, of this shape, and of dtype or other."""
     if not isinstance(t, torch.Tensor):
         raise TypeError("%s must be a torch.Tensor" % name)
-    if t.device != device or not t.is_cuda:
+    if t.device != device:
         raise ValueError("%s must be on %s, got %s" % (name, device, t.device))
-    if dtype is not None and t.dtype not in (dtype if isinstance(dtype, tuple) else (dtype,)):
-        raise TypeError("%s must be %s, got %s" % (name, dtype, t.dtype))
-    if tuple(t.shape) != tuple(shape):
+    if dtype is not None and t.dtype is not dtype and t.dtype is not other:
+        raise TypeError("%s must be %s, got %s" % (name, dtype if other in (None, dtype) else "%s or %s" % (dtype, other), t.dtype))
+    if t.shape != shape:
         raise ValueError("%s must have shape %s, got %s" % (name, tuple(shape), tuple(t.shape)))
     if dense and not t.is_contiguous():
         raise ValueError("%s must be contiguous" % name)
@@ -116,43 +131,41 @@ def _device(t, name):
     return t.device
 
 
-class _On:
-    """Makes the tensors' device and the stream that the work goes to current,
-    so that what is allocated inside belongs to that stream; ``handle`` is the
-    stream's."""
-
-    def __init__(self, device, stream):
-        if stream is not None and stream.device != device:
-            raise ValueError("the stream is on %s, the tensors on %s" % (stream.device, device))
-        index = device.index
-        if stream is None:
-            self.handle = torch.cuda.current_stream(index).cuda_stream
-            self.ctx = contextlib.nullcontext() if torch.cuda.current_device() == index else torch.cuda.device(index)
-        else:
-            self.handle = stream.cuda_stream
-            self.ctx = torch.cuda.stream(stream)
-
-    def __enter__(self):
-        self.ctx.__enter__()
-        return self.handle
-
-    def __exit__(self, *exc):
-        return self.ctx.__exit__(*exc)
+def _on(device, stream, work, *args):
+    """work(handle, *args) with the tensors' device current, and the stream that
+    the work goes to, so that what is allocated in it belongs to that stream;
+    handle is the stream's."""
+    index = device.index
+    if stream is None:
+        if torch.cuda.current_device() == index:
+            return work(torch._C._cuda_getCurrentRawStream(index), *args)
+        with torch.cuda.device(index):
+            return work(torch._C._cuda_getCurrentRawStream(index), *args)
+    if stream.device != device:
+        raise ValueError("the stream is on %s, the tensors on %s" % (stream.device, device))
+    with torch.cuda.stream(stream):
+        return work(stream.cuda_stream, *args)
 
 
 def _ptr(t):
-    return None if t is None or t.numel() == 0 else t.data_ptr()
+    return None if t is None else t.data_ptr() or None
+
+
+def _span(t):
+    """The addresses a tensor reaches, [first, last + 1)."""
+    lo = t.data_ptr()
+    if t.is_contiguous():
+        return lo, lo + t.numel() * t.element_size()
+    return lo, lo + t.element_size() * (1 + sum((n - 1) * s for n, s in zip(t.shape, t.stride())))
 
 
 def _apart(out, name, *inputs):
     """Outputs do not alias inputs."""
     if out is not None and out.numel():
-        lo = out.data_ptr()
-        hi = lo + out.element_size() * (1 + sum((n - 1) * s for n, s in zip(out.shape, out.stride())))
+        lo, hi = _span(out)
         for t in inputs:
             if t is not None and t.numel():
-                a = t.data_ptr()
-                b = a + t.element_size() * (1 + sum((n - 1) * s for n, s in zip(t.shape, t.stride())))
+                a, b = _span(t)
                 if a < hi and lo < b:
                     raise ValueError("%s must not share memory with an input" % name)
 
@@ -210,79 +223,93 @@ def norm_forward(x, weight, residual=None, *, eps=1e-6, out_dtype=None, group=0,
     None without a residual, scales [..., groups] fp32 or None.  A given s
     may be the residual."""
     dev = _device(x, "x")
-    if x.dim() < 1 or x.shape[-1] < 1:
-        raise ValueError("x must have a last dimension of at least 1, got %s" % (tuple(x.shape),))
-    D = x.shape[-1]
+    shape, dt = x.shape, x.dtype
+    if x.dim() < 1 or shape[-1] < 1:
+        raise ValueError("x must have a last dimension of at least 1, got %s" % (tuple(shape),))
     code = _io_code(x, "x")
-    merged = _rows(x)
-    if merged is None:
-        raise ValueError("x's rows must be contiguous and lie at one stride")
-    _check(weight, "weight", dev, (D,), (x.dtype, torch.float32))
-    sdt = x.dtype
+    _check(weight, "weight", dev, shape[-1:], dt, torch.float32)
     if residual is not None:
-        _check(residual, "residual", dev, x.shape, (x.dtype, torch.float32))
-        sdt = residual.dtype
-    od = out_dtype or x.dtype
-    if od not in (x.dtype, _FP8):
-        raise TypeError("out_dtype must be %s or %s, got %s" % (x.dtype, _FP8, od))
+        _check(residual, "residual", dev, shape, dt, torch.float32)
+    if out_dtype not in (None, dt, _FP8):
+        raise TypeError("out_dtype must be %s or %s, got %s" % (dt, _FP8, out_dtype))
     if group not in (0, 128):
         raise ValueError("group must be 0 (a scale per row) or 128, got %r" % (group,))
-    with _On(dev, stream) as handle:
-        y = _out(y, "y", dev, x.shape, od, (x, weight, residual))
-        if residual is not None and (s is None or s.data_ptr() != residual.data_ptr()):
-            s = _out(s, "s", dev, x.shape, sdt, (x, weight, residual, y))
-        elif residual is not None:
-            _check(s, "s", dev, x.shape, sdt)
-        if od == _FP8:
-            ng = (D + group - 1) // group if group else 1
-            scales = _out(scales, "scales", dev, tuple(x.shape[:-1]) + (ng,), torch.float32, (x, weight, residual, y))
+    return _on(dev, stream, _norm_forward, dev, code, x, weight, residual, eps, out_dtype or dt, group, y, s, scales)
+
+
+def _norm_forward(handle, dev, code, x, weight, residual, eps, od, group, y, s, scales):
+    shape, D = x.shape, x.shape[-1]
+    if x.is_contiguous():
+        rows, stride = x.numel() // D, D
+    else:
+        merged = _rows(x)
+        if merged is None:
+            raise ValueError("x's rows must be contiguous and lie at one stride")
+        rows, stride = merged
+    y = _out(y, "y", dev, shape, od, (x, weight, residual))
+    scode = code
+    if residual is not None:
+        scode = _CODE[residual.dtype]
+        if s is not None and s.data_ptr() == residual.data_ptr():
+            _check(s, "s", dev, shape, residual.dtype)
         else:
-            scales = None
-        pr = NormProblem(merged[0], D, merged[1], code, _CODE[sdt], _CODE[weight.dtype], _CODE[od], group, eps)
-        _call("gdn_norm_forward", ctypes.byref(pr), _ptr(x), _ptr(residual), _ptr(weight), _ptr(y),
-              _ptr(s) if residual is not None else None, _ptr(scales), handle)
-    return y, (None if residual is None else s), scales
+            s = _out(s, "s", dev, shape, residual.dtype, (x, weight, residual, y))
+    else:
+        s = None
+    if od is _FP8:
+        scales = _out(scales, "scales", dev, shape[:-1] + ((D + group - 1) // group if group else 1,), torch.float32,
+                      (x, weight, residual, y, s))
+    else:
+        scales = None
+    pr, _ = _problem(NormProblem, None, rows, D, stride, code, scode, _CODE[weight.dtype], _CODE[od], group, eps)
+    _call("gdn_norm_forward", pr, _ptr(x), _ptr(residual), _ptr(weight), _ptr(y), _ptr(s), _ptr(scales), handle)
+    return y, s, scales
 
 
 def norm_backward(dy, s, weight, dres=None, *, eps=1e-6, x_dtype=None, ds=None, dx=None, dweight=None,
                   workspace=None, stream=None):
     """The norm's gradients from dy [..., D] (of y, in x's type), s as
-    norm_forward returned it (x where there was no residual), and dres (of s, in s's type, or None).  Returns
-    (ds, dx, dweight): ds in s's type is the gradient of the residual; dx in
-    x_dtype (default: dy's type) is that of x, ds itself where the types are
-    equal; dweight [D] fp32.  A given ds may be dres."""
+    norm_forward returned it (x where there was no residual), and dres (of s, in
+    s's type, or None).  Returns (ds, dx, dweight): ds in s's type is the
+    gradient of the residual; dx in x_dtype (default: dy's type) is that of x,
+    ds itself where the types are equal; dweight [D] fp32.  A given ds may be
+    dres."""
     dev = _device(dy, "dy")
-    if dy.dim() < 1 or dy.shape[-1] < 1:
-        raise ValueError("dy must have a last dimension of at least 1, got %s" % (tuple(dy.shape),))
-    D = dy.shape[-1]
+    shape, dt = dy.shape, dy.dtype
+    if dy.dim() < 1 or shape[-1] < 1:
+        raise ValueError("dy must have a last dimension of at least 1, got %s" % (tuple(shape),))
     code = _io_code(dy, "dy")
-    if x_dtype not in (None, dy.dtype):
-        raise TypeError("dy has x's type: got %s for x of %s" % (dy.dtype, x_dtype))
-    _check(dy, "dy", dev, dy.shape)
-    _check(s, "s", dev, dy.shape, (dy.dtype, torch.float32))
-    _check(weight, "weight", dev, (D,), (dy.dtype, torch.float32))
+    if x_dtype not in (None, dt):
+        raise TypeError("dy has x's type: got %s for x of %s" % (dt, x_dtype))
+    if not dy.is_contiguous():
+        raise ValueError("dy must be contiguous")
+    _check(s, "s", dev, shape, dt, torch.float32)
+    _check(weight, "weight", dev, shape[-1:], dt, torch.float32)
     if dres is not None:
-        _check(dres, "dres", dev, dy.shape, s.dtype)
-    lib = _library()
-    with _On(dev, stream) as handle:
-        ins = (dy, s, weight)
-        if dres is not None and ds is not None and ds.data_ptr() == dres.data_ptr():
-            _check(ds, "ds", dev, dy.shape, s.dtype)
-        else:
-            ds = _out(ds, "ds", dev, dy.shape, s.dtype, ins + (dres,))
-        if s.dtype == dy.dtype:
-            if dx is not None and dx is not ds:
-                raise ValueError("dx is ds where x and s have one type")
-            dx = ds
-        else:
-            dx = _out(dx, "dx", dev, dy.shape, dy.dtype, ins + (dres, ds))
-        dweight = _out(dweight, "dweight", dev, (D,), torch.float32, ins + (dres, ds, dx))
-        pr = NormProblem(dy.numel() // D, D, D, code, _CODE[s.dtype], _CODE[weight.dtype], code, 0, eps)
-        need = int(lib.gdn_workspace_bytes_norm_backward(ctypes.byref(pr)))
-        workspace, size = _workspace(need, dev, workspace)
-        _call("gdn_norm_backward", ctypes.byref(pr), _ptr(dy), _ptr(s), _ptr(weight), _ptr(dres), _ptr(ds),
-              None if dx is ds else _ptr(dx), _ptr(dweight), _ptr(workspace), size, handle)
-    return ds, dx, dweight
+        _check(dres, "dres", dev, shape, s.dtype)
+    return _on(dev, stream, _norm_backward, dev, code, dy, s, weight, dres, eps, ds, dx, dweight, workspace)
+
+
+def _norm_backward(handle, dev, code, dy, s, weight, dres, eps, ds, dx, dweight, workspace):
+    shape, D = dy.shape, dy.shape[-1]
+    ins = (dy, s, weight)
+    if dres is not None and ds is not None and ds.data_ptr() == dres.data_ptr():
+        _check(ds, "ds", dev, shape, s.dtype)
+    else:
+        ds = _out(ds, "ds", dev, shape, s.dtype, ins + (dres,))
+    if s.dtype is dy.dtype:
+        if dx is not None and dx is not ds:
+            raise ValueError("dx is ds where x and s have one type")
+        dx = None
+    else:
+        dx = _out(dx, "dx", dev, shape, dy.dtype, ins + (dres, ds))
+    dweight = _out(dweight, "dweight", dev, shape[-1:], torch.float32, ins + (dres, ds, dx))
+    pr, need = _problem(NormProblem, "gdn_workspace_bytes_norm_backward", dy.numel() // D, D, D, code, _CODE[s.dtype],
+                        _CODE[weight.dtype], code, 0, eps)
+    workspace, size = _workspace(need, dev, workspace)
+    _call("gdn_norm_backward", pr, _ptr(dy), _ptr(s), _ptr(weight), _ptr(dres), _ptr(ds), _ptr(dx), _ptr(dweight),
+          _ptr(workspace), size, handle)
+    return ds, ds if dx is None else dx, dweight
 
 
 # ---------------------------------------------------------------------------
@@ -297,34 +324,38 @@ def _silu(activation):
 
 def _strides(t, name):
     """(batch, token) strides of [B, T, ...] whose other dimensions are dense."""
+    shape, strides = t.shape, t.stride()
     want = 1
-    for n, s in zip(reversed(t.shape[2:]), reversed(t.stride()[2:])):
-        if n != 1 and s != want and t.numel():
+    for i in range(len(shape) - 1, 1, -1):
+        n = shape[i]
+        if strides[i] != want and n != 1 and t.numel():
             raise ValueError("%s must be contiguous behind its token dimension" % name)
         want *= n
-    return (t.stride(0) if t.shape[0] != 1 else 0), (t.stride(1) if t.shape[1] != 1 else want)
+    return (strides[0] if shape[0] != 1 else 0), (strides[1] if shape[1] != 1 else want)
 
 
 def _packed(cu, dev, B):
     if cu is None:
         return 0
-    if not isinstance(cu, torch.Tensor) or cu.dim() != 1 or cu.numel() < 2:
+    if not isinstance(cu, torch.Tensor) or cu.dim() != 1 or cu.shape[0] < 2:
         raise ValueError("cu_seqlens must hold N + 1 >= 2 offsets")
-    _check(cu, "cu_seqlens", dev, (cu.numel(),), torch.int32)
+    _check(cu, "cu_seqlens", dev, cu.shape, torch.int32)
     if B != 1:
         raise ValueError("packed sequences use a batch of 1, got %d" % B)
-    return cu.numel() - 1
+    return cu.shape[0] - 1
 
 
-def _conv_checks(x, weight, bias):
+def _conv_checks(x, weight, bias, dims):
     dev = _device(x, "x")
     code = _io_code(x, "x")
+    if x.dim() != dims:
+        raise ValueError("x must be %s, got %s" % ("[B, T, D]" if dims == 3 else "[B, D]", tuple(x.shape)))
     if not isinstance(weight, torch.Tensor) or weight.dim() != 2:
         raise ValueError("weight must be [D, W]")
     D, W = x.shape[-1], weight.shape[1]
     if W not in (2, 3, 4):
         raise ValueError("weight must have 2, 3 or 4 taps, got %d" % W)
-    _check(weight, "weight", dev, (D, W), (x.dtype, torch.float32))
+    _check(weight, "weight", dev, (D, W), x.dtype, torch.float32)
     if bias is not None:
         _check(bias, "bias", dev, (D,), weight.dtype)
     return dev, code, D, W
@@ -337,24 +368,24 @@ def conv_forward(x, weight, bias=None, *, activation="silu", initial_state=None,
     [D, W] with W 2 to 4, bias [D]; both in x's type or fp32.  States hold the
     last W - 1 inputs: [B, W-1, D], or [N, W-1, D] with cu_seqlens (int32, N + 1
     offsets, a batch of 1).  Returns (y, final_state or None)."""
-    dev, code, D, W = _conv_checks(x, weight, bias)
-    if x.dim() != 3:
-        raise ValueError("x must be [B, T, D], got %s" % (tuple(x.shape),))
-    B, T, _ = x.shape
-    n = _packed(cu_seqlens, dev, B)
-    st = (n or B, W - 1, D)
+    dev, code, D, W = _conv_checks(x, weight, bias, 3)
+    n = _packed(cu_seqlens, dev, x.shape[0])
     if initial_state is not None:
-        _check(initial_state, "initial_state", dev, st, x.dtype)
-    sb, stt = _strides(x, "x")
-    silu = _silu(activation)
-    with _On(dev, stream) as handle:
-        ins = (x, weight, bias, initial_state, cu_seqlens)
-        y = _out(y, "y", dev, (B, T, D), x.dtype, ins)
-        if final_state is not None or output_final_state:
-            final_state = _out(final_state, "final_state", dev, st, x.dtype, ins + (y,))
-        pr = ConvProblem(B, T, D, W, sb, stt, 0, 0, n, code, _CODE[weight.dtype], silu)
-        _call("gdn_conv_forward", ctypes.byref(pr), _ptr(x), _ptr(weight), _ptr(bias), _ptr(initial_state),
-              _ptr(cu_seqlens), _ptr(y), _ptr(final_state), handle)
+        _check(initial_state, "initial_state", dev, (n or x.shape[0], W - 1, D), x.dtype)
+    return _on(dev, stream, _conv_forward, dev, code, x, weight, bias, _silu(activation), initial_state, cu_seqlens, n, y,
+               final_state, output_final_state)
+
+
+def _conv_forward(handle, dev, code, x, weight, bias, silu, initial_state, cu_seqlens, n, y, final_state, want):
+    B, T, D = x.shape
+    W = weight.shape[1]
+    ins = (x, weight, bias, initial_state, cu_seqlens)
+    y = _out(y, "y", dev, x.shape, x.dtype, ins)
+    if final_state is not None or want:
+        final_state = _out(final_state, "final_state", dev, (n or B, W - 1, D), x.dtype, ins + (y,))
+    pr, _ = _problem(ConvProblem, None, B, T, D, W, *_strides(x, "x"), 0, 0, n, code, _CODE[weight.dtype], silu)
+    _call("gdn_conv_forward", pr, _ptr(x), _ptr(weight), _ptr(bias), _ptr(initial_state), _ptr(cu_seqlens), _ptr(y),
+          _ptr(final_state), handle)
     return y, final_state
 
 
@@ -364,40 +395,32 @@ def conv_backward(dy, x, weight, bias=None, *, activation="silu", initial_state=
     dfinal (of the final states, or None).  Returns (dx, dweight [D, W] fp32,
     dbias [D] fp32 or None, dinitial or None): dbias with a bias, dinitial
     with an initial_state."""
-    dev, code, D, W = _conv_checks(x, weight, bias)
-    if x.dim() != 3:
-        raise ValueError("x must be [B, T, D], got %s" % (tuple(x.shape),))
-    B, T, _ = x.shape
-    _check(dy, "dy", dev, (B, T, D), x.dtype, dense=False)
-    n = _packed(cu_seqlens, dev, B)
-    st = (n or B, W - 1, D)
+    dev, code, D, W = _conv_checks(x, weight, bias, 3)
+    _check(dy, "dy", dev, x.shape, x.dtype, dense=False)
+    n = _packed(cu_seqlens, dev, x.shape[0])
     for t, name in ((initial_state, "initial_state"), (dfinal, "dfinal")):
         if t is not None:
-            _check(t, name, dev, st, x.dtype)
-    sb, stt = _strides(x, "x")
-    gb, gt = _strides(dy, "dy")
-    silu = _silu(activation)
-    lib = _library()
-    with _On(dev, stream) as handle:
-        ins = (dy, x, weight, bias, initial_state, cu_seqlens, dfinal)
-        dx = _out(dx, "dx", dev, (B, T, D), x.dtype, ins)
-        dweight = _out(dweight, "dweight", dev, (D, W), torch.float32, ins + (dx,))
-        if bias is not None:
-            dbias = _out(dbias, "dbias", dev, (D,), torch.float32, ins + (dx, dweight))
-        if initial_state is not None:
-            dinitial = _out(dinitial, "dinitial", dev, st, x.dtype, ins + (dx, dweight, dbias))
-        pr = ConvProblem(B, T, D, W, sb, stt, gb, gt, n, code, _CODE[weight.dtype], silu)
-        workspace, size = _workspace(int(lib.gdn_workspace_bytes_conv_backward(ctypes.byref(pr))), dev, workspace)
-        _call("gdn_conv_backward", ctypes.byref(pr), _ptr(dy), _ptr(x), _ptr(weight), _ptr(bias),
-              _ptr(initial_state), _ptr(cu_seqlens), _ptr(dfinal), _ptr(dx), _ptr(dweight),
-              _ptr(dbias) if bias is not None else None, _ptr(dinitial) if initial_state is not None else None,
-              _ptr(workspace), size, handle)
-    return dx, dweight, dbias if bias is not None else None, dinitial if initial_state is not None else None
+            _check(t, name, dev, (n or x.shape[0], W - 1, D), x.dtype)
+    return _on(dev, stream, _conv_backward, dev, code, dy, x, weight, bias, _silu(activation), initial_state, cu_seqlens, n,
+               dfinal, dx, dweight, dbias, dinitial, workspace)
 
 
-def _slots(slots, dev, B):
-    if slots is not None:
-        _check(slots, "slots", dev, (B,), torch.int32)
+def _conv_backward(handle, dev, code, dy, x, weight, bias, silu, initial_state, cu_seqlens, n, dfinal, dx, dweight, dbias,
+                   dinitial, workspace):
+    B, T, D = x.shape
+    W = weight.shape[1]
+    ins = (dy, x, weight, bias, initial_state, cu_seqlens, dfinal)
+    dx = _out(dx, "dx", dev, x.shape, x.dtype, ins)
+    dweight = _out(dweight, "dweight", dev, (D, W), torch.float32, ins + (dx,))
+    dbias = None if bias is None else _out(dbias, "dbias", dev, (D,), torch.float32, ins + (dx, dweight))
+    dinitial = None if initial_state is None else _out(dinitial, "dinitial", dev, initial_state.shape, x.dtype,
+                                                       ins + (dx, dweight, dbias))
+    pr, need = _problem(ConvProblem, "gdn_workspace_bytes_conv_backward", B, T, D, W, *_strides(x, "x"), *_strides(dy, "dy"),
+                        n, code, _CODE[weight.dtype], silu)
+    workspace, size = _workspace(need, dev, workspace)
+    _call("gdn_conv_backward", pr, _ptr(dy), _ptr(x), _ptr(weight), _ptr(bias), _ptr(initial_state), _ptr(cu_seqlens),
+          _ptr(dfinal), _ptr(dx), _ptr(dweight), _ptr(dbias), _ptr(dinitial), _ptr(workspace), size, handle)
+    return dx, dweight, dbias, dinitial
 
 
 def conv_step(x, state, weight, bias=None, *, activation="silu", slots=None, y=None, stream=None):
@@ -406,24 +429,27 @@ def conv_step(x, state, weight, bias=None, *, activation="silu", slots=None, y=N
     each row's state (None: row b has state b).  A row whose slot is outside
     [0, S), or that an earlier row names already, is padding: its y is zero
     and no state changes.  Returns y [B, D]."""
-    dev, code, D, W = _conv_checks(x, weight, bias)
-    if x.dim() != 2:
-        raise ValueError("x must be [B, D], got %s" % (tuple(x.shape),))
+    dev, code, D, W = _conv_checks(x, weight, bias, 2)
     B = x.shape[0]
-    if B and D > 1 and x.stride(1) != 1:
+    if D > 1 and B and x.stride(1) != 1:
         raise ValueError("x's rows must be contiguous")
     if not isinstance(state, torch.Tensor) or state.dim() != 3:
         raise ValueError("state must be [S, W-1, D]")
     _check(state, "state", dev, (state.shape[0], W - 1, D), x.dtype)
-    _slots(slots, dev, B)
-    _apart(state, "state", x, weight, bias, slots)
-    silu = _silu(activation)
-    with _On(dev, stream) as handle:
-        y = _out(y, "y", dev, (B, D), x.dtype, (x, weight, bias, state, slots))
-        if B:
-            pr = ConvProblem(B, 1, D, W, x.stride(0) if B > 1 else D, D, 0, 0, 0, code, _CODE[weight.dtype], silu)
-            _call("gdn_conv_step", ctypes.byref(pr), _ptr(x), _ptr(weight), _ptr(bias), _ptr(state), _ptr(slots),
-                  state.shape[0], _ptr(y), handle)
+    if slots is not None:
+        _check(slots, "slots", dev, (B,), torch.int32)
+    _apart(state, "state", x)
+    return _on(dev, stream, _conv_step, dev, code, x, state, weight, bias, _silu(activation), slots, y)
+
+
+def _conv_step(handle, dev, code, x, state, weight, bias, silu, slots, y):
+    B, D = x.shape
+    y = _out(y, "y", dev, (B, D), x.dtype, (x, weight, bias, state, slots))
+    if B:
+        pr, _ = _problem(ConvProblem, None, B, 1, D, weight.shape[1], x.stride(0) if B > 1 else D, D, 0, 0, 0, code,
+                         _CODE[weight.dtype], silu)
+        _call("gdn_conv_step", pr, _ptr(x), _ptr(weight), _ptr(bias), _ptr(state), _ptr(slots), state.shape[0], _ptr(y),
+              handle)
     return y
 
 
@@ -437,26 +463,23 @@ def _ssm_checks(x, dt, A, B, C, D, dt_bias, lead):
     code = _io_code(x, "x")
     if x.dim() != lead + 2 or not isinstance(B, torch.Tensor) or B.dim() != lead + 2:
         raise ValueError("x and B must have %d dimensions" % (lead + 2))
-    H, P = x.shape[-2:]
-    G, N = B.shape[-2:]
-    _check(B, "B", dev, tuple(x.shape[:lead]) + (G, N), x.dtype, dense=False)
+    H = x.shape[-2]
+    _check(B, "B", dev, x.shape[:lead] + B.shape[lead:], x.dtype, dense=False)
     _check(C, "C", dev, B.shape, x.dtype, dense=False)
-    _check(dt, "dt", dev, tuple(x.shape[:lead]) + (H,), (x.dtype, torch.float32), dense=False)
+    _check(dt, "dt", dev, x.shape[:-1], x.dtype, torch.float32, dense=False)
     _check(A, "A", dev, (H,), torch.float32)
-    for t, name in ((D, "D"), (dt_bias, "dt_bias")):
-        if t is not None:
-            _check(t, name, dev, (H,), torch.float32)
-    return dev, code, H, P, G, N
+    if D is not None:
+        _check(D, "D", dev, (H,), torch.float32)
+    if dt_bias is not None:
+        _check(dt_bias, "dt_bias", dev, (H,), torch.float32)
+    return dev, code
 
 
-def _ssm_problem(x, dt, B, C, code, softplus, n, grads=(0, 0)):
-    H, P = x.shape[-2:]
-    G, N = B.shape[-2:]
-    sb, sc = _strides(B, "B"), _strides(C, "C")
-    if sb != sc:
-        raise ValueError("B and C must have the same strides, got %s and %s" % (sb, sc))
-    return SsmProblem(x.shape[0], x.shape[1], H, P, N, G, *_strides(x, "x"), *sb, *_strides(dt, "dt"), *grads, n,
-                      code, _CODE[dt.dtype], 1 if softplus else 0)
+def _bc_strides(B, C):
+    sb = _strides(B, "B")
+    if _strides(C, "C") != sb:
+        raise ValueError("B and C must have the same strides, got %s and %s" % (sb, _strides(C, "C")))
+    return sb
 
 
 def ssm_forward(x, dt, A, B, C, D=None, dt_bias=None, h0=None, *, dt_softplus=True, cu_seqlens=None, y=None,
@@ -469,21 +492,25 @@ def ssm_forward(x, dt, A, B, C, D=None, dt_bias=None, h0=None, *, dt_softplus=Tr
     fp32; A, D, dt_bias [H] fp32; h0 [b, H, N, P] fp32, or [n, H, N, P] with
     cu_seqlens (as in conv_forward).  Returns (y [b, T, H, P], hT like h0 or
     None)."""
-    dev, code, H, P, G, N = _ssm_checks(x, dt, A, B, C, D, dt_bias, 2)
+    dev, code = _ssm_checks(x, dt, A, B, C, D, dt_bias, 2)
     n = _packed(cu_seqlens, dev, x.shape[0])
-    st = (n or x.shape[0], H, N, P)
+    st = (n or x.shape[0], x.shape[2], B.shape[3], x.shape[3])
     if h0 is not None:
         _check(h0, "h0", dev, st, torch.float32)
-    pr = _ssm_problem(x, dt, B, C, code, dt_softplus, n)
-    lib = _library()
-    with _On(dev, stream) as handle:
-        ins = (x, dt, A, B, C, D, dt_bias, h0, cu_seqlens)
-        y = _out(y, "y", dev, x.shape, x.dtype, ins)
-        if hT is not None or output_final_state:
-            hT = _out(hT, "hT", dev, st, torch.float32, ins + (y,))
-        workspace, size = _workspace(int(lib.gdn_workspace_bytes_ssm(ctypes.byref(pr))), dev, workspace)
-        _call("gdn_ssm_forward", ctypes.byref(pr), _ptr(x), _ptr(dt), _ptr(A), _ptr(B), _ptr(C), _ptr(D),
-              _ptr(dt_bias), _ptr(h0), _ptr(cu_seqlens), _ptr(y), _ptr(hT), _ptr(workspace), size, handle)
+    return _on(dev, stream, _ssm_forward, dev, code, x, dt, A, B, C, D, dt_bias, h0, 1 if dt_softplus else 0, cu_seqlens, n,
+               st, y, hT, output_final_state, workspace)
+
+
+def _ssm_forward(handle, dev, code, x, dt, A, B, C, D, dt_bias, h0, softplus, cu_seqlens, n, st, y, hT, want, workspace):
+    ins = (x, dt, A, B, C, D, dt_bias, h0, cu_seqlens)
+    y = _out(y, "y", dev, x.shape, x.dtype, ins)
+    if hT is not None or want:
+        hT = _out(hT, "hT", dev, st, torch.float32, ins + (y,))
+    pr, need = _problem(SsmProblem, "gdn_workspace_bytes_ssm", *x.shape, B.shape[3], B.shape[2], *_strides(x, "x"),
+                        *_bc_strides(B, C), *_strides(dt, "dt"), 0, 0, n, code, _CODE[dt.dtype], softplus)
+    workspace, size = _workspace(need, dev, workspace)
+    _call("gdn_ssm_forward", pr, _ptr(x), _ptr(dt), _ptr(A), _ptr(B), _ptr(C), _ptr(D), _ptr(dt_bias), _ptr(h0),
+          _ptr(cu_seqlens), _ptr(y), _ptr(hT), _ptr(workspace), size, handle)
     return y, hT
 
 
@@ -496,73 +523,89 @@ def ssm_backward(dy, x, dt, A, B, C, D=None, dt_bias=None, h0=None, dhT=None, *,
     others fp32; dD, ddt_bias and dh0 are None where D, dt_bias and h0 are.
     dx, dB and dC may be given as parts of one buffer (with the same strides
     between tokens), as the gradient of a convolution's output."""
-    dev, code, H, P, G, N = _ssm_checks(x, dt, A, B, C, D, dt_bias, 2)
-    b, T = x.shape[:2]
-    n = _packed(cu_seqlens, dev, b)
-    st = (n or b, H, N, P)
+    dev, code = _ssm_checks(x, dt, A, B, C, D, dt_bias, 2)
+    n = _packed(cu_seqlens, dev, x.shape[0])
+    st = (n or x.shape[0], x.shape[2], B.shape[3], x.shape[3])
     _check(dy, "dy", dev, x.shape, x.dtype)
     for t, name in ((h0, "h0"), (dhT, "dhT")):
         if t is not None:
             _check(t, name, dev, st, torch.float32)
-    lib = _library()
+    return _on(dev, stream, _ssm_backward, dev, code, dy, x, dt, A, B, C, D, dt_bias, h0, dhT, 1 if dt_softplus else 0,
+               cu_seqlens, n, st, (dx, dB, dC), ddt, dA, dD, ddt_bias, dh0, workspace)
+
+
+def _ssm_backward(handle, dev, code, dy, x, dt, A, B, C, D, dt_bias, h0, dhT, softplus, cu_seqlens, n, st, dxbc, ddt, dA,
+                  dD, ddt_bias, dh0, workspace):
+    b, T, H, P = x.shape
+    G, N = B.shape[2:]
     ins = (dy, x, dt, A, B, C, D, dt_bias, h0, dhT, cu_seqlens)
-    with _On(dev, stream) as handle:
-        given = [t is not None for t in (dx, dB, dC)]
-        if any(given):
-            if not all(given):
-                raise ValueError("dx, dB and dC are given together or not at all")
-            for t, name, like in ((dx, "dx", x), (dB, "dB", B), (dC, "dC", C)):
-                _check(t, name, dev, like.shape, x.dtype, dense=False)
-            grads = _strides(dx, "dx")
-            if any(_strides(t, name) != grads for t, name in ((dB, "dB"), (dC, "dC"))):
-                raise ValueError("dx, dB and dC must have the same strides between batches and tokens")
-            lo = min(t.data_ptr() for t in (dx, dB, dC))
-            for t in ins:
-                if t is not None and t.numel() and T and lo < t.data_ptr() + t.numel() * t.element_size():
-                    for o, name in ((dx, "dx"), (dB, "dB"), (dC, "dC")):
-                        _apart(o, name, t)
-        else:
-            # side by side, as the convolution that feeds the scan laid them out
-            both = torch.empty(b, T, H * P + 2 * G * N, device=dev, dtype=x.dtype)
-            dx = both[..., :H * P].unflatten(-1, (H, P))
-            dB = both[..., H * P:H * P + G * N].unflatten(-1, (G, N))
-            dC = both[..., H * P + G * N:].unflatten(-1, (G, N))
-            grads = _strides(dx, "dx")
-        ddt = _out(ddt, "ddt", dev, (b, T, H), dt.dtype, ins)
-        dA = _out(dA, "dA", dev, (H,), torch.float32, ins)
-        if D is not None:
-            dD = _out(dD, "dD", dev, (H,), torch.float32, ins)
-        if dt_bias is not None:
-            ddt_bias = _out(ddt_bias, "ddt_bias", dev, (H,), torch.float32, ins)
-        if h0 is not None:
-            dh0 = _out(dh0, "dh0", dev, st, torch.float32, ins)
-        pr = _ssm_problem(x, dt, B, C, code, dt_softplus, n, grads)
-        workspace, size = _workspace(int(lib.gdn_workspace_bytes_ssm_backward(ctypes.byref(pr))), dev, workspace)
-        _call("gdn_ssm_backward", ctypes.byref(pr), _ptr(dy), _ptr(x), _ptr(dt), _ptr(A), _ptr(B), _ptr(C), _ptr(D),
-              _ptr(dt_bias), _ptr(h0), _ptr(cu_seqlens), _ptr(dhT), _ptr(dx), _ptr(ddt), _ptr(dA), _ptr(dB), _ptr(dC),
-              _ptr(dD) if D is not None else None, _ptr(ddt_bias) if dt_bias is not None else None,
-              _ptr(dh0) if h0 is not None else None, _ptr(workspace), size, handle)
-    return (dx, ddt, dA, dB, dC, dD if D is not None else None, ddt_bias if dt_bias is not None else None,
-            dh0 if h0 is not None else None)
+    dx, dB, dC = dxbc
+    if dx is None and dB is None and dC is None:
+        # side by side, as the convolution that feeds the scan laid them out
+        both = torch.empty(b, T, H * P + 2 * G * N, device=dev, dtype=x.dtype)
+        dx, dB, dC = both.split((H * P, G * N, G * N), -1)
+        dx, dB, dC = dx.unflatten(-1, (H, P)), dB.unflatten(-1, (G, N)), dC.unflatten(-1, (G, N))
+        grads = _strides(dx, "dx")
+    else:
+        if any(t is None for t in dxbc):
+            raise ValueError("dx, dB and dC are given together or not at all")
+        for t, name, like in ((dx, "dx", x), (dB, "dB", B), (dC, "dC", C)):
+            _check(t, name, dev, like.shape, x.dtype, dense=False)
+            _apart(t, name, *ins)
+        grads = _strides(dx, "dx")
+        if T > 1 and any(_strides(t, name) != grads for t, name in ((dB, "dB"), (dC, "dC"))):
+            raise ValueError("dx, dB and dC must have the same strides between batches and tokens")
+    ddt = _out(ddt, "ddt", dev, (b, T, H), dt.dtype, ins)
+    dA = _out(dA, "dA", dev, (H,), torch.float32, ins)
+    dD = None if D is None else _out(dD, "dD", dev, (H,), torch.float32, ins)
+    ddt_bias = None if dt_bias is None else _out(ddt_bias, "ddt_bias", dev, (H,), torch.float32, ins)
+    dh0 = None if h0 is None else _out(dh0, "dh0", dev, st, torch.float32, ins)
+    pr, need = _problem(SsmProblem, "gdn_workspace_bytes_ssm_backward", b, T, H, P, N, G, *_strides(x, "x"),
+                        *_bc_strides(B, C), *_strides(dt, "dt"), *grads, n, code, _CODE[dt.dtype], softplus)
+    workspace, size = _workspace(need, dev, workspace)
+    _call("gdn_ssm_backward", pr, _ptr(dy), _ptr(x), _ptr(dt), _ptr(A), _ptr(B), _ptr(C), _ptr(D), _ptr(dt_bias), _ptr(h0),
+          _ptr(cu_seqlens), _ptr(dhT), _ptr(dx), _ptr(ddt), _ptr(dA), _ptr(dB), _ptr(dC), _ptr(dD), _ptr(ddt_bias),
+          _ptr(dh0), _ptr(workspace), size, handle)
+    return dx, ddt, dA, dB, dC, dD, ddt_bias, dh0
 
 
 def ssm_step(x, dt, A, B, C, state, D=None, dt_bias=None, *, dt_softplus=True, slots=None, y=None, stream=None):
     """One token for each of b sequences: x [b, H, P], dt [b, H], B and C
     [b, G, N] (rows may be strided); state [S, H, N, P] fp32, moved on in place;
     slots as in conv_step.  Returns y [b, H, P]."""
-    dev, code, H, P, G, N = _ssm_checks(x, dt, A, B, C, D, dt_bias, 1)
+    dev, code = _ssm_checks(x, dt, A, B, C, D, dt_bias, 1)
     if not isinstance(state, torch.Tensor) or state.dim() != 4:
         raise ValueError("state must be [S, H, N, P]")
-    _check(state, "state", dev, (state.shape[0], H, N, P), torch.float32)
-    b = x.shape[0]
-    _slots(slots, dev, b)
-    ins = (x, dt, A, B, C, D, dt_bias, slots)
-    _apart(state, "state", *ins)
-    with _On(dev, stream) as handle:
-        y = _out(y, "y", dev, x.shape, x.dtype, ins + (state,))
-        if b:
-            # a row is a batch of one token
-            pr = _ssm_problem(x[:, None], dt[:, None], B[:, None], C[:, None], code, dt_softplus, 0)
-            _call("gdn_ssm_step", ctypes.byref(pr), _ptr(x), _ptr(dt), _ptr(A), _ptr(B), _ptr(C), _ptr(D),
-                  _ptr(dt_bias), _ptr(state), _ptr(slots), state.shape[0], _ptr(y), handle)
+    b, H, P = x.shape
+    _check(state, "state", dev, (state.shape[0], H, B.shape[2], P), torch.float32)
+    if slots is not None:
+        _check(slots, "slots", dev, (b,), torch.int32)
+    _apart(state, "state", x)
+    return _on(dev, stream, _ssm_step, dev, code, x, dt, A, B, C, state, D, dt_bias, 1 if dt_softplus else 0, slots, y)
+
+
+def _row_stride(t, name):
+    """Between the rows of a step's input [b, ...] whose rows are dense."""
+    if t.is_contiguous():
+        return t.numel() // t.shape[0]
+    want = 1
+    for n, s in zip(reversed(t.shape[1:]), reversed(t.stride()[1:])):
+        if n != 1 and s != want:
+            raise ValueError("%s's rows must be contiguous" % name)
+        want *= n
+    return t.stride(0) if t.shape[0] != 1 else want
+
+
+def _ssm_step(handle, dev, code, x, dt, A, B, C, state, D, dt_bias, softplus, slots, y):
+    b, H, P = x.shape
+    y = _out(y, "y", dev, x.shape, x.dtype, (x, dt, A, B, C, D, dt_bias, slots, state))
+    if b:
+        G, N = B.shape[1:]
+        sb = _row_stride(B, "B")
+        if _row_stride(C, "C") != sb:
+            raise ValueError("B and C must have the same strides")
+        pr, _ = _problem(SsmProblem, None, b, 1, H, P, N, G, _row_stride(x, "x"), H * P, sb, G * N, _row_stride(dt, "dt"), H,
+                         0, 0, 0, code, _CODE[dt.dtype], softplus)
+        _call("gdn_ssm_step", pr, _ptr(x), _ptr(dt), _ptr(A), _ptr(B), _ptr(C), _ptr(D), _ptr(dt_bias), _ptr(state),
+              _ptr(slots), state.shape[0], _ptr(y), handle)
     return y
