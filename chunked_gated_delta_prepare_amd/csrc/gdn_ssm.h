@@ -60,6 +60,8 @@
 // exceeds 1 while A <= 0.
 #pragma once
 
+#include <type_traits>
+
 #include "gdn_layer.h"
 
 namespace gdn {
@@ -87,6 +89,7 @@ struct SsmParams {
     int T, H, P, n_seqs, heads_per_group;
     int seg_tokens, n_items, n_hb;          // tokens of a segment, segments in all, blocks of columns
     int softplus, swizzle, dt_f32;
+    int all_ends;                           // the last segments' end states are in the workspace too
 };
 
 // x, unknown to the compiler: what is computed from it inside a loop stays
@@ -290,14 +293,28 @@ __device__ __forceinline__ void store_row4(rsrc_t r, uint32_t off, const float4v
 // softplus(v) = log(1 + e^v), to fp32's accuracy for every v
 __device__ __forceinline__ float softplus(float v) { return fmaxf(v, 0.f) + log1pf(expf(-fabsf(v))); }
 
-// Inclusive sum over the lanes of a wave.
+// Inclusive sum over the lanes of a wave: within rows of 16 lanes, then the
+// rows' sums handed on (lanes that take nothing add 0).
+template <int CTRL, int ROWS>
+__device__ __forceinline__ double dpp_add(double v) {
+    const uint64_t u = __builtin_bit_cast(uint64_t, v);
+    const uint32_t lo = __builtin_amdgcn_update_dpp(0, (int)(uint32_t)u, CTRL, ROWS, 0xf, false);
+    const uint32_t hi = __builtin_amdgcn_update_dpp(0, (int)(uint32_t)(u >> 32), CTRL, ROWS, 0xf, false);
+    return v + __builtin_bit_cast(double, (uint64_t)hi << 32 | lo);
+}
 __device__ __forceinline__ double wave_scan(double v) {
-#pragma unroll
-    for (int m = 1; m < 64; m <<= 1) {
-        const double u = __shfl_up(v, m, 64);
-        if (lane_id() >= m) v += u;
-    }
-    return v;
+    v = dpp_add<0x111, 0xf>(v);      // row_shr 1, 2, 4, 8
+    v = dpp_add<0x112, 0xf>(v);
+    v = dpp_add<0x114, 0xf>(v);
+    v = dpp_add<0x118, 0xf>(v);
+    v = dpp_add<0x142, 0xa>(v);      // lane 15 of rows 0 and 2 to rows 1 and 3
+    return dpp_add<0x143, 0xc>(v);   // lane 31 to rows 2 and 3
+}
+// lane 63's value
+__device__ __forceinline__ double last_lane(double v) {
+    const uint64_t u = __builtin_bit_cast(uint64_t, v);
+    const uint32_t lo = __builtin_amdgcn_readlane((int)(uint32_t)u, 63), hi = __builtin_amdgcn_readlane((int)(uint32_t)(u >> 32), 63);
+    return __builtin_bit_cast(double, (uint64_t)hi << 32 | lo);
 }
 
 // A chunk's gates of one head, a lane a row.  (w is dt forward, 1 in reverse.)
@@ -333,7 +350,7 @@ __device__ __forceinline__ void make_gates(Gates &g, float dt, float A) {
     const int l = again(lane_id());
     asm volatile("" : "+s"(A));                // (its double is not kept in registers either)
     const double own = (double)dt * (double)A * 1.4426950408889634074, upto = wave_scan(own);
-    const double total = __shfl(upto, 63, 64), cum = REV ? upto - own : upto;
+    const double total = last_lane(upto), cum = REV ? upto - own : upto;
     const float hi = (float)cum, w = REV ? 1.f : dt;
     g.cum[l] = make_float2(hi, (float)(cum - (double)hi));
     g.ecum[l] = fast_exp2(hi);
@@ -405,15 +422,15 @@ __device__ __forceinline__ Segment find_segment(const SsmParams &p, int item) {
     return s;
 }
 
-// blockIdx -> (segment, block of columns).  The blocks of one segment share
-// its B and C: with swizzle they go to one XCD (workgroups are dealt to the
-// eight XCDs in turn), else they are neighbours.
+// blockIdx -> (segment, block of columns).  The blocks of one segment and
+// group share its B and C: with swizzle they go to one XCD (workgroups are
+// dealt to the eight XCDs in turn), else they are neighbours.
 __device__ __forceinline__ void place(const SsmParams &p, int &item, int &hb) {
     const int i = blockIdx.x;
     if (p.swizzle) {
-        const int j = i >> 3;
-        hb = j % p.n_hb;
-        item = (j / p.n_hb) * 8 + (i & 7);
+        const int groups = p.H / p.heads_per_group, per = p.n_hb / groups, j = i >> 3, unit = (j / per) * 8 + (i & 7);
+        item = unit / groups;
+        hb = (unit % groups) * per + j % per;
     } else {
         hb = i % p.n_hb;
         item = i / p.n_hb;
@@ -522,10 +539,12 @@ __device__ __forceinline__ float segments_before(const SsmParams &p, const Segme
 //   2  out1 = M v + e^cum S^T q, transposed, so that a lane stores four columns
 //   3  S' = e^total S + k^T (w v)
 // The state's products take w v in PARTS bf16 parts: two (relative error 2^-18)
-// for a state that is an output and is read on by every later chunk, three
-// where it goes into dA, a sum over all tokens of both signs in which two
-// left errors of up to 5e-5.  out1's operands are rounded once to bf16, its
-// own type.  The next chunk's rows are in flight while one is worked on, and
+// for a state that is an output or another segment's start, three where it
+// goes into dA, a sum over all tokens of both signs in which two left errors
+// of up to 5e-5.  Where only out1 is read from the state (an output state comes
+// from the segments' end states if there are any), w v is rounded once to
+// bf16, as out1's other operands are and out1 itself, and S too before it is
+// multiplied.  The next chunk's rows are in flight while one is worked on, and
 // its gates are formed by the waves with the fewest blocks.
 // ENDS: only the state, from a zero start, to the workspace.
 //
@@ -548,7 +567,10 @@ __global__ void __launch_bounds__(4 * COLS, sizeof(IO) == 4 ? 1 : COLS == 64 && 
     if (item >= p.n_items) return;
     const Segment seg = find_segment(p, item);
     if (!seg.live) return;
-    if (ENDS && (REV ? seg.begin == seg.seq_begin : seg.end == seg.seq_end)) return;
+    const bool last = REV ? seg.begin == seg.seq_begin : seg.end == seg.seq_end;      // of the scan
+    // an output state comes from the end states, but for a sequence's only segment
+    const bool via_ends = last && p.all_ends && !(seg.begin == seg.seq_begin && seg.end == seg.seq_end);
+    if (ENDS && last && !via_ends) return;
     const int w = wave_id(), l = lane_id(), q = l >> 4, j = l & 15;
     const int col0 = hb * COLS, head0 = col0 / p.P, mine = w * 16 / P, head = head0 + mine, grp = head0 / p.heads_per_group;
     const int wc = w * 16;                        // this wave's first column
@@ -579,6 +601,17 @@ __global__ void __launch_bounds__(4 * COLS, sizeof(IO) == 4 ? 1 : COLS == 64 && 
             for (int nb = 0; nb < NB; ++nb)
 #pragma unroll
                 for (int e = 0; e < 4; ++e) h[nb][e] += d * p.s0[state_at(l) + row_of(nb, e) * p.P];
+        }
+        if (p.sT && via_ends) {
+            // the state behind the last segment, from that segment's own
+            const int64_t mark = (int64_t)item * p.n_hb + hb;
+            const float *e0 = p.ends + mark * (N * COLS) + wc + j;
+            const float f = fast_exp2((float)p.total[mark * NH + mine]);
+#pragma unroll
+            for (int nb = 0; nb < NB; ++nb)
+#pragma unroll
+                for (int e = 0; e < 4; ++e)
+                    p.sT[state_at(l) + row_of(nb, e) * p.P] = f * h[nb][e] + e0[row_of(nb, e) * COLS];
         }
         // the blocks of M right of the diagonal that a 32-wide step touches
         for (int i = threadIdx.x; i < NH * 2 * 16 * 16; i += kThreads) {
@@ -613,6 +646,7 @@ __global__ void __launch_bounds__(4 * COLS, sizeof(IO) == 4 ? 1 : COLS == 64 && 
             make_gates<REV>(gates[gc][gh], dt_of(p, raw_value<IO>(p, raw), bias, again(lane_id()) < rows), A);
         }
     };
+    const bool exact = p.sT && last && !via_ends;
     double total = 0.0;
     if (nc > 0) {
         fetch_dt(0);
@@ -625,14 +659,12 @@ __global__ void __launch_bounds__(4 * COLS, sizeof(IO) == 4 ? 1 : COLS == 64 && 
         const Lane<E, COLS> aP(l);
         const Lane<E, C> aM(l);
         lds_barrier();                            // the last chunk's tiles are done with
-        if (c % GC == 0) {
-            form_gates(c);
-            fetch_dt(c + GC);
-        }
+        if (c % GC == 0) form_gates(c);
         tv.put(tid, sv, rows);
         tk.put(tid, sk, rows);
         if constexpr (!ENDS) tq.put(tid, sq, rows);
         if (c + 1 < nc) fetch(c + 1);
+        if (c % GC == 0) fetch_dt(c + GC);
         lds_barrier();
         const Gates *gs = gates[c % GC], &g = gs[mine];
         float4v y[ENDS ? 1 : 4];
@@ -668,32 +700,15 @@ __global__ void __launch_bounds__(4 * COLS, sizeof(IO) == 4 ? 1 : COLS == 64 && 
             for (int bi = 0; bi < 4; ++bi) y[bi] *= g.ecum[16 * bi + j];
         }
         if constexpr (!ENDS) lds_barrier();       // M is whole
-        // 2 and 3: both take v by columns
-        const double tot = g.total;
-        if constexpr (ENDS) total += tot;
-        const float et = fast_exp2((float)tot);
+        // 2; its stores go out before the state's part, which they have time
+        // to end behind (the next tiles wait for everything in flight)
+        if constexpr (!ENDS) {
 #pragma unroll
-        for (int i = 0; i < NB; ++i) h[i] *= et;
-#pragma unroll
-        for (int s0 = 0; s0 < C; s0 += 32) {
-            float wt[8];
-#pragma unroll
-            for (int e = 0; e < 8; ++e) wt[e] = g.end[s0 + 8 * q + e];
-            const typename O::frag vf = O::template col<COLS>(sv, aP, wc, s0);
-            typename O::frag vw[kP];
-            O::scaled(vf, wt, vw);
-            if constexpr (!ENDS) {
+            for (int s0 = 0; s0 < C; s0 += 32) {
+                const typename O::frag vf = O::template col<COLS>(sv, aP, wc, s0);
 #pragma unroll
                 for (int bi = s0 / 16; bi < 4; ++bi) O::mma(y[bi], vf, O::template row<C>(sm[mine], aM, 16 * bi, s0));
             }
-#pragma unroll
-            for (int nb = 0; nb < NB; ++nb) {
-                const typename O::frag kf = O::template pair<N>(sk, aN, 32 * (nb >> 1), nb & 1, s0);
-#pragma unroll
-                for (int k = 0; k < kP; ++k) O::mma(h[nb], kf, vw[k]);
-            }
-        }
-        if constexpr (!ENDS) {
             // y = out1 + D x, dx = dt out1 + D dy
             const rsrc_t ry = make_rsrc((IO *)p.out + seg.batch * p.ob + lo * p.ot + col0, 0x7fffffffu);
 #pragma unroll
@@ -708,6 +723,41 @@ __global__ void __launch_bounds__(4 * COLS, sizeof(IO) == 4 ? 1 : COLS == 64 && 
                 store_row4<IO>(ry, ii < rows ? (uint32_t)(t * (uint32_t)p.ot + cc) * (uint32_t)sizeof(IO) : 0xfffffff0u, o);
             }
         }
+        // 3
+        const double tot = g.total;
+        if constexpr (ENDS) total += tot;
+        const float et = fast_exp2((float)tot);
+#pragma unroll
+        for (int i = 0; i < NB; ++i) h[i] *= et;
+        // parts [from, to) of w v
+        auto add_parts = [&](auto from, auto to) {
+            constexpr int k0 = decltype(from)::value, k1 = decltype(to)::value;
+#pragma unroll
+            for (int s0 = 0; s0 < C; s0 += 32) {
+                float wt[8];
+#pragma unroll
+                for (int e = 0; e < 8; ++e) wt[e] = g.end[s0 + 8 * q + e];
+                typename O::frag vw[k1];
+                O::scaled(O::template col<COLS>(sv, aP, wc, s0), wt, vw);
+#pragma unroll
+                for (int nb = 0; nb < NB; ++nb) {
+                    const typename O::frag kf = O::template pair<N>(sk, aN, 32 * (nb >> 1), nb & 1, s0);
+#pragma unroll
+                    for (int k = k0; k < k1; ++k) O::mma(h[nb], kf, vw[k]);
+                }
+            }
+        };
+        typedef std::integral_constant<int, 0> I0;
+        typedef std::integral_constant<int, 1> I1;
+        typedef std::integral_constant<int, kP> IP;
+        if constexpr (ENDS) {
+            add_parts(I0(), IP());
+        } else {
+            add_parts(I0(), I1());
+            if constexpr (kP > 1) {
+                if (exact) add_parts(I1(), IP());
+            }
+        }
     }
     if constexpr (ENDS) {
         const int64_t place_at = (int64_t)item * p.n_hb + hb;
@@ -717,7 +767,7 @@ __global__ void __launch_bounds__(4 * COLS, sizeof(IO) == 4 ? 1 : COLS == 64 && 
 #pragma unroll
             for (int e = 0; e < 4; ++e) e0[row_of(nb, e) * COLS] = h[nb][e];
         if (!REV && l == 0 && w == mine * (NW / NH)) p.total[place_at * NH + mine] = total;
-    } else if (p.sT && (REV ? seg.begin == seg.seq_begin : seg.end == seg.seq_end)) {
+    } else if (exact) {
         const int l = again(lane_id()), q = l >> 4;
         float *sT = p.sT + state_at(l) + 8 * q * p.P;
 #pragma unroll
@@ -736,6 +786,6 @@ gdn_status check_ssm_pointers(const gdn_ssm_problem *pr, const void *x, const vo
                               const void *Cm, const float *D, const float *bias, bool rows);
 void fill_ssm(const gdn_ssm_problem *pr, SsmParams &sp);
 SsmPlan ssm_plan(const gdn_ssm_problem *pr, bool packed);
-int ssm_grid(SsmParams &sp, const SsmPlan &s);
+int ssm_grid(const gdn_ssm_problem *pr, SsmParams &sp, const SsmPlan &s);
 
 }  // namespace gdn

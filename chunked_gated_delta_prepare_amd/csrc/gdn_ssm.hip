@@ -109,13 +109,19 @@ SsmPlan ssm_plan(const gdn_ssm_problem *pr, bool packed) {
     return s;
 }
 
-int ssm_grid(SsmParams &sp, const SsmPlan &s) {
+// Blocks that share B and C go to one XCD where the (segment, group) pairs come
+// out even over the eight: B and C are then read once from HBM, not once per
+// XCD (16 % of the time of 65536 tokens, 64 heads, 8 groups).  Packed sequences
+// have segments of all lengths, and places without one: there an even spread
+// is worth more.
+int ssm_grid(const gdn_ssm_problem *pr, SsmParams &sp, const SsmPlan &s) {
     sp.seg_tokens = s.seg_tokens;
     sp.n_items = s.n_items;
     sp.n_hb = s.n_hb;
     sp.n_seqs = s.seqs;
-    sp.swizzle = s.n_items >= 16;
-    return (sp.swizzle ? (s.n_items + 7) / 8 * 8 : s.n_items) * s.n_hb;
+    const int64_t units = (int64_t)s.n_items * pr->G;
+    sp.swizzle = !sp.cu && units % 8 == 0 && s.n_hb % pr->G == 0;
+    return s.n_items * s.n_hb;
 }
 
 static size_t forward_ws(const gdn_ssm_problem *pr, const SsmPlan &s) {
@@ -240,8 +246,9 @@ gdn_status gdn_ssm_forward(const gdn_ssm_problem *pr, const void *x, const void 
     sp.sT = hT;
     sp.total = (double *)workspace;
     sp.ends = (float *)workspace + (int64_t)s.n_items * s.n_hb * 4;
-    const int grid = ssm_grid(sp, s);
+    const int grid = ssm_grid(pr, sp, s);
     if (need) {
+        sp.all_ends = hT != nullptr;
         st = launch_kernel(ssm_pick(pr, s, true), grid, &sp, (hipStream_t)stream, 256 * s.ncb);
         if (st != GDN_OK) return st;
     }

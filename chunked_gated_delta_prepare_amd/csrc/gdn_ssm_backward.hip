@@ -20,7 +20,7 @@ namespace gdn {
 // once to out2's own type.
 // ---------------------------------------------------------------------------
 template <typename IO, int N, int COLS, int NH, bool REV>
-__global__ void __launch_bounds__(4 * N, sizeof(IO) == 2 ? 2 : 1) ssm_key_kernel(SsmParams p) {
+__global__ void __launch_bounds__(4 * N, sizeof(IO) == 4 ? 1 : NH == 1 && N == 128 ? 4 : 2) ssm_key_kernel(SsmParams p) {
     typedef SOp<IO> O;
     typedef typename O::elem E;
     constexpr int C = kSsmChunk, NW = N / 16, PB = COLS / 16, kThreads = 4 * N;      // PB: blocks of columns
@@ -98,7 +98,6 @@ __global__ void __launch_bounds__(4 * N, sizeof(IO) == 2 ? 2 : 1) ssm_key_kernel
     };
     if (nc > 0) {
         fetch_dt(0);
-        fetch(0);
     }
     for (int c = 0; c < nc; ++c) {
         int lo;
@@ -106,6 +105,9 @@ __global__ void __launch_bounds__(4 * N, sizeof(IO) == 2 ? 2 : 1) ssm_key_kernel
         const Lane<E, N> aN(l);
         const Lane<E, COLS> aP(l);
         const Lane<E, C> aM(l);
+        // (not a chunk ahead: the registers that would take leave one workgroup a
+        // CU; the other one's work covers the wait)
+        fetch(c);
         lds_barrier();                            // the last chunk's tiles and sums are done with
         if (c % GC == 0) {
             form_gates(c);
@@ -115,7 +117,6 @@ __global__ void __launch_bounds__(4 * N, sizeof(IO) == 2 ? 2 : 1) ssm_key_kernel
         tz.put(tid, sz, rows);
         tk.put(tid, sk, rows);
         tq.put(tid, sq, rows);
-        if (c + 1 < nc) fetch(c + 1);
         const int mark = mark_slot(p, seg, REV ? nc - 1 - c : c);
         if constexpr (REV) {
             // behind this chunk h meets the state's gradient
@@ -228,7 +229,24 @@ __global__ void __launch_bounds__(4 * N, sizeof(IO) == 2 ? 2 : 1) ssm_key_kernel
             p.inside[to] = sum;
             p.across[to] = out;
         }
-        // 2 and 3: both take k by its N values
+        // 2; z goes out before the state's part
+#pragma unroll
+        for (int s0 = 0; s0 < C; s0 += 32) {
+            const typename O::frag kf = O::template col<N>(sk, aN, wn, s0);
+#pragma unroll
+            for (int bi = s0 / 16; bi < 4; ++bi) O::mma(z[bi], kf, O::template row<C>(sm, aM, 16 * bi, s0));
+        }
+        // (the sum over the blocks of columns of a group follows in ssm_sum_kernel)
+        const int slot = chunk_slot(p, seg, REV ? nc - 1 - c : c);
+        if (slot < p.n_slots) {
+            float2 *part = (float2 *)p.part + ((int64_t)slot * p.n_hb + hb) * (8 * kThreads) + tid;
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                part[(2 * i) * kThreads] = make_float2(z[i][0], z[i][1]);
+                part[(2 * i + 1) * kThreads] = make_float2(z[i][2], z[i][3]);
+            }
+        }
+        // 3
 #pragma unroll
         for (int hh = 0; hh < NH; ++hh) {
             const float et = fast_exp2((float)gs[hh].total);
@@ -238,8 +256,6 @@ __global__ void __launch_bounds__(4 * N, sizeof(IO) == 2 ? 2 : 1) ssm_key_kernel
 #pragma unroll
         for (int s0 = 0; s0 < C; s0 += 32) {
             const typename O::frag kf = O::template col<N>(sk, aN, wn, s0);
-#pragma unroll
-            for (int bi = s0 / 16; bi < 4; ++bi) O::mma(z[bi], kf, O::template row<C>(sm, aM, 16 * bi, s0));
 #pragma unroll
             for (int hh = 0; hh < NH; ++hh) {
                 typename O::frag kw[kP];
@@ -263,16 +279,6 @@ __global__ void __launch_bounds__(4 * N, sizeof(IO) == 2 ? 2 : 1) ssm_key_kernel
                     m[(2 * pb) * kThreads] = make_float2(h[pb][0], h[pb][1]);
                     m[(2 * pb + 1) * kThreads] = make_float2(h[pb][2], h[pb][3]);
                 }
-            }
-        }
-        // (the sum over the blocks of columns of a group follows in ssm_sum_kernel)
-        const int slot = chunk_slot(p, seg, REV ? nc - 1 - c : c);
-        if (slot < p.n_slots) {
-            float2 *part = (float2 *)p.part + ((int64_t)slot * p.n_hb + hb) * (8 * kThreads) + tid;
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                part[(2 * i) * kThreads] = make_float2(z[i][0], z[i][1]);
-                part[(2 * i + 1) * kThreads] = make_float2(z[i][2], z[i][3]);
             }
         }
     }
@@ -372,9 +378,9 @@ __global__ void __launch_bounds__(256) ssm_gate_kernel(GateParams gp) {
         const float dt = on ? (p.softplus ? softplus(raw) : raw) : 0.f;
         const double dca = (double)dt * (double)ca, in = (double)ri - (double)dt * (double)ci + (double)ra;
         const double pre_in = wave_scan(in), pre_ca = wave_scan(dca), pre_ra = wave_scan((double)ra);
-        const double all_in = __shfl(pre_in, 63, 64), all_ca = __shfl(pre_ca, 63, 64), all_ra = __shfl(pre_ra, 63, 64);
+        const double all_in = last_lane(pre_in), all_ca = last_lane(pre_ca), all_ra = last_lane(pre_ra);
         // nothing of weight crosses a chunk whose decay is below fp32's step
-        const bool cut = (float)__shfl(wave_scan((double)dt * (double)A), 63, 64) < -16.6f;
+        const bool cut = (float)last_lane(wave_scan((double)dt * (double)A)) < -16.6f;
         __syncthreads();
         if (l == 0) {
             const int mark = c0 >= w ? mark_slot(p, seg, c0 - w) : -1;
@@ -494,13 +500,14 @@ gdn_status bwd_launches(const gdn_ssm_problem *pr, const BwdPlan &b, const SsmPa
                         void *dx, void *dB, void *dC, float *dh0, hipStream_t s) {
     const bool one = b.s.n_items == b.s.seqs;      // one segment each
     SsmParams f = fwd, r = rev;
-    const int grid = ssm_grid(f, b.s);
-    ssm_grid(r, b.s);
+    const int grid = ssm_grid(pr, f, b.s);
+    ssm_grid(pr, r, b.s);
     gdn_status st = GDN_OK;
     auto go = [&](const void *fn, int g, SsmParams &sp, int threads) {
         if (st == GDN_OK) st = launch_kernel(fn, g, &sp, s, threads);
     };
     if (!one) {
+        f.all_ends = r.all_ends = dh0 != nullptr;
         go(F::ends(false), grid, f, F::kScanThreads);
         go(F::ends(true), grid, r, F::kScanThreads);
     }
