@@ -141,6 +141,8 @@ gdn_status check_ssm(const gdn_ssm_problem *pr, bool packed) {
     if (pr->T > (1 << 30) || pr->B > (1 << 20) || pr->H > (1 << 14)) return GDN_ERR_UNSUPPORTED;
     for (int64_t v : {pr->x_stride_t, pr->bc_stride_t, pr->dt_stride_t, pr->dxbc_stride_t})
         if (v < 0 || v > (1 << 22)) return GDN_ERR_UNSUPPORTED;
+    // what lies behind a chunk's last row is told by its place: rows do not overlap
+    if (pr->T > 1 && (pr->x_stride_t < pr->H * pr->P || pr->bc_stride_t < pr->G * pr->N)) return GDN_ERR_UNSUPPORTED;
     const int64_t items = (packed ? pr->n_seqs : pr->B) + (pr->T + 255) / 256 * pr->B;
     if (items * pr->H * 2 > ((int64_t)1 << 30)) return GDN_ERR_UNSUPPORTED;
     return GDN_OK;

@@ -325,7 +325,7 @@ struct GateParams {
     SsmParams s;                          // the forward scan's
     const float *c_inside, *c_across;     // the reverse scan's sums
     void *ddt;
-    double *grads;                        // [item][H][3]: dA, d(dt_bias), dD
+    double *grads;                        // [3][item][H]: dA, d(dt_bias), dD
     float *dA, *dD, *dbias;
     int ncb;
 };
@@ -347,7 +347,7 @@ __global__ void __launch_bounds__(256) ssm_gate_kernel(GateParams gp) {
     const Segment seg = find_segment(p, item);
     if (!seg.live) {
         // a place that no segment has
-        if (tid < 3) gp.grads[((int64_t)item * p.H + head) * 3 + tid] = 0.0;
+        if (tid < 3) gp.grads[((int64_t)tid * p.n_items + item) * p.H + head] = 0.0;
         return;
     }
     const int cols = 64 * gp.ncb, per_hb = cols / p.P;          // heads of a block of columns (0: a part of one)
@@ -418,10 +418,11 @@ __global__ void __launch_bounds__(256) ssm_gate_kernel(GateParams gp) {
     db = block_sum(db, red);
     dD = block_sum(dD, red);
     if (tid == 0) {
-        double *o = gp.grads + ((int64_t)item * p.H + head) * 3;
+        const int64_t plane = (int64_t)p.n_items * p.H;
+        double *o = gp.grads + (int64_t)item * p.H + head;
         o[0] = dA;
-        o[1] = db;
-        o[2] = dD;
+        o[plane] = db;
+        o[2 * plane] = dD;
     }
 }
 
@@ -433,7 +434,7 @@ __global__ void __launch_bounds__(64) ssm_head_kernel(GateParams gp) {
     for (int i0 = 0; i0 < p.n_items; i0 += 64) {
         const int i = i0 + lane_id();
         if (i < p.n_items)
-            for (int k = 0; k < 3; ++k) a[k] += gp.grads[((int64_t)i * p.H + head) * 3 + k];
+            for (int k = 0; k < 3; ++k) a[k] += gp.grads[((int64_t)k * p.n_items + i) * p.H + head];
     }
 #pragma unroll
     for (int k = 0; k < 3; ++k)
@@ -507,7 +508,9 @@ gdn_status bwd_launches(const gdn_ssm_problem *pr, const BwdPlan &b, const SsmPa
         if (st == GDN_OK) st = launch_kernel(fn, g, &sp, s, threads);
     };
     if (!one) {
-        f.all_ends = r.all_ends = dh0 != nullptr;
+        // (the last segments' decays stand between dhT and the others)
+        r.all_ends = dh0 != nullptr;
+        f.all_ends = r.all_ends || r.s0;
         go(F::ends(false), grid, f, F::kScanThreads);
         go(F::ends(true), grid, r, F::kScanThreads);
     }
@@ -547,6 +550,7 @@ gdn_status gdn_ssm_backward(const gdn_ssm_problem *pr, const void *dy, const voi
                             void *stream) {
     gdn_status st = check_ssm(pr, cu_seqlens != nullptr);
     if (st != GDN_OK) return st;
+    if (pr->T > 1 && (pr->dxbc_stride_t < pr->H * pr->P || pr->dxbc_stride_t < pr->G * pr->N)) return GDN_ERR_UNSUPPORTED;
     if (!A || !dA) return GDN_ERR_NULL_ARG;
     const int64_t eb = dtype_bytes(pr->io_dtype);
     if (pr->T > 0) {

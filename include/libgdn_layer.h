@@ -24,7 +24,9 @@
  * Strides are in elements; the innermost index is always contiguous.  Where a
  * stride is not given the tensor is dense.  Rows need only their element's
  * alignment in the norm and the convolution (rows of four aligned elements
- * take a faster path); the scan's x, B and C rows must be 16-byte aligned.
+ * take a faster path); the scan's x, B and C rows must be 16-byte aligned and
+ * not overlap.  Strides between tokens are 0 <= stride <= 2^22 (2^23 in the
+ * convolution).
  */
 #ifndef LIBGDN_LAYER_H
 #define LIBGDN_LAYER_H

@@ -1,0 +1,390 @@
+"""Selective state space scan on the GPU against its recurrence in 64 bits.
+
+Tolerances, from sums of the terms' sizes (the same recurrence with every factor
+replaced by its size), Y for y, Z for the states:
+  fp32 io: products and their sums in fp32.  A chunk adds 64 terms to a sum, a
+    state goes through one product and at most 64 additions a chunk and fades
+    with its decays; exponentials and softplus are good to a few units.  All in
+    all at most 2^9 roundings of 2^-24: 2^-15 of the terms' size.
+  bf16 io: y's operands are rounded once each, three of them on one way (the
+    weighted value into the state, the state into y or the chunk's matrix into
+    y): 2 * 2^-8 Y, and 2^-8 |y| for y itself.  The final state's weighted
+    values are held in two bf16 parts, 2^-16 Z, over fp32's 2^-15.
+  dx as y (with its own sizes); dB, dC: the chunk's matrix once, 2^-8 of the
+    terms, and 2^-8 of the result; ddt, dA: fp32 throughout, but for a gate the
+    differences of up to four chunks' sums: 2^-15 of the sizes of all pairs
+    that meet the 256 tokens around."""
+import pytest
+
+torch = pytest.importorskip("torch")
+
+import chunked_gated_delta_prepare_amd as gdn
+from oracle import layer as L
+
+pytestmark = pytest.mark.gpu
+DEV = "cuda:0"
+BF, F32 = torch.bfloat16, torch.float32
+HALF = {BF: 2.0 ** -8, F32: 2.0 ** -24}
+FP = 2.0 ** -15
+
+
+def rnd(*shape, seed, dtype=F32, scale=1.0):
+    g = torch.Generator().manual_seed(seed)
+    return (torch.randn(*shape, generator=g) * scale).to(dtype).to(DEV)
+
+
+def close(got, ref, tol, what):
+    d = (got.detach().cpu().double() - ref).abs()
+    bad = ~(d <= tol)
+    assert not bad.any(), "%s: %d of %d off, worst %.3e over its tolerance" % (what, int(bad.sum()), bad.numel(),
+                                                                               float((d - tol).max()))
+
+
+def offsets(lens):
+    return torch.tensor([0] + list(lens)).cumsum(0).to(torch.int32).to(DEV)
+
+
+def inputs(B, T, H, P, N, G, dt, dtt, n, h0, seed=0, strong=False, joint=True):
+    """x, B and C side by side in one buffer, as a convolution leaves them."""
+    buf = rnd(B, T, H * P + 2 * G * N, seed=seed + 1, dtype=dt)
+    x, Bm, Cm = buf.split((H * P, G * N, G * N), -1)
+    d = dict(x=x.unflatten(-1, (H, P)), B=Bm.unflatten(-1, (G, N)), C=Cm.unflatten(-1, (G, N)))
+    if not joint:
+        d = {k: v.contiguous() for k, v in d.items()}
+    wide = rnd(B, T, H + 3, seed=seed + 2, dtype=dtt)
+    d["dt"] = wide[..., 2:2 + H]
+    g = torch.Generator().manual_seed(seed + 3)
+    lo, hi = (0.5, 3.0) if strong else (1e-3, 1e-1)
+    dt0 = torch.exp(torch.rand(H, generator=g) * (torch.tensor(hi).log() - torch.tensor(lo).log()) + torch.tensor(lo).log())
+    d["dt_bias"] = (dt0 + torch.log(-torch.expm1(-dt0))).to(DEV)
+    d["A"] = (-(1 + 15 * torch.rand(H, generator=g))).to(DEV)
+    d["D"] = rnd(H, seed=seed + 4)
+    d["h0"] = rnd(n, H, N, P, seed=seed + 5) if h0 else None
+    return d
+
+
+def forward(d, **kw):
+    return gdn.ssm_forward(d["x"], d["dt"], d["A"], d["B"], d["C"], d["D"], d["dt_bias"], d["h0"], **kw)
+
+
+def flat(t):
+    return t.reshape(-1, *t.shape[2:])
+
+
+CASES = [  # lens (batch, tokens; or packed), H, P, N, G, type, dt's type, h0, softplus, strong gates
+    ((1, 1), 2, 64, 64, 1, BF, BF, False, True, False), ((2, 63), 3, 64, 128, 1, BF, F32, True, True, False),
+    ((1, 64), 4, 128, 64, 2, BF, BF, True, True, False), ((1, 65), 2, 128, 128, 2, F32, F32, True, True, False),
+    ((1, 300), 2, 64, 64, 2, BF, BF, True, False, False), ((2, 700), 4, 64, 128, 2, BF, BF, True, True, False),
+    ((1, 1100), 1, 128, 128, 1, BF, F32, False, True, False), ((1, 600), 3, 64, 64, 3, F32, F32, True, True, False),
+    ((1, 520), 2, 128, 64, 1, F32, F32, False, True, False), ((1, 400), 4, 64, 128, 1, BF, BF, True, True, True),
+    ([70, 0, 1, 256, 64, 0, 5], 4, 64, 128, 2, BF, BF, True, True, False),
+    ([0, 0, 3], 2, 128, 128, 1, BF, BF, True, True, False), ([600, 30], 1, 64, 64, 1, BF, F32, False, True, False),
+    ([1] * 70, 2, 64, 64, 1, F32, F32, True, True, False), ([257, 1, 300], 2, 128, 128, 2, BF, BF, True, True, True)]
+
+
+@pytest.mark.parametrize("lens,H,P,N,G,dt,dtt,h0,softplus,strong", CASES)
+def test_forward_and_backward(lens, H, P, N, G, dt, dtt, h0, softplus, strong):
+    packed = isinstance(lens, list)
+    B, T = (1, sum(lens)) if packed else lens
+    each = lens if packed else [T] * B
+    n = len(each)
+    d = inputs(B, T, H, P, N, G, dt, dtt, n, h0, strong=strong)
+    if not softplus:
+        d["dt"], d["dt_bias"] = d["dt"].abs() * 0.1, None
+    cu = offsets(lens) if packed else None
+    y, hT = forward(d, dt_softplus=softplus, cu_seqlens=cu)
+    step, raw = L.step_sizes(flat(d["dt"]), d["dt_bias"], softplus)
+    args = (flat(d["x"]), step, d["A"], flat(d["B"]), flat(d["C"]), d["D"], d["h0"], each)
+    ref, rT = L.ssm(*args)
+    Y, Z = L.ssm(*args, absolute=True)
+    b = dt is BF
+    close(flat(y), ref, ref.abs() * HALF[dt] + Y * (2 * 2.0 ** -8 * b + FP), "y")
+    close(hT, rT, Z * (2.0 ** -16 * b + FP), "hT")
+
+    dy, dhT = rnd(B, T, H, P, seed=8, dtype=dt), rnd(n, H, N, P, seed=9)
+    got = gdn.ssm_backward(dy, d["x"], d["dt"], d["A"], d["B"], d["C"], d["D"], d["dt_bias"], d["h0"], dhT,
+                           dt_softplus=softplus, cu_seqlens=cu)
+    dx, ddt, dA, dB, dC, dD, dbias, dh0 = got
+    g = L.ssm_grad(flat(dy), *args[:7], each, dhT)
+    a = L.ssm_grad(flat(dy), *args[:7], each, dhT, absolute=True)
+    close(flat(dx), g["dx"], g["dx"].abs() * HALF[dt] + a["dx"] * (2 * 2.0 ** -8 * b + FP), "dx")
+    for k, v in (("dB", dB), ("dC", dC)):
+        close(flat(v), g[k], g[k].abs() * HALF[dt] + a[k] * (2.0 ** -8 * b + FP), k)
+    close(dD, g["dD"], (flat(dy).cpu().double() * flat(d["x"]).cpu().double()).abs().sum((0, 2)) * FP, "dD")
+    # pairs that meet the 256 tokens on either side, sequence by sequence
+    near, at = torch.zeros_like(a["pairs"]), 0
+    for k in each:
+        c = torch.cat([torch.zeros(1, H, dtype=torch.float64), a["pairs"][at:at + k].cumsum(0)])
+        i = torch.arange(k)
+        near[at:at + k] = c[(i + 257).clamp(max=k)] - c[(i - 256).clamp(min=0)]
+        at += k
+    slope = torch.sigmoid(raw) if softplus else 1.0
+    size = (a["ddt"] + near * d["A"].cpu().double().abs()) * slope
+    want = g["ddt"] * slope
+    close(flat(ddt), want, want.abs() * HALF[dtt] + size * FP, "ddt")
+    close(dA, g["dA"], (near * step).sum(0) * FP, "dA")
+    if dbias is not None:
+        close(dbias, want.sum(0), size.sum(0) * FP, "ddt_bias")
+    else:
+        assert d["dt_bias"] is None
+    if dh0 is not None:
+        close(dh0, g["dh0"], a["dh0"] * (2.0 ** -16 * b + FP), "dh0")
+    else:
+        assert d["h0"] is None
+
+
+def test_gradients_without_a_final_states_gradient():
+    d = inputs(1, 900, 2, 64, 64, 1, BF, BF, 1, True)
+    dy = rnd(1, 900, 2, 64, seed=8, dtype=BF)
+    a = gdn.ssm_backward(dy, d["x"], d["dt"], d["A"], d["B"], d["C"], d["D"], d["dt_bias"], d["h0"])
+    b = gdn.ssm_backward(dy, d["x"], d["dt"], d["A"], d["B"], d["C"], d["D"], d["dt_bias"], d["h0"], torch.zeros_like(d["h0"]))
+    assert all(torch.equal(u, v) for u, v in zip(a, b))
+    c = gdn.ssm_backward(dy, d["x"], d["dt"], d["A"], d["B"], d["C"])
+    assert c[5] is None and c[6] is None and c[7] is None
+
+
+@pytest.mark.parametrize("dt", [BF, F32])
+@pytest.mark.parametrize("P,N", [(64, 64), (128, 128), (64, 128), (128, 64)])
+def test_steps_are_the_recurrence(P, N, dt):
+    """Steps in fp32 from a pool of states; a product, a sum and two
+    exponentials a step: 2^-20 of the terms' size after ten of them."""
+    B, T, H, G = 3, 10, 4, 2
+    d = inputs(B, T, H, P, N, G, dt, dt, B, True)
+    step, _ = L.step_sizes(flat(d["dt"]), d["dt_bias"], True)
+    args = (flat(d["x"]), step, d["A"], flat(d["B"]), flat(d["C"]), d["D"], d["h0"], [T] * B)
+    ref, rT = L.ssm(*args)
+    Y, Z = L.ssm(*args, absolute=True)
+    pool = torch.full((5, H, N, P), float("nan"), device=DEV)
+    slots = torch.tensor([3, 0, 4], device=DEV, dtype=torch.int32)
+    pool[slots.long()] = d["h0"]
+    ys = [gdn.ssm_step(d["x"][:, t], d["dt"][:, t], d["A"], d["B"][:, t], d["C"][:, t], pool, d["D"], d["dt_bias"], slots=slots)
+          for t in range(T)]
+    y = torch.stack(ys, 1)
+    close(flat(y), ref, ref.abs() * HALF[dt] + Y * 2.0 ** -18, "y")
+    close(pool[slots.long()], rT, Z * 2.0 ** -20, "state")
+    assert pool[[1, 2]].isnan().all()
+    direct = d["h0"].clone()
+    for t in range(T):
+        one = gdn.ssm_step(d["x"][:, t], d["dt"][:, t], d["A"], d["B"][:, t], d["C"][:, t], direct, d["D"], d["dt_bias"])
+        assert torch.equal(one, ys[t])
+
+
+def test_step_padding_and_repeated_slots():
+    B, H, P, N = 70, 2, 64, 64
+    d = inputs(B, 1, H, P, N, 1, BF, BF, 1, False)
+    one = {k: d[k][:, 0] for k in ("x", "dt", "B", "C")}
+    pool = rnd(80, H, N, P, seed=3)
+    slots = torch.randperm(80, generator=torch.Generator().manual_seed(4))[:B].to(torch.int32).to(DEV)
+    slots[5], slots[6], slots[7] = -1, 80, -2 ** 31
+    slots[66] = slots[2]
+    slots[67] = slots[2]
+    before = pool.clone()
+    y = gdn.ssm_step(one["x"], one["dt"], d["A"], one["B"], one["C"], pool, d["D"], d["dt_bias"], slots=slots)
+    pad = [5, 6, 7, 66, 67]
+    keep = [i for i in range(B) if i not in pad]
+    alone = before.clone()
+    ref = gdn.ssm_step(one["x"][keep], one["dt"][keep], d["A"], one["B"][keep], one["C"][keep], alone, d["D"], d["dt_bias"],
+                       slots=slots[keep])
+    assert y[pad].eq(0).all() and torch.equal(y[keep], ref) and torch.equal(pool, alone)
+    assert gdn.ssm_step(one["x"][:0], one["dt"][:0], d["A"], one["B"][:0], one["C"][:0], pool).shape == (0, H, P)
+
+
+def test_segments_and_single_pass_agree():
+    """A long stream alone is cut into segments; the same tokens as two calls, the
+    second from the first one's state, give the same numbers."""
+    d = inputs(1, 2000, 4, 64, 128, 2, BF, BF, 1, True)
+    y, hT = forward(d)
+    cut = 256
+    parts = [{k: (v[:, s] if k in ("x", "dt", "B", "C") else v) for k, v in d.items()} for s in (slice(0, cut), slice(cut, 2000))]
+    y0, h1 = forward(parts[0])
+    parts[1]["h0"] = h1
+    y1, h2 = forward(parts[1])
+    step, _ = L.step_sizes(flat(d["dt"]), d["dt_bias"], True)
+    Y, Z = L.ssm(flat(d["x"]), step, d["A"], flat(d["B"]), flat(d["C"]), d["D"], d["h0"], [2000], absolute=True)
+    both = torch.cat([y0, y1], 1)
+    # each way within y's tolerance of the recurrence
+    close(flat(y), flat(both).cpu().double(), 2 * (flat(both).cpu().double().abs() * 2.0 ** -8 + Y * (2 * 2.0 ** -8 + FP)), "y")
+    close(hT, h2.cpu().double(), Z * 2 * (2.0 ** -16 + FP), "hT")
+
+
+def test_gates_at_their_ends():
+    """A = 0 (nothing fades), dt = 0 (a token without effect) and gates so strong
+    that every decay is 0: finite, and what the recurrence gives."""
+    T, H, P, N = 200, 3, 64, 64
+    d = inputs(1, T, H, P, N, 1, BF, F32, 1, True)
+    d["A"] = torch.tensor([0.0, -1.0, -1e4], device=DEV)
+    d["dt"] = rnd(1, T, H, seed=5).abs() * 0.05
+    d["dt"][:, ::3] = 0.0
+    d["dt_bias"] = None
+    y, hT = forward(d, dt_softplus=False)
+    step, _ = L.step_sizes(flat(d["dt"]), None, False)
+    args = (flat(d["x"]), step, d["A"], flat(d["B"]), flat(d["C"]), d["D"], d["h0"], [T])
+    ref, rT = L.ssm(*args)
+    Y, Z = L.ssm(*args, absolute=True)
+    close(flat(y), ref, ref.abs() * 2.0 ** -8 + Y * (2 * 2.0 ** -8 + FP), "y")
+    close(hT, rT, Z * (2.0 ** -16 + FP), "hT")
+    dy = rnd(1, T, H, P, seed=8, dtype=BF)
+    got = gdn.ssm_backward(dy, d["x"], d["dt"], d["A"], d["B"], d["C"], d["D"], None, d["h0"], dt_softplus=False)
+    assert all(t.isfinite().all() for t in got if t is not None)
+
+
+def test_weak_gates_behind_strong_ones():
+    """A decay of e^-2000 early in each chunk and gates of 1e-5 behind it: a sum of
+    gates held in 32 bits would be off by 2^-14 there, all later decays with it."""
+    T, H, P, N = 128, 1, 64, 64
+    d = inputs(1, T, H, P, N, 1, F32, F32, 1, False)
+    d["A"], d["dt_bias"], d["D"] = torch.tensor([-1.0], device=DEV), None, None
+    d["dt"] = torch.full((1, T, H), 1e-5, device=DEV)
+    d["dt"][:, 1] = 2000.0
+    d["dt"][:, 65] = 2000.0
+    y, hT = forward(d, dt_softplus=False)
+    step, _ = L.step_sizes(flat(d["dt"]), None, False)
+    args = (flat(d["x"]), step, d["A"], flat(d["B"]), flat(d["C"]), None, None, [T])
+    ref, rT = L.ssm(*args)
+    Y, Z = L.ssm(*args, absolute=True)
+    close(flat(y), ref, Y * 2.0 ** -18, "y")
+    close(hT, rT, Z * 2.0 ** -18, "hT")
+
+
+def test_rows_behind_the_sequences_and_malformed_offsets():
+    lens, T, H, P, N = [30, 0, 100], 160, 2, 64, 64
+    d = inputs(1, T, H, P, N, 1, BF, BF, 3, True)
+    for k in ("x", "B", "C", "dt"):
+        d[k][:, 130:] = float("nan")
+    cu = offsets(lens)
+    y = torch.full((1, T, H, P), 7.0, device=DEV, dtype=BF)
+    _, hT = forward(d, cu_seqlens=cu, y=y)
+    cutd = {k: (v[:, :130] if k in ("x", "dt", "B", "C") else v) for k, v in d.items()}
+    ref, rT = forward(cutd, cu_seqlens=cu)
+    assert torch.equal(y[:, :130], ref) and y[:, 130:].eq(7.0).all() and torch.equal(hT, rT) and hT.isfinite().all()
+    assert torch.equal(hT[1], d["h0"][1])                        # an empty sequence keeps its state
+    dy = rnd(1, T, H, P, seed=8, dtype=BF)
+    dy[:, 130:] = float("nan")
+    grads = {k: torch.full_like(d[k].contiguous(), 7.0) for k in ("x", "B", "C", "dt")}
+    one = torch.full((1, T, H * P + 2 * N), 7.0, device=DEV, dtype=BF)
+    dx, dB, dC = one.split((H * P, N, N), -1)
+    out = dict(dx=dx.unflatten(-1, (H, P)), dB=dB.unflatten(-1, (1, N)), dC=dC.unflatten(-1, (1, N)), ddt=grads["dt"])
+    a = gdn.ssm_backward(dy, d["x"], d["dt"], d["A"], d["B"], d["C"], d["D"], d["dt_bias"], d["h0"], cu_seqlens=cu, **out)
+    b = gdn.ssm_backward(dy[:, :130].contiguous(), *(cutd[k] for k in ("x", "dt", "A", "B", "C", "D", "dt_bias", "h0")), cu_seqlens=cu)
+    for u, v in zip(a, b):
+        same = u[:, :130] if u.dim() > 1 and u.shape[:2] == (1, T) else u
+        assert torch.equal(same, v) and v.isfinite().all()
+    assert one[:, 130:].eq(7.0).all() and grads["dt"][:, 130:].eq(7.0).all()
+    for bad in ([0, 1000, 160], [-5, 60, 20, 160], [150, 10], [2 ** 31 - 1, -2 ** 31]):
+        m = inputs(1, T, H, P, N, 1, BF, BF, len(bad) - 1, True)
+        off = torch.tensor(bad, device=DEV, dtype=torch.int32)
+        forward(m, cu_seqlens=off)
+        gdn.ssm_backward(rnd(1, T, H, P, seed=8, dtype=BF), *(m[k] for k in ("x", "dt", "A", "B", "C", "D", "dt_bias", "h0")), cu_seqlens=off)
+    torch.cuda.synchronize()
+
+
+def test_dense_and_side_by_side_inputs_agree():
+    a, b = (inputs(2, 130, 4, 64, 64, 2, BF, BF, 2, True, joint=j) for j in (True, False))
+    ya, ha = forward(a)
+    yb, hb = forward(b)
+    assert torch.equal(ya, yb) and torch.equal(ha, hb)
+
+
+def test_empty_and_refused():
+    d = inputs(2, 10, 2, 64, 64, 1, F32, F32, 2, True)
+    names = ("x", "dt", "A", "B", "C", "D", "dt_bias", "h0")
+    none = {k: (v[:, :0] if k in ("x", "dt", "B", "C") else v) for k, v in d.items()}
+    y, hT = forward(none)
+    assert y.shape == (2, 0, 2, 64) and torch.equal(hT, d["h0"])
+    g = gdn.ssm_backward(y, *(none[k] for k in names), d["h0"])
+    assert g[2].eq(0).all() and g[5].eq(0).all() and g[6].eq(0).all() and torch.equal(g[7], d["h0"])
+    f = lambda **kw: gdn.ssm_forward(*({**d, **kw}[k] for k in names))  # noqa: E731
+    for bad, err in ((lambda: f(x=d["x"].to(BF)), TypeError), (lambda: f(A=d["A"][:1]), ValueError),
+                     (lambda: f(dt=d["dt"].double()), TypeError), (lambda: f(h0=d["h0"][:1]), ValueError),
+                     (lambda: f(C=d["C"].contiguous()), ValueError), (lambda: f(D=d["D"].to(BF)), TypeError),
+                     (lambda: f(x=d["x"][..., :32].contiguous(), h0=None), gdn.GdnError),
+                     (lambda: f(x=d["x"][:, :1].expand(2, 10, 2, 64)), gdn.GdnError),
+                     (lambda: gdn.ssm_forward(*(d[k] for k in names), hT=d["h0"]), ValueError),
+                     (lambda: gdn.ssm_forward(*(d[k] for k in names), cu_seqlens=offsets([20])), ValueError),
+                     (lambda: gdn.ssm_forward(*(d[k] for k in names), stream=torch.cuda.Stream(), y=d["x"]), ValueError)):
+        with pytest.raises(err):
+            bad()
+
+
+def test_gradient_against_differences():
+    """fp32 io: a difference over 2 h, h = 2^-8, of a loss known to 2^-15 of its
+    terms, so to 2^-8 of them over h; and a third derivative of the same sizes."""
+    H, P, N, h = 2, 64, 64, 2.0 ** -8
+    d = inputs(1, 300, H, P, N, 1, F32, F32, 1, True, joint=False)
+    d["dt"] = d["dt"].contiguous()
+    dy, dhT = rnd(1, 300, H, P, seed=8), rnd(1, H, N, P, seed=9, scale=0.1)
+    names = ("x", "dt", "A", "B", "C", "D", "dt_bias", "h0")
+
+    def loss(v):
+        y, hT = gdn.ssm_forward(*v)
+        return float((y.double() * dy.double()).sum() + (hT.double() * dhT.double()).sum())
+
+    leaves = [d[k] for k in names]
+    g = gdn.ssm_backward(dy, *leaves, dhT)
+    step, _ = L.step_sizes(flat(d["dt"]), d["dt_bias"], True)
+    args = (flat(d["x"]), step, d["A"], flat(d["B"]), flat(d["C"]), d["D"], d["h0"], [300])
+    Y, Z = L.ssm(*args, absolute=True)
+    terms = float((Y * dy[0].cpu().double().abs()).sum() + (Z * dhT.cpu().double().abs()).sum())
+    for i, name in enumerate(names):
+        v = rnd(*leaves[i].shape, seed=20 + i)
+        plus, minus = list(leaves), list(leaves)
+        plus[i], minus[i] = leaves[i] + h * v, leaves[i] - h * v
+        num = (loss(plus) - loss(minus)) / (2 * h)
+        assert abs(num - float((g[i].double() * v.double()).sum())) <= terms * 2.0 ** -7, name
+
+
+def test_streams_graphs_and_repeats():
+    d = inputs(2, 700, 4, 64, 128, 2, BF, BF, 2, True)
+    dy = rnd(2, 700, 4, 64, seed=8, dtype=BF)
+    names = ("x", "dt", "A", "B", "C", "D", "dt_bias", "h0")
+    pool0 = rnd(3, 4, 128, 64, seed=9)
+    pool = pool0.clone()
+    slots = torch.tensor([2, 0], device=DEV, dtype=torch.int32)
+
+    def work():
+        pool.copy_(pool0)
+        y, hT = forward(d)
+        s = gdn.ssm_step(d["x"][:, 5], d["dt"][:, 5], d["A"], d["B"][:, 5], d["C"][:, 5], pool, d["D"], d["dt_bias"], slots=slots)
+        return [y, hT, s, *gdn.ssm_backward(dy, *(d[k] for k in names))]
+
+    ref = [t.clone() for t in work()]
+    assert all(torch.equal(a, b) for a, b in zip(ref, work()))
+    st = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    y, hT = forward(d, stream=st)
+    st.synchronize()
+    assert torch.equal(y, ref[0]) and torch.equal(hT, ref[1])
+    # two at once, each with its own workspace
+    st2 = torch.cuda.Stream()
+    a = [forward(d, stream=s) for s in (st, st2, st, st2)]
+    torch.cuda.synchronize()
+    assert all(torch.equal(u[0], ref[0]) and torch.equal(u[1], ref[1]) for u in a)
+    with torch.cuda.stream(st):
+        work()
+    st.synchronize()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        out = work()
+    for k in range(3):
+        d["x"].copy_(rnd(2, 700, 4, 64, seed=10 + k, dtype=BF))
+        g.replay()
+        torch.cuda.synchronize()
+        kept = [t.clone() for t in out]
+        assert all(torch.equal(a, b) for a, b in zip(kept, work())), k
+
+
+def test_given_workspace_and_outputs():
+    d = inputs(1, 1500, 2, 64, 64, 1, BF, BF, 1, True)
+    y, hT = forward(d)
+    y2, h2 = torch.empty_like(y), torch.empty_like(hT)
+    ws = torch.full((1 << 22,), 0xff, device=DEV, dtype=torch.uint8)      # NaN in every type
+    got = forward(d, y=y2, hT=h2, workspace=ws)
+    assert got[0] is y2 and got[1] is h2 and torch.equal(y, y2) and torch.equal(hT, h2)
+    with pytest.raises(gdn.GdnError) as e:
+        forward(d, workspace=ws[:1024])
+    assert e.value.status == 6
+    dy = rnd(1, 1500, 2, 64, seed=8, dtype=BF)
+    names = ("x", "dt", "A", "B", "C", "D", "dt_bias", "h0")
+    a = gdn.ssm_backward(dy, *(d[k] for k in names))
+    b = gdn.ssm_backward(dy, *(d[k] for k in names), workspace=torch.full((1 << 25,), 0xff, device=DEV, dtype=torch.uint8))
+    assert all(torch.equal(u, v) for u, v in zip(a, b))
