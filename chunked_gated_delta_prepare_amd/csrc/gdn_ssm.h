@@ -345,16 +345,18 @@ __device__ __forceinline__ float dt_of(const SsmParams &p, float raw, float bias
     return live ? (p.softplus ? softplus(v) : v) : 0.f;
 }
 
+// `before` and `behind` are the signs that the state is held with before and
+// behind the chunk.
 template <bool REV>
-__device__ __forceinline__ void make_gates(Gates &g, float dt, float A) {
+__device__ __forceinline__ void make_gates(Gates &g, float dt, float A, float before, float behind) {
     const int l = again(lane_id());
     asm volatile("" : "+s"(A));                // (its double is not kept in registers either)
     const double own = (double)dt * (double)A * 1.4426950408889634074, upto = wave_scan(own);
     const double total = last_lane(upto), cum = REV ? upto - own : upto;
     const float hi = (float)cum, w = REV ? 1.f : dt;
     g.cum[l] = make_float2(hi, (float)(cum - (double)hi));
-    g.ecum[l] = fast_exp2(hi);
-    g.end[l] = w * fast_exp2((float)(total - cum));
+    g.ecum[l] = before * fast_exp2(hi);
+    g.end[l] = behind * w * fast_exp2((float)(total - cum));
     g.dt[l] = dt;
     if (l == 63) g.total = total;
 }
@@ -538,10 +540,10 @@ __device__ __forceinline__ float segments_before(const SsmParams &p, const Segme
 //      blocks, dealt to the waves); S^T q on the way
 //   2  out1 = M v + e^cum S^T q, transposed, so that a lane stores four columns
 //   3  S' = e^total S + k^T (w v)
-// The state's products take w v in PARTS bf16 parts: two (relative error 2^-18)
-// for a state that is an output or another segment's start, three where it
-// goes into dA, a sum over all tokens of both signs in which two left errors
-// of up to 5e-5.  Where only out1 is read from the state (an output state comes
+// The products of a state that is an output or another segment's start take
+// w v in three bf16 parts (relative error 2^-27): with two the final state was
+// 2.4e-6 off, against 1e-7 of fp32 arithmetic throughout, and dA, a sum over
+// all tokens of both signs, 5e-5.  Where only out1 is read from the state (an output state comes
 // from the segments' end states if there are any), w v is rounded once to
 // bf16, as out1's other operands are and out1 itself, and S too before it is
 // multiplied.  The next chunk's rows are in flight while one is worked on, and
@@ -552,12 +554,12 @@ __device__ __forceinline__ float segments_before(const SsmParams &p, const Segme
 // and four waves the kernel read a third less from LDS but held 375
 // registers a lane, one wave per SIMD (1.8 ms at 65536 tokens, 64 heads).
 // ---------------------------------------------------------------------------
-template <typename IO, int N, int COLS, int NH, bool ENDS, bool REV, int PARTS>
+template <typename IO, int N, int COLS, int NH, bool ENDS, bool REV>
 __global__ void __launch_bounds__(4 * COLS, sizeof(IO) == 4 ? 1 : COLS == 64 && N == 128 ? 3 : 4) ssm_scan_kernel(SsmParams p) {
     typedef SOp<IO> O;
     typedef typename O::elem E;
     constexpr int C = kSsmChunk, NW = COLS / 16, NB = N / 16, kThreads = 4 * COLS, P = COLS / NH;
-    constexpr int kP = O::template kParts<PARTS>;
+    constexpr int kP = O::template kParts<3>;
     __shared__ __align__(16) E sv[C * COLS], sk[C * N], sq[ENDS ? 8 : C * N], sm[ENDS ? 1 : NH][ENDS ? 8 : C * C];
     // chunks whose gates are formed at once, one chunk and head a wave
     constexpr int GC = NW / NH;
@@ -643,7 +645,7 @@ __global__ void __launch_bounds__(4 * COLS, sizeof(IO) == 4 ? 1 : COLS == 64 && 
         if (gater && c + gc < nc) {
             int lo;
             const int rows = chunk_of<REV>(seg, c + gc, lo);
-            make_gates<REV>(gates[gc][gh], dt_of(p, raw_value<IO>(p, raw), bias, again(lane_id()) < rows), A);
+            make_gates<REV>(gates[gc][gh], dt_of(p, raw_value<IO>(p, raw), bias, again(lane_id()) < rows), A, 1.f, 1.f);
         }
     };
     const bool exact = p.sT && last && !via_ends;

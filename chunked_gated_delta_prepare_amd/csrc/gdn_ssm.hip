@@ -182,8 +182,8 @@ namespace {
 template <typename IO, int COLS, int NH>
 const void *ssm_fn(int N, bool ends) {
     if (N == 64)
-        return ends ? (const void *)&ssm_scan_kernel<IO, 64, COLS, NH, true, false, 2> : (const void *)&ssm_scan_kernel<IO, 64, COLS, NH, false, false, 2>;
-    return ends ? (const void *)&ssm_scan_kernel<IO, 128, COLS, NH, true, false, 2> : (const void *)&ssm_scan_kernel<IO, 128, COLS, NH, false, false, 2>;
+        return ends ? (const void *)&ssm_scan_kernel<IO, 64, COLS, NH, true, false> : (const void *)&ssm_scan_kernel<IO, 64, COLS, NH, false, false>;
+    return ends ? (const void *)&ssm_scan_kernel<IO, 128, COLS, NH, true, false> : (const void *)&ssm_scan_kernel<IO, 128, COLS, NH, false, false>;
 }
 
 const void *ssm_pick(const gdn_ssm_problem *pr, const SsmPlan &s, bool ends) {

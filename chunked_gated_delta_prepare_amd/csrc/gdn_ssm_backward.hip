@@ -18,6 +18,13 @@ namespace gdn {
 // S enters its product in three bf16 parts and (w k) in three (relative error
 // 2^-27): the sums feed dt's and A's gradients, which are fp32.  M is rounded
 // once to out2's own type.
+//
+// S changes its sign from chunk to chunk (its weights and decays bring that
+// about).  The matrix cores' sums lean to one side by some 2.5e-10 of their
+// terms, which inputs of one sign (x, B and C behind a silu) add up over N x P
+// products to 3e-8 of X a chunk, always the same way: over 16384 tokens dA was
+// 2.6e-6 and d(dt_bias) 4.9e-6 off.  With the sign alternating the chunks'
+// shares cancel (4.7e-7 and 1.9e-6).
 // ---------------------------------------------------------------------------
 template <typename IO, int N, int COLS, int NH, bool REV>
 __global__ void __launch_bounds__(4 * N, sizeof(IO) == 4 ? 1 : NH == 1 && N == 128 ? 4 : 2) ssm_key_kernel(SsmParams p) {
@@ -93,7 +100,8 @@ __global__ void __launch_bounds__(4 * N, sizeof(IO) == 4 ? 1 : NH == 1 && N == 1
         if (gater && c + gc < nc) {
             int lo;
             const int rows = chunk_of<REV>(seg, c + gc, lo);
-            make_gates<REV>(gates[gc][gh], dt_of(p, raw_value<IO>(p, raw), bias, again(lane_id()) < rows), A);
+            make_gates<REV>(gates[gc][gh], dt_of(p, raw_value<IO>(p, raw), bias, again(lane_id()) < rows), A,
+                             (c + gc) & 1 ? -1.f : 1.f, (c + gc) & 1 ? 1.f : -1.f);
         }
     };
     if (nc > 0) {
@@ -142,7 +150,8 @@ __global__ void __launch_bounds__(4 * N, sizeof(IO) == 4 ? 1 : NH == 1 && N == 1
                 double d = 0.0;
 #pragma unroll
                 for (int k = 0; k < NW; ++k) d += (double)dots[w][k];
-                p.X[((int64_t)mark * p.n_hb + hb) * NH + w] = d;
+                // h behind chunk nc - 1 - c has that one's sign turned, dh chunk c's
+                p.X[((int64_t)mark * p.n_hb + hb) * NH + w] = nc & 1 ? -d : d;
             }
         }
         // 1
@@ -249,7 +258,7 @@ __global__ void __launch_bounds__(4 * N, sizeof(IO) == 4 ? 1 : NH == 1 && N == 1
         // 3
 #pragma unroll
         for (int hh = 0; hh < NH; ++hh) {
-            const float et = fast_exp2((float)gs[hh].total);
+            const float et = -fast_exp2((float)gs[hh].total);
 #pragma unroll
             for (int pb = hh * (PB / NH); pb < (hh + 1) * (PB / NH); ++pb) h[pb] *= et;
         }
@@ -376,7 +385,7 @@ __global__ void __launch_bounds__(256) ssm_gate_kernel(GateParams gp) {
             raw = (p.dt_f32 ? ((const float *)p.dt)[at] : io_traits<IO>::load((const IO *)p.dt + at)) + bias;
         }
         const float dt = on ? (p.softplus ? softplus(raw) : raw) : 0.f;
-        const double dca = (double)dt * (double)ca, in = (double)ri - (double)dt * (double)ci + (double)ra;
+        const double dca = (double)dt * (double)ca, in = (double)ri - (double)dt * (double)ci;
         const double pre_in = wave_scan(in), pre_ca = wave_scan(dca), pre_ra = wave_scan((double)ra);
         const double all_in = last_lane(pre_in), all_ca = last_lane(pre_ca), all_ra = last_lane(pre_ra);
         // nothing of weight crosses a chunk whose decay is below fp32's step
@@ -401,7 +410,12 @@ __global__ void __launch_bounds__(256) ssm_gate_kernel(GateParams gp) {
             x = qk + wsum[k][1];
         }
         if (on) {
-            const double dg = (all_in - pre_in + in) + (pre_ca - dca) + Q;
+            const int n = seg.end - (t - l) < kSsmChunk ? seg.end - (t - l) : kSsmChunk;
+            // The pairs inside sum to zero over the chunk; what they sum to
+            // instead is the roundings of the n rows' sums, taken back evenly
+            // (d(dt_bias) at 2 x 8192 tokens 1.9e-6 -> 1.2e-6 off, dA 4.7e-7 -> 2.3e-7)
+            const double pairs = all_in - pre_in + in - all_in * (double)(n - l) / (double)n;
+            const double dg = pairs + (all_ra - pre_ra + (double)ra) + (pre_ca - dca) + Q;
             double g = (double)ci + (double)ca + (double)wtt + (double)A * dg;
             if (p.softplus) g /= 1.0 + (double)expf(-raw);
             const int64_t at = ((int64_t)seg.batch * p.T + t) * p.H + head;
@@ -485,9 +499,9 @@ template <typename IO, int N, int COLS, int NH>
 struct BwdFns {
     static constexpr int kScanThreads = 4 * COLS, kKeyThreads = 4 * N;
     static const void *ends(bool rev) {
-        return rev ? (const void *)&ssm_scan_kernel<IO, N, COLS, NH, true, true, 3> : (const void *)&ssm_scan_kernel<IO, N, COLS, NH, true, false, 3>;
+        return rev ? (const void *)&ssm_scan_kernel<IO, N, COLS, NH, true, true> : (const void *)&ssm_scan_kernel<IO, N, COLS, NH, true, false>;
     }
-    static const void *dx() { return (const void *)&ssm_scan_kernel<IO, N, COLS, NH, false, true, 2>; }
+    static const void *dx() { return (const void *)&ssm_scan_kernel<IO, N, COLS, NH, false, true>; }
     static const void *key(bool rev) {
         return rev ? (const void *)&ssm_key_kernel<IO, N, COLS, NH, true> : (const void *)&ssm_key_kernel<IO, N, COLS, NH, false>;
     }
