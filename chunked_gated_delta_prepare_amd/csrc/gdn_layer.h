@@ -1,5 +1,5 @@
 // Building blocks shared by the layer operators' kernels (norm, convolution,
-// selective scan): rows of four elements a lane through buffer descriptors,
+// selective scan): rows of up to four elements a lane through buffer descriptors,
 // wave and workgroup sums, and the checks of their entry points.
 //
 // Every store is at most 8 bytes a lane, and no lane stores two adjacent
@@ -27,6 +27,14 @@ template <typename T, int VEC>
 __device__ __forceinline__ void row_load(rsrc_t r, uint32_t e, float (&x)[VEC]) {
     if constexpr (VEC == 1) {
         x[0] = BufElem<T>::load(r, e * io_traits<T>::bytes, 0);
+    } else if constexpr (VEC == 2 && sizeof(T) == 2) {
+        const uint32_t v = bload32(r, e * 2, 0);
+        x[0] = __uint_as_float(v << 16);
+        x[1] = __uint_as_float(v & 0xffff0000u);
+    } else if constexpr (VEC == 2) {
+        const u32x2 v = __builtin_amdgcn_raw_buffer_load_b64(r, e * 4, 0, 0);
+        x[0] = __uint_as_float(v[0]);
+        x[1] = __uint_as_float(v[1]);
     } else if constexpr (sizeof(T) == 2) {
         const u32x2 v = __builtin_amdgcn_raw_buffer_load_b64(r, e * 2, 0, 0);
         x[0] = __uint_as_float(v[0] << 16);
@@ -58,6 +66,10 @@ template <typename T, int VEC>
 __device__ __forceinline__ void row_store(rsrc_t r, uint32_t e, const float (&x)[VEC]) {
     if constexpr (VEC == 1) {
         BufElem<T>::store(x[0], r, e * io_traits<T>::bytes, 0);
+    } else if constexpr (VEC == 2 && sizeof(T) == 2) {
+        bstore32(pack_bf16(x[0], x[1]), r, e * 2, 0);
+    } else if constexpr (VEC == 2) {
+        __builtin_amdgcn_raw_buffer_store_b64(u32x2{__float_as_uint(x[0]), __float_as_uint(x[1])}, r, e * 4, 0, 0);
     } else if constexpr (sizeof(T) == 2) {
         __builtin_amdgcn_raw_buffer_store_b64(u32x2{pack_bf16(x[0], x[1]), pack_bf16(x[2], x[3])}, r, e * 2, 0, 0);
     } else {

@@ -11,7 +11,12 @@
 //   D <= 8192     one workgroup of 256 threads per row
 //   D <= 16384    one workgroup of 512 threads per row
 // VEC is 4 (8 bytes of bf16) where every row starts at four aligned elements,
-// else 1.
+// else 2 or 1 (1003 rows of 2050, bf16 with fp32 sums, at VEC 2 and 1: 7.7 and
+// 10.6 us forward, 12.1 and 24.2 us backward).
+// Measured: 16384 rows of 8192 in bf16 with a residual to e4m3 190 us, 4.9 TB/s;
+// 16384 rows of 4096 in bf16 with a residual forward 85 us (6.3 TB/s, part of
+// it out of the last cache), backward 120 us (4.5 TB/s); 32 rows 5 us, a
+// launch's own time and one reduction's.
 #include "gdn_layer.h"
 
 namespace gdn {
@@ -64,6 +69,8 @@ __device__ __forceinline__ void store_e4m3(rsrc_t r, uint32_t e, const float (&v
     if constexpr (VEC == 4) {
         q = __builtin_amdgcn_cvt_pk_fp8_f32(c[2], c[3], q, true);
         bstore32((uint32_t)q, r, e, 0);
+    } else if constexpr (VEC == 2) {
+        __builtin_amdgcn_raw_buffer_store_b16((uint16_t)q, r, e, 0, 0);
     } else {
         __builtin_amdgcn_raw_buffer_store_b8((uint8_t)q, r, e, 0, 0);
     }
@@ -144,18 +151,19 @@ __global__ void __launch_bounds__(TPR < 256 ? 256 : TPR) norm_forward_kernel(Nor
         return;
     }
     const int ng = (D + 127) >> 7;
-    if constexpr (VEC == 4) {
-        // 128 columns are 32 lanes of one vector index
+    if constexpr (VEC > 1) {
+        // 128 columns are 32 (64) lanes of one vector index
+        constexpr int kL = 128 / VEC;
 #pragma unroll
         for (int k = 0; k < K; ++k) {
             float m = 0.f;
 #pragma unroll
-            for (int i = 0; i < 4; ++i) m = fmaxf(m, fabsf(s[k][i]));
-            m = lanes_max<32>(m);
+            for (int i = 0; i < VEC; ++i) m = fmaxf(m, fabsf(s[k][i]));
+            m = lanes_max<kL>(m);
             const float scale = fmaxf(m / kE4m3Max, kTinyScale);
             store_e4m3<VEC>(ry, (k * TPR + tid) * VEC, s[k], 1.f / scale);
             const int gi = ((k * TPR + tid) * VEC) >> 7;
-            if ((tid & 31) == 0 && gi < ng && live) p.scales[at * ng + gi] = scale;
+            if ((tid & (kL - 1)) == 0 && gi < ng && live) p.scales[at * ng + gi] = scale;
         }
     } else {
         // 128 columns are two waves of one element: their maxima meet in LDS
@@ -243,23 +251,30 @@ __global__ void __launch_bounds__(TPR < 256 ? 256 : TPR) norm_backward_kernel(No
     for (int k = 0; k < K; ++k) row_store<float, VEC>(rp, (k * TPR + tid) * VEC, dw[k]);
 }
 
-// dw[c] = the sum of column c of n rows: 64 columns a workgroup, every
-// sixteenth row a wave.
+// dw[c] = the sum of column c of n rows: kDwCols columns a workgroup, and
+// 1024 / kDwCols rows at a time (768 rows of 2050 columns: 4.0 us; with 64
+// columns a workgroup only 33 have work, 15.4 us).
+constexpr int kDwCols = 16, kDwRows = 1024 / kDwCols;
 __global__ void __launch_bounds__(1024) norm_dw_kernel(NormParams p) {
-    __shared__ float red[16][64];
-    const int c = blockIdx.x * 64 + lane_id(), w = wave_id();
+    __shared__ float red[kDwRows][kDwCols];
+    const int j = threadIdx.x % kDwCols, w = threadIdx.x / kDwCols, c = blockIdx.x * kDwCols + j;
     float a = 0.f;
     if (c < p.D) {
         const float *q = p.part + c;
-        for (int64_t i = w; i < p.nwg; i += 16) a += q[i * p.D];
+#pragma unroll 4
+        for (int64_t i = w; i < p.nwg; i += kDwRows) a += q[i * p.D];
     }
-    red[w][lane_id()] = a;
+    red[w][j] = a;
     __syncthreads();
-    if (w == 0 && c < p.D) {
+    if (w < 4) {
+        a = 0.f;
 #pragma unroll
-        for (int i = 1; i < 16; ++i) a += red[i][lane_id()];
-        p.dw[c] = a;
+        for (int i = 0; i < kDwRows / 4; ++i) a += red[4 * i + w][j];
     }
+    __syncthreads();
+    if (w < 4) red[w][j] = a;
+    __syncthreads();
+    if (w == 0 && c < p.D) p.dw[c] = (red[0][j] + red[1][j]) + (red[2][j] + red[3][j]);
 }
 
 namespace {
@@ -291,28 +306,29 @@ gdn_status run_norm(NormParams &np, int64_t grid, hipStream_t s) {
     return launch_kernel(fn, (int)grid, &np, s, TPR < 256 ? 256 : TPR);
 }
 
-template <bool BWD, typename IO, typename RS>
-gdn_status norm_d(NormParams &np, bool vec, int64_t grid, hipStream_t s) {
+template <bool BWD, typename IO, typename RS, int VEC>
+gdn_status norm_d(NormParams &np, int64_t grid, hipStream_t s) {
     const int D = np.D;
-    if (vec) {
-        if (D <= 256) return run_norm<BWD, IO, RS, 4, 64, 1>(np, grid, s);
-        if (D <= 1024) return run_norm<BWD, IO, RS, 4, 256, 1>(np, grid, s);
-        if (D <= 2048) return run_norm<BWD, IO, RS, 4, 256, 2>(np, grid, s);
-        if (D <= 4096) return run_norm<BWD, IO, RS, 4, 256, 4>(np, grid, s);
-        if (D <= 8192) return run_norm<BWD, IO, RS, 4, 256, 8>(np, grid, s);
-        return run_norm<BWD, IO, RS, 4, 512, 8>(np, grid, s);
-    }
-    if (D <= 256) return run_norm<BWD, IO, RS, 1, 64, 4>(np, grid, s);
-    if (D <= 2048) return run_norm<BWD, IO, RS, 1, 256, 8>(np, grid, s);
-    if (D <= 8192) return run_norm<BWD, IO, RS, 1, 256, 32>(np, grid, s);
-    return run_norm<BWD, IO, RS, 1, 512, 32>(np, grid, s);
+    if (D <= 256) return run_norm<BWD, IO, RS, VEC, 64, 4 / VEC>(np, grid, s);
+    if (D <= 1024) return run_norm<BWD, IO, RS, VEC, 256, 4 / VEC>(np, grid, s);
+    if (D <= 2048) return run_norm<BWD, IO, RS, VEC, 256, 8 / VEC>(np, grid, s);
+    if (D <= 4096) return run_norm<BWD, IO, RS, VEC, 256, 16 / VEC>(np, grid, s);
+    if (D <= 8192) return run_norm<BWD, IO, RS, VEC, 256, 32 / VEC>(np, grid, s);
+    return run_norm<BWD, IO, RS, VEC, 512, 32 / VEC>(np, grid, s);
+}
+
+template <bool BWD, typename IO, typename RS>
+gdn_status norm_vec(NormParams &np, int vec, int64_t grid, hipStream_t s) {
+    if (vec == 4) return norm_d<BWD, IO, RS, 4>(np, grid, s);
+    if (vec == 2) return norm_d<BWD, IO, RS, 2>(np, grid, s);
+    return norm_d<BWD, IO, RS, 1>(np, grid, s);
 }
 
 template <bool BWD>
-gdn_status norm_types(const gdn_norm_problem *pr, NormParams &np, bool vec, int64_t grid, hipStream_t s) {
-    if (pr->x_dtype == GDN_F32) return norm_d<BWD, float, float>(np, vec, grid, s);
-    if (pr->s_dtype == GDN_F32) return norm_d<BWD, bf16_t, float>(np, vec, grid, s);
-    return norm_d<BWD, bf16_t, bf16_t>(np, vec, grid, s);
+gdn_status norm_types(const gdn_norm_problem *pr, NormParams &np, int vec, int64_t grid, hipStream_t s) {
+    if (pr->x_dtype == GDN_F32) return norm_vec<BWD, float, float>(np, vec, grid, s);
+    if (pr->s_dtype == GDN_F32) return norm_vec<BWD, bf16_t, float>(np, vec, grid, s);
+    return norm_vec<BWD, bf16_t, bf16_t>(np, vec, grid, s);
 }
 
 void fill_norm(const gdn_norm_problem *pr, NormParams &np) {
@@ -355,8 +371,10 @@ gdn_status gdn_norm_forward(const gdn_norm_problem *pr, const void *x, const voi
     np.y = y;
     np.s = s;
     np.scales = scales;
-    const bool vec = pr->D % 4 == 0 && pr->x_stride % 4 == 0 && aligned_to(x, 4 * eb) && aligned_to(weight, 4 * wb) &&
-                     aligned_to(y, 4 * ob) && aligned_to(residual, 4 * sb) && (!residual || aligned_to(s, 4 * sb));
+    int vec = 4;
+    while (vec > 1 && !(pr->D % vec == 0 && pr->x_stride % vec == 0 && aligned_to(x, vec * eb) && aligned_to(weight, vec * wb) &&
+                        aligned_to(y, vec * ob) && aligned_to(residual, vec * sb) && (!residual || aligned_to(s, vec * sb))))
+        vec /= 2;
     const int k = rows_per_wg(pr->D);
     return norm_types<false>(pr, np, vec, (pr->rows + k - 1) / k, (hipStream_t)stream);
 }
@@ -391,12 +409,14 @@ gdn_status gdn_norm_backward(const gdn_norm_problem *pr, const void *dy, const v
     np.dw = dweight;
     np.part = (float *)workspace;
     np.nwg = (int)norm_wgs(pr);
-    const bool vec = pr->D % 4 == 0 && aligned_to(dy, 4 * eb) && aligned_to(s, 4 * sb) && aligned_to(weight, 4 * wb) &&
-                     aligned_to(dres, 4 * sb) && aligned_to(ds, 4 * sb) && aligned_to(dx, 4 * eb);
+    int vec = 4;
+    while (vec > 1 && !(pr->D % vec == 0 && aligned_to(dy, vec * eb) && aligned_to(s, vec * sb) && aligned_to(weight, vec * wb) &&
+                        aligned_to(dres, vec * sb) && aligned_to(ds, vec * sb) && aligned_to(dx, vec * eb)))
+        vec /= 2;
     st = norm_types<true>(pr, np, vec, np.nwg, (hipStream_t)stream);
     if (st != GDN_OK) return st;
     np.nwg *= rows_per_wg(pr->D);
-    return launch_kernel((const void *)&norm_dw_kernel, (int)((pr->D + 63) / 64), &np, (hipStream_t)stream, 1024);
+    return launch_kernel((const void *)&norm_dw_kernel, (int)((pr->D + kDwCols - 1) / kDwCols), &np, (hipStream_t)stream, 1024);
 }
 
 }  // extern "C"
