@@ -531,7 +531,7 @@ gdn_status check_conv(const gdn_conv_problem *pr, bool packed) {
         if (v < 0 || v > (1 << 23)) return GDN_ERR_UNSUPPORTED;
     if (pr->D > (1 << 23)) return GDN_ERR_UNSUPPORTED;
     const int64_t waves = ((pr->D + 63) / 64) * (pr->B * ((pr->T + 31) / 32) + (packed ? pr->n_seqs : pr->B));
-    if (waves > ((int64_t)1 << 30)) return GDN_ERR_UNSUPPORTED;
+    if (!grid_ok(waves, 64)) return GDN_ERR_UNSUPPORTED;
     return GDN_OK;
 }
 

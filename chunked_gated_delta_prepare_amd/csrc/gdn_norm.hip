@@ -279,6 +279,7 @@ __global__ void __launch_bounds__(1024) norm_dw_kernel(NormParams p) {
 
 namespace {
 
+constexpr int64_t kNormRows = 1 << 22;      // a forward launch's: a multiple of 4, under 2^32 threads
 constexpr int kNormWgs = 768;      // workgroups of the backward pass, at most
 
 int rows_per_wg(int64_t D) { return D <= 256 ? 4 : 1; }
@@ -365,18 +366,25 @@ gdn_status gdn_norm_forward(const gdn_norm_problem *pr, const void *x, const voi
         return GDN_ERR_ALIGNMENT;
     NormParams np;
     fill_norm(pr, np);
-    np.x = x;
-    np.res = residual;
     np.w = weight;
-    np.y = y;
-    np.s = s;
-    np.scales = scales;
     int vec = 4;
     while (vec > 1 && !(pr->D % vec == 0 && pr->x_stride % vec == 0 && aligned_to(x, vec * eb) && aligned_to(weight, vec * wb) &&
                         aligned_to(y, vec * ob) && aligned_to(residual, vec * sb) && (!residual || aligned_to(s, vec * sb))))
         vec /= 2;
+    // (as many launches as rows need; one up to kNormRows)
     const int k = rows_per_wg(pr->D);
-    return norm_types<false>(pr, np, vec, (pr->rows + k - 1) / k, (hipStream_t)stream);
+    const int64_t ng = pr->group ? (pr->D + pr->group - 1) / pr->group : 1;
+    for (int64_t r = 0; r < pr->rows; r += kNormRows) {
+        np.rows = pr->rows - r < kNormRows ? pr->rows - r : kNormRows;
+        np.x = (const char *)x + r * pr->x_stride * (int64_t)eb;
+        np.res = residual ? (const char *)residual + r * pr->D * (int64_t)sb : nullptr;
+        np.y = (char *)y + r * pr->D * (int64_t)ob;
+        np.s = s ? (char *)s + r * pr->D * (int64_t)sb : nullptr;
+        np.scales = scales ? scales + r * ng : nullptr;
+        const gdn_status at = norm_types<false>(pr, np, vec, (np.rows + k - 1) / k, (hipStream_t)stream);
+        if (at != GDN_OK) return at;
+    }
+    return GDN_OK;
 }
 
 size_t gdn_workspace_bytes_norm_backward(const gdn_norm_problem *pr) {

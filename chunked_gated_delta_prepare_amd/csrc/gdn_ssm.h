@@ -351,7 +351,10 @@ template <bool REV>
 __device__ __forceinline__ void make_gates(Gates &g, float dt, float A, float before, float behind) {
     const int l = again(lane_id());
     asm volatile("" : "+s"(A));                // (its double is not kept in registers either)
-    const double own = (double)dt * (double)A * 1.4426950408889634074, upto = wave_scan(own);
+    // a gate below e^-1000 is 0 to all that follows; without the bound one of
+    // -1e20 would take the digits of the sums behind it, one of -inf all of them
+    // (a NaN stays one)
+    const double raw = (double)dt * (double)A, own = (raw < -1000.0 ? -1000.0 : raw) * 1.4426950408889634074, upto = wave_scan(own);
     const double total = last_lane(upto), cum = REV ? upto - own : upto;
     const float hi = (float)cum, w = REV ? 1.f : dt;
     g.cum[l] = make_float2(hi, (float)(cum - (double)hi));

@@ -136,15 +136,17 @@ gdn_status check_ssm(const gdn_ssm_problem *pr, bool packed) {
     if (packed && (pr->B != 1 || pr->n_seqs < 1 || pr->n_seqs > (1 << 24))) return GDN_ERR_BAD_SHAPE;
     if (!io_dtype_ok(pr->io_dtype) || (pr->dt_dtype != pr->io_dtype && pr->dt_dtype != GDN_F32)) return GDN_ERR_UNSUPPORTED;
     if ((pr->P != 64 && pr->P != 128) || (pr->N != 64 && pr->N != 128)) return GDN_ERR_UNSUPPORTED;
-    // a chunk's rows are addressed with 32-bit byte offsets, workgroups are
-    // numbered in 31 bits
+    // a chunk's rows are addressed with 32-bit byte offsets
     if (pr->T > (1 << 30) || pr->B > (1 << 20) || pr->H > (1 << 14)) return GDN_ERR_UNSUPPORTED;
     for (int64_t v : {pr->x_stride_t, pr->bc_stride_t, pr->dt_stride_t, pr->dxbc_stride_t})
         if (v < 0 || v > (1 << 22)) return GDN_ERR_UNSUPPORTED;
     // what lies behind a chunk's last row is told by its place: rows do not overlap
     if (pr->T > 1 && (pr->x_stride_t < pr->H * pr->P || pr->bc_stride_t < pr->G * pr->N)) return GDN_ERR_UNSUPPORTED;
-    const int64_t items = (packed ? pr->n_seqs : pr->B) + (pr->T + 255) / 256 * pr->B;
-    if (items * pr->H * 2 > ((int64_t)1 << 30)) return GDN_ERR_UNSUPPORTED;
+    // the scans', the sums' and the gates' workgroups
+    const SsmPlan s = ssm_plan(pr, packed);
+    const int64_t n = s.n_items;
+    if (!grid_ok(n * s.n_hb, 512) || !grid_ok(n * pr->H, 256) || !grid_ok(n * (s.seg_tokens / kSsmChunk) * pr->G, 4 * pr->N))
+        return GDN_ERR_UNSUPPORTED;
     return GDN_OK;
 }
 

@@ -195,10 +195,10 @@ def _rows(t):
     None if its leading dimensions do not merge."""
     D = t.shape[-1]
     rows = t.numel() // D if D else 0
-    if t.dim() == 1:
-        return 1, D
     if D > 1 and t.stride(-1) != 1 and rows:
         return None
+    if t.dim() == 1:
+        return 1, D
     stride, want = None, None
     for n, s in zip(reversed(t.shape[:-1]), reversed(t.stride()[:-1])):
         if n == 1:
@@ -252,6 +252,7 @@ def _norm_forward(handle, dev, code, x, weight, residual, eps, od, group, y, s, 
         scode = _CODE[residual.dtype]
         if s is not None and s.data_ptr() == residual.data_ptr():
             _check(s, "s", dev, shape, residual.dtype)
+            _apart(s, "s", x, weight, y)
         else:
             s = _out(s, "s", dev, shape, residual.dtype, (x, weight, residual, y))
     else:
@@ -295,6 +296,7 @@ def _norm_backward(handle, dev, code, dy, s, weight, dres, eps, ds, dx, dweight,
     ins = (dy, s, weight)
     if dres is not None and ds is not None and ds.data_ptr() == dres.data_ptr():
         _check(ds, "ds", dev, shape, s.dtype)
+        _apart(ds, "ds", *ins)
     else:
         ds = _out(ds, "ds", dev, shape, s.dtype, ins + (dres,))
     if s.dtype is dy.dtype:
@@ -490,7 +492,8 @@ def ssm_forward(x, dt, A, B, C, D=None, dt_bias=None, h0=None, *, dt_softplus=Tr
     x [b, T, H, P], B and C [b, T, G, N] (tokens may be strided, rows 16-byte
     aligned), P and N 64 or 128, H a multiple of G; dt [b, T, H] in x's type or
     fp32; A, D, dt_bias [H] fp32; h0 [b, H, N, P] fp32, or [n, H, N, P] with
-    cu_seqlens (as in conv_forward).  Returns (y [b, T, H, P], hT like h0 or
+    cu_seqlens (as in conv_forward).  A NaN in a token also reaches those before
+    it in the same 64 of its sequence.  Returns (y [b, T, H, P], hT like h0 or
     None)."""
     dev, code = _ssm_checks(x, dt, A, B, C, D, dt_bias, 2)
     n = _packed(cu_seqlens, dev, x.shape[0])
@@ -534,6 +537,24 @@ def ssm_backward(dy, x, dt, A, B, C, D=None, dt_bias=None, h0=None, dhT=None, *,
                cu_seqlens, n, st, (dx, dB, dC), ddt, dA, dD, ddt_bias, dh0, workspace)
 
 
+def _side_by_side(grads, strides, b, T):
+    """dx, dB and dC of one batch and token stride do not overlap."""
+    if not grads[0].numel():
+        return
+    sb, st = strides
+    first = sorted((t.data_ptr() // t.element_size(), t[0, 0].numel()) for t in grads)
+    end = max(at + n for at, n in first)
+    rows = all(a + n <= c for (a, n), (c, _) in zip(first, first[1:]))
+    extent = end - first[0][0]                    # of one token's rows
+    if rows and (T == 1 or extent <= st) and (b == 1 or extent + (T - 1) * st <= sb):
+        return
+    spans = sorted(_span(t) for t in grads)
+    each = all(t[0, 0].numel() <= st or T == 1 for t in grads) and \
+        all(t[0, 0].numel() + (T - 1) * st <= sb or b == 1 for t in grads)
+    if not each or any(hi > lo for (_, hi), (lo, _) in zip(spans, spans[1:])):
+        raise ValueError("dx, dB and dC must not share memory")
+
+
 def _ssm_backward(handle, dev, code, dy, x, dt, A, B, C, D, dt_bias, h0, dhT, softplus, cu_seqlens, n, st, dxbc, ddt, dA,
                   dD, ddt_bias, dh0, workspace):
     b, T, H, P = x.shape
@@ -544,7 +565,7 @@ def _ssm_backward(handle, dev, code, dy, x, dt, A, B, C, D, dt_bias, h0, dhT, so
         # side by side, as the convolution that feeds the scan laid them out
         both = torch.empty(b, T, H * P + 2 * G * N, device=dev, dtype=x.dtype)
         dx, dB, dC = both.split((H * P, G * N, G * N), -1)
-        dx, dB, dC = dx.unflatten(-1, (H, P)), dB.unflatten(-1, (G, N)), dC.unflatten(-1, (G, N))
+        dxbc = dx, dB, dC = dx.unflatten(-1, (H, P)), dB.unflatten(-1, (G, N)), dC.unflatten(-1, (G, N))
         grads = _strides(dx, "dx")
     else:
         if any(t is None for t in dxbc):
@@ -555,11 +576,13 @@ def _ssm_backward(handle, dev, code, dy, x, dt, A, B, C, D, dt_bias, h0, dhT, so
         grads = _strides(dx, "dx")
         if T > 1 and any(_strides(t, name) != grads for t, name in ((dB, "dB"), (dC, "dC"))):
             raise ValueError("dx, dB and dC must have the same strides between batches and tokens")
+        _side_by_side(dxbc, grads, b, T)
+    ins += dxbc
     ddt = _out(ddt, "ddt", dev, (b, T, H), dt.dtype, ins)
-    dA = _out(dA, "dA", dev, (H,), torch.float32, ins)
-    dD = None if D is None else _out(dD, "dD", dev, (H,), torch.float32, ins)
-    ddt_bias = None if dt_bias is None else _out(ddt_bias, "ddt_bias", dev, (H,), torch.float32, ins)
-    dh0 = None if h0 is None else _out(dh0, "dh0", dev, st, torch.float32, ins)
+    dA = _out(dA, "dA", dev, (H,), torch.float32, ins + (ddt,))
+    dD = None if D is None else _out(dD, "dD", dev, (H,), torch.float32, ins + (ddt, dA))
+    ddt_bias = None if dt_bias is None else _out(ddt_bias, "ddt_bias", dev, (H,), torch.float32, ins + (ddt, dA, dD))
+    dh0 = None if h0 is None else _out(dh0, "dh0", dev, st, torch.float32, ins + (ddt, dA, dD, ddt_bias))
     pr, need = _problem(SsmProblem, "gdn_workspace_bytes_ssm_backward", b, T, H, P, N, G, *_strides(x, "x"),
                         *_bc_strides(B, C), *_strides(dt, "dt"), *grads, n, code, _CODE[dt.dtype], softplus)
     workspace, size = _workspace(need, dev, workspace)

@@ -26,7 +26,8 @@
  * alignment in the norm and the convolution (rows of four aligned elements
  * take a faster path); the scan's x, B and C rows must be 16-byte aligned and
  * not overlap.  Strides between tokens are 0 <= stride <= 2^22 (2^23 in the
- * convolution).
+ * convolution).  A problem whose launches would have 2^32 threads or more is
+ * GDN_ERR_UNSUPPORTED (the norm's forward splits its rows instead).
  */
 #ifndef LIBGDN_LAYER_H
 #define LIBGDN_LAYER_H
@@ -67,7 +68,7 @@ typedef struct gdn_norm_problem {
  *   scales [rows, ceil(D / group)] (one column for group 0) fp32.  A NaN
  *   stays a NaN in y and does not enter the scale.  For other types scales
  *   is not used and may be NULL.
- * One launch.
+ * One launch (for every 2^22 rows).
  */
 gdn_status gdn_norm_forward(const gdn_norm_problem *problem, const void *x, const void *residual,
                             const void *weight, void *y, void *s, float *scales, void *stream);
@@ -160,7 +161,9 @@ gdn_status gdn_conv_step(const gdn_conv_problem *problem, const void *x, const v
  * with dt_t = softplus(raw_t + dt_bias) or raw_t + dt_bias, A <= 0 and D per
  * head, and B_t, C_t [N] shared by the H / G heads of a group: the gated
  * recurrence of gdn_forward (q = C, k = B, v = dt x, g = dt A) without its
- * erase term.
+ * erase term.  Tokens are worked on 64 at a time from a sequence's first: a NaN
+ * or an infinity in one of them reaches those of the same 64 before it too, but
+ * neither earlier ones nor another sequence.
  */
 typedef struct gdn_ssm_problem {
     int64_t B, T, H, P, N, G; /* P, N in {64, 128}; H a multiple of G */

@@ -144,6 +144,31 @@ def test_empty_and_refused():
             bad()
 
 
+def test_more_rows_than_a_launch_takes():
+    rows, D = (1 << 22) + 5, 8
+    x, res = rnd(rows, D, seed=1, dtype=BF), rnd(rows, D, seed=2, dtype=BF)
+    w = rnd(D, seed=3) + 1.0
+    y, s, _ = gdn.norm_forward(x, w, res)
+    q, t, scales = gdn.norm_forward(x, w, res, out_dtype=torch.float8_e4m3fn, group=128)
+    # each row is its own: those of a second launch and of the first are what
+    # they are among few
+    for at in (slice(0, 64), slice((1 << 22) - 3, rows)):
+        a, b, _ = gdn.norm_forward(x[at], w, res[at])
+        assert torch.equal(y[at], a) and torch.equal(s[at], b) and torch.equal(t[at], b)
+        a, _, b = gdn.norm_forward(x[at], w, res[at], out_dtype=torch.float8_e4m3fn, group=128)
+        assert torch.equal(q[at].view(torch.uint8), a.view(torch.uint8)) and torch.equal(scales[at], b)
+
+
+def test_overlapping_arguments_refused():
+    x, w = rnd(4, 64, seed=1), torch.ones(64, device=DEV)
+    with pytest.raises(ValueError):                 # every second element of a buffer
+        gdn.norm_forward(rnd(128, seed=1)[::2], w)
+    with pytest.raises(ValueError):                 # s may be the residual, but not x too
+        gdn.norm_forward(x, w, x, s=x)
+    with pytest.raises(ValueError):                 # ds may be dres, but not dy too
+        gdn.norm_backward(x, x + 1, w, x, ds=x)
+
+
 def test_gradient_against_differences():
     """fp32 along a direction: the loss, summed in 64 bits from fp32 outputs, is
     known to 2^-18 of its terms (see above), a difference over 2 * 2^-8 so to

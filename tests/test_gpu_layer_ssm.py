@@ -246,6 +246,48 @@ def test_weak_gates_behind_strong_ones():
     close(hT, rT, Z * 2.0 ** -18, "hT")
 
 
+def test_a_gate_that_clears_the_state():
+    """A token whose decay is e^-1e20 clears the state; the decays of the tokens
+    behind it are those without it."""
+    T, H, P, N = 150, 1, 64, 64
+    d = inputs(1, T, H, P, N, 1, F32, F32, 1, True)
+    d["A"], d["dt_bias"], d["D"] = torch.tensor([-1.0], device=DEV), None, None
+    d["dt"] = rnd(1, T, H, seed=5).abs() * 0.02
+    at = 70
+    alone = {k: (v[:, at + 1:] if k in ("x", "dt", "B", "C") else v) for k, v in d.items()}
+    alone["x"], alone["h0"] = alone["x"].contiguous(), None
+    d["dt"][:, at] = 1e20
+    d["x"] = d["x"].clone()
+    d["x"][:, at] = 0.0
+    y, hT = forward(d, dt_softplus=False)
+    ref, rT = forward(alone, dt_softplus=False)
+    step, _ = L.step_sizes(flat(alone["dt"]), None, False)
+    Y, Z = L.ssm(flat(alone["x"]), step, d["A"], flat(alone["B"]), flat(alone["C"]), None, None, [T - at - 1], absolute=True)
+    close(flat(y[:, at + 1:]), flat(ref).double().cpu(), Y * 2.0 ** -15, "y")
+    close(hT, rT.double().cpu(), Z * 2.0 ** -15, "hT")
+
+
+@pytest.mark.parametrize("name", ["x", "B", "C", "dt"])
+def test_a_nan_reaches_its_chunk_and_what_follows(name):
+    """...and neither the chunks before it nor another sequence."""
+    lens, H, P, N = [150, 90], 2, 64, 64
+    d = inputs(1, 240, H, P, N, 1, BF, BF, 2, True)
+    cu = offsets(lens)
+    dy = rnd(1, 240, H, P, seed=8, dtype=BF)
+    names = ("x", "dt", "A", "B", "C", "D", "dt_bias", "h0")
+    y, hT = forward(d, cu_seqlens=cu)
+    g = gdn.ssm_backward(dy, *(d[k] for k in names), cu_seqlens=cu)
+    d[name] = d[name].clone() if name in ("x", "dt") else d[name]
+    d[name][:, 70] = float("nan")
+    z, kT = forward(d, cu_seqlens=cu)
+    h = gdn.ssm_backward(dy, *(d[k] for k in names), cu_seqlens=cu)
+    assert torch.equal(z[:, :64], y[:, :64]) and torch.equal(z[:, 150:], y[:, 150:]) and torch.equal(kT[1], hT[1])
+    assert z[:, 70].isnan().any()
+    for k in (0, 1, 3, 4):
+        assert torch.equal(h[k][:, 150:], g[k][:, 150:])
+    assert torch.equal(h[7][1], g[7][1])
+
+
 def test_rows_behind_the_sequences_and_malformed_offsets():
     lens, T, H, P, N = [30, 0, 100], 160, 2, 64, 64
     d = inputs(1, T, H, P, N, 1, BF, BF, 3, True)
@@ -388,3 +430,25 @@ def test_given_workspace_and_outputs():
     a = gdn.ssm_backward(dy, *(d[k] for k in names))
     b = gdn.ssm_backward(dy, *(d[k] for k in names), workspace=torch.full((1 << 25,), 0xff, device=DEV, dtype=torch.uint8))
     assert all(torch.equal(u, v) for u, v in zip(a, b))
+
+
+def test_gradients_that_overlap_are_refused():
+    b, T, H, P, N, G = 2, 70, 2, 64, 64, 1
+    d = inputs(b, T, H, P, N, G, BF, BF, 1, False)
+    dy = rnd(b, T, H, P, seed=8, dtype=BF)
+    names = ("x", "dt", "A", "B", "C", "D", "dt_bias", "h0")
+    run = lambda *g: gdn.ssm_backward(dy, *(d[k] for k in names), dx=g[0], dB=g[1], dC=g[2])  # noqa: E731
+    new = lambda w: torch.empty(b, T, w, device=DEV, dtype=BF)  # noqa: E731
+    part = lambda t, at, heads, n: t[..., at:at + heads * n].unflatten(-1, (heads, n))  # noqa: E731
+    ref = gdn.ssm_backward(dy, *(d[k] for k in names))
+    both = new(256)
+    got = run(part(both, 0, H, P), part(both, 128, G, N), part(both, 192, G, N))
+    wide = [new(256) for _ in range(3)]                      # or three buffers
+    also = run(*(part(t, 0, h, 64) for t, h in zip(wide, (H, G, G))))
+    for k in (0, 3, 4):
+        assert torch.equal(got[k], ref[k]) and torch.equal(also[k], ref[k])
+    for at in ((0, 64, 192), (0, 128, 128), (64, 128, 0), (0, 128, 160)):
+        with pytest.raises(ValueError):
+            run(part(both, at[0], H, P), part(both, at[1], G, N), part(both, at[2], G, N))
+    with pytest.raises(ValueError):
+        run(part(wide[0], 0, H, P), part(wide[1], 0, G, N), part(wide[1], 64 - 8, G, N))

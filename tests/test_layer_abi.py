@@ -208,6 +208,18 @@ def test_ssm_problems_refused(lib, field, value, status):
     assert lib.gdn_workspace_bytes_ssm_backward(ctypes.byref(pr)) == 0
 
 
+def test_launches_of_too_many_threads_refused(lib):
+    # 2^32 threads in a launch: runs of 32 tokens a wave; heads and their blocks a workgroup
+    assert conv_forward(lib, conv_problem(B=2, T=1 << 30, D=1)) == UNSUPPORTED
+    assert conv_step(lib, conv_problem(B=1 << 24, T=1, D=200), n=1 << 24) == UNSUPPORTED
+    many = ssm_problem(B=1 << 20, T=1, H=64, G=1, x_stride_t=64 * 64, dxbc_stride_t=64 * 64)
+    assert ssm_forward(lib, many) == UNSUPPORTED and ssm_backward(lib, many) == UNSUPPORTED
+    assert ssm_step(lib, many, n=1 << 20) == UNSUPPORTED
+    assert lib.gdn_workspace_bytes_ssm(ctypes.byref(many)) == 0
+    # a problem under them has a workspace
+    assert lib.gdn_workspace_bytes_ssm_backward(ctypes.byref(ssm_problem(B=1 << 14, T=1, H=64, G=1, x_stride_t=64 * 64))) > 0
+
+
 def test_ssm_overlapping_rows_refused(lib):
     # a token's row would reach into the next one's
     assert ssm_forward(lib, ssm_problem(x_stride_t=128)) == UNSUPPORTED
