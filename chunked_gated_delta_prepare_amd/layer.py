@@ -137,7 +137,7 @@ def _on(device, stream, work, *args):
     handle is the stream's."""
     index = device.index
     if stream is None:
-        if torch.cuda.current_device() == index:
+        if torch._C._cuda_getDevice() == index:
             return work(torch._C._cuda_getCurrentRawStream(index), *args)
         with torch.cuda.device(index):
             return work(torch._C._cuda_getCurrentRawStream(index), *args)
@@ -178,9 +178,13 @@ def _workspace(need, device, workspace):
     return workspace, (0 if workspace is None else workspace.numel() * workspace.element_size())
 
 
-def _out(t, name, device, shape, dtype, inputs):
+def _out(t, name, device, shape, dtype, inputs, like=None):
+    """A given output, checked, or a new one; like: a tensor of its shape, if there
+    is one (a call less to torch's slower ways)."""
     if t is None:
-        return torch.empty(shape, device=device, dtype=dtype)
+        if like is not None and like.is_contiguous():
+            return torch.empty_like(like, dtype=dtype)
+        return torch.empty(tuple(shape), device=device, dtype=dtype)
     _check(t, name, device, shape, dtype)
     _apart(t, name, *inputs)
     return t
@@ -246,7 +250,7 @@ def _norm_forward(handle, dev, code, x, weight, residual, eps, od, group, y, s, 
         if merged is None:
             raise ValueError("x's rows must be contiguous and lie at one stride")
         rows, stride = merged
-    y = _out(y, "y", dev, shape, od, (x, weight, residual))
+    y = _out(y, "y", dev, shape, od, (x, weight, residual), x)
     scode = code
     if residual is not None:
         scode = _CODE[residual.dtype]
@@ -254,7 +258,7 @@ def _norm_forward(handle, dev, code, x, weight, residual, eps, od, group, y, s, 
             _check(s, "s", dev, shape, residual.dtype)
             _apart(s, "s", x, weight, y)
         else:
-            s = _out(s, "s", dev, shape, residual.dtype, (x, weight, residual, y))
+            s = _out(s, "s", dev, shape, residual.dtype, (x, weight, residual, y), residual)
     else:
         s = None
     if od is _FP8:
@@ -298,13 +302,13 @@ def _norm_backward(handle, dev, code, dy, s, weight, dres, eps, ds, dx, dweight,
         _check(ds, "ds", dev, shape, s.dtype)
         _apart(ds, "ds", *ins)
     else:
-        ds = _out(ds, "ds", dev, shape, s.dtype, ins + (dres,))
+        ds = _out(ds, "ds", dev, shape, s.dtype, ins + (dres,), s)
     if s.dtype is dy.dtype:
         if dx is not None and dx is not ds:
             raise ValueError("dx is ds where x and s have one type")
         dx = None
     else:
-        dx = _out(dx, "dx", dev, shape, dy.dtype, ins + (dres, ds))
+        dx = _out(dx, "dx", dev, shape, dy.dtype, ins + (dres, ds), dy)
     dweight = _out(dweight, "dweight", dev, shape[-1:], torch.float32, ins + (dres, ds, dx))
     pr, need = _problem(NormProblem, "gdn_workspace_bytes_norm_backward", dy.numel() // D, D, D, code, _CODE[s.dtype],
                         _CODE[weight.dtype], code, 0, eps)
@@ -382,9 +386,9 @@ def _conv_forward(handle, dev, code, x, weight, bias, silu, initial_state, cu_se
     B, T, D = x.shape
     W = weight.shape[1]
     ins = (x, weight, bias, initial_state, cu_seqlens)
-    y = _out(y, "y", dev, x.shape, x.dtype, ins)
+    y = _out(y, "y", dev, x.shape, x.dtype, ins, x)
     if final_state is not None or want:
-        final_state = _out(final_state, "final_state", dev, (n or B, W - 1, D), x.dtype, ins + (y,))
+        final_state = _out(final_state, "final_state", dev, (n or B, W - 1, D), x.dtype, ins + (y,), initial_state)
     pr, _ = _problem(ConvProblem, None, B, T, D, W, *_strides(x, "x"), 0, 0, n, code, _CODE[weight.dtype], silu)
     _call("gdn_conv_forward", pr, _ptr(x), _ptr(weight), _ptr(bias), _ptr(initial_state), _ptr(cu_seqlens), _ptr(y),
           _ptr(final_state), handle)
@@ -412,7 +416,7 @@ def _conv_backward(handle, dev, code, dy, x, weight, bias, silu, initial_state, 
     B, T, D = x.shape
     W = weight.shape[1]
     ins = (dy, x, weight, bias, initial_state, cu_seqlens, dfinal)
-    dx = _out(dx, "dx", dev, x.shape, x.dtype, ins)
+    dx = _out(dx, "dx", dev, x.shape, x.dtype, ins, x)
     dweight = _out(dweight, "dweight", dev, (D, W), torch.float32, ins + (dx,))
     dbias = None if bias is None else _out(dbias, "dbias", dev, (D,), torch.float32, ins + (dx, dweight))
     dinitial = None if initial_state is None else _out(dinitial, "dinitial", dev, initial_state.shape, x.dtype,
@@ -446,7 +450,7 @@ def conv_step(x, state, weight, bias=None, *, activation="silu", slots=None, y=N
 
 def _conv_step(handle, dev, code, x, state, weight, bias, silu, slots, y):
     B, D = x.shape
-    y = _out(y, "y", dev, (B, D), x.dtype, (x, weight, bias, state, slots))
+    y = _out(y, "y", dev, (B, D), x.dtype, (x, weight, bias, state, slots), x)
     if B:
         pr, _ = _problem(ConvProblem, None, B, 1, D, weight.shape[1], x.stride(0) if B > 1 else D, D, 0, 0, 0, code,
                          _CODE[weight.dtype], silu)
@@ -506,9 +510,9 @@ def ssm_forward(x, dt, A, B, C, D=None, dt_bias=None, h0=None, *, dt_softplus=Tr
 
 def _ssm_forward(handle, dev, code, x, dt, A, B, C, D, dt_bias, h0, softplus, cu_seqlens, n, st, y, hT, want, workspace):
     ins = (x, dt, A, B, C, D, dt_bias, h0, cu_seqlens)
-    y = _out(y, "y", dev, x.shape, x.dtype, ins)
+    y = _out(y, "y", dev, x.shape, x.dtype, ins, x)
     if hT is not None or want:
-        hT = _out(hT, "hT", dev, st, torch.float32, ins + (y,))
+        hT = _out(hT, "hT", dev, st, torch.float32, ins + (y,), h0)
     pr, need = _problem(SsmProblem, "gdn_workspace_bytes_ssm", *x.shape, B.shape[3], B.shape[2], *_strides(x, "x"),
                         *_bc_strides(B, C), *_strides(dt, "dt"), 0, 0, n, code, _CODE[dt.dtype], softplus)
     workspace, size = _workspace(need, dev, workspace)
@@ -579,10 +583,10 @@ def _ssm_backward(handle, dev, code, dy, x, dt, A, B, C, D, dt_bias, h0, dhT, so
         _side_by_side(dxbc, grads, b, T)
     ins += dxbc
     ddt = _out(ddt, "ddt", dev, (b, T, H), dt.dtype, ins)
-    dA = _out(dA, "dA", dev, (H,), torch.float32, ins + (ddt,))
-    dD = None if D is None else _out(dD, "dD", dev, (H,), torch.float32, ins + (ddt, dA))
-    ddt_bias = None if dt_bias is None else _out(ddt_bias, "ddt_bias", dev, (H,), torch.float32, ins + (ddt, dA, dD))
-    dh0 = None if h0 is None else _out(dh0, "dh0", dev, st, torch.float32, ins + (ddt, dA, dD, ddt_bias))
+    dA = _out(dA, "dA", dev, (H,), torch.float32, ins + (ddt,), A)
+    dD = None if D is None else _out(dD, "dD", dev, (H,), torch.float32, ins + (ddt, dA), A)
+    ddt_bias = None if dt_bias is None else _out(ddt_bias, "ddt_bias", dev, (H,), torch.float32, ins + (ddt, dA, dD), A)
+    dh0 = None if h0 is None else _out(dh0, "dh0", dev, st, torch.float32, ins + (ddt, dA, dD, ddt_bias), h0)
     pr, need = _problem(SsmProblem, "gdn_workspace_bytes_ssm_backward", b, T, H, P, N, G, *_strides(x, "x"),
                         *_bc_strides(B, C), *_strides(dt, "dt"), *grads, n, code, _CODE[dt.dtype], softplus)
     workspace, size = _workspace(need, dev, workspace)
@@ -621,7 +625,7 @@ def _row_stride(t, name):
 
 def _ssm_step(handle, dev, code, x, dt, A, B, C, state, D, dt_bias, softplus, slots, y):
     b, H, P = x.shape
-    y = _out(y, "y", dev, x.shape, x.dtype, (x, dt, A, B, C, D, dt_bias, slots, state))
+    y = _out(y, "y", dev, x.shape, x.dtype, (x, dt, A, B, C, D, dt_bias, slots, state), x)
     if b:
         G, N = B.shape[1:]
         sb = _row_stride(B, "B")
