@@ -11,6 +11,11 @@
 // window is loaded anew from the next sequence's state where one begins.
 // States are a copy of W - 1 rows, done by workgroups of their own behind the
 // runs.
+// Runs of 32 tokens, rows eight ahead in flight: 16384 packed tokens of 10240
+// channels in bf16 133 us (5.1 TB/s; 211 us without rows in flight); 2 x 8192
+// tokens of 6144 channels 73 us forward (5.5 TB/s, part of it out of the last
+// cache) and 139 us backward (4.4 TB/s); a token for 64 rows of 10240 channels
+// 4.7 us, a launch's own time.
 #include "gdn_layer.h"
 
 namespace gdn {
@@ -92,8 +97,8 @@ __device__ __forceinline__ rsrc_t row_of(const void *base, int64_t elems, int D)
 }
 
 // (the reciprocal is good to one unit in the last place; a division proper
-// costs ten instructions, which with the exponential made the kernels bound by
-// arithmetic: 249 -> 180 us forward at 16384 tokens, 10240 channels)
+// costs ten instructions: with it and a descriptor per row the forward pass of
+// 16384 tokens, 10240 channels took 249 us, without 211)
 __device__ __forceinline__ float sigmoid(float v) { return __builtin_amdgcn_rcpf(1.f + fast_exp2(v * -kLog2e)); }
 
 // A lane's VEC columns in rows at one stride: a descriptor at the first row,

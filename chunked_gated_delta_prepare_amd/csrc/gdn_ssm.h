@@ -546,16 +546,20 @@ __device__ __forceinline__ float segments_before(const SsmParams &p, const Segme
 // The products of a state that is an output or another segment's start take
 // w v in three bf16 parts (relative error 2^-27): with two the final state was
 // 2.4e-6 off, against 1e-7 of fp32 arithmetic throughout, and dA, a sum over
-// all tokens of both signs, 5e-5.  Where only out1 is read from the state (an output state comes
-// from the segments' end states if there are any), w v is rounded once to
-// bf16, as out1's other operands are and out1 itself, and S too before it is
-// multiplied.  The next chunk's rows are in flight while one is worked on, and
-// its gates are formed by the waves with the fewest blocks.
+// all tokens of both signs, 5e-5.  Where only out1 is read from the state (an
+// output state comes from the segments' end states if there are any), w v is
+// rounded once to bf16, as out1's other operands are and out1 itself, and S too
+// before it is multiplied.  The next chunk's rows are in flight while one is
+// worked on, and the gates of several chunks are formed at a time, one a wave.
 // ENDS: only the state, from a zero start, to the workspace.
 //
-// Sixteen columns a wave, eight waves for 128 columns: with 32 columns a wave
-// and four waves the kernel read a third less from LDS but held 375
-// registers a lane, one wave per SIMD (1.8 ms at 65536 tokens, 64 heads).
+// Sixteen columns a wave, eight waves for 128 columns, two workgroups a CU: with
+// 32 columns a wave and four waves the kernel read a third less from LDS but
+// held 375 registers a lane, one wave per SIMD (65536 tokens, 64 heads of 128 x
+// 128: 1.8 ms against 1.3 ms for both launches, of 2.4 GB of rows and 774 GFLOP
+// on the matrix cores).  What bounds it: some 390 vector instructions a wave and
+// chunk (decays, roundings, the state's scaling) fill half of the time, waiting
+// for LDS a third.
 // ---------------------------------------------------------------------------
 template <typename IO, int N, int COLS, int NH, bool ENDS, bool REV>
 __global__ void __launch_bounds__(4 * COLS, sizeof(IO) == 4 ? 1 : COLS == 64 && N == 128 ? 3 : 4) ssm_scan_kernel(SsmParams p) {

@@ -25,6 +25,12 @@ namespace gdn {
 // products to 3e-8 of X a chunk, always the same way: over 16384 tokens dA was
 // 2.6e-6 and d(dt_bias) 4.9e-6 off.  With the sign alternating the chunks'
 // shares cancel (4.7e-7 and 1.9e-6).
+//
+// 2 x 8192 tokens, 32 heads of 128 x 128: 230 to 260 us in either direction, of
+// which the products are 100 us at a large product's rate and the 268 MB that
+// the heads leave for ssm_sum_kernel 55 us at a copy's.  A group's heads do not
+// fit one workgroup (a state is 64 KB of registers), and atomic sums would
+// depend on their order.
 // ---------------------------------------------------------------------------
 template <typename IO, int N, int COLS, int NH, bool REV>
 __global__ void __launch_bounds__(4 * N, sizeof(IO) == 4 ? 1 : NH == 1 && N == 128 ? 4 : 2) ssm_key_kernel(SsmParams p) {
@@ -330,6 +336,8 @@ __global__ void __launch_bounds__(4 * N) ssm_sum_kernel(SsmParams p) {
 
 // The gradients of a segment's gates, one head a workgroup, a chunk a wave
 // (see gdn_ssm.h): ddt_t = c_t + A dg_t, through softplus; dA += dt_t dg_t.
+// 21 us at 2 x 8192 tokens, 32 heads: six rows of floats a head and two barriers
+// for every four chunks.
 struct GateParams {
     SsmParams s;                          // the forward scan's
     const float *c_inside, *c_across;     // the reverse scan's sums
