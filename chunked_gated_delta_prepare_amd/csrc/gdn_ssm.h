@@ -525,8 +525,9 @@ template <bool REV, typename F>
 __device__ __forceinline__ float segments_before(const SsmParams &p, const Segment &s, int hb, int nh, int hh, F f) {
     double d = 0.0;
     const int per = (s.seq_end - s.seq_begin + p.seg_tokens - 1) / p.seg_tokens;
-    const int stop = REV ? s.first + per : s.first - 1;
-    for (int i = REV ? s.item + 1 : s.item - 1; i != stop && (REV ? i < stop : i > stop); i += REV ? 1 : -1) {
+    // (overlapping sequences have more segments than there are places)
+    const int stop = REV ? (s.first + per < p.n_items ? s.first + per : p.n_items) : s.first - 1;
+    for (int i = REV ? s.item + 1 : s.item - 1; REV ? i < stop : i > stop; i += REV ? 1 : -1) {
         const int64_t at = (int64_t)i * p.n_hb + hb;
         f(at, fast_exp2((float)d));
         d += p.total[at * nh + hh];

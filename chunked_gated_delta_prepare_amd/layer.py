@@ -329,15 +329,16 @@ def _silu(activation):
 
 
 def _strides(t, name):
-    """(batch, token) strides of [B, T, ...] whose other dimensions are dense."""
+    """(batch, token) strides of [B, T, D] or [B, T, H, D] whose tokens are dense."""
     shape, strides = t.shape, t.stride()
-    want = 1
-    for i in range(len(shape) - 1, 1, -1):
-        n = shape[i]
-        if strides[i] != want and n != 1 and t.numel():
-            raise ValueError("%s must be contiguous behind its token dimension" % name)
-        want *= n
-    return (strides[0] if shape[0] != 1 else 0), (strides[1] if shape[1] != 1 else want)
+    row = shape[-1]
+    dense = row == 1 or strides[-1] == 1
+    if len(shape) == 4:
+        dense = dense and (shape[2] == 1 or strides[2] == row)
+        row *= shape[2]
+    if not dense and t.numel():
+        raise ValueError("%s must be contiguous behind its token dimension" % name)
+    return (strides[0] if shape[0] != 1 else 0), (strides[1] if shape[1] != 1 else row)
 
 
 def _packed(cu, dev, B):

@@ -312,7 +312,9 @@ def test_rows_behind_the_sequences_and_malformed_offsets():
         same = u[:, :130] if u.dim() > 1 and u.shape[:2] == (1, T) else u
         assert torch.equal(same, v) and v.isfinite().all()
     assert one[:, 130:].eq(7.0).all() and grads["dt"][:, 130:].eq(7.0).all()
-    for bad in ([0, 1000, 160], [-5, 60, 20, 160], [150, 10], [2 ** 31 - 1, -2 ** 31]):
+    # (the last two: more segments than a list in order can have)
+    for bad, T in (([0, 1000, 160], T), ([-5, 60, 20, 160], T), ([150, 10], T), ([2 ** 31 - 1, -2 ** 31], T),
+                   ([0, 1100, 0, 1100], 1100), ([0, 3000, 0, 3000, 0, 3000, 0, 3000], 3000)):
         m = inputs(1, T, H, P, N, 1, BF, BF, len(bad) - 1, True)
         off = torch.tensor(bad, device=DEV, dtype=torch.int32)
         forward(m, cu_seqlens=off)
