@@ -88,7 +88,7 @@ def _function(name):
 
 
 def _call(name, *args):
-    rc = _function(name)(*args)
+    rc = (_functions.get(name) or _function(name))(*args)
     if rc != 0:
         from . import GdnError, load_library
         raise GdnError(name, rc, load_library().gdn_status_str(rc).decode())
@@ -267,7 +267,7 @@ def _norm_forward(handle, dev, code, x, weight, residual, eps, od, group, y, s, 
     else:
         scales = None
     pr, _ = _problem(NormProblem, None, rows, D, stride, code, scode, _CODE[weight.dtype], _CODE[od], group, eps)
-    _call("gdn_norm_forward", pr, _ptr(x), _ptr(residual), _ptr(weight), _ptr(y), _ptr(s), _ptr(scales), handle)
+    _call("gdn_norm_forward", pr, x.data_ptr(), _ptr(residual), weight.data_ptr(), y.data_ptr(), _ptr(s), _ptr(scales), handle)
     return y, s, scales
 
 
@@ -313,7 +313,7 @@ def _norm_backward(handle, dev, code, dy, s, weight, dres, eps, ds, dx, dweight,
     pr, need = _problem(NormProblem, "gdn_workspace_bytes_norm_backward", dy.numel() // D, D, D, code, _CODE[s.dtype],
                         _CODE[weight.dtype], code, 0, eps)
     workspace, size = _workspace(need, dev, workspace)
-    _call("gdn_norm_backward", pr, _ptr(dy), _ptr(s), _ptr(weight), _ptr(dres), _ptr(ds), _ptr(dx), _ptr(dweight),
+    _call("gdn_norm_backward", pr, dy.data_ptr(), s.data_ptr(), weight.data_ptr(), _ptr(dres), ds.data_ptr(), _ptr(dx), dweight.data_ptr(),
           _ptr(workspace), size, handle)
     return ds, ds if dx is None else dx, dweight
 
@@ -391,7 +391,7 @@ def _conv_forward(handle, dev, code, x, weight, bias, silu, initial_state, cu_se
     if final_state is not None or want:
         final_state = _out(final_state, "final_state", dev, (n or B, W - 1, D), x.dtype, ins + (y,), initial_state)
     pr, _ = _problem(ConvProblem, None, B, T, D, W, *_strides(x, "x"), 0, 0, n, code, _CODE[weight.dtype], silu)
-    _call("gdn_conv_forward", pr, _ptr(x), _ptr(weight), _ptr(bias), _ptr(initial_state), _ptr(cu_seqlens), _ptr(y),
+    _call("gdn_conv_forward", pr, x.data_ptr(), weight.data_ptr(), _ptr(bias), _ptr(initial_state), _ptr(cu_seqlens), y.data_ptr(),
           _ptr(final_state), handle)
     return y, final_state
 
@@ -425,8 +425,8 @@ def _conv_backward(handle, dev, code, dy, x, weight, bias, silu, initial_state, 
     pr, need = _problem(ConvProblem, "gdn_workspace_bytes_conv_backward", B, T, D, W, *_strides(x, "x"), *_strides(dy, "dy"),
                         n, code, _CODE[weight.dtype], silu)
     workspace, size = _workspace(need, dev, workspace)
-    _call("gdn_conv_backward", pr, _ptr(dy), _ptr(x), _ptr(weight), _ptr(bias), _ptr(initial_state), _ptr(cu_seqlens),
-          _ptr(dfinal), _ptr(dx), _ptr(dweight), _ptr(dbias), _ptr(dinitial), _ptr(workspace), size, handle)
+    _call("gdn_conv_backward", pr, dy.data_ptr(), x.data_ptr(), weight.data_ptr(), _ptr(bias), _ptr(initial_state), _ptr(cu_seqlens),
+          _ptr(dfinal), dx.data_ptr(), dweight.data_ptr(), _ptr(dbias), _ptr(dinitial), _ptr(workspace), size, handle)
     return dx, dweight, dbias, dinitial
 
 
@@ -455,7 +455,7 @@ def _conv_step(handle, dev, code, x, state, weight, bias, silu, slots, y):
     if B:
         pr, _ = _problem(ConvProblem, None, B, 1, D, weight.shape[1], x.stride(0) if B > 1 else D, D, 0, 0, 0, code,
                          _CODE[weight.dtype], silu)
-        _call("gdn_conv_step", pr, _ptr(x), _ptr(weight), _ptr(bias), _ptr(state), _ptr(slots), state.shape[0], _ptr(y),
+        _call("gdn_conv_step", pr, x.data_ptr(), weight.data_ptr(), _ptr(bias), state.data_ptr(), _ptr(slots), state.shape[0], y.data_ptr(),
               handle)
     return y
 
@@ -517,8 +517,8 @@ def _ssm_forward(handle, dev, code, x, dt, A, B, C, D, dt_bias, h0, softplus, cu
     pr, need = _problem(SsmProblem, "gdn_workspace_bytes_ssm", *x.shape, B.shape[3], B.shape[2], *_strides(x, "x"),
                         *_bc_strides(B, C), *_strides(dt, "dt"), 0, 0, n, code, _CODE[dt.dtype], softplus)
     workspace, size = _workspace(need, dev, workspace)
-    _call("gdn_ssm_forward", pr, _ptr(x), _ptr(dt), _ptr(A), _ptr(B), _ptr(C), _ptr(D), _ptr(dt_bias), _ptr(h0),
-          _ptr(cu_seqlens), _ptr(y), _ptr(hT), _ptr(workspace), size, handle)
+    _call("gdn_ssm_forward", pr, x.data_ptr(), dt.data_ptr(), A.data_ptr(), B.data_ptr(), C.data_ptr(), _ptr(D), _ptr(dt_bias), _ptr(h0),
+          _ptr(cu_seqlens), y.data_ptr(), _ptr(hT), _ptr(workspace), size, handle)
     return y, hT
 
 
@@ -591,8 +591,8 @@ def _ssm_backward(handle, dev, code, dy, x, dt, A, B, C, D, dt_bias, h0, dhT, so
     pr, need = _problem(SsmProblem, "gdn_workspace_bytes_ssm_backward", b, T, H, P, N, G, *_strides(x, "x"),
                         *_bc_strides(B, C), *_strides(dt, "dt"), *grads, n, code, _CODE[dt.dtype], softplus)
     workspace, size = _workspace(need, dev, workspace)
-    _call("gdn_ssm_backward", pr, _ptr(dy), _ptr(x), _ptr(dt), _ptr(A), _ptr(B), _ptr(C), _ptr(D), _ptr(dt_bias), _ptr(h0),
-          _ptr(cu_seqlens), _ptr(dhT), _ptr(dx), _ptr(ddt), _ptr(dA), _ptr(dB), _ptr(dC), _ptr(dD), _ptr(ddt_bias),
+    _call("gdn_ssm_backward", pr, dy.data_ptr(), x.data_ptr(), dt.data_ptr(), A.data_ptr(), B.data_ptr(), C.data_ptr(), _ptr(D), _ptr(dt_bias), _ptr(h0),
+          _ptr(cu_seqlens), _ptr(dhT), dx.data_ptr(), ddt.data_ptr(), dA.data_ptr(), dB.data_ptr(), dC.data_ptr(), _ptr(dD), _ptr(ddt_bias),
           _ptr(dh0), _ptr(workspace), size, handle)
     return dx, ddt, dA, dB, dC, dD, ddt_bias, dh0
 
@@ -634,6 +634,6 @@ def _ssm_step(handle, dev, code, x, dt, A, B, C, state, D, dt_bias, softplus, sl
             raise ValueError("B and C must have the same strides")
         pr, _ = _problem(SsmProblem, None, b, 1, H, P, N, G, _row_stride(x, "x"), H * P, sb, G * N, _row_stride(dt, "dt"), H,
                          0, 0, 0, code, _CODE[dt.dtype], softplus)
-        _call("gdn_ssm_step", pr, _ptr(x), _ptr(dt), _ptr(A), _ptr(B), _ptr(C), _ptr(D), _ptr(dt_bias), _ptr(state),
-              _ptr(slots), state.shape[0], _ptr(y), handle)
+        _call("gdn_ssm_step", pr, x.data_ptr(), dt.data_ptr(), A.data_ptr(), B.data_ptr(), C.data_ptr(), _ptr(D), _ptr(dt_bias), state.data_ptr(),
+              _ptr(slots), state.shape[0], y.data_ptr(), handle)
     return y
