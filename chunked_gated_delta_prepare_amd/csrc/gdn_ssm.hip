@@ -100,9 +100,13 @@ SsmPlan ssm_plan(const gdn_ssm_problem *pr, bool packed) {
     // segments for about 512 workgroups, two a CU, of four chunks or a multiple,
     // and 32 a stream at most (each reads the end states of those before it).
     // For 256, 512 and 1024 workgroups 65536 tokens of 64 heads take 1.48, 1.33
-    // and 1.35 ms, 16384 tokens 401, 348 and 392 us.
+    // and 1.35 ms, 16384 tokens 401, 348 and 392 us.  Packed sequences end
+    // inside a segment, so a quarter more (16384 tokens for 512 and 640: 80 heads
+    // of 64 columns, 9 sequences 303 and 289 us, 3 sequences 321 and 275; 64
+    // heads of 128, 8 sequences 403 and 393).
     const int64_t streams = (int64_t)s.n_hb * (packed ? 1 : pr->B);
-    int64_t per = (512 + streams - 1) / streams;
+    const int64_t wgs = packed ? 640 : 512;
+    int64_t per = (wgs + streams - 1) / streams;
     per = per > 32 ? 32 : per;
     int64_t seg = (chunks + per - 1) / per;
     seg = (seg < 4 ? 4 : seg + 3) / 4 * 4;
