@@ -35,7 +35,9 @@ def close(got, ref, tol, what):
 CASES = [  # rows, D, x type, residual type
     (1, 1, BF, BF), (3, 5, F32, F32), (7, 64, BF, F32), (5, 255, BF, BF), (9, 256, F32, F32), (2, 260, BF, BF),
     (6, 1023, BF, F32), (4, 1024, BF, BF), (3, 2050, F32, F32), (5, 4100, BF, BF), (2, 8192, BF, BF), (3, 8191, BF, F32),
-    (2, 8200, F32, F32), (2, 16384, BF, BF), (2, 16383, BF, BF), (769, 96, BF, BF), (1600, 257, BF, F32)]
+    (2, 8200, F32, F32), (2, 16384, BF, BF), (2, 16383, BF, BF), (769, 96, BF, BF), (1600, 257, BF, F32),
+    (3, 2, BF, F32), (5, 130, BF, BF), (4, 1022, F32, F32), (3, 1030, BF, BF), (3, 4098, BF, F32), (2, 8190, BF, BF),
+    (2, 16382, BF, F32), (1700, 254, BF, BF)]
 
 
 @pytest.mark.parametrize("rows,D,dt,rt", CASES)
@@ -58,12 +60,13 @@ def test_forward_and_backward(rows, D, dt, rt):
     close(ds, rs, rs.abs() * HALF[rt] + size * ARITH, "ds")
     close(dx, rs, rs.abs() * HALF[dt] + size * ARITH, "dx")
     assert (dx is ds) == (dt == rt)
-    # dw: rows / 768 of a workgroup's, then its partial sums in 16 lines
+    # dw: rows / 768 of a workgroup's, then the partial sums in 64 lines
     terms = (dy.cpu().double() * kept * r).abs().sum(0)
     close(dw, rw, terms * (ARITH + (rows / 768 + 64) * 2.0 ** -24), "dw")
 
 
-@pytest.mark.parametrize("rows,D", [(4, 64), (3, 130), (5, 256), (2, 1000), (3, 1001), (2, 8192), (2, 9000)])
+@pytest.mark.parametrize("rows,D", [(4, 64), (3, 130), (5, 256), (2, 1000), (3, 1001), (2, 8192), (2, 9000), (3, 1002),
+                                    (2, 4098), (2, 16382)])
 @pytest.mark.parametrize("group", [0, 128])
 @pytest.mark.parametrize("dt", [BF, F32])
 def test_eight_bit_output(rows, D, group, dt):
