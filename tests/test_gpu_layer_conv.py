@@ -250,3 +250,15 @@ def test_streams_graphs_and_repeats():
         torch.cuda.synchronize()
         kept = [t.clone() for t in out]
         assert all(torch.equal(a, c) for a, c in zip(kept, work())), k
+
+
+def test_slots_behind_32_bit_offsets():
+    S, D, W = 90000, 8192, 4
+    pool = torch.zeros(S, W - 1, D, device=DEV, dtype=BF)
+    assert pool.numel() * 2 > 1 << 32
+    x, w, st = rnd(3, D, seed=1, dtype=BF), rnd(D, W, seed=2, dtype=BF), rnd(3, W - 1, D, seed=3, dtype=BF)
+    slots = torch.tensor([S - 1, 7, 88000], device=DEV, dtype=torch.int32)
+    pool[slots.long()] = st
+    y = gdn.conv_step(x, pool, w, slots=slots)
+    ref = gdn.conv_step(x, st, w)
+    assert torch.equal(y, ref) and torch.equal(pool[slots.long()], st)

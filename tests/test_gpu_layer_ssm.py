@@ -454,3 +454,41 @@ def test_gradients_that_overlap_are_refused():
             run(part(both, at[0], H, P), part(both, at[1], G, N), part(both, at[2], G, N))
     with pytest.raises(ValueError):
         run(part(wide[0], 0, H, P), part(wide[1], 0, G, N), part(wide[1], 64 - 8, G, N))
+
+
+def test_tokens_behind_32_bit_offsets():
+    """More than 2^32 bytes of x: the last tokens are those of a run of their own from
+    the state before them.  Either is off by at most 2 2^-8 of the terms' sizes and a
+    rounding (see above), of which 2^-6 of the result's norm leaves room for both."""
+    T, H, P, N, k = (1 << 17) + 77, 128, 128, 64, 700
+    g = torch.Generator(device=DEV).manual_seed(1)
+    new = lambda *s, dtype=BF: torch.randn(*s, generator=g, device=DEV, dtype=dtype)  # noqa: E731
+    x, dy, B, C = new(1, T, H, P), new(1, T, H, P), new(1, T, 1, N), new(1, T, 1, N)
+    dt, A = new(1, T, H, dtype=F32), -torch.rand(H, generator=g, device=DEV) - 0.1
+    assert x.numel() * 2 > 1 << 32
+    rest = dict(D=new(H, dtype=F32), dt_bias=torch.full((H,), -3.0, device=DEV))
+    y, hT = gdn.ssm_forward(x, dt, A, B, C, **rest)
+    grads = gdn.ssm_backward(dy, x, dt, A, B, C, **rest)
+    _, before = gdn.ssm_forward(x[:, :T - k], dt[:, :T - k], A, B[:, :T - k], C[:, :T - k], **rest)
+    tail = [t[:, T - k:] for t in (x, dt, B, C)]
+    y2, h2 = gdn.ssm_forward(tail[0], tail[1], A, *tail[2:], **rest, h0=before)
+    grads2 = gdn.ssm_backward(dy[:, T - k:], tail[0], tail[1], A, *tail[2:], **rest, h0=before)
+    off = lambda a, b: float((a.float() - b.float()).norm() / b.float().norm())  # noqa: E731
+    assert off(y[:, T - k:], y2) < 2.0 ** -6 and off(hT, h2) < 2.0 ** -12
+    for i in (0, 1, 3, 4):
+        assert off(grads[i][:, T - k:], grads2[i]) < 2.0 ** -6, i
+
+
+def test_slots_behind_32_bit_offsets():
+    S, H, P, N = 1100, 64, 128, 128
+    pool = torch.zeros(S, H, N, P, device=DEV)
+    assert pool.numel() * 4 > 1 << 32
+    d = inputs(3, 1, H, P, N, 8, BF, BF, 3, True)
+    one = {k: d[k][:, 0] for k in ("x", "dt", "B", "C")}
+    slots = torch.tensor([S - 1, 5, 1024], device=DEV, dtype=torch.int32)
+    pool[slots.long()] = d["h0"]
+    small = d["h0"].clone()
+    args = (one["x"], one["dt"], d["A"], one["B"], one["C"])
+    y = gdn.ssm_step(*args, pool, d["D"], d["dt_bias"], slots=slots)
+    ref = gdn.ssm_step(*args, small, d["D"], d["dt_bias"])
+    assert torch.equal(y, ref) and torch.equal(pool[slots.long()], small)
