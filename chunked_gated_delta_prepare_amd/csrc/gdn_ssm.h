@@ -544,7 +544,7 @@ __device__ __forceinline__ float segments_before(const SsmParams &p, const Segme
 //      blocks, dealt to the waves); S^T q on the way
 //   2  out1 = M v + e^cum S^T q, transposed, so that a lane stores four columns
 //   3  S' = e^total S + k^T (w v)
-// The products of a state that is an output or another segment's start take
+// The products of a state that is an output, or the start of the key scans, take
 // w v in three bf16 parts (relative error 2^-27): with two the final state was
 // 2.4e-6 off, against 1e-7 of fp32 arithmetic throughout, and dA, a sum over
 // all tokens of both signs, 5e-5.  Where only out1 is read from the state (an
@@ -552,7 +552,9 @@ __device__ __forceinline__ float segments_before(const SsmParams &p, const Segme
 // rounded once to bf16, as out1's other operands are and out1 itself, and S too
 // before it is multiplied.  The next chunk's rows are in flight while one is
 // worked on, and the gates of several chunks are formed at a time, one a wave.
-// ENDS: only the state, from a zero start, to the workspace.
+// ENDS: only the state, from a zero start, to the workspace; FINE where it feeds
+// more than out1 (65536 tokens, 64 heads of 128 x 128, both launches: 1.37 ms
+// with a final state, 1.13 ms without one).
 //
 // Sixteen columns a wave, eight waves for 128 columns, two workgroups a CU: with
 // 32 columns a wave and four waves the kernel read a third less from LDS but
@@ -562,12 +564,12 @@ __device__ __forceinline__ float segments_before(const SsmParams &p, const Segme
 // chunk (decays, roundings, the state's scaling) fill half of the time, waiting
 // for LDS a third.
 // ---------------------------------------------------------------------------
-template <typename IO, int N, int COLS, int NH, bool ENDS, bool REV>
+template <typename IO, int N, int COLS, int NH, bool ENDS, bool REV, bool FINE = true>
 __global__ void __launch_bounds__(4 * COLS, sizeof(IO) == 4 ? 1 : COLS == 64 && N == 128 ? 3 : 4) ssm_scan_kernel(SsmParams p) {
     typedef SOp<IO> O;
     typedef typename O::elem E;
     constexpr int C = kSsmChunk, NW = COLS / 16, NB = N / 16, kThreads = 4 * COLS, P = COLS / NH;
-    constexpr int kP = O::template kParts<3>;
+    constexpr int kP = O::template kParts<FINE ? 3 : 1>;
     __shared__ __align__(16) E sv[C * COLS], sk[C * N], sq[ENDS ? 8 : C * N], sm[ENDS ? 1 : NH][ENDS ? 8 : C * C];
     // chunks whose gates are formed at once, one chunk and head a wave
     constexpr int GC = NW / NH;

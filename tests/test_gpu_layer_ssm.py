@@ -100,6 +100,10 @@ def test_forward_and_backward(lens, H, P, N, G, dt, dtt, h0, softplus, strong):
     b = dt is BF
     close(flat(y), ref, ref.abs() * HALF[dt] + Y * (2 * 2.0 ** -8 * b + FP), "y")
     close(hT, rT, Z * FP, "hT")
+    # without a final state the segments' starts are rounded like y's other operands
+    alone, none = forward(d, cu_seqlens=cu, dt_softplus=softplus, output_final_state=False)
+    assert none is None
+    close(flat(alone), ref, ref.abs() * HALF[dt] + Y * (2 * 2.0 ** -8 * b + FP), "y without a final state")
 
     dy, dhT = rnd(B, T, H, P, seed=8, dtype=dt), rnd(n, H, N, P, seed=9)
     got = gdn.ssm_backward(dy, d["x"], d["dt"], d["A"], d["B"], d["C"], d["D"], d["dt_bias"], d["h0"], dhT,
