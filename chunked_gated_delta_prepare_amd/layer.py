@@ -530,7 +530,8 @@ def ssm_backward(dy, x, dt, A, B, C, D=None, dt_bias=None, h0=None, dhT=None, *,
     dA, dB, dC, dD, ddt_bias, dh0): dx, dB and dC in x's type, ddt in dt's, the
     others fp32; dD, ddt_bias and dh0 are None where D, dt_bias and h0 are.
     dx, dB and dC may be given as parts of one buffer (with the same strides
-    between tokens), as the gradient of a convolution's output."""
+    between batches and between tokens), as the gradient of a convolution's
+    output."""
     dev, code = _ssm_checks(x, dt, A, B, C, D, dt_bias, 2)
     n = _packed(cu_seqlens, dev, x.shape[0])
     st = (n or x.shape[0], x.shape[2], B.shape[3], x.shape[3])
@@ -579,8 +580,12 @@ def _ssm_backward(handle, dev, code, dy, x, dt, A, B, C, D, dt_bias, h0, dhT, so
             _check(t, name, dev, like.shape, x.dtype, dense=False)
             _apart(t, name, *ins)
         grads = _strides(dx, "dx")
-        if T > 1 and any(_strides(t, name) != grads for t, name in ((dB, "dB"), (dC, "dC"))):
-            raise ValueError("dx, dB and dC must have the same strides between batches and tokens")
+        # (one token has no stride to the next, one batch none to the next: _strides
+        # gives a token's own width and 0 there)
+        for t, name in ((dB, "dB"), (dC, "dC")):
+            sb, stt = _strides(t, name)
+            if t.numel() and (sb != grads[0] or (T > 1 and stt != grads[1])):
+                raise ValueError("dx, dB and dC must have the same strides between batches and tokens")
         _side_by_side(dxbc, grads, b, T)
     ins += dxbc
     ddt = _out(ddt, "ddt", dev, (b, T, H), dt.dtype, ins)

@@ -496,3 +496,28 @@ def test_slots_behind_32_bit_offsets():
     y = gdn.ssm_step(*args, pool, d["D"], d["dt_bias"], slots=slots)
     ref = gdn.ssm_step(*args, small, d["D"], d["dt_bias"])
     assert torch.equal(y, ref) and torch.equal(pool[slots.long()], small)
+
+
+@pytest.mark.parametrize("H,P,N,G,dt", [(4, 64, 64, 1, BF), (2, 128, 64, 2, F32)])
+def test_gradients_of_single_tokens_in_a_batch(H, P, N, G, dt):
+    """T = 1 and several batches: parts of one buffer, which hold what the binding's
+    own outputs do, with nothing written beside them; tensors of their own have no
+    common stride between batches and are refused."""
+    b = 3
+    d = inputs(b, 1, H, P, N, G, dt, dt, b, True)
+    dy = rnd(b, 1, H, P, seed=8, dtype=dt)
+    names = ("x", "dt", "A", "B", "C", "D", "dt_bias", "h0")
+    ref = gdn.ssm_backward(dy, *(d[k] for k in names))
+    step, raw = L.step_sizes(flat(d["dt"]), d["dt_bias"], True)
+    args = (flat(d["x"]), step, d["A"], flat(d["B"]), flat(d["C"]), d["D"], d["h0"], [1] * b)
+    g, a = (L.ssm_grad(flat(dy), *args, None, absolute=k) for k in (False, True))
+    for k, v in (("dx", ref[0]), ("dB", ref[3]), ("dC", ref[4])):
+        close(flat(v), g[k], g[k].abs() * HALF[dt] + a[k] * (2 * 2.0 ** -8 * (dt is BF) + FP), k)
+    wide = torch.full((b, 1, H * P + 2 * G * N + 64), 7.0, device=DEV, dtype=dt)
+    dx, dB, dC, rest = wide.split((H * P, G * N, G * N, 64), -1)
+    one = dict(dx=dx.unflatten(-1, (H, P)), dB=dB.unflatten(-1, (G, N)), dC=dC.unflatten(-1, (G, N)))
+    got = gdn.ssm_backward(dy, *(d[k] for k in names), **one)
+    assert all(torch.equal(u, v) for u, v in zip(got, ref)) and rest.eq(7.0).all()
+    with pytest.raises(ValueError, match="same strides"):
+        gdn.ssm_backward(dy, *(d[k] for k in names), dx=torch.empty_like(dy), dB=torch.empty(b, 1, G, N, device=DEV, dtype=dt),
+                         dC=torch.empty(b, 1, G, N, device=DEV, dtype=dt))
