@@ -235,6 +235,10 @@ gdn_status gdn_ssm_forward(const gdn_ssm_problem *pr, const void *x, const void 
         st = check_ssm_pointers(pr, x, dt, A, Bm, Cm, D, dt_bias, true);
         if (st != GDN_OK) return st;
         if (!y) return GDN_ERR_NULL_ARG;
+    } else if (hT) {
+        // (the scan reads its heads' A, D and bias before it knows of no token)
+        if (!A) return GDN_ERR_NULL_ARG;
+        if (!aligned_to(A, 4) || !aligned_to(D, 4) || !aligned_to(dt_bias, 4)) return GDN_ERR_ALIGNMENT;
     }
     if (!aligned_to(y, 16) || !aligned_to(h0, 4) || !aligned_to(hT, 4) || !aligned_to(cu_seqlens, 4)) return GDN_ERR_ALIGNMENT;
     if (pr->T == 0 && !hT) return GDN_OK;

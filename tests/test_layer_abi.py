@@ -263,6 +263,18 @@ def test_ssm_arguments(lib):
     assert ssm_step(lib, one, slots=ODD2) == ALIGN
 
 
+def test_ssm_gates_wanted_without_tokens(lib):
+    # no token, but final states to write: the kernel reads A
+    none = dict(x=None, dt=None, B=None, C=None, y=None, ws=None)
+    for packed in (dict(), dict(B=1, n_seqs=2)):
+        pr = ssm_problem(T=0, **packed)
+        cu = FAKE if packed else None
+        assert ssm_forward(lib, pr, A=None, cu=cu, **none) == NULL
+        for k in ("A", "D", "bias"):
+            assert ssm_forward(lib, pr, **{**none, k: ODD2}, cu=cu) == ALIGN, k
+    assert ssm_forward(lib, ssm_problem(T=0), A=None, hT=None, **none) == OK
+
+
 # ---------------------------------------------------------------------------
 # the binding
 # ---------------------------------------------------------------------------
