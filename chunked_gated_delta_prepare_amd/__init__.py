@@ -135,8 +135,8 @@ def load_library(path: str | None = None):
         lib.gdn_abi_version.restype = ctypes.c_int
         lib.gdn_wait_timeouts.argtypes = [ctypes.POINTER(ctypes.c_uint32), ctypes.c_int]
         lib.gdn_wait_timeouts.restype = ctypes.c_int
-        from . import layer
-        layer.declare(lib)
+        from . import layer_abi
+        layer_abi.declare(lib)
         if lib.gdn_abi_version() != ABI_VERSION:
             raise RuntimeError("libgdn ABI %d, binding expects %d"
                                % (lib.gdn_abi_version(), ABI_VERSION))

@@ -1,6 +1,9 @@
 """The layer operators' binding on the CPU: what it hands to the library, and
 what it refuses before that.  Calls are caught at the library's door, with CPU
 tensors in the place of the device's."""
+import os
+import subprocess
+import sys
 import types
 
 import pytest
@@ -66,3 +69,14 @@ def test_scan_gradients_of_one_batch_or_no_tokens_need_no_common_stride(calls):
         d = scan(b, T)
         gdn.ssm_backward(*d.args, dx=torch.zeros_like(d.x), dB=torch.zeros_like(d.B), dC=torch.zeros_like(d.C))
     assert len(calls) == 2
+
+
+def test_the_library_loads_without_torch():
+    """As the rest of the package: torch is imported where tensors are worked on."""
+    code = ("import sys; sys.modules['torch'] = None\n"
+            "import chunked_gated_delta_prepare_amd as gdn\n"
+            "lib = gdn.load_library()\n"
+            "assert lib.gdn_ssm_forward.argtypes and lib.gdn_workspace_bytes_ssm.restype\n")
+    run = subprocess.run([sys.executable, "-c", code], capture_output=True, text=True,
+                         cwd=os.path.dirname(os.path.dirname(os.path.abspath(__file__))))
+    assert run.returncode == 0, run.stderr
