@@ -544,17 +544,18 @@ __device__ __forceinline__ float segments_before(const SsmParams &p, const Segme
 //      blocks, dealt to the waves); S^T q on the way
 //   2  out1 = M v + e^cum S^T q, transposed, so that a lane stores four columns
 //   3  S' = e^total S + k^T (w v)
-// The products of a state that is an output, or the start of the key scans, take
+// The products of a state that is an output or another segment's start take
 // w v in three bf16 parts (relative error 2^-27): with two the final state was
 // 2.4e-6 off, against 1e-7 of fp32 arithmetic throughout, and dA, a sum over
-// all tokens of both signs, 5e-5.  Where only out1 is read from the state (an
-// output state comes from the segments' end states if there are any), w v is
-// rounded once to bf16, as out1's other operands are and out1 itself, and S too
-// before it is multiplied.  The next chunk's rows are in flight while one is
-// worked on, and the gates of several chunks are formed at a time, one a wave.
-// ENDS: only the state, from a zero start, to the workspace; FINE where it feeds
-// more than out1 (65536 tokens, 64 heads of 128 x 128, both launches: 1.37 ms
-// with a final state, 1.13 ms without one).
+// all tokens of both signs, 5e-5.  So do those of a sequence's only segment,
+// whose state is the final one, whether or not it is asked for: out1 has the
+// same bits either way.  In the segments of longer sequences only out1 is read
+// from the main pass's state (an output state comes from the segments' end
+// states), and w v is rounded once to bf16, as out1's other operands are and
+// out1 itself, and S too before it is multiplied.  The next chunk's rows are in
+// flight while one is worked on, and the gates of several chunks are formed at a
+// time, one a wave.
+// ENDS: only the state, from a zero start, to the workspace.
 //
 // Sixteen columns a wave, eight waves for 128 columns, two workgroups a CU: with
 // 32 columns a wave and four waves the kernel read a third less from LDS but
@@ -564,12 +565,12 @@ __device__ __forceinline__ float segments_before(const SsmParams &p, const Segme
 // chunk (decays, roundings, the state's scaling) fill half of the time, waiting
 // for LDS a third.
 // ---------------------------------------------------------------------------
-template <typename IO, int N, int COLS, int NH, bool ENDS, bool REV, bool FINE = true>
+template <typename IO, int N, int COLS, int NH, bool ENDS, bool REV>
 __global__ void __launch_bounds__(4 * COLS, sizeof(IO) == 4 ? 1 : COLS == 64 && N == 128 ? 3 : 4) ssm_scan_kernel(SsmParams p) {
     typedef SOp<IO> O;
     typedef typename O::elem E;
     constexpr int C = kSsmChunk, NW = COLS / 16, NB = N / 16, kThreads = 4 * COLS, P = COLS / NH;
-    constexpr int kP = O::template kParts<FINE ? 3 : 1>;
+    constexpr int kP = O::template kParts<3>;
     __shared__ __align__(16) E sv[C * COLS], sk[C * N], sq[ENDS ? 8 : C * N], sm[ENDS ? 1 : NH][ENDS ? 8 : C * C];
     // chunks whose gates are formed at once, one chunk and head a wave
     constexpr int GC = NW / NH;
@@ -581,7 +582,7 @@ __global__ void __launch_bounds__(4 * COLS, sizeof(IO) == 4 ? 1 : COLS == 64 && 
     if (!seg.live) return;
     const bool last = REV ? seg.begin == seg.seq_begin : seg.end == seg.seq_end;      // of the scan
     // an output state comes from the end states, but for a sequence's only segment
-    const bool via_ends = last && p.all_ends && !(seg.begin == seg.seq_begin && seg.end == seg.seq_end);
+    const bool only = seg.begin == seg.seq_begin && seg.end == seg.seq_end, via_ends = last && p.all_ends && !only;
     if (ENDS && last && !via_ends) return;
     const int w = wave_id(), l = lane_id(), q = l >> 4, j = l & 15;
     const int col0 = hb * COLS, head0 = col0 / p.P, mine = w * 16 / P, head = head0 + mine, grp = head0 / p.heads_per_group;
@@ -658,7 +659,6 @@ __global__ void __launch_bounds__(4 * COLS, sizeof(IO) == 4 ? 1 : COLS == 64 && 
             make_gates<REV>(gates[gc][gh], dt_of(p, raw_value<IO>(p, raw), bias, again(lane_id()) < rows), A, 1.f, 1.f);
         }
     };
-    const bool exact = p.sT && last && !via_ends;
     double total = 0.0;
     if (nc > 0) {
         fetch_dt(0);
@@ -767,7 +767,7 @@ __global__ void __launch_bounds__(4 * COLS, sizeof(IO) == 4 ? 1 : COLS == 64 && 
         } else {
             add_parts(I0(), I1());
             if constexpr (kP > 1) {
-                if (exact) add_parts(I1(), IP());
+                if (only) add_parts(I1(), IP());
             }
         }
     }
@@ -779,7 +779,7 @@ __global__ void __launch_bounds__(4 * COLS, sizeof(IO) == 4 ? 1 : COLS == 64 && 
 #pragma unroll
             for (int e = 0; e < 4; ++e) e0[row_of(nb, e) * COLS] = h[nb][e];
         if (!REV && l == 0 && w == mine * (NW / NH)) p.total[place_at * NH + mine] = total;
-    } else if (exact) {
+    } else if (p.sT && only) {
         const int l = again(lane_id()), q = l >> 4;
         float *sT = p.sT + state_at(l) + 8 * q * p.P;
 #pragma unroll

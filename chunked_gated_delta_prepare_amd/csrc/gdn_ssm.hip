@@ -188,22 +188,20 @@ void fill_ssm(const gdn_ssm_problem *pr, SsmParams &sp) {
 
 namespace {
 
-// The main pass, or one for the end states: `fine` where they are an output too.
+// The main pass, or the one for the end states.
 template <typename IO, int N, int COLS, int NH>
-const void *ssm_fn(bool ends, bool fine) {
-    if (!ends) return (const void *)&ssm_scan_kernel<IO, N, COLS, NH, false, false>;
-    if (fine || sizeof(IO) == 4) return (const void *)&ssm_scan_kernel<IO, N, COLS, NH, true, false>;
-    return (const void *)&ssm_scan_kernel<IO, N, COLS, NH, true, false, sizeof(IO) == 4>;
+const void *ssm_fn(bool ends) {
+    return ends ? (const void *)&ssm_scan_kernel<IO, N, COLS, NH, true, false> : (const void *)&ssm_scan_kernel<IO, N, COLS, NH, false, false>;
 }
 
 template <int N>
-const void *ssm_pick(const gdn_ssm_problem *pr, const SsmPlan &s, bool ends, bool fine) {
-    if (pr->io_dtype == GDN_F32) return ssm_fn<float, N, 64, 1>(ends, fine);
-    if (s.ncb == 1) return ssm_fn<bf16_t, N, 64, 1>(ends, fine);
-    return s.nh == 2 ? ssm_fn<bf16_t, N, 128, 2>(ends, fine) : ssm_fn<bf16_t, N, 128, 1>(ends, fine);
+const void *ssm_pick(const gdn_ssm_problem *pr, const SsmPlan &s, bool ends) {
+    if (pr->io_dtype == GDN_F32) return ssm_fn<float, N, 64, 1>(ends);
+    if (s.ncb == 1) return ssm_fn<bf16_t, N, 64, 1>(ends);
+    return s.nh == 2 ? ssm_fn<bf16_t, N, 128, 2>(ends) : ssm_fn<bf16_t, N, 128, 1>(ends);
 }
-const void *ssm_pick(const gdn_ssm_problem *pr, const SsmPlan &s, bool ends, bool fine) {
-    return pr->N == 64 ? ssm_pick<64>(pr, s, ends, fine) : ssm_pick<128>(pr, s, ends, fine);
+const void *ssm_pick(const gdn_ssm_problem *pr, const SsmPlan &s, bool ends) {
+    return pr->N == 64 ? ssm_pick<64>(pr, s, ends) : ssm_pick<128>(pr, s, ends);
 }
 
 template <typename IO>
@@ -268,10 +266,10 @@ gdn_status gdn_ssm_forward(const gdn_ssm_problem *pr, const void *x, const void 
     const int grid = ssm_grid(pr, sp, s);
     if (need) {
         sp.all_ends = hT != nullptr;
-        st = launch_kernel(ssm_pick(pr, s, true, hT != nullptr), grid, &sp, (hipStream_t)stream, 256 * s.ncb);
+        st = launch_kernel(ssm_pick(pr, s, true), grid, &sp, (hipStream_t)stream, 256 * s.ncb);
         if (st != GDN_OK) return st;
     }
-    return launch_kernel(ssm_pick(pr, s, false, true), grid, &sp, (hipStream_t)stream, 256 * s.ncb);
+    return launch_kernel(ssm_pick(pr, s, false), grid, &sp, (hipStream_t)stream, 256 * s.ncb);
 }
 
 gdn_status gdn_ssm_step(const gdn_ssm_problem *pr, const void *x, const void *dt, const float *A, const void *Bm,

@@ -453,7 +453,7 @@ def ssm_forward(x, dt, A, B, C, D=None, dt_bias=None, h0=None, *, dt_softplus=Tr
     fp32; A, D, dt_bias [H] fp32; h0 [b, H, N, P] fp32, or [n, H, N, P] with
     cu_seqlens (as in conv_forward).  A NaN in a token also reaches those before
     it in the same 64 of its sequence.  Returns (y [b, T, H, P], hT like h0 or
-    None); a long prompt without hT (output_final_state False) is faster."""
+    None); y does not depend on whether hT is asked for."""
     dev, code = _ssm_checks(x, dt, A, B, C, D, dt_bias, 2)
     n = _packed(cu_seqlens, dev, x.shape[0])
     st = (n or x.shape[0], x.shape[2], B.shape[3], x.shape[3])

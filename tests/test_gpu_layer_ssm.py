@@ -521,3 +521,19 @@ def test_gradients_of_single_tokens_in_a_batch(H, P, N, G, dt):
     with pytest.raises(ValueError, match="same strides"):
         gdn.ssm_backward(dy, *(d[k] for k in names), dx=torch.empty_like(dy), dB=torch.empty(b, 1, G, N, device=DEV, dtype=dt),
                          dC=torch.empty(b, 1, G, N, device=DEV, dtype=dt))
+
+
+@pytest.mark.parametrize("lens,H,P,N,G,dt", [
+    ((1, 2000), 4, 64, 128, 2, BF), ((2, 100), 2, 128, 128, 1, BF), ((1, 1500), 1, 128, 64, 1, BF),
+    ([70, 0, 600, 1, 256], 4, 64, 64, 2, BF), ([1000, 30], 3, 64, 128, 3, BF), ((1, 700), 2, 64, 64, 1, F32)])
+def test_the_final_state_changes_nothing_else(lens, H, P, N, G, dt):
+    """y has the same bits whether or not the final state is asked for, for
+    sequences of one segment and of several."""
+    packed = isinstance(lens, list)
+    B, T = (1, sum(lens)) if packed else lens
+    n = len(lens) if packed else B
+    d = inputs(B, T, H, P, N, G, dt, dt, n, True)
+    cu = offsets(lens) if packed else None
+    y, hT = forward(d, cu_seqlens=cu)
+    alone, none = forward(d, cu_seqlens=cu, output_final_state=False)
+    assert none is None and hT is not None and torch.equal(y, alone)
