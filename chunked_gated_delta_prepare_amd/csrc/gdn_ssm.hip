@@ -149,11 +149,10 @@ gdn_status check_ssm(const gdn_ssm_problem *pr, bool packed) {
         if (v < 0 || v > (1 << 22)) return GDN_ERR_UNSUPPORTED;
     // what lies behind a chunk's last row is told by its place: rows do not overlap
     if (pr->T > 1 && (pr->x_stride_t < pr->H * pr->P || pr->bc_stride_t < pr->G * pr->N)) return GDN_ERR_UNSUPPORTED;
-    // the scans', the sums' and the gates' workgroups
+    // the scans' and the gates' workgroups
     const SsmPlan s = ssm_plan(pr, packed);
     const int64_t n = s.n_items;
-    if (!grid_ok(n * s.n_hb, 512) || !grid_ok(n * pr->H, 256) || !grid_ok(n * (s.seg_tokens / kSsmChunk) * pr->G, 4 * pr->N))
-        return GDN_ERR_UNSUPPORTED;
+    if (!grid_ok(n * s.n_hb, 512) || !grid_ok(n * pr->H, 256)) return GDN_ERR_UNSUPPORTED;
     return GDN_OK;
 }
 

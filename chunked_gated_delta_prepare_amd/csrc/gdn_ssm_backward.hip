@@ -300,17 +300,36 @@ __global__ void __launch_bounds__(4 * N, sizeof(IO) == 4 ? 1 : NH == 1 && N == 1
 }
 
 // out2 of a chunk and group: the sum over the group's blocks of columns, in
-// the lanes' own layout.
+// the lanes' own layout.  A workgroup for every place that a chunk can have (see
+// chunk_slot), so that the launch grows with the tokens and the sequences, not
+// with segments of which most are not there.
 template <typename IO, int N, bool REV>
 __global__ void __launch_bounds__(4 * N) ssm_sum_kernel(SsmParams p) {
     constexpr int kThreads = 4 * N;
-    const int cps = p.seg_tokens / kSsmChunk, G = p.H / p.heads_per_group;
-    const int g = blockIdx.x % G, c = blockIdx.x / G % cps, item = blockIdx.x / G / cps;
-    const Segment seg = find_segment(p, item);
-    const int nc = chunks_of(seg);
-    if (!seg.live || c >= nc) return;
-    const int slot = chunk_slot(p, seg, REV ? nc - 1 - c : c);
-    if (slot >= p.n_slots) return;
+    const int G = p.H / p.heads_per_group, g = blockIdx.x % G, slot = blockIdx.x / G;
+    int batch = 0, lo = 0, rows = 0;
+    if (!p.cu) {
+        const int per = (p.T + kSsmChunk - 1) / kSsmChunk;
+        batch = slot / per;
+        lo = slot % per * kSsmChunk;
+        rows = p.T - lo;
+    } else {
+        // the last sequence whose places begin at or before this one
+        int n = 0, hi = p.n_seqs - 1;
+        while (n < hi) {
+            const int mid = (n + hi + 1) >> 1;
+            if (ssm_cu(p, mid) / kSsmChunk + mid <= slot)
+                n = mid;
+            else
+                hi = mid - 1;
+        }
+        const int begin = ssm_cu(p, n), in = slot - (begin / kSsmChunk + n);
+        if (in < 0) return;
+        lo = begin + in * kSsmChunk;
+        rows = ssm_cu(p, n + 1) - lo;
+    }
+    if (rows <= 0) return;
+    rows = rows < kSsmChunk ? rows : kSsmChunk;
     const int w = wave_id(), l = lane_id(), q = l >> 4, j = l & 15, per = p.n_hb / G;
     float4v z[4];
 #pragma unroll
@@ -323,9 +342,7 @@ __global__ void __launch_bounds__(4 * N) ssm_sum_kernel(SsmParams p) {
             z[i] += float4v{a.x, a.y, b.x, b.y};
         }
     }
-    int lo;
-    const int rows = chunk_of<REV>(seg, c, lo);
-    const rsrc_t r = make_rsrc((IO *)p.out + seg.batch * p.ob + lo * p.ot + (int64_t)g * N, 0x7fffffffu);
+    const rsrc_t r = make_rsrc((IO *)p.out + batch * p.ob + lo * p.ot + (int64_t)g * N, 0x7fffffffu);
 #pragma unroll
     for (int bi = 0; bi < 4; ++bi) {
         const int ii = 16 * bi + j, t = REV ? rows - 1 - ii : ii;
@@ -503,6 +520,13 @@ BwdPlan bwd_plan(const gdn_ssm_problem *pr, bool packed) {
     return b;
 }
 
+gdn_status check_ssm_backward(const gdn_ssm_problem *pr, bool packed) {
+    const gdn_status st = check_ssm(pr, packed);
+    if (st != GDN_OK) return st;
+    // the sums' workgroups
+    return grid_ok(bwd_plan(pr, packed).slots * pr->G, 4 * pr->N) ? GDN_OK : GDN_ERR_UNSUPPORTED;
+}
+
 template <typename IO, int N, int COLS, int NH>
 struct BwdFns {
     static constexpr int kScanThreads = 4 * COLS, kKeyThreads = 4 * N;
@@ -540,7 +564,7 @@ gdn_status bwd_launches(const gdn_ssm_problem *pr, const BwdPlan &b, const SsmPa
     d.out = dx;
     d.sT = dh0;
     go(F::dx(), grid, d, F::kScanThreads);
-    const int sgrid = b.s.n_items * (b.s.seg_tokens / kSsmChunk) * (int)pr->G;
+    const int sgrid = (int)(b.slots * pr->G);
     f.out = dC;
     go(F::key(false), grid, f, F::kKeyThreads);
     go(F::sum(false), sgrid, f, F::kKeyThreads);
@@ -561,7 +585,7 @@ extern "C" {
 
 size_t gdn_workspace_bytes_ssm_backward(const gdn_ssm_problem *pr) {
     const bool packed = pr && pr->n_seqs > 0;
-    if (check_ssm(pr, packed) != GDN_OK) return 0;
+    if (check_ssm_backward(pr, packed) != GDN_OK) return 0;
     return bwd_plan(pr, packed).bytes;
 }
 
@@ -570,7 +594,7 @@ gdn_status gdn_ssm_backward(const gdn_ssm_problem *pr, const void *dy, const voi
                             const int32_t *cu_seqlens, const float *dhT, void *dx, void *ddt, float *dA, void *dB,
                             void *dC, float *dD, float *ddt_bias, float *dh0, void *workspace, size_t workspace_bytes,
                             void *stream) {
-    gdn_status st = check_ssm(pr, cu_seqlens != nullptr);
+    gdn_status st = check_ssm_backward(pr, cu_seqlens != nullptr);
     if (st != GDN_OK) return st;
     if (pr->T > 1 && (pr->dxbc_stride_t < pr->H * pr->P || pr->dxbc_stride_t < pr->G * pr->N)) return GDN_ERR_UNSUPPORTED;
     if (!A || !dA) return GDN_ERR_NULL_ARG;

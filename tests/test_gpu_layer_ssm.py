@@ -537,3 +537,31 @@ def test_the_final_state_changes_nothing_else(lens, H, P, N, G, dt):
     y, hT = forward(d, cu_seqlens=cu)
     alone, none = forward(d, cu_seqlens=cu, output_final_state=False)
     assert none is None and hT is not None and torch.equal(y, alone)
+
+
+@pytest.mark.parametrize("H,P,N,G,dt", [(4, 64, 128, 2, BF), (2, 128, 64, 1, BF), (2, 64, 64, 2, F32)])
+def test_many_packed_sequences_are_each_their_own(H, P, N, G, dt):
+    """Two hundred short sequences and a few long ones between them: every one has the
+    bits of a call of its own (the long ones within rounding: their segments differ)."""
+    g = torch.Generator().manual_seed(3)
+    lens = torch.randint(0, 90, (200,), generator=g).tolist()
+    lens[20], lens[77], lens[140], lens[199] = 700, 64, 0, 1300
+    n, T = len(lens), sum(lens)
+    d = inputs(1, T, H, P, N, G, dt, F32, n, True)
+    cu = offsets(lens)
+    dy, dhT = rnd(1, T, H, P, seed=8, dtype=dt), rnd(n, H, N, P, seed=9)
+    names = ("x", "dt", "A", "B", "C", "D", "dt_bias", "h0")
+    y, hT = forward(d, cu_seqlens=cu)
+    grads = gdn.ssm_backward(dy, *(d[k] for k in names), dhT, cu_seqlens=cu)
+    at = [0] + torch.tensor(lens).cumsum(0).tolist()
+    for k in [0, 1, 19, 20, 21, 76, 77, 78, 140, 141, 198, 199]:
+        s = slice(at[k], at[k + 1])
+        one = {m: (v[:, s] if m in ("x", "dt", "B", "C") else v[k:k + 1] if m == "h0" else v) for m, v in d.items()}
+        y1, h1 = forward(one)
+        g1 = gdn.ssm_backward(dy[:, s].contiguous(), *(one[m] for m in names), dhT[k:k + 1])
+        pairs = [(y[:, s], y1), (hT[k:k + 1], h1), (grads[7][k:k + 1], g1[7])] + [(grads[i][:, s], g1[i]) for i in (0, 1, 3, 4)]
+        for u, v in pairs:
+            if lens[k] < 256:
+                assert torch.equal(u, v), k
+            else:
+                assert float((u.double() - v.double()).norm()) <= 2.0 ** -6 * float(v.double().norm()), k

@@ -275,6 +275,21 @@ def test_ssm_gates_wanted_without_tokens(lib):
     assert ssm_forward(lib, ssm_problem(T=0), A=None, hT=None, **none) == OK
 
 
+def packed_scan(T, n, H, P, N, G):
+    return ssm_problem(B=1, T=T, n_seqs=n, H=H, P=P, N=N, G=G, x_stride_t=H * P, bc_stride_t=G * N, dt_stride_t=H,
+                       dxbc_stride_t=H * P)
+
+
+def test_many_short_packed_sequences_are_taken(lib):
+    # the backward's launches follow the tokens, not sequences times segments
+    for T, n in ((262144, 4096), (1 << 20, 1 << 14)):
+        pr = packed_scan(T, n, 64, 128, 128, 8)
+        assert ssm_forward(lib, pr, cu=FAKE, ws=None, size=0) == WORKSPACE
+        assert ssm_backward(lib, pr, cu=FAKE, ws=None, size=0) == WORKSPACE
+        assert lib.gdn_workspace_bytes_ssm(ctypes.byref(pr)) > 0
+        assert lib.gdn_workspace_bytes_ssm_backward(ctypes.byref(pr)) > 0
+
+
 # ---------------------------------------------------------------------------
 # the binding
 # ---------------------------------------------------------------------------
