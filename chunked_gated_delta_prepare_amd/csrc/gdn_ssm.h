@@ -77,8 +77,8 @@ struct SsmParams {
     const int32_t *cu;
     int64_t qkb, qkt, vb, vt, q2b, q2t, db, dt_, ob, ot;   // strides: batch, token
     // workspace
-    double *total;                          // [item][n_hb][NH]: log2 of a segment's decay
-    float *ends;                            // [item][n_hb][N][64 NCB]: end states from zero
+    double *total;                          // [end][n_hb][NH]: log2 of a segment's decay
+    float *ends;                            // [end][n_hb][N][64 NCB]: end states from zero
     float *part;                            // out2 by block of columns, for ssm_sum_kernel
     float *inside, *across;                 // [n_hb][NH][B T]: q . out2 in two parts
     float *dyx, *wtt;                       // the same: dy_t . x_t, and W_tt / dt_t
@@ -88,6 +88,7 @@ struct SsmParams {
     int n_slots, n_marks;                   // places for chunks in part, and for marks
     int T, H, P, n_seqs, heads_per_group;
     int seg_tokens, n_items, n_hb;          // tokens of a segment, segments in all, blocks of columns
+    int n_ends, n_units;                    // places for end states; segments or ends that this launch works on
     int softplus, swizzle, dt_f32;
     int all_ends;                           // the last segments' end states are in the workspace too
 };
@@ -364,10 +365,11 @@ __device__ __forceinline__ void make_gates(Gates &g, float dt, float A, float be
     if (l == 63) g.total = total;
 }
 
-// A segment of a sequence: its place in the workspace, its tokens, and the
-// sequence it belongs to.
+// A segment of a sequence, its tokens, and the sequence it belongs to.  Segments
+// of sequences that have several are counted apart too: those have a place for
+// an end state (see SsmPlan), one behind the other.
 struct Segment {
-    int item, first;            // this segment and the first of its sequence
+    int end_at, first_end;      // that place and the one of the sequence's first segment; -1 without
     int seq, batch;             // number of the sequence; batch its rows lie in
     int begin, end;             // tokens of the segment
     int seq_begin, seq_end;
@@ -379,19 +381,22 @@ __device__ __forceinline__ int ssm_cu(const SsmParams &p, int n) {
     return v < 0 ? 0 : v > p.T ? p.T : v;
 }
 
-__device__ __forceinline__ Segment find_segment(const SsmParams &p, int item) {
+// The segment of number `unit`, or (BY_END) the one whose end state's place that is.
+template <bool BY_END>
+__device__ __forceinline__ Segment find_segment(const SsmParams &p, int unit) {
     Segment s;
-    s.item = item;
     s.live = true;
+    int in;                     // its number within the sequence
     if (!p.cu) {
         const int per = p.n_items / p.n_seqs;
-        s.seq = s.batch = item / per;
-        s.first = s.seq * per;
+        s.seq = s.batch = unit / per;
+        in = unit - s.seq * per;
         s.seq_begin = 0;
         s.seq_end = p.T;
+        s.first_end = per > 1 ? s.seq * per : -1;
     } else {
         // every sequence has at least one segment; 64 sequences a step
-        int base = 0;
+        int items = 0, ends = 0;
         s.live = false;
         s.batch = 0;
         for (int n0 = 0; n0 < p.n_seqs && !s.live; n0 += 64) {
@@ -403,42 +408,51 @@ __device__ __forceinline__ Segment find_segment(const SsmParams &p, int item) {
                 e = e < b ? b : e;
                 cnt = e > b ? (e - b + p.seg_tokens - 1) / p.seg_tokens : 1;
             }
-            int upto = cnt;
+            // segments of sequences with several, up to this one, and lone segments before it
+            const int several = cnt > 1 ? cnt : 0;
+            int upto = several;
 #pragma unroll
             for (int m = 1; m < 64; m <<= 1) {
                 const int u = __shfl_up(upto, m, 64);
                 if (lane_id() >= m) upto += u;
             }
-            const uint64_t hit = __ballot(cnt > 0 && item >= base + upto - cnt && item < base + upto);
+            const uint64_t lone = __ballot(cnt == 1);
+            const int before = (int)__builtin_amdgcn_mbcnt_hi((uint32_t)(lone >> 32), __builtin_amdgcn_mbcnt_lo((uint32_t)lone, 0));
+            const int first_end = ends + upto - several, first = BY_END ? first_end : items + upto - several + before;
+            const uint64_t hit = __ballot((BY_END ? several : cnt) > 0 && unit >= first && unit < first + cnt);
             if (hit) {
                 const int l = __builtin_ctzll(hit);
                 s.live = true;
                 s.seq = __builtin_amdgcn_readfirstlane(n0 + l);
-                s.first = __builtin_amdgcn_readfirstlane(base + __shfl(upto - cnt, l, 64));
+                in = unit - __builtin_amdgcn_readfirstlane(__shfl(first, l, 64));
+                s.first_end = __builtin_amdgcn_readfirstlane(__shfl(several ? first_end : -1, l, 64));
                 s.seq_begin = __builtin_amdgcn_readfirstlane(__shfl(b, l, 64));
                 s.seq_end = __builtin_amdgcn_readfirstlane(__shfl(e, l, 64));
             }
-            base += __builtin_amdgcn_readfirstlane(__shfl(upto, 63, 64));
+            const int sum = __builtin_amdgcn_readfirstlane(__shfl(upto, 63, 64));
+            ends += sum;
+            items += sum + (int)__builtin_popcountll(lone);
         }
         if (!s.live) return s;
     }
-    s.begin = s.seq_begin + (item - s.first) * p.seg_tokens;
+    s.end_at = s.first_end < 0 ? -1 : s.first_end + in;
+    s.begin = s.seq_begin + in * p.seg_tokens;
     s.end = s.begin + p.seg_tokens < s.seq_end ? s.begin + p.seg_tokens : s.seq_end;
     return s;
 }
 
-// blockIdx -> (segment, block of columns).  The blocks of one segment and
+// blockIdx -> (segment or end, block of columns).  The blocks of one segment and
 // group share its B and C: with swizzle they go to one XCD (workgroups are
 // dealt to the eight XCDs in turn), else they are neighbours.
-__device__ __forceinline__ void place(const SsmParams &p, int &item, int &hb) {
+__device__ __forceinline__ void place(const SsmParams &p, int &unit, int &hb) {
     const int i = blockIdx.x;
     if (p.swizzle) {
-        const int groups = p.H / p.heads_per_group, per = p.n_hb / groups, j = i >> 3, unit = (j / per) * 8 + (i & 7);
-        item = unit / groups;
-        hb = (unit % groups) * per + j % per;
+        const int groups = p.H / p.heads_per_group, per = p.n_hb / groups, j = i >> 3, at = (j / per) * 8 + (i & 7);
+        unit = at / groups;
+        hb = (at % groups) * per + j % per;
     } else {
         hb = i % p.n_hb;
-        item = i / p.n_hb;
+        unit = i / p.n_hb;
     }
 }
 
@@ -524,10 +538,12 @@ __device__ __forceinline__ float raw_value(const SsmParams &p, uint32_t bits) {
 template <bool REV, typename F>
 __device__ __forceinline__ float segments_before(const SsmParams &p, const Segment &s, int hb, int nh, int hh, F f) {
     double d = 0.0;
+    if (s.first_end < 0) return 1.f;
     const int per = (s.seq_end - s.seq_begin + p.seg_tokens - 1) / p.seg_tokens;
     // (overlapping sequences have more segments than there are places)
-    const int stop = REV ? (s.first + per < p.n_items ? s.first + per : p.n_items) : s.first - 1;
-    for (int i = REV ? s.item + 1 : s.item - 1; REV ? i < stop : i > stop; i += REV ? 1 : -1) {
+    const int top = s.first_end + per < p.n_ends ? s.first_end + per : p.n_ends;
+    const int stop = REV ? top : s.first_end - 1;
+    for (int i = REV ? s.end_at + 1 : (s.end_at < top ? s.end_at : top) - 1; REV ? i < stop : i > stop; i += REV ? 1 : -1) {
         const int64_t at = (int64_t)i * p.n_hb + hb;
         f(at, fast_exp2((float)d));
         d += p.total[at * nh + hh];
@@ -575,14 +591,14 @@ __global__ void __launch_bounds__(4 * COLS, sizeof(IO) == 4 ? 1 : COLS == 64 && 
     // chunks whose gates are formed at once, one chunk and head a wave
     constexpr int GC = NW / NH;
     __shared__ Gates gates[GC][NH];
-    int item, hb;
-    place(p, item, hb);
-    if (item >= p.n_items) return;
-    const Segment seg = find_segment(p, item);
+    int unit, hb;
+    place(p, unit, hb);
+    if (unit >= p.n_units) return;
+    const Segment seg = find_segment<ENDS>(p, unit);
     if (!seg.live) return;
     const bool last = REV ? seg.begin == seg.seq_begin : seg.end == seg.seq_end;      // of the scan
     // an output state comes from the end states, but for a sequence's only segment
-    const bool only = seg.begin == seg.seq_begin && seg.end == seg.seq_end, via_ends = last && p.all_ends && !only;
+    const bool only = seg.begin == seg.seq_begin && seg.end == seg.seq_end, via_ends = last && p.all_ends && !only && seg.end_at < p.n_ends;
     if (ENDS && last && !via_ends) return;
     const int w = wave_id(), l = lane_id(), q = l >> 4, j = l & 15;
     const int col0 = hb * COLS, head0 = col0 / p.P, mine = w * 16 / P, head = head0 + mine, grp = head0 / p.heads_per_group;
@@ -617,7 +633,7 @@ __global__ void __launch_bounds__(4 * COLS, sizeof(IO) == 4 ? 1 : COLS == 64 && 
         }
         if (p.sT && via_ends) {
             // the state behind the last segment, from that segment's own
-            const int64_t mark = (int64_t)item * p.n_hb + hb;
+            const int64_t mark = (int64_t)seg.end_at * p.n_hb + hb;
             const float *e0 = p.ends + mark * (N * COLS) + wc + j;
             const float f = fast_exp2((float)p.total[mark * NH + mine]);
 #pragma unroll
@@ -772,7 +788,7 @@ __global__ void __launch_bounds__(4 * COLS, sizeof(IO) == 4 ? 1 : COLS == 64 && 
         }
     }
     if constexpr (ENDS) {
-        const int64_t place_at = (int64_t)item * p.n_hb + hb;
+        const int64_t place_at = (int64_t)unit * p.n_hb + hb;
         float *e0 = p.ends + place_at * (N * COLS) + wc + j;
 #pragma unroll
         for (int nb = 0; nb < NB; ++nb)
@@ -789,8 +805,9 @@ __global__ void __launch_bounds__(4 * COLS, sizeof(IO) == 4 ? 1 : COLS == 64 && 
     }
 }
 
+// n_ends: places for the end states of sequences with several segments
 struct SsmPlan {
-    int ncb, nh, n_hb, n_items, seg_tokens, seqs;
+    int ncb, nh, n_hb, n_items, n_ends, seg_tokens, seqs;
 };
 
 gdn_status check_ssm(const gdn_ssm_problem *pr, bool packed);
@@ -798,6 +815,6 @@ gdn_status check_ssm_pointers(const gdn_ssm_problem *pr, const void *x, const vo
                               const void *Cm, const float *D, const float *bias, bool rows);
 void fill_ssm(const gdn_ssm_problem *pr, SsmParams &sp);
 SsmPlan ssm_plan(const gdn_ssm_problem *pr, bool packed);
-int ssm_grid(const gdn_ssm_problem *pr, SsmParams &sp, const SsmPlan &s);
+int ssm_grid(const gdn_ssm_problem *pr, SsmParams &sp, const SsmPlan &s, bool ends);
 
 }  // namespace gdn

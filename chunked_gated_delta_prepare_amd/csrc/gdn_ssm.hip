@@ -113,6 +113,13 @@ SsmPlan ssm_plan(const gdn_ssm_problem *pr, bool packed) {
     s.seg_tokens = (int)(seg * kSsmChunk);
     const int64_t cut = (pr->T + s.seg_tokens - 1) / s.seg_tokens;
     s.n_items = (int)(packed ? cut + pr->n_seqs : pr->B * (cut > 0 ? cut : 1));
+    // A sequence of L tokens with several segments has (L - 1) / seg + 1 of them; of
+    // m such ones, T tokens in all, the segments are at most (T - m) / seg + m,
+    // which grows with m.  (A lone segment has no end state to hand on: with a place
+    // for every segment 16384 tokens of 64 heads of 128 x 128 took 42 MB as one
+    // sequence and 1.1 GB as 256, now 42 and 75.)
+    const int64_t m = packed ? (pr->n_seqs < pr->T / (s.seg_tokens + 1) ? pr->n_seqs : pr->T / (s.seg_tokens + 1)) : 0;
+    s.n_ends = (int)(packed ? (m > 0 ? (pr->T - m) / s.seg_tokens + m : 0) : cut > 1 ? s.n_items : 0);
     return s;
 }
 
@@ -121,19 +128,19 @@ SsmPlan ssm_plan(const gdn_ssm_problem *pr, bool packed) {
 // XCD (64 heads of 128 columns, 8 groups, with and without: 65536 tokens 1.33
 // and 1.37 ms, 16384 tokens 348 and 362 us, 16384 tokens in 8 packed sequences
 // 402 and 412 us).
-int ssm_grid(const gdn_ssm_problem *pr, SsmParams &sp, const SsmPlan &s) {
+int ssm_grid(const gdn_ssm_problem *pr, SsmParams &sp, const SsmPlan &s, bool ends) {
     sp.seg_tokens = s.seg_tokens;
     sp.n_items = s.n_items;
+    sp.n_ends = s.n_ends;
+    sp.n_units = ends ? s.n_ends : s.n_items;
     sp.n_hb = s.n_hb;
     sp.n_seqs = s.seqs;
-    const int64_t units = (int64_t)s.n_items * pr->G;
-    sp.swizzle = units % 8 == 0 && s.n_hb % pr->G == 0;
-    return s.n_items * s.n_hb;
+    sp.swizzle = (int64_t)sp.n_units * pr->G % 8 == 0 && s.n_hb % pr->G == 0;
+    return sp.n_units * s.n_hb;
 }
 
 static size_t forward_ws(const gdn_ssm_problem *pr, const SsmPlan &s) {
-    if (s.n_items == s.seqs) return 0;            // one segment each
-    return (size_t)s.n_items * s.n_hb * (8 * 2 + 4 * pr->N * 64 * s.ncb);
+    return (size_t)s.n_ends * s.n_hb * (8 * 2 + 4 * pr->N * 64 * s.ncb);
 }
 
 gdn_status check_ssm(const gdn_ssm_problem *pr, bool packed) {
@@ -261,13 +268,14 @@ gdn_status gdn_ssm_forward(const gdn_ssm_problem *pr, const void *x, const void 
     sp.ob = sp.ot * pr->T;
     sp.sT = hT;
     sp.total = (double *)workspace;
-    sp.ends = (float *)workspace + (int64_t)s.n_items * s.n_hb * 4;
-    const int grid = ssm_grid(pr, sp, s);
-    if (need) {
-        sp.all_ends = hT != nullptr;
+    sp.ends = (float *)workspace + (int64_t)s.n_ends * s.n_hb * 4;
+    sp.all_ends = hT != nullptr && s.n_ends > 0;
+    if (s.n_ends > 0) {
+        const int grid = ssm_grid(pr, sp, s, true);
         st = launch_kernel(ssm_pick(pr, s, true), grid, &sp, (hipStream_t)stream, 256 * s.ncb);
         if (st != GDN_OK) return st;
     }
+    const int grid = ssm_grid(pr, sp, s, false);
     return launch_kernel(ssm_pick(pr, s, false), grid, &sp, (hipStream_t)stream, 256 * s.ncb);
 }
 

@@ -43,10 +43,10 @@ __global__ void __launch_bounds__(4 * N, sizeof(IO) == 4 ? 1 : NH == 1 && N == 1
     constexpr int GC = 2;
     __shared__ Gates gates[GC][NH];
     __shared__ float inner[NH][4][C], outer[NH][NW][C], dots[NH][NW];
-    int item, hb;
-    place(p, item, hb);
-    if (item >= p.n_items) return;
-    const Segment seg = find_segment(p, item);
+    int unit, hb;
+    place(p, unit, hb);
+    if (unit >= p.n_units) return;
+    const Segment seg = find_segment<false>(p, unit);
     if (!seg.live) return;
     const int w = wave_id(), l = lane_id(), q = l >> 4, j = l & 15;
     const int col0 = hb * COLS, head0 = col0 / p.P, grp = head0 / p.heads_per_group;
@@ -378,7 +378,7 @@ __global__ void __launch_bounds__(256) ssm_gate_kernel(GateParams gp) {
     const SsmParams &p = gp.s;
     __shared__ double red[4], wsum[4][5];
     const int head = blockIdx.x % p.H, item = blockIdx.x / p.H, tid = threadIdx.x;
-    const Segment seg = find_segment(p, item);
+    const Segment seg = find_segment<false>(p, item);
     if (!seg.live) {
         // a place that no segment has
         if (tid < 3) gp.grads[((int64_t)tid * p.n_items + item) * p.H + head] = 0.0;
@@ -501,7 +501,7 @@ BwdPlan bwd_plan(const gdn_ssm_problem *pr, bool packed) {
     b.slots = packed ? pr->T / kSsmChunk + pr->n_seqs + 1 : pr->B * ((pr->T + kSsmChunk - 1) / kSsmChunk);
     const int64_t per = 4 * kSsmChunk;
     b.marks = packed ? pr->T / per + pr->n_seqs + 1 : pr->B * ((pr->T + per - 1) / per);
-    const size_t blocks = (size_t)b.s.n_items * b.s.n_hb;
+    const size_t blocks = (size_t)b.s.n_ends * b.s.n_hb;
     size_t at = 0;
     auto take = [&](size_t n) {
         const size_t was = at;
@@ -545,21 +545,22 @@ struct BwdFns {
 template <typename F>
 gdn_status bwd_launches(const gdn_ssm_problem *pr, const BwdPlan &b, const SsmParams &fwd, const SsmParams &rev, GateParams &gp,
                         void *dx, void *dB, void *dC, float *dh0, hipStream_t s) {
-    const bool one = b.s.n_items == b.s.seqs;      // one segment each
     SsmParams f = fwd, r = rev;
-    const int grid = ssm_grid(pr, f, b.s);
-    ssm_grid(pr, r, b.s);
     gdn_status st = GDN_OK;
     auto go = [&](const void *fn, int g, SsmParams &sp, int threads) {
         if (st == GDN_OK) st = launch_kernel(fn, g, &sp, s, threads);
     };
-    if (!one) {
+    if (b.s.n_ends > 0) {
         // (the last segments' decays stand between dhT and the others)
         r.all_ends = dh0 != nullptr;
         f.all_ends = r.all_ends || r.s0;
-        go(F::ends(false), grid, f, F::kScanThreads);
-        go(F::ends(true), grid, r, F::kScanThreads);
+        const int ends = ssm_grid(pr, f, b.s, true);
+        ssm_grid(pr, r, b.s, true);
+        go(F::ends(false), ends, f, F::kScanThreads);
+        go(F::ends(true), ends, r, F::kScanThreads);
     }
+    const int grid = ssm_grid(pr, f, b.s, false);
+    ssm_grid(pr, r, b.s, false);
     SsmParams d = r;
     d.out = dx;
     d.sT = dh0;

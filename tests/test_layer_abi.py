@@ -290,6 +290,18 @@ def test_many_short_packed_sequences_are_taken(lib):
         assert lib.gdn_workspace_bytes_ssm_backward(ctypes.byref(pr)) > 0
 
 
+@pytest.mark.parametrize("T,H,P,N,G", [(16384, 64, 128, 128, 8), (16384, 80, 64, 128, 1), (131072, 64, 128, 128, 8), (5000, 3, 64, 64, 3)])
+def test_scan_workspace_has_no_state_for_a_short_sequence(lib, T, H, P, N, G):
+    # only sequences of several segments leave end states: at most twice as many
+    # places as one long sequence has, whatever the number of sequences
+    one = lib.gdn_workspace_bytes_ssm(ctypes.byref(packed_scan(T, 1, H, P, N, G)))
+    assert one > 0
+    for n in (2, 9, 256, 2048):
+        assert one <= lib.gdn_workspace_bytes_ssm(ctypes.byref(packed_scan(T, n, H, P, N, G))) <= 2 * one, n
+    # and none where no sequence can have two
+    assert lib.gdn_workspace_bytes_ssm(ctypes.byref(packed_scan(200, 7, H, P, N, G))) == 0
+
+
 # ---------------------------------------------------------------------------
 # the binding
 # ---------------------------------------------------------------------------
