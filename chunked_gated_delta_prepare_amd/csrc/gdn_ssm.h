@@ -44,9 +44,11 @@
 // the chunk before.  Every difference is one of terms inside one chunk: the
 // sum of r - dt c over a long stream, which is the same number, would drown
 // short memories in the rounding of far tokens.  For the same reason X is formed
-// anew every four chunks, and at a segment's end, as <h, dh>: the forward scan
-// leaves h there, and the reverse one meets it with dh.  (dA of 2 x 8192
-// tokens, 32 heads: 1.2e-5 off with X passed on over 16 chunks.)
+// anew every four chunks as <h, dh>: the forward scan leaves h there, and the
+// reverse one meets it with dh.  Behind a sequence's last chunk dh is the final
+// state's own gradient, so the forward scan forms X there itself and leaves no
+// state.  (dA of 2 x 8192 tokens, 32 heads: 1.2e-5 off with X passed on over 16
+// chunks.)
 //
 // Streams are cut into segments that run side by side: a first launch forms
 // every segment's end state from a zero start, a second one starts each
@@ -82,10 +84,11 @@ struct SsmParams {
     float *part;                            // out2 by block of columns, for ssm_sum_kernel
     float *inside, *across;                 // [n_hb][NH][B T]: q . out2 in two parts
     float *dyx, *wtt;                       // the same: dy_t . x_t, and W_tt / dt_t
-    float *marks;                           // [place][n_hb][N][64 NCB]: h every four chunks
-    double *X;                              // [place][n_hb][NH]: <h, dh> there
+    const float *dT;                        // the final states' gradient
+    float *marks;                           // [mark][n_hb][N][64 NCB]: h every four chunks
+    double *X;                              // [place][n_hb][NH]: <h, dh> there, and behind sequences
     int64_t rows;                           // B T
-    int n_slots, n_marks;                   // places for chunks in part, and for marks
+    int n_slots, n_marks, n_x;              // places for chunks in part, for marks and in X
     int T, H, P, n_seqs, heads_per_group;
     int seg_tokens, n_items, n_hb;          // tokens of a segment, segments in all, blocks of columns
     int n_ends, n_units;                    // places for end states; segments or ends that this launch works on
@@ -506,15 +509,26 @@ __device__ __forceinline__ int chunk_slot(const SsmParams &p, const Segment &s, 
     const int in = (s.begin - s.seq_begin) / kSsmChunk + c;
     return p.cu ? s.seq_begin / kSsmChunk + s.seq + in : s.seq * ((p.T + kSsmChunk - 1) / kSsmChunk) + in;
 }
-// The place of the state behind a chunk, or -1 where none is kept: behind
-// every fourth chunk of a sequence and behind a segment's last (a segment is a
-// multiple of four chunks, unless it is a sequence's last).
-__device__ __forceinline__ int mark_slot(const SsmParams &p, const Segment &s, int c) {
-    const int in = (s.begin - s.seq_begin) / kSsmChunk + c;
-    if ((in & 3) != 3 && c != chunks_of(s) - 1) return -1;
+// The places of the state behind a chunk and of its X, -1 where none is kept.  States
+// are kept behind every fourth chunk of a sequence but its last one; a sequence's
+// begin at its first token's 256th, since its places end before the next one's.
+// (With one for its last chunk too, places would be numbered by sequences, a
+// state each: 256 sequences of 64 tokens, 64 heads of 128 x 128, 1.3 GB and not
+// 0.3.)  X is a number, and has a place there too.
+struct Mark {
+    int state, x;
+};
+__device__ __forceinline__ Mark mark_of(const SsmParams &p, const Segment &s, int c) {
+    const int in = (s.begin - s.seq_begin) / kSsmChunk + c, chunks = (s.seq_end - s.seq_begin + kSsmChunk - 1) / kSsmChunk;
+    const bool last = in == chunks - 1;
+    Mark m{-1, -1};
+    if ((in & 3) != 3 && !last) return m;
     const int per = 4 * kSsmChunk;
-    const int m = (p.cu ? s.seq_begin / per + s.seq : s.seq * ((p.T + per - 1) / per)) + in / 4;
-    return m < p.n_marks ? m : -1;
+    m.x = (p.cu ? s.seq_begin / per + s.seq : s.seq * ((p.T + per - 1) / per)) + in / 4;
+    if (m.x >= p.n_x) m.x = -1;
+    if (!last) m.state = (p.cu ? s.seq_begin / per : s.seq * ((p.T - 1) / per)) + in / 4;
+    if (m.state >= p.n_marks) m.state = -1;
+    return m;
 }
 
 // The raw dt of row l of a chunk, as its bits: turned into a number only where

@@ -131,11 +131,11 @@ __global__ void __launch_bounds__(4 * N, sizeof(IO) == 4 ? 1 : NH == 1 && N == 1
         tz.put(tid, sz, rows);
         tk.put(tid, sk, rows);
         tq.put(tid, sq, rows);
-        const int mark = mark_slot(p, seg, REV ? nc - 1 - c : c);
+        const Mark mark = mark_of(p, seg, REV ? nc - 1 - c : c);
         if constexpr (REV) {
             // behind this chunk h meets the state's gradient
-            if (mark >= 0) {
-                const float2 *m = (const float2 *)p.marks + ((int64_t)mark * p.n_hb + hb) * (N * COLS / 2) + tid;
+            if (mark.state >= 0) {
+                const float2 *m = (const float2 *)p.marks + ((int64_t)mark.state * p.n_hb + hb) * (N * COLS / 2) + tid;
 #pragma unroll
                 for (int hh = 0; hh < NH; ++hh) {
                     float d = 0.f;
@@ -152,12 +152,12 @@ __global__ void __launch_bounds__(4 * N, sizeof(IO) == 4 ? 1 : NH == 1 && N == 1
         lds_barrier();
         const Gates *gs = gates[c % GC];
         if constexpr (REV) {
-            if (mark >= 0 && w < NH && l == 0) {
+            if (mark.state >= 0 && mark.x >= 0 && w < NH && l == 0) {
                 double d = 0.0;
 #pragma unroll
                 for (int k = 0; k < NW; ++k) d += (double)dots[w][k];
                 // h behind chunk nc - 1 - c has that one's sign turned, dh chunk c's
-                p.X[((int64_t)mark * p.n_hb + hb) * NH + w] = nc & 1 ? -d : d;
+                p.X[((int64_t)mark.x * p.n_hb + hb) * NH + w] = nc & 1 ? -d : d;
             }
         }
         // 1
@@ -287,14 +287,41 @@ __global__ void __launch_bounds__(4 * N, sizeof(IO) == 4 ? 1 : NH == 1 && N == 1
             }
         }
         if constexpr (!REV) {
-            if (mark >= 0) {
-                float2 *m = (float2 *)p.marks + ((int64_t)mark * p.n_hb + hb) * (N * COLS / 2) + tid;
+            if (mark.state >= 0) {
+                float2 *m = (float2 *)p.marks + ((int64_t)mark.state * p.n_hb + hb) * (N * COLS / 2) + tid;
 #pragma unroll
                 for (int pb = 0; pb < PB; ++pb) {
                     m[(2 * pb) * kThreads] = make_float2(h[pb][0], h[pb][1]);
                     m[(2 * pb + 1) * kThreads] = make_float2(h[pb][2], h[pb][3]);
                 }
             }
+        }
+    }
+    if constexpr (!REV) {
+        // behind a sequence: h, as the last chunk left its sign, and the final state's gradient
+        if (nc == 0 || seg.end != seg.seq_end) return;
+#pragma unroll
+        for (int hh = 0; hh < NH; ++hh) {
+            float d = 0.f;
+            if (p.dT) {
+#pragma unroll
+                for (int pb = hh * (PB / NH); pb < (hh + 1) * (PB / NH); ++pb) {
+                    const int col = col0 + col_of(pb);
+                    const float *s = p.dT + (((int64_t)seg.seq * p.H + col / p.P) * N + wn + j) * p.P + col % p.P;
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) d += h[pb][e] * s[e];
+                }
+            }
+            d = wave_sum(d);
+            if (l == 0) dots[hh][w] = d;
+        }
+        lds_barrier();
+        const Mark mark = mark_of(p, seg, nc - 1);
+        if (mark.x >= 0 && w < NH && l == 0) {
+            double d = 0.0;
+#pragma unroll
+            for (int k = 0; k < NW; ++k) d += (double)dots[w][k];
+            p.X[((int64_t)mark.x * p.n_hb + hb) * NH + w] = nc & 1 ? -d : d;
         }
     }
 }
@@ -417,7 +444,7 @@ __global__ void __launch_bounds__(256) ssm_gate_kernel(GateParams gp) {
         const bool cut = (float)last_lane(wave_scan((double)dt * (double)A)) < -16.6f;
         __syncthreads();
         if (l == 0) {
-            const int mark = c0 >= w ? mark_slot(p, seg, c0 - w) : -1;
+            const int mark = c0 >= w ? mark_of(p, seg, c0 - w).x : -1;
             wsum[w][0] = all_ca;
             wsum[w][1] = all_ra;
             wsum[w][2] = cut ? 0.0 : 1.0;
@@ -490,7 +517,7 @@ namespace {
 
 struct BwdPlan {
     SsmPlan s;
-    int64_t slots, marks, rows;
+    int64_t slots, marks, xs, rows;
     size_t total, ends, ends_rev, sums[6], mark, X, part, grads, bytes;      // offsets
 };
 
@@ -500,7 +527,8 @@ BwdPlan bwd_plan(const gdn_ssm_problem *pr, bool packed) {
     b.rows = pr->B * pr->T;
     b.slots = packed ? pr->T / kSsmChunk + pr->n_seqs + 1 : pr->B * ((pr->T + kSsmChunk - 1) / kSsmChunk);
     const int64_t per = 4 * kSsmChunk;
-    b.marks = packed ? pr->T / per + pr->n_seqs + 1 : pr->B * ((pr->T + per - 1) / per);
+    b.marks = packed ? pr->T / per : pr->T > 0 ? pr->B * ((pr->T - 1) / per) : 0;
+    b.xs = packed ? pr->T / per + pr->n_seqs + 1 : pr->B * ((pr->T + per - 1) / per);
     const size_t blocks = (size_t)b.s.n_ends * b.s.n_hb;
     size_t at = 0;
     auto take = [&](size_t n) {
@@ -513,7 +541,7 @@ BwdPlan bwd_plan(const gdn_ssm_problem *pr, bool packed) {
     b.ends_rev = take(blocks * pr->N * 64 * b.s.ncb * 4);
     for (size_t &o : b.sums) o = take((size_t)b.s.n_hb * b.s.nh * b.rows * 4);
     b.mark = take((size_t)b.marks * b.s.n_hb * pr->N * 64 * b.s.ncb * 4);
-    b.X = take((size_t)b.marks * b.s.n_hb * b.s.nh * 8);
+    b.X = take((size_t)b.xs * b.s.n_hb * b.s.nh * 8);
     b.part = take((size_t)b.slots * b.s.n_hb * kSsmChunk * pr->N * 4);
     b.grads = take((size_t)b.s.n_items * pr->H * 3 * 8);
     b.bytes = at;
@@ -628,6 +656,7 @@ gdn_status gdn_ssm_backward(const gdn_ssm_problem *pr, const void *dy, const voi
     f.marks = (float *)(ws + b.mark);
     f.X = (double *)(ws + b.X);
     f.n_marks = (int)b.marks;
+    f.n_x = (int)b.xs;
     f.rows = b.rows;
     f.ob = pr->dxbc_stride_b;
     f.ot = pr->dxbc_stride_t;
@@ -642,6 +671,7 @@ gdn_status gdn_ssm_backward(const gdn_ssm_problem *pr, const void *dy, const voi
     f.q2b = yb;
     f.q2t = yt;
     f.s0 = h0;
+    f.dT = dhT;
     f.ends = (float *)(ws + b.ends);
     f.inside = (float *)(ws + b.sums[0]);
     f.across = (float *)(ws + b.sums[1]);

@@ -302,6 +302,17 @@ def test_scan_workspace_has_no_state_for_a_short_sequence(lib, T, H, P, N, G):
     assert lib.gdn_workspace_bytes_ssm(ctypes.byref(packed_scan(200, 7, H, P, N, G))) == 0
 
 
+@pytest.mark.parametrize("T,H,P,N,G", [(16384, 64, 128, 128, 8), (16384, 80, 64, 128, 1), (131072, 64, 128, 128, 8), (5000, 3, 64, 64, 3)])
+def test_scan_backward_workspace_has_no_state_for_a_short_sequence(lib, T, H, P, N, G):
+    # a sequence brings at most one more chunk of the heads' shares of dB and dC (64 x N
+    # fp32 a block of columns), its sums, and end states as above
+    size = lambda n: lib.gdn_workspace_bytes_ssm_backward(ctypes.byref(packed_scan(T, n, H, P, N, G)))  # noqa: E731
+    blocks = H if P == 128 or (H // G) % 2 else H // 2
+    ends = 2 * lib.gdn_workspace_bytes_ssm(ctypes.byref(packed_scan(T, 1, H, P, N, G)))
+    for n in (2, 9, 256, 2048):
+        assert size(n) - size(1) <= (n - 1) * (blocks * 64 * N * 4 + 64 * H) + ends, n
+
+
 # ---------------------------------------------------------------------------
 # the binding
 # ---------------------------------------------------------------------------
