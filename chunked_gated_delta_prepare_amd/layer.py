@@ -399,7 +399,7 @@ def conv_step(x, state, weight, bias=None, *, activation="silu", slots=None, y=N
     _check(state, "state", dev, (state.shape[0], W - 1, D), x.dtype)
     if slots is not None:
         _check(slots, "slots", dev, (B,), torch.int32)
-    _apart(state, "state", x)
+    _apart(state, "state", x, weight, bias, slots)
     return _on(dev, stream, _conv_step, dev, code, x, state, weight, bias, _silu(activation), slots, y)
 
 
@@ -567,7 +567,7 @@ def ssm_step(x, dt, A, B, C, state, D=None, dt_bias=None, *, dt_softplus=True, s
     _check(state, "state", dev, (state.shape[0], H, B.shape[2], P), torch.float32)
     if slots is not None:
         _check(slots, "slots", dev, (b,), torch.int32)
-    _apart(state, "state", x)
+    _apart(state, "state", x, dt, A, B, C, D, dt_bias, slots)
     return _on(dev, stream, _ssm_step, dev, code, x, dt, A, B, C, state, D, dt_bias, 1 if dt_softplus else 0, slots, y)
 
 

@@ -80,3 +80,27 @@ def test_the_library_loads_without_torch():
     run = subprocess.run([sys.executable, "-c", code], capture_output=True, text=True,
                          cwd=os.path.dirname(os.path.dirname(os.path.abspath(__file__))))
     assert run.returncode == 0, run.stderr
+
+
+def test_the_steps_states_share_memory_with_no_input(calls):
+    """A state is written in place while other rows and heads still read the inputs."""
+    B, D, W, S = 3, 64, 4, 5
+    pool = torch.zeros(S, W - 1, D)
+    at = lambda *shape, first=0: pool.view(-1)[first:first + torch.Size(shape).numel()].view(*shape)  # noqa: E731
+    x, w, b = torch.zeros(B, D), torch.zeros(D, W), torch.zeros(D)
+    slots = torch.zeros(B, dtype=torch.int32)
+    gdn.conv_step(x, pool, w, b, slots=slots)
+    for kw in (dict(x=at(B, D)), dict(weight=at(D, W, first=7)), dict(bias=at(D, first=S * (W - 1) * D - D)),
+               dict(slots=pool.view(torch.int32).view(-1)[:B])):
+        with pytest.raises(ValueError, match="share memory"):
+            gdn.conv_step(**{**dict(x=x, state=pool, weight=w, bias=b, slots=slots), **kw})
+    H, P, N, G = 2, 64, 64, 1
+    pool = torch.zeros(S, H, N, P)
+    d = dict(x=torch.zeros(B, H, P), dt=torch.zeros(B, H), A=-torch.ones(H), B=torch.zeros(B, G, N), C=torch.zeros(B, G, N),
+             D=torch.ones(H), dt_bias=torch.zeros(H), slots=slots)
+    gdn.ssm_step(**d, state=pool)
+    for k in d:
+        inside = (pool.view(torch.int32) if k == "slots" else pool).view(-1)[64:64 + d[k].numel()].view(d[k].shape)
+        with pytest.raises(ValueError, match="share memory"):
+            gdn.ssm_step(**{**d, k: inside}, state=pool)
+    assert [c[0] for c in calls] == ["gdn_conv_step", "gdn_ssm_step"]
