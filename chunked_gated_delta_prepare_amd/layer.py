@@ -132,6 +132,12 @@ def _workspace(need, device, workspace):
     return workspace, (0 if workspace is None else workspace.numel() * workspace.element_size())
 
 
+def _unwritten(t, name, without):
+    """A given output that the call has no values for."""
+    if t is not None:
+        raise ValueError("%s is not written without %s" % (name, without))
+
+
 def _out(t, name, device, shape, dtype, inputs, like=None):
     """A given output, checked, or a new one; like: a tensor of its shape, if there
     is one (a call less to torch's slower ways)."""
@@ -214,12 +220,12 @@ def _norm_forward(handle, dev, code, x, weight, residual, eps, od, group, y, s, 
         else:
             s = _out(s, "s", dev, shape, residual.dtype, (x, weight, residual, y), residual)
     else:
-        s = None
+        _unwritten(s, "s", "a residual")
     if od is _FP8:
         scales = _out(scales, "scales", dev, shape[:-1] + ((D + group - 1) // group if group else 1,), torch.float32,
                       (x, weight, residual, y, s))
     else:
-        scales = None
+        _unwritten(scales, "scales", "an 8-bit output")
     pr, _ = _problem(NormProblem, None, rows, D, stride, code, scode, _CODE[weight.dtype], _CODE[od], group, eps)
     _call("gdn_norm_forward", pr, x.data_ptr(), _ptr(residual), weight.data_ptr(), y.data_ptr(), _ptr(s), _ptr(scales), handle)
     return y, s, scales
@@ -357,6 +363,10 @@ def conv_backward(dy, x, weight, bias=None, *, activation="silu", initial_state=
     dbias [D] fp32 or None, dinitial or None): dbias with a bias, dinitial
     with an initial_state."""
     dev, code, D, W = _conv_checks(x, weight, bias, 3)
+    if bias is None:
+        _unwritten(dbias, "dbias", "a bias")
+    if initial_state is None:
+        _unwritten(dinitial, "dinitial", "an initial_state")
     _check(dy, "dy", dev, x.shape, x.dtype, dense=False)
     n = _packed(cu_seqlens, dev, x.shape[0])
     for t, name in ((initial_state, "initial_state"), (dfinal, "dfinal")):
@@ -490,6 +500,9 @@ def ssm_backward(dy, x, dt, A, B, C, D=None, dt_bias=None, h0=None, dhT=None, *,
     n = _packed(cu_seqlens, dev, x.shape[0])
     st = (n or x.shape[0], x.shape[2], B.shape[3], x.shape[3])
     _check(dy, "dy", dev, x.shape, x.dtype)
+    for t, name, of, what in ((dD, "dD", D, "D"), (ddt_bias, "ddt_bias", dt_bias, "dt_bias"), (dh0, "dh0", h0, "h0")):
+        if of is None:
+            _unwritten(t, name, what)
     for t, name in ((h0, "h0"), (dhT, "dhT")):
         if t is not None:
             _check(t, name, dev, st, torch.float32)

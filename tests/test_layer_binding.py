@@ -104,3 +104,21 @@ def test_the_steps_states_share_memory_with_no_input(calls):
         with pytest.raises(ValueError, match="share memory"):
             gdn.ssm_step(**{**d, k: inside}, state=pool)
     assert [c[0] for c in calls] == ["gdn_conv_step", "gdn_ssm_step"]
+
+
+def test_outputs_that_would_not_be_written_are_refused(calls):
+    x, w = torch.zeros(4, 64), torch.ones(64)
+    with pytest.raises(ValueError, match="residual"):
+        gdn.norm_forward(x, w, s=torch.zeros(4, 64))
+    with pytest.raises(ValueError, match="scales"):
+        gdn.norm_forward(x, w, scales=torch.zeros(4, 1))
+    taps, tokens = torch.zeros(64, 4), torch.zeros(1, 7, 64)
+    with pytest.raises(ValueError, match="dbias"):
+        gdn.conv_backward(tokens, tokens, taps, dbias=torch.zeros(64))
+    with pytest.raises(ValueError, match="dinitial"):
+        gdn.conv_backward(tokens, tokens, taps, dinitial=torch.zeros(1, 3, 64))
+    d = scan(1, 5)
+    for name, shape in (("dD", (4,)), ("ddt_bias", (4,)), ("dh0", (1, 4, 64, 64))):
+        with pytest.raises(ValueError, match=name):
+            gdn.ssm_backward(*d.args, **{name: torch.zeros(shape)})
+    assert not calls
