@@ -350,15 +350,16 @@ __device__ __forceinline__ float dt_of(const SsmParams &p, float raw, float bias
 }
 
 // `before` and `behind` are the signs that the state is held with before and
-// behind the chunk.
+// behind the chunk.  A row without a token has gate 0 by `live`, not by its dt of
+// 0: A may be -inf, and 0 times that is no number.
 template <bool REV>
-__device__ __forceinline__ void make_gates(Gates &g, float dt, float A, float before, float behind) {
+__device__ __forceinline__ void make_gates(Gates &g, float dt, float A, bool live, float before, float behind) {
     const int l = again(lane_id());
     asm volatile("" : "+s"(A));                // (its double is not kept in registers either)
     // a gate below e^-1000 is 0 to all that follows; without the bound one of
     // -1e20 would take the digits of the sums behind it, one of -inf all of them
     // (a NaN stays one)
-    const double raw = (double)dt * (double)A, own = (raw < -1000.0 ? -1000.0 : raw) * 1.4426950408889634074, upto = wave_scan(own);
+    const double raw = (double)dt * (double)A, own = live ? (raw < -1000.0 ? -1000.0 : raw) * 1.4426950408889634074 : 0.0, upto = wave_scan(own);
     const double total = last_lane(upto), cum = REV ? upto - own : upto;
     const float hi = (float)cum, w = REV ? 1.f : dt;
     g.cum[l] = make_float2(hi, (float)(cum - (double)hi));
@@ -686,7 +687,8 @@ __global__ void __launch_bounds__(4 * COLS, sizeof(IO) == 4 ? 1 : COLS == 64 && 
         if (gater && c + gc < nc) {
             int lo;
             const int rows = chunk_of<REV>(seg, c + gc, lo);
-            make_gates<REV>(gates[gc][gh], dt_of(p, raw_value<IO>(p, raw), bias, again(lane_id()) < rows), A, 1.f, 1.f);
+            const bool live = again(lane_id()) < rows;
+            make_gates<REV>(gates[gc][gh], dt_of(p, raw_value<IO>(p, raw), bias, live), A, live, 1.f, 1.f);
         }
     };
     double total = 0.0;

@@ -106,7 +106,8 @@ __global__ void __launch_bounds__(4 * N, sizeof(IO) == 4 ? 1 : NH == 1 && N == 1
         if (gater && c + gc < nc) {
             int lo;
             const int rows = chunk_of<REV>(seg, c + gc, lo);
-            make_gates<REV>(gates[gc][gh], dt_of(p, raw_value<IO>(p, raw), bias, again(lane_id()) < rows), A,
+            const bool live = again(lane_id()) < rows;
+            make_gates<REV>(gates[gc][gh], dt_of(p, raw_value<IO>(p, raw), bias, live), A, live,
                              (c + gc) & 1 ? -1.f : 1.f, (c + gc) & 1 ? 1.f : -1.f);
         }
     };
@@ -441,7 +442,7 @@ __global__ void __launch_bounds__(256) ssm_gate_kernel(GateParams gp) {
         const double pre_in = wave_scan(in), pre_ca = wave_scan(dca), pre_ra = wave_scan((double)ra);
         const double all_in = last_lane(pre_in), all_ca = last_lane(pre_ca), all_ra = last_lane(pre_ra);
         // nothing of weight crosses a chunk whose decay is below fp32's step
-        const bool cut = (float)last_lane(wave_scan((double)dt * (double)A)) < -16.6f;
+        const bool cut = (float)last_lane(wave_scan(on ? (double)dt * (double)A : 0.0)) < -16.6f;
         __syncthreads();
         if (l == 0) {
             const int mark = c0 >= w ? mark_of(p, seg, c0 - w).x : -1;

@@ -565,3 +565,36 @@ def test_many_packed_sequences_are_each_their_own(H, P, N, G, dt):
                 assert torch.equal(u, v), k
             else:
                 assert float((u.double() - v.double()).norm()) <= 2.0 ** -6 * float(v.double().norm()), k
+
+
+@pytest.mark.parametrize("dt", [BF, F32])
+@pytest.mark.parametrize("lens", [(2, 150), [100, 0, 64, 37], (1, 700)])
+def test_a_gate_of_minus_infinity(lens, dt):
+    """A = -inf: every token clears the state before it, also where a sequence ends
+    inside a chunk.  (dt's gradient has A times a zero there: no number.)"""
+    packed = isinstance(lens, list)
+    B, T = (1, sum(lens)) if packed else lens
+    each = lens if packed else [T] * B
+    n, H, P, N = len(each), 2, 64, 64
+    d = inputs(B, T, H, P, N, 1, dt, F32, n, True)
+    d["A"] = torch.tensor([float("-inf"), -2.0], device=DEV)
+    d["dt"], d["dt_bias"] = rnd(B, T, H, seed=5).abs() * 0.1 + 0.01, None
+    cu = offsets(lens) if packed else None
+    y, hT = forward(d, dt_softplus=False, cu_seqlens=cu)
+    args = (flat(d["x"]), flat(d["dt"]), d["A"], flat(d["B"]), flat(d["C"]), d["D"], d["h0"], each)
+    ref, rT = L.ssm(*args)
+    Y, Z = L.ssm(*args, absolute=True)
+    b = dt is BF
+    close(flat(y), ref, ref.abs() * HALF[dt] + Y * (2 * 2.0 ** -8 * b + FP), "y")
+    close(hT, rT, Z * FP, "hT")
+    dy, dhT = rnd(B, T, H, P, seed=8, dtype=dt), rnd(n, H, N, P, seed=9)
+    dx, ddt, dA, dB, dC, dD, _, dh0 = gdn.ssm_backward(dy, d["x"], d["dt"], d["A"], d["B"], d["C"], d["D"], None, d["h0"], dhT,
+                                                       dt_softplus=False, cu_seqlens=cu)
+    g = L.ssm_grad(flat(dy), *args, dhT)
+    a = L.ssm_grad(flat(dy), *args, dhT, absolute=True)
+    close(flat(dx), g["dx"], g["dx"].abs() * HALF[dt] + a["dx"] * (2 * 2.0 ** -8 * b + FP), "dx")
+    for k, v in (("dB", dB), ("dC", dC)):
+        close(flat(v), g[k], g[k].abs() * HALF[dt] + a[k] * (2.0 ** -8 * b + FP), k)
+    close(dh0, g["dh0"], a["dh0"] * FP, "dh0")
+    close(dA, g["dA"], (a["pairs"] * flat(d["dt"]).cpu().double()).sum(0) * FP, "dA")
+    assert ddt[..., 1].isfinite().all()
