@@ -60,11 +60,19 @@ __device__ __forceinline__ uint32_t clamp_e4m3(float x) {
     return __float_as_uint(x > kE4m3Max ? kE4m3Max : x < -kE4m3Max ? -kE4m3Max : x);
 }
 
+// v / scale as a division rounds it: the product with the reciprocal, and what that
+// leaves over of v once more.  (bf16 rows and weights put many quotients at e4m3's
+// halfway points exactly, where the product alone goes to either side; a division
+// costs ten instructions.)  A scale of infinity leaves nothing over.
 template <int VEC>
-__device__ __forceinline__ void store_e4m3(rsrc_t r, uint32_t e, const float (&v)[VEC], float inv) {
+__device__ __forceinline__ void store_e4m3(rsrc_t r, uint32_t e, const float (&v)[VEC], float scale) {
+    const float inv = 1.f / scale, back = scale <= 3.40282347e38f ? scale : 0.f;
     float c[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-    for (int i = 0; i < VEC; ++i) c[i] = __uint_as_float(clamp_e4m3(v[i] * inv));
+    for (int i = 0; i < VEC; ++i) {
+        const float q = v[i] * inv;
+        c[i] = __uint_as_float(clamp_e4m3(fmaf(fmaf(-q, back, v[i]), inv, q)));
+    }
     int q = __builtin_amdgcn_cvt_pk_fp8_f32(c[0], c[1], 0, false);
     if constexpr (VEC == 4) {
         q = __builtin_amdgcn_cvt_pk_fp8_f32(c[2], c[3], q, true);
@@ -144,9 +152,9 @@ __global__ void __launch_bounds__(TPR < 256 ? 256 : TPR) norm_forward_kernel(Nor
 #pragma unroll
             for (int k = 0; k < TPR / 64; ++k) amax = fmaxf(amax, red[k]);
         }
-        const float scale = fmaxf(amax / kE4m3Max, kTinyScale), inv = 1.f / scale;
+        const float scale = fmaxf(amax / kE4m3Max, kTinyScale);
 #pragma unroll
-        for (int k = 0; k < K; ++k) store_e4m3<VEC>(ry, (k * TPR + tid) * VEC, s[k], inv);
+        for (int k = 0; k < K; ++k) store_e4m3<VEC>(ry, (k * TPR + tid) * VEC, s[k], scale);
         if (tid == 0 && live) p.scales[at] = scale;
         return;
     }
@@ -161,7 +169,7 @@ __global__ void __launch_bounds__(TPR < 256 ? 256 : TPR) norm_forward_kernel(Nor
             for (int i = 0; i < VEC; ++i) m = fmaxf(m, fabsf(s[k][i]));
             m = lanes_max<kL>(m);
             const float scale = fmaxf(m / kE4m3Max, kTinyScale);
-            store_e4m3<VEC>(ry, (k * TPR + tid) * VEC, s[k], 1.f / scale);
+            store_e4m3<VEC>(ry, (k * TPR + tid) * VEC, s[k], scale);
             const int gi = ((k * TPR + tid) * VEC) >> 7;
             if ((tid & (kL - 1)) == 0 && gi < ng && live) p.scales[at * ng + gi] = scale;
         }
@@ -180,7 +188,7 @@ __global__ void __launch_bounds__(TPR < 256 ? 256 : TPR) norm_forward_kernel(Nor
         for (int k = 0; k < K; ++k) {
             const int gi = (k * TPR + tid) >> 7;
             const float scale = fmaxf(__uint_as_float(gmax[sub][gi]) / kE4m3Max, kTinyScale);
-            store_e4m3<VEC>(ry, k * TPR + tid, s[k], 1.f / scale);
+            store_e4m3<VEC>(ry, k * TPR + tid, s[k], scale);
             if (((k * TPR + tid) & 127) == 0 && gi < ng && live) p.scales[at * ng + gi] = scale;
         }
     }

@@ -222,3 +222,41 @@ def test_streams_graphs_and_repeats():
         g.replay()
         torch.cuda.synchronize()
         assert all(torch.equal(a, b) for a, b in zip(out, work())), k
+
+
+@pytest.mark.parametrize("D,group", [(64, 0), (256, 0), (1024, 128), (4096, 0), (8192, 128), (16384, 128)])
+@pytest.mark.parametrize("at", [0, 1, 2])
+def test_eight_bit_ties_are_those_of_the_quotient(D, group, at):
+    """Rows of ones: r = 1 and y is the weight itself, so the stored values are e4m3 of
+    weight / scale, bit for bit.  The weights lie at halfway points times the scale,
+    where a product with 1 / scale rounds to the other side now and then."""
+    g = torch.Generator().manual_seed(D + at)
+    n = group or D
+    amax = torch.rand(D // n, generator=g) * 6 + 1
+    scale = amax / 448
+    tie = (torch.randint(8, 16, (D // n, n), generator=g) + 0.5) * 2.0 ** torch.randint(-8, 5, (D // n, n), generator=g).float()
+    w = tie * scale[:, None] * torch.where(torch.rand(D // n, n, generator=g) < 0.5, -1.0, 1.0)
+    w[:, 0] = amax
+    want = (w / scale[:, None]).to(FP8).reshape(-1)
+    # (the weight's alignment chooses how many elements a lane takes)
+    weight = torch.empty(D + at, device=DEV)[at:].copy_(w.reshape(-1))
+    q, _, s = gdn.norm_forward(torch.ones(3, D, device=DEV), weight, eps=0.0, out_dtype=FP8, group=group)
+    assert torch.equal(s.cpu(), scale.reshape(1, -1).expand(3, -1))
+    assert torch.equal(q.cpu().view(torch.uint8), want.view(torch.uint8).expand(3, -1))
+
+
+def test_eight_bit_rows_with_infinite_values():
+    """An infinite weight: the largest value is infinite, its quotient no number, and
+    every finite value over the infinite scale zero."""
+    x = torch.ones(2, 256, device=DEV)
+    w = torch.full((256,), 2.0, device=DEV)
+    w[200] = float("inf")
+    for group in (0, 128):
+        q, _, scale = gdn.norm_forward(x, w, eps=0.0, out_dtype=FP8, group=group)
+        hit = slice(128 if group else 0, 256)
+        f = q.float()
+        assert f[:, 200].isnan().all() and scale[:, -1].isinf().all()
+        rest = torch.cat([f[:, hit][:, :200 - hit.start], f[:, 201:]], 1)
+        assert rest.eq(0).all()
+        if group:
+            assert f[:, :128].eq(448).all() and scale[:, 0].eq(2.0 / 448).all()
