@@ -178,7 +178,7 @@ __global__ void __launch_bounds__(4 * N, sizeof(IO) == 4 ? 1 : NH == 1 && N == 1
 #pragma unroll
                     for (int k = hh * (COLS / NH); k < (hh + 1) * (COLS / NH); k += 32)
                         O::mma(x, O::template row<COLS>(sv, aP, 16 * bk, k), O::template row<COLS>(sz, aP, 16 * bi, k));
-                    const float4v d = x * decays<REV>(gs[hh], ii, k0);
+                    const float4v d = until(ii, k0, x * decays<REV>(gs[hh], ii, k0));
                     m += d * (REV ? gs[hh].dt[ii] : 1.f);
                     float sum = 0.f;
 #pragma unroll

@@ -461,8 +461,8 @@ def ssm_forward(x, dt, A, B, C, D=None, dt_bias=None, h0=None, *, dt_softplus=Tr
     x [b, T, H, P], B and C [b, T, G, N] (tokens may be strided, rows 16-byte
     aligned), P and N 64 or 128, H a multiple of G; dt [b, T, H] in x's type or
     fp32; A, D, dt_bias [H] fp32; h0 [b, H, N, P] fp32, or [n, H, N, P] with
-    cu_seqlens (as in conv_forward).  A NaN in a token also reaches those before
-    it in the same 64 of its sequence.  Returns (y [b, T, H, P], hT like h0 or
+    cu_seqlens (as in conv_forward).  A NaN in a token reaches neither the
+    tokens before it nor other sequences.  Returns (y [b, T, H, P], hT like h0 or
     None); y does not depend on whether hT is asked for."""
     dev, code = _ssm_checks(x, dt, A, B, C, D, dt_bias, 2)
     n = _packed(cu_seqlens, dev, x.shape[0])

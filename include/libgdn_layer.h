@@ -161,9 +161,10 @@ gdn_status gdn_conv_step(const gdn_conv_problem *problem, const void *x, const v
  * with dt_t = softplus(raw_t + dt_bias) or raw_t + dt_bias, A <= 0 and D per
  * head, and B_t, C_t [N] shared by the H / G heads of a group: the gated
  * recurrence of gdn_forward (q = C, k = B, v = dt x, g = dt A) without its
- * erase term.  Tokens are worked on 64 at a time from a sequence's first: a NaN
- * or an infinity in one of them reaches those of the same 64 before it too, but
- * neither earlier ones nor another sequence.
+ * erase term.  A token's y is of the tokens up to it: a NaN or an infinity in a
+ * later one, or in another sequence, does not reach it.  A sequence that holds
+ * one may have NaN in any of its gradients; another sequence's dx, ddt, dB, dC
+ * and dh0 are not touched by it.
  */
 typedef struct gdn_ssm_problem {
     int64_t B, T, H, P, N, G; /* P, N in {64, 128}; H a multiple of G */

@@ -598,3 +598,30 @@ def test_a_gate_of_minus_infinity(lens, dt):
     close(dh0, g["dh0"], a["dh0"] * FP, "dh0")
     close(dA, g["dA"], (a["pairs"] * flat(d["dt"]).cpu().double()).sum(0) * FP, "dA")
     assert ddt[..., 1].isfinite().all()
+
+
+@pytest.mark.parametrize("value", [float("nan"), float("inf")])
+@pytest.mark.parametrize("name", ["x", "B", "C", "dt"])
+@pytest.mark.parametrize("P,N,dt", [(64, 128, BF), (128, 64, BF), (128, 128, F32), (64, 64, F32)])
+def test_tokens_before_a_nan_do_not_see_it(name, value, P, N, dt):
+    """A token's y is of the tokens up to it: NaN and infinity behind it, in its chunk
+    or later, leave it as it is, as single-token steps do."""
+    B, T, H, G, bad = 2, 150, 4, 2, 101
+    d = inputs(B, T, H, P, N, G, dt, dt, B, True)
+    step, _ = L.step_sizes(flat(d["dt"]), d["dt_bias"], True)
+    args = (flat(d["x"]), step, d["A"], flat(d["B"]), flat(d["C"]), d["D"], d["h0"], [T] * B)
+    ref, _ = L.ssm(*args)
+    Y, _ = L.ssm(*args, absolute=True)
+    clean, hT = forward(d)
+    d[name][0, bad] = value
+    y, kT = forward(d)
+    tol = ref.abs() * HALF[dt] + Y * (2 * 2.0 ** -8 * (dt is BF) + FP)
+    before = slice(0, bad)                              # of the first batch
+    close(flat(y)[before], ref[before], tol[before], "y before")
+    assert torch.equal(y[1], clean[1]) and torch.equal(kT[1], hT[1])
+    if name == "C":                                     # only its own token reads C
+        close(flat(y)[bad + 1:], ref[bad + 1:], tol[bad + 1:], "y behind")
+        assert torch.equal(kT, hT)
+    else:
+        assert not kT[0].isfinite().all()
+    assert not y[0, bad].isfinite().all()
