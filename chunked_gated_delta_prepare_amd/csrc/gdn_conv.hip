@@ -535,8 +535,8 @@ gdn_status check_conv(const gdn_conv_problem *pr, bool packed) {
     for (int64_t v : {pr->x_stride_t, pr->dy_stride_t})
         if (v < 0 || v > (1 << 23)) return GDN_ERR_UNSUPPORTED;
     if (pr->D > (1 << 23)) return GDN_ERR_UNSUPPORTED;
-    const int64_t waves = ((pr->D + 63) / 64) * (pr->B * ((pr->T + 31) / 32) + (packed ? pr->n_seqs : pr->B));
-    if (!grid_ok(waves, 64)) return GDN_ERR_UNSUPPORTED;
+    const int64_t jobs = pr->B * ((pr->T + 31) / 32) + (packed ? pr->n_seqs : pr->B);
+    if (!grid_ok(jobs, (pr->D + 63) / 64 * 64)) return GDN_ERR_UNSUPPORTED;
     return GDN_OK;
 }
 

@@ -16,8 +16,8 @@ bool tracing();
 
 inline bool aligned_to(const void *p, size_t n) { return ((uintptr_t)p & (n - 1)) == 0; }
 inline int dtype_bytes(int dt) { return dt == GDN_F32 ? 4 : dt == GDN_BF16 ? 2 : 1; }
-// A launch has fewer than 2^32 threads.
-inline bool grid_ok(int64_t wgs, int64_t threads) { return wgs * threads < ((int64_t)1 << 32); }
+// A launch has fewer than 2^32 threads (threads > 0; the product itself may pass 64 bits).
+inline bool grid_ok(int64_t wgs, int64_t threads) { return wgs <= (((int64_t)1 << 32) - 1) / threads; }
 inline bool io_dtype_ok(int dt) { return dt == GDN_F32 || dt == GDN_BF16; }
 
 // ---------------------------------------------------------------------------

@@ -220,6 +220,14 @@ def test_launches_of_too_many_threads_refused(lib):
     assert lib.gdn_workspace_bytes_ssm_backward(ctypes.byref(ssm_problem(B=1 << 14, T=1, H=64, G=1, x_stride_t=64 * 64))) > 0
 
 
+@pytest.mark.parametrize("B,T,D", [(1 << 24, ((1 << 24) - 1) * 32, 1 << 23), (1 << 24, ((1 << 25) - 1) * 32, 1 << 22),
+                                   (1 << 22, ((1 << 22) - 1) * 32, 1 << 20)])
+def test_launches_whose_size_passes_64_bits_refused(lib, B, T, D):
+    pr = conv_problem(B=B, T=T, D=D, x_stride_b=0, x_stride_t=0, dy_stride_b=0, dy_stride_t=0)
+    assert conv_forward(lib, pr) == UNSUPPORTED and conv_backward(lib, pr) == UNSUPPORTED
+    assert lib.gdn_workspace_bytes_conv_backward(ctypes.byref(pr)) == 0
+
+
 def test_ssm_overlapping_rows_refused(lib):
     # a token's row would reach into the next one's
     assert ssm_forward(lib, ssm_problem(x_stride_t=128)) == UNSUPPORTED
