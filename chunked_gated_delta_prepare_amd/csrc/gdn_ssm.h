@@ -604,10 +604,13 @@ __device__ __forceinline__ float segments_before(const SsmParams &p, const Segme
 // Sixteen columns a wave, eight waves for 128 columns, two workgroups a CU: with
 // 32 columns a wave and four waves the kernel read a third less from LDS but
 // held 375 registers a lane, one wave per SIMD (65536 tokens, 64 heads of 128 x
-// 128: 1.8 ms against 1.3 ms for both launches, of 2.4 GB of rows and 774 GFLOP
-// on the matrix cores).  What bounds it: some 390 vector instructions a wave and
-// chunk (decays, roundings, the state's scaling) fill half of the time, waiting
-// for LDS a third.
+// 128: 1.8 ms when tried; now 1.31 ms for both launches, of 2.4 GB of rows and
+// 774 GFLOP on the matrix cores).  What bounds it: no unit is full.  In the main
+// pass the matrix cores are busy 0.21 of the time, vector issue 0.53 (some 390
+// instructions a wave and chunk: decays, roundings, the state's scaling) and LDS
+// 0.46, and 0.43 of the waves' time is waiting: three barriers a chunk, between
+// them one chain of loads, products and stores for all waves, and ten blocks of
+// M for eight waves, so that six wait for two.
 // ---------------------------------------------------------------------------
 template <typename IO, int N, int COLS, int NH, bool ENDS, bool REV>
 __global__ void __launch_bounds__(4 * COLS, sizeof(IO) == 4 ? 1 : COLS == 64 && N == 128 ? 3 : 4) ssm_scan_kernel(SsmParams p) {
@@ -778,8 +781,7 @@ __global__ void __launch_bounds__(4 * COLS, sizeof(IO) == 4 ? 1 : COLS == 64 && 
                 }
             } else {
                 // M's zeros times what is none would reach the rows before it: row by row
-                // instead (65536 tokens, 64 heads, 1.30 ms with the question and without
-                // one such value, 1.29 without both)
+                // instead (to ask costs 0.5 to 0.8 % of 65536 tokens, 64 heads)
 #pragma unroll
                 for (int bi = 0; bi < 4; ++bi) {
                     const int ii = 16 * bi + j;

@@ -99,11 +99,11 @@ SsmPlan ssm_plan(const gdn_ssm_problem *pr, bool packed) {
     const int64_t chunks = (pr->T + kSsmChunk - 1) / kSsmChunk;
     // segments for about 512 workgroups, two a CU, of four chunks or a multiple,
     // and 32 a stream at most (each reads the end states of those before it).
-    // For 256, 512 and 1024 workgroups 65536 tokens of 64 heads take 1.48, 1.33
-    // and 1.35 ms, 16384 tokens 401, 348 and 392 us.  Packed sequences end
+    // For 256, 512 and 1024 workgroups 65536 tokens of 64 heads take 1.52, 1.31
+    // and 1.35 ms, 16384 tokens 404, 350 and 383 us.  Packed sequences end
     // inside a segment, so a quarter more (16384 tokens for 512 and 640: 80 heads
-    // of 64 columns, 9 sequences 303 and 289 us, 3 sequences 321 and 275; 64
-    // heads of 128, 8 sequences 403 and 393).
+    // of 64 columns, 9 sequences 269 and 266 us, 3 sequences 291 and 262; but 64
+    // heads of 128, 8 sequences 378 and 386).
     const int64_t streams = (int64_t)s.n_hb * (packed ? 1 : pr->B);
     const int64_t wgs = packed ? 640 : 512;
     int64_t per = (wgs + streams - 1) / streams;
@@ -116,8 +116,8 @@ SsmPlan ssm_plan(const gdn_ssm_problem *pr, bool packed) {
     // A sequence of L tokens with several segments has (L - 1) / seg + 1 of them; of
     // m such ones, T tokens in all, the segments are at most (T - m) / seg + m,
     // which grows with m.  (A lone segment has no end state to hand on: with a place
-    // for every segment 16384 tokens of 64 heads of 128 x 128 took 42 MB as one
-    // sequence and 1.1 GB as 256, now 42 and 75.)
+    // for every segment 16384 tokens of 64 heads of 128 x 128 took 46 MB as one
+    // sequence and 1.1 GB as 256, now 42 and 76 MB.)
     const int64_t m = packed ? (pr->n_seqs < pr->T / (s.seg_tokens + 1) ? pr->n_seqs : pr->T / (s.seg_tokens + 1)) : 0;
     s.n_ends = (int)(packed ? (m > 0 ? (pr->T - m) / s.seg_tokens + m : 0) : cut > 1 ? s.n_items : 0);
     return s;
@@ -125,9 +125,9 @@ SsmPlan ssm_plan(const gdn_ssm_problem *pr, bool packed) {
 
 // Blocks that share B and C go to one XCD where the (segment, group) pairs come
 // out even over the eight: B and C are then read from HBM once, not once per
-// XCD (64 heads of 128 columns, 8 groups, with and without: 65536 tokens 1.33
-// and 1.37 ms, 16384 tokens 348 and 362 us, 16384 tokens in 8 packed sequences
-// 402 and 412 us).
+// XCD (64 heads of 128 columns, 8 groups, with and without: 65536 tokens 1.31
+// and 1.36 ms, 16384 tokens 350 and 365 us, 16384 tokens in 8 packed sequences
+// 386 and 400 us).
 int ssm_grid(const gdn_ssm_problem *pr, SsmParams &sp, const SsmPlan &s, bool ends) {
     sp.seg_tokens = s.seg_tokens;
     sp.n_items = s.n_items;

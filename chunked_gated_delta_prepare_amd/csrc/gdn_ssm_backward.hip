@@ -24,9 +24,11 @@ namespace gdn {
 // terms, which inputs of one sign (x, B and C behind a silu) add up over N x P
 // products to 3e-8 of X a chunk, always the same way: over 16384 tokens dA was
 // 2.6e-6 and d(dt_bias) 4.9e-6 off.  With the sign alternating the chunks'
-// shares cancel (4.7e-7 and 1.9e-6).
+// shares cancel (4.7e-7 and 1.9e-6 at the same inputs).  What is left varies with
+// the inputs: over ten seeds, with the gate kernel's part below, dA is 0.2 to
+// 5e-6 of its norm off and d(dt_bias) 1 to 3.3e-6.
 //
-// 2 x 8192 tokens, 32 heads of 128 x 128: 230 to 260 us in either direction, of
+// 2 x 8192 tokens, 32 heads of 128 x 128: 246 and 267 us in the two directions, of
 // which the products are 100 us at a large product's rate and the 268 MB that
 // the heads leave for ssm_sum_kernel 55 us at a copy's.  A group's heads do not
 // fit one workgroup (a state is 64 KB of registers), and atomic sums would
@@ -466,7 +468,7 @@ __global__ void __launch_bounds__(256) ssm_gate_kernel(GateParams gp) {
             const int n = seg.end - (t - l) < kSsmChunk ? seg.end - (t - l) : kSsmChunk;
             // The pairs inside sum to zero over the chunk; what they sum to
             // instead is the roundings of the n rows' sums, taken back evenly
-            // (d(dt_bias) at 2 x 8192 tokens 1.9e-6 -> 1.2e-6 off, dA 4.7e-7 -> 2.3e-7)
+            // (d(dt_bias) of one seed's 2 x 8192 tokens 1.9e-6 -> 1.2e-6 off, dA 4.7e-7 -> 2.3e-7)
             const double pairs = all_in - pre_in + in - all_in * (double)(n - l) / (double)n;
             const double dg = pairs + (all_ra - pre_ra + (double)ra) + (pre_ca - dca) + Q;
             double g = (double)ci + (double)ca + (double)wtt + (double)A * dg;

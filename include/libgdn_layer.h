@@ -19,7 +19,9 @@
  *
  * Types: GDN_BF16 and GDN_F32 as in libgdn.h; a norm's output may also be
  * GDN_E4M3 (OCP e4m3: largest finite value 448).  Sums, statistics and states
- * are fp32; a value is rounded once, to nearest even, when it is stored.
+ * are fp32 and results are rounded to nearest even when they are stored.  The
+ * norm and the convolution round nowhere else; the scan in bf16 also rounds
+ * operands of its matrix products (see there).
  *
  * Strides are in elements; the innermost index is always contiguous.  Where a
  * stride is not given the tensor is dense.  Rows need only their element's
@@ -165,6 +167,14 @@ gdn_status gdn_conv_step(const gdn_conv_problem *problem, const void *x, const v
  * later one, or in another sequence, does not reach it.  A sequence that holds
  * one may have NaN in any of its gradients; another sequence's dx, ddt, dB, dC
  * and dh0 are not touched by it.
+ *
+ * Accuracy.  fp32 io: products and sums in fp32.  bf16 io: on the way to y and dx
+ * the weighted values, the state and the chunk's 64 x 64 matrix are each rounded
+ * to bf16 once, in all at most 2 2^-8 of the sum of the terms' sizes (about a
+ * tenth more than y's own rounding on random inputs); to dB and dC the matrix,
+ * 2^-8 of the terms' sizes.  Final states, dh0 and the gates' gradients take their
+ * products in three bf16 parts, as good as fp32.  y does not depend on whether
+ * hT is asked for.
  */
 typedef struct gdn_ssm_problem {
     int64_t B, T, H, P, N, G; /* P, N in {64, 128}; H a multiple of G */
@@ -200,8 +210,10 @@ size_t gdn_workspace_bytes_ssm(const gdn_ssm_problem *problem);
  * dxbc_stride_*), ddt [B, T, H] dense in dt's type, dA, dD, ddt_bias [H] fp32
  * (dD, ddt_bias may be NULL), dh0 fp32 like h0 (or NULL).  With cu_seqlens,
  * dx, dB, dC and ddt of rows that belong to no sequence are left as they
- * were.  Workspace: gdn_workspace_bytes_ssm_backward(problem) bytes, 16-byte
- * aligned.
+ * were.  dx, dB and dC have one stride between batches and one between tokens,
+ * their places apart.  Workspace: gdn_workspace_bytes_ssm_backward(problem)
+ * bytes, 16-byte aligned; it holds fp32 shares of dB and dC for every head (or
+ * two) and started chunk of 64 tokens of a sequence.
  */
 gdn_status gdn_ssm_backward(const gdn_ssm_problem *problem, const void *dy, const void *x,
                             const void *dt, const float *A, const void *Bm, const void *Cm,
