@@ -625,3 +625,27 @@ def test_tokens_before_a_nan_do_not_see_it(name, value, P, N, dt):
     else:
         assert not kT[0].isfinite().all()
     assert not y[0, bad].isfinite().all()
+
+
+def test_thousands_of_packed_sequences():
+    """Nine thousand sequences of some thirty tokens, and one of many segments at the
+    end: more than the sums of dB and dC had workgroups for."""
+    H, P, N, G = 8, 64, 128, 8
+    lens = torch.randint(0, 60, (9000,), generator=torch.Generator().manual_seed(5)).tolist() + [20000]
+    n, T = len(lens), sum(lens)
+    g = torch.Generator(device=DEV).manual_seed(6)
+    new = lambda *s, dtype=BF: torch.randn(*s, generator=g, device=DEV, dtype=dtype)  # noqa: E731
+    x, dy, B, C, dt = new(1, T, H, P), new(1, T, H, P), new(1, T, G, N), new(1, T, G, N), new(1, T, H, dtype=F32)
+    A, rest = -torch.rand(H, generator=g, device=DEV) - 0.1, dict(dt_bias=torch.full((H,), -3.0, device=DEV))
+    cu = offsets(lens)
+    y, hT = gdn.ssm_forward(x, dt, A, B, C, **rest, cu_seqlens=cu)
+    grads = gdn.ssm_backward(dy, x, dt, A, B, C, **rest, cu_seqlens=cu)
+    at = [0] + torch.tensor(lens).cumsum(0).tolist()
+    off = lambda a, b: float((a.float() - b.float()).norm() / b.float().norm())  # noqa: E731
+    for k in (0, 1, 63, 64, 4999, 8998, 8999, 9000):
+        s = slice(at[k], at[k + 1])
+        args = [t[:, s].contiguous() for t in (x, dt)] + [A] + [t[:, s].contiguous() for t in (B, C)]
+        y1, h1 = gdn.ssm_forward(*args, **rest)
+        g1 = gdn.ssm_backward(dy[:, s].contiguous(), *args, **rest)
+        pairs = [(y[:, s], y1), (hT[k:k + 1], h1)] + [(grads[i][:, s], g1[i]) for i in (0, 1, 3, 4)]
+        assert all(torch.equal(u, v) if k < 9000 else off(u, v) < 2.0 ** -6 for u, v in pairs), k
