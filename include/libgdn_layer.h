@@ -193,7 +193,7 @@ typedef struct gdn_ssm_problem {
  *   A [H] fp32; D, dt_bias [H] fp32 or NULL (zero); h0, hT [B, H, N, P] fp32
  *   ([n_seqs, H, N, P] with cu_seqlens) or NULL.
  *   cu_seqlens as in gdn_conv_forward; rows of y that belong to no sequence
- *   are left as they were.
+ *   are left as they were.  With T = 0 x, dt, B, C and y may be NULL.
  * Workspace: gdn_workspace_bytes_ssm(problem) bytes (may be 0), 16-byte
  * aligned.  One or two launches.
  */
