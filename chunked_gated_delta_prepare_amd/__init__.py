@@ -32,7 +32,8 @@ __all__ = ["prepare", "scan", "forward", "forward_states", "forward_varlen", "re
            "GdnError", "LIB_PATH", "POISON_LIB_PATH", "STATUS",
            # the layer's other operators (layer.py)
            "norm_forward", "norm_backward", "conv_forward", "conv_backward", "conv_step",
-           "ssm_forward", "ssm_backward", "ssm_step"]
+           "ssm_forward", "ssm_backward", "ssm_step", "layer_norm_forward", "layer_norm_backward",
+           "gate_norm_forward", "gate_norm_backward", "glr_forward", "glr_backward", "glr_step"]
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(_HERE, "libgdn.so")
@@ -55,11 +56,12 @@ EXPORTS = ["gdn_prepare", "gdn_scan", "gdn_forward", "gdn_forward_states",
            "gdn_workspace_bytes_split", "gdn_backward", "gdn_workspace_bytes_backward",
            "gdn_forward_split_point"]
 NOALLOC_SCRATCH_BYTES = 32 << 20
-ABI_VERSION = 11
+ABI_VERSION = 12
 
 
 _LAYER = ("norm_forward", "norm_backward", "conv_forward", "conv_backward", "conv_step",
-          "ssm_forward", "ssm_backward", "ssm_step")
+          "ssm_forward", "ssm_backward", "ssm_step", "layer_norm_forward", "layer_norm_backward",
+          "gate_norm_forward", "gate_norm_backward", "glr_forward", "glr_backward", "glr_step")
 
 
 def __getattr__(name):

@@ -59,6 +59,10 @@ UNITS = {
     "gdn_conv.hip": [],
     "gdn_ssm.hip": [],
     "gdn_ssm_backward.hip": [],
+    "gdn_layer_norm.hip": [],
+    "gdn_gate_norm.hip": [],
+    "gdn_glr.hip": [],
+    "gdn_glr_backward.hip": [],
 }
 
 

@@ -118,38 +118,10 @@ struct Cols {
             hi = at + 16 < (uint32_t)D * 4 ? at + 16 : kNone;
         }
     }
-    // as loaded; turned into floats where they are used
-    struct Raw {
-        uint32_t u[VEC == 1 ? 1 : kB];
-        __device__ __forceinline__ void get(float (&x)[VEC]) const {
-            if constexpr (VEC == 1) {
-                x[0] = __uint_as_float(kB == 2 ? u[0] << 16 : u[0]);
-            } else if constexpr (kB == 2) {
-                x[0] = __uint_as_float(u[0] << 16);
-                x[1] = __uint_as_float(u[0] & 0xffff0000u);
-                x[2] = __uint_as_float(u[1] << 16);
-                x[3] = __uint_as_float(u[1] & 0xffff0000u);
-            } else {
-#pragma unroll
-                for (int i = 0; i < 4; ++i) x[i] = __uint_as_float(u[i]);
-            }
-        }
-    };
+    typedef RawRow<IO, VEC> Raw;
     __device__ __forceinline__ Raw load(rsrc_t r, uint32_t soff) const {
         Raw x;
-        if constexpr (VEC == 1 && kB == 2) {
-            x.u[0] = bload16(r, off, soff);
-        } else if constexpr (VEC == 1) {
-            x.u[0] = bload32(r, off, soff);
-        } else if constexpr (kB == 2) {
-            const u32x2 v = __builtin_amdgcn_raw_buffer_load_b64(r, off, soff, 0);
-            x.u[0] = v[0];
-            x.u[1] = v[1];
-        } else {
-            const u32x4 v = bload128(r, off, soff);
-#pragma unroll
-            for (int i = 0; i < 4; ++i) x.u[i] = v[i];
-        }
+        x.load(r, off, soff);
         return x;
     }
     __device__ __forceinline__ void store(rsrc_t r, uint32_t soff, const float (&x)[VEC]) const {
@@ -479,16 +451,6 @@ __global__ void __launch_bounds__(1024) conv_dw_kernel(ConvParams p) {
         p.dw[(int64_t)c * W + j] = a;
     else if (p.db)
         p.db[c] = a;
-}
-
-// Whether row b has slot s to itself or is the first to name it.
-__device__ __forceinline__ bool first_with_slot(const int32_t *slots, int b, int s) {
-    bool seen = false;
-    for (int i = 0; i < b; i += 64) {
-        const int k = i + lane_id();
-        seen |= k < b && slots[k] == s;
-    }
-    return __ballot(seen) == 0;
 }
 
 template <typename IO, int VEC, int W>

@@ -1,0 +1,354 @@
+// Gated linear recurrence, forward and step (see gdn_glr.h for the mathematics).
+#include "gdn_glr.h"
+
+namespace gdn {
+
+constexpr int kGlrWaves = 8;
+constexpr int kGlrRun = 16;            // tokens of a thread at a time
+
+template <int VEC>
+constexpr int kGlrTile = kGlrWaves * GlrLane<VEC>::kTG * kGlrRun;      // tokens of a workgroup at a time
+
+// y and the final states: a workgroup walks one segment of 64 channels, tile by
+// tile; the state at a segment's start comes from the segments' moves in the
+// workspace.  One read of x and the gate and one write of y; the next tile's
+// rows are in flight while one is worked on.
+template <typename IO, typename GT, int VEC, bool PK, int FORM>
+__global__ void __launch_bounds__(64 * kGlrWaves) glr_forward_kernel(GlrParams p) {
+    constexpr int L = kGlrRun, NW = kGlrWaves;
+    __shared__ float lds_q[2][NW][kGlrCols], lds_h[2][NW][kGlrCols];
+    const int group = blockIdx.x % p.groups, rest = blockIdx.x / p.groups, seg = rest % p.segs, b = rest / p.segs;
+    const GlrLane<VEC> ln(group);
+    const int w = wave_id(), row = (w * ln.kTG + ln.tg) * L;
+    const int t_begin = seg * p.seg_len, t_end = t_begin + p.seg_len < p.T ? t_begin + p.seg_len : p.T;
+    Run<IO, GT, VEC, FORM, L> run;
+    if (t_begin < t_end) run.fetch(p, b, t_begin, row, ln.c);
+    float bias[VEC], rate[VEC], h[VEC];
+    channel_load<VEC>(p.bias, ln.c, p.D, bias);
+    channel_load<VEC>(p.rate, ln.c, p.D, rate);
+#pragma unroll
+    for (int e = 0; e < VEC; ++e) h[e] = 0.f;
+    for (int j = 0; j < seg; ++j) {
+        const float *s = p.ws + ((int64_t)b * (p.segs - 1) + j) * 2 * p.D;
+        float q[VEC], H[VEC];
+        channel_load<VEC>(s, ln.c, p.D, q);
+        channel_load<VEC>(s + p.D, ln.c, p.D, H);
+#pragma unroll
+        for (int e = 0; e < VEC; ++e) h[e] = packed_move<PK>(q[e], h[e], H[e]);
+    }
+    if (seg == 0) pass_empty(p, PK, b, group * kGlrCols, p.h0, p.hT);
+    Span span;
+    int turn = 0;
+    for (int t = t_begin; t < t_end; t += kGlrTile<VEC>, turn ^= 1) {
+        run.form(p.scale, bias, rate);
+        if (t + kGlrTile<VEC> < t_end) run.fetch(p, b, t + kGlrTile<VEC>, row, ln.c);
+        const Marks marks = marks_of<PK, L>(p, t + row, span);
+        run.template begin<PK>(p, b, t + row, ln.c, marks.first);
+        Moves<VEC> before;
+        float E[VEC];
+        join_wave<PK, VEC>(run.m, run.H, before, E);
+        if (ln.tg == 0) {
+#pragma unroll
+            for (int e = 0; e < VEC; ++e) {
+                lds_q[turn][w][ln.local() + e] = pack_move<PK>(run.m.P[e], run.m.C[e]);
+                lds_h[turn][w][ln.local() + e] = run.H[e];
+            }
+        }
+        // (one barrier a tile: the other half of LDS is next, and its readers are behind the next barrier)
+        lds_barrier();
+        float mine[VEC];
+#pragma unroll
+        for (int j = 0; j < NW; ++j) {
+#pragma unroll
+            for (int e = 0; e < VEC; ++e) {
+                if (j == w) mine[e] = h[e];
+                h[e] = packed_move<PK>(lds_q[turn][j][ln.local() + e], h[e], lds_h[turn][j][ln.local() + e]);
+            }
+        }
+#pragma unroll
+        for (int e = 0; e < VEC; ++e)
+            if (ln.tg > 0) mine[e] = move<PK>(before.P[e], before.C[e], mine[e], E[e]);
+        const TileRows<IO, VEC> ry(p.y, ((int64_t)b * p.T + t) * p.D, p.D, row, ln.c, p.D);
+        if (__ballot(marks.valid != (1u << L) - 1 || (marks.first | marks.last) != 0) == 0) {
+#pragma unroll
+            for (int i = 0; i < L; ++i) {
+#pragma unroll
+                for (int e = 0; e < VEC; ++e) mine[e] = fmaf(run.a[i][e], mine[e], run.u[i][e]);
+                ry.store(mine, i, true);
+            }
+        } else {
+#pragma unroll
+            for (int i = 0; i < L; ++i) {
+                // (u of a first token holds its sequence's initial state)
+                const bool f = PK && (marks.first >> i & 1);
+#pragma unroll
+                for (int e = 0; e < VEC; ++e) mine[e] = f ? run.u[i][e] : fmaf(run.a[i][e], mine[e], run.u[i][e]);
+                ry.store(mine, i, marks.valid >> i & 1);
+                if (p.hT && (marks.last >> i & 1)) state_store<VEC>(p, p.hT, state_of<PK>(p, b, t + row + i), ln.c, true, mine);
+            }
+        }
+    }
+}
+
+// The moves of all segments but the last: a wave walks its share of the segment
+// backwards, so that what it reads last is what the next launch reads first.
+template <typename IO, typename GT, int VEC, bool PK, int FORM>
+__global__ void __launch_bounds__(64 * kGlrWaves) glr_moves_kernel(GlrParams p) {
+    constexpr int L = kGlrRun, NW = kGlrWaves, kStep = GlrLane<VEC>::kTG * L;
+    __shared__ float lds_p[NW][kGlrCols], lds_c[NW][kGlrCols], lds_h[NW][kGlrCols];
+    const int segs = p.segs - 1;
+    const int group = blockIdx.x % p.groups, rest = blockIdx.x / p.groups, seg = rest % segs, b = rest / segs;
+    const GlrLane<VEC> ln(group);
+    const int w = wave_id(), row = ln.tg * L, share = p.seg_len / NW;
+    const int t0 = seg * p.seg_len + w * share;
+    float bias[VEC], rate[VEC];
+    channel_load<VEC>(p.bias, ln.c, p.D, bias);
+    channel_load<VEC>(p.rate, ln.c, p.D, rate);
+    Moves<VEC> all;
+    float H[VEC];
+    all.none();
+#pragma unroll
+    for (int e = 0; e < VEC; ++e) H[e] = 0.f;
+    Run<IO, GT, VEC, FORM, L> run;
+    run.fetch(p, b, t0 + share - kStep, row, ln.c);
+    Span span;
+    for (int t = t0 + share - kStep; t >= t0; t -= kStep) {
+        run.form(p.scale, bias, rate);
+        if (t > t0) run.fetch(p, b, t - kStep, row, ln.c);
+        const Marks marks = marks_of<PK, L>(p, t + row, span);
+        run.template begin<PK>(p, b, t + row, ln.c, marks.first);
+        Moves<VEC> before;
+        float E[VEC];
+        join_wave<PK, VEC>(run.m, run.H, before, E);
+#pragma unroll
+        for (int e = 0; e < VEC; ++e) {
+            H[e] = move<PK>(all.P[e], all.C[e], run.H[e], H[e]);
+            join<PK>(run.m.P[e], run.m.C[e], all.P[e], all.C[e], all.P[e], all.C[e]);
+        }
+    }
+    if (ln.tg == 0) {
+#pragma unroll
+        for (int e = 0; e < VEC; ++e) {
+            lds_p[w][ln.local() + e] = all.P[e];
+            lds_c[w][ln.local() + e] = all.C[e];
+            lds_h[w][ln.local() + e] = H[e];
+        }
+    }
+    __syncthreads();
+    const int l = threadIdx.x, c = group * kGlrCols + l;
+    if (l >= kGlrCols || c >= p.D) return;
+    float P = lds_p[0][l], C = lds_c[0][l], S = lds_h[0][l];
+#pragma unroll
+    for (int j = 1; j < NW; ++j) {
+        S = move<PK>(lds_p[j][l], lds_c[j][l], S, lds_h[j][l]);
+        join<PK>(P, C, lds_p[j][l], lds_c[j][l], P, C);
+    }
+    float *out = p.ws + ((int64_t)b * segs + seg) * 2 * p.D + c;
+    out[0] = pack_move<PK>(P, C);
+    out[p.D] = S;
+}
+
+// One token for each of B rows, 256 channels a workgroup.
+template <typename IO, typename GT, int FORM>
+__global__ void __launch_bounds__(256) glr_step_kernel(GlrParams p) {
+    const int col = blockIdx.x % p.groups, b = blockIdx.x / p.groups, c = col * 256 + threadIdx.x;
+    const int64_t s = p.slots ? p.slots[b] : b;
+    IO *y = (IO *)p.y + (int64_t)b * p.D + c;
+    if (s < 0 || s >= p.n_slots || (p.slots && !first_with_slot(p.slots, b, (int)s))) {
+        if (c < p.D) io_traits<IO>::store(y, 0.f);
+        return;
+    }
+    if (c >= p.D) return;
+    float *h = p.state + s * p.D + c;
+    const float x = io_traits<IO>::load((const IO *)p.x + b * p.xb + c), g = io_traits<GT>::load((const GT *)p.g + b * p.gb + c);
+    float a, k, slope, sig;
+    gate_of<FORM>(g + (p.bias ? p.bias[c] : 0.f), p.rate ? p.rate[c] : 0.f, a, k, slope, sig);
+    const float v = fmaf(a, *h, x * input_scale(p.scale, a, k));
+    *h = v;
+    io_traits<IO>::store(y, v);
+}
+
+gdn_status check_glr(const gdn_glr_problem *pr, bool packed) {
+    if (!pr) return GDN_ERR_NULL_ARG;
+    if (pr->B < 1 || pr->T < 0 || pr->D < 1) return GDN_ERR_BAD_SHAPE;
+    if (packed && (pr->B != 1 || pr->n_seqs < 1 || pr->n_seqs > (1 << 24))) return GDN_ERR_BAD_SHAPE;
+    if (!io_dtype_ok(pr->io_dtype) || (pr->g_dtype != pr->io_dtype && pr->g_dtype != GDN_F32)) return GDN_ERR_UNSUPPORTED;
+    if (pr->form < GDN_GLR_LOG || pr->form > GDN_GLR_RATE || pr->scale < GDN_GLR_PLAIN || pr->scale > GDN_GLR_NORM)
+        return GDN_ERR_UNSUPPORTED;
+    if (pr->T > (1 << 30) || pr->B > (1 << 24) || pr->D > (1 << 23)) return GDN_ERR_UNSUPPORTED;
+    // a tile's rows and the states are addressed with 32-bit byte offsets
+    for (int64_t v : {pr->x_stride_t, pr->g_stride_t, pr->dy_stride_t, pr->dx_stride_t, pr->dg_stride_t})
+        if (v < 0 || v > (1 << 20)) return GDN_ERR_UNSUPPORTED;
+    if (pr->D > (1 << 20) || (packed ? pr->n_seqs : pr->B) * pr->D >= (1 << 29)) return GDN_ERR_UNSUPPORTED;
+    return GDN_OK;
+}
+
+// Channels two at a time (bf16): every row of every tensor at an even element.
+bool glr_pairs(const gdn_glr_problem *pr, std::initializer_list<const void *> io, std::initializer_list<const void *> gates,
+               std::initializer_list<int64_t> strides) {
+    if (pr->io_dtype != GDN_BF16 || pr->g_dtype != GDN_BF16 || pr->D % 2 != 0) return false;
+    for (int64_t v : strides)
+        if (v % 2 != 0) return false;
+    for (const void *q : io)
+        if (!aligned_to(q, 4)) return false;
+    for (const void *q : gates)
+        if (!aligned_to(q, 4)) return false;
+    return true;
+}
+
+void fill_glr(const gdn_glr_problem *pr, GlrParams &gp, const int32_t *cu) {
+    gp = GlrParams{};
+    gp.cu = cu;
+    gp.xb = pr->x_stride_b;
+    gp.xt = pr->x_stride_t;
+    gp.gb = pr->g_stride_b;
+    gp.gt = pr->g_stride_t;
+    gp.yb = pr->dy_stride_b;
+    gp.yt = pr->dy_stride_t;
+    gp.dxb = pr->dx_stride_b;
+    gp.dxt = pr->dx_stride_t;
+    gp.dgb = pr->dg_stride_b;
+    gp.dgt = pr->dg_stride_t;
+    gp.B = (int)pr->B;
+    gp.T = (int)pr->T;
+    gp.D = (int)pr->D;
+    gp.n_seqs = cu ? (int)pr->n_seqs : 0;
+    gp.n_states = cu ? pr->n_seqs : pr->B;
+    gp.scale = pr->scale;
+    gp.groups = (int)((pr->D + kGlrCols - 1) / kGlrCols);
+}
+
+namespace {
+
+struct GlrPlan {
+    int64_t segs, seg_len;
+};
+
+// Segments for about 512 workgroups of 64 channels, two a CU, of four tiles at least
+// (a segment's rows are read once more for its move).
+GlrPlan glr_plan(const gdn_glr_problem *pr) {
+    constexpr int64_t kTile = kGlrTile<2>;         // (a multiple of the tile of single channels)
+    const int64_t streams = pr->B * ((pr->D + kGlrCols - 1) / kGlrCols), tiles = (pr->T + kTile - 1) / kTile;
+    int64_t segs = (512 + streams - 1) / streams;
+    segs = segs < tiles / 4 ? segs : tiles / 4;
+    segs = segs < 1 ? 1 : segs;
+    GlrPlan s;
+    s.seg_len = (tiles + segs - 1) / segs * kTile;
+    s.seg_len = s.seg_len < kTile ? kTile : s.seg_len;
+    s.segs = (pr->T + s.seg_len - 1) / s.seg_len;
+    s.segs = s.segs < 1 ? 1 : s.segs;
+    return s;
+}
+
+template <typename IO, typename GT, int VEC, bool PK>
+const void *glr_fn(int form, bool moves) {
+    switch (form) {
+        case GDN_GLR_LOG:
+            return moves ? (const void *)&glr_moves_kernel<IO, GT, VEC, PK, 0> : (const void *)&glr_forward_kernel<IO, GT, VEC, PK, 0>;
+        case GDN_GLR_SIGMOID:
+            return moves ? (const void *)&glr_moves_kernel<IO, GT, VEC, PK, 1> : (const void *)&glr_forward_kernel<IO, GT, VEC, PK, 1>;
+        default:
+            return moves ? (const void *)&glr_moves_kernel<IO, GT, VEC, PK, 2> : (const void *)&glr_forward_kernel<IO, GT, VEC, PK, 2>;
+    }
+}
+template <bool PK>
+const void *glr_pick(const gdn_glr_problem *pr, bool pairs, bool moves) {
+    if (pairs) return glr_fn<bf16_t, bf16_t, 2, PK>(pr->form, moves);
+    if (pr->io_dtype == GDN_F32) return glr_fn<float, float, 1, PK>(pr->form, moves);
+    return pr->g_dtype == GDN_F32 ? glr_fn<bf16_t, float, 1, PK>(pr->form, moves) : glr_fn<bf16_t, bf16_t, 1, PK>(pr->form, moves);
+}
+
+template <typename IO, typename GT>
+const void *glr_step_fn(int form) {
+    return form == GDN_GLR_LOG ? (const void *)&glr_step_kernel<IO, GT, 0>
+           : form == GDN_GLR_SIGMOID ? (const void *)&glr_step_kernel<IO, GT, 1> : (const void *)&glr_step_kernel<IO, GT, 2>;
+}
+
+}  // namespace
+
+bool glr_aligned(const gdn_glr_problem *pr, std::initializer_list<const void *> io, std::initializer_list<const void *> gates,
+                 std::initializer_list<const void *> f32) {
+    for (const void *q : io)
+        if (!aligned_to(q, dtype_bytes(pr->io_dtype))) return false;
+    for (const void *q : gates)
+        if (!aligned_to(q, dtype_bytes(pr->g_dtype))) return false;
+    for (const void *q : f32)
+        if (!aligned_to(q, 4)) return false;
+    return true;
+}
+
+}  // namespace gdn
+
+using namespace gdn;
+
+extern "C" {
+
+size_t gdn_workspace_bytes_glr(const gdn_glr_problem *pr) {
+    if (check_glr(pr, pr && pr->n_seqs > 0) != GDN_OK) return 0;
+    return (size_t)(pr->B * (glr_plan(pr).segs - 1)) * 2 * pr->D * 4;
+}
+
+gdn_status gdn_glr_forward(const gdn_glr_problem *pr, const void *x, const void *gate, const float *bias, const float *rate,
+                           const float *h0, const int32_t *cu_seqlens, void *y, float *hT, void *workspace,
+                           size_t workspace_bytes, void *stream) {
+    gdn_status st = check_glr(pr, cu_seqlens != nullptr);
+    if (st != GDN_OK) return st;
+    if ((pr->form == GDN_GLR_RATE) != (rate != nullptr)) return rate ? GDN_ERR_UNSUPPORTED : GDN_ERR_NULL_ARG;
+    if (pr->T > 0 && (!x || !gate || !y)) return GDN_ERR_NULL_ARG;
+    if (!glr_aligned(pr, {x, y}, {gate}, {bias, rate, h0, cu_seqlens, hT})) return GDN_ERR_ALIGNMENT;
+    if (pr->T == 0 && !hT) return GDN_OK;
+    const GlrPlan s = glr_plan(pr);
+    GlrParams gp;
+    fill_glr(pr, gp, cu_seqlens);
+    if (!grid_ok(s.segs * pr->B, (int64_t)gp.groups * 64 * kGlrWaves)) return GDN_ERR_UNSUPPORTED;
+    const size_t need = (size_t)(pr->B * (s.segs - 1)) * 2 * pr->D * 4;
+    if (need && (!workspace || workspace_bytes < need)) return GDN_ERR_WORKSPACE;
+    if (!aligned_to(workspace, 16)) return GDN_ERR_ALIGNMENT;
+    gp.x = x;
+    gp.g = gate;
+    gp.bias = bias;
+    gp.rate = rate;
+    gp.h0 = h0;
+    gp.y = y;
+    gp.hT = hT;
+    gp.ws = (float *)workspace;
+    gp.segs = (int)s.segs;
+    gp.seg_len = (int)s.seg_len;
+    const bool pairs = glr_pairs(pr, {x, y}, {gate}, {pr->x_stride_b, pr->x_stride_t, pr->g_stride_b, pr->g_stride_t});
+    const int64_t wgs = pr->B * gp.groups;
+    if (s.segs > 1) {
+        st = launch_kernel(cu_seqlens ? glr_pick<true>(pr, pairs, true) : glr_pick<false>(pr, pairs, true), (int)(wgs * (s.segs - 1)), &gp,
+                           (hipStream_t)stream, 64 * kGlrWaves);
+        if (st != GDN_OK) return st;
+    }
+    return launch_kernel(cu_seqlens ? glr_pick<true>(pr, pairs, false) : glr_pick<false>(pr, pairs, false), (int)(wgs * s.segs), &gp,
+                         (hipStream_t)stream, 64 * kGlrWaves);
+}
+
+gdn_status gdn_glr_step(const gdn_glr_problem *pr, const void *x, const void *gate, const float *bias, const float *rate,
+                        float *state, const int32_t *slots, int64_t n_slots, void *y, void *stream) {
+    const gdn_status st = check_glr(pr, false);
+    if (st != GDN_OK) return st;
+    if ((pr->form == GDN_GLR_RATE) != (rate != nullptr)) return rate ? GDN_ERR_UNSUPPORTED : GDN_ERR_NULL_ARG;
+    if (pr->T != 1 || n_slots < 0 || n_slots >= ((int64_t)1 << 31) || (!slots && n_slots < pr->B)) return GDN_ERR_BAD_SHAPE;
+    if (!x || !gate || !y || (!state && n_slots > 0)) return GDN_ERR_NULL_ARG;
+    if (!glr_aligned(pr, {x, y}, {gate}, {bias, rate, state, slots})) return GDN_ERR_ALIGNMENT;
+    GlrParams gp;
+    fill_glr(pr, gp, nullptr);
+    gp.x = x;
+    gp.g = gate;
+    gp.bias = bias;
+    gp.rate = rate;
+    gp.state = state;
+    gp.slots = slots;
+    gp.n_slots = n_slots;
+    gp.y = y;
+    gp.groups = (int)((pr->D + 255) / 256);
+    if (!grid_ok(pr->B, (int64_t)gp.groups * 256)) return GDN_ERR_UNSUPPORTED;
+    const void *fn = pr->io_dtype == GDN_F32   ? glr_step_fn<float, float>(pr->form)
+                     : pr->g_dtype == GDN_F32 ? glr_step_fn<bf16_t, float>(pr->form)
+                                              : glr_step_fn<bf16_t, bf16_t>(pr->form);
+    return launch_kernel(fn, (int)(pr->B * gp.groups), &gp, (hipStream_t)stream);
+}
+
+}  // extern "C"

@@ -1,0 +1,415 @@
+// Gated linear recurrence, backward (see gdn_glr.h).  With h_t formed again,
+//
+//   dh_t = dy_t + e_{t+1},  e_t = a_t dh_t        (e behind the last token: dhT)
+//   dx_t = c_t dh_t,  d(log a_t) = e_t h_{t-1} + dh_t x_t dc/d(log a)
+//
+// so two recurrences with the same decays, h forwards and e backwards, whose
+// runs join alike.  A workgroup has one tile of tokens and 64 channels and needs
+// the h in front of it and the e behind it: a first launch leaves every tile's
+// moves in the workspace, a second turns them into those states, and the third
+// reads its tile again and writes the gradients.  It takes the tiles in the
+// other order, so that the last ones come out of the last cache.
+#include "gdn_glr.h"
+#include "gdn_norm_rows.h"
+
+namespace gdn {
+
+constexpr int kGbWaves = 8;
+constexpr int kGbRun = 8;              // tokens of a thread
+
+template <int VEC>
+constexpr int kGbTile = kGbWaves * GlrLane<VEC>::kTG * kGbRun;
+
+// A thread's run with dy: the run's moves of h (m, H) and of e (m, E).
+template <typename IO, typename GT, int VEC, int FORM, int L>
+struct BackRun : Run<IO, GT, VEC, FORM, L> {
+    RawRow<IO, VEC> dyr[L];
+    float dy[L][VEC], E[VEC];
+
+    __device__ __forceinline__ void fetch_all(const GlrParams &p, int b, int t_base, int row, int c) {
+        this->fetch(p, b, t_base, row, c);
+        const TileRows<IO, VEC> rd(p.dy, b * p.yb + (int64_t)t_base * p.yt, p.yt, row, c, p.D);
+        const int n = p.T - t_base - row;
+#pragma unroll
+        for (int i = 0; i < L; ++i) rd.load(dyr[i], i, i < n);
+    }
+    // (tokens of no sequence move nothing; the last of a sequence takes dhT, and e does not
+    // pass the first)
+    template <bool PK>
+    __device__ __forceinline__ void form_all(const GlrParams &p, int b, int t0, int c, const Marks &marks, const float (&bias)[VEC],
+                                             const float (&rate)[VEC]) {
+        this->form(p.scale, bias, rate);
+#pragma unroll
+        for (int i = 0; i < L; ++i) dyr[i].get(dy[i]);
+        const bool odd = marks.valid != (1u << L) - 1 || (marks.first | marks.last) != 0;
+        if (__ballot(odd) != 0) {
+#pragma unroll
+            for (int i = 0; i < L; ++i) {
+                if (!(marks.valid >> i & 1)) {
+#pragma unroll
+                    for (int e = 0; e < VEC; ++e) {
+                        this->a[i][e] = 1.f;
+                        this->u[i][e] = dy[i][e] = 0.f;
+                    }
+                }
+                if (p.dhT && (marks.last >> i & 1)) {
+                    float d[VEC];
+                    state_load<VEC>(p, p.dhT, state_of<PK>(p, b, t0 + i), c, d);
+#pragma unroll
+                    for (int e = 0; e < VEC; ++e) dy[i][e] += d[e];
+                }
+            }
+            if (marks.valid != (1u << L) - 1) {
+                // the run's move without them (they are at its ends, or it is all of them)
+#pragma unroll
+                for (int e = 0; e < VEC; ++e) {
+                    this->H[e] = 0.f;
+                    this->m.P[e] = 1.f;
+#pragma unroll
+                    for (int i = 0; i < L; ++i) {
+                        this->H[e] = fmaf(this->a[i][e], this->H[e], this->u[i][e]);
+                        this->m.P[e] *= this->a[i][e];
+                    }
+                    this->m.C[e] = 1.f - this->m.P[e];
+                }
+            }
+        }
+        this->template begin<PK>(p, b, t0, c, marks.first);
+#pragma unroll
+        for (int e = 0; e < VEC; ++e) E[e] = 0.f;
+        if (PK && __ballot(marks.first != 0) != 0) {
+#pragma unroll
+            for (int i = L - 1; i >= 0; --i)
+#pragma unroll
+                for (int e = 0; e < VEC; ++e) E[e] = marks.first >> i & 1 ? 0.f : this->a[i][e] * (dy[i][e] + E[e]);
+        } else {
+#pragma unroll
+            for (int i = L - 1; i >= 0; --i)
+#pragma unroll
+                for (int e = 0; e < VEC; ++e) E[e] = this->a[i][e] * (dy[i][e] + E[e]);
+        }
+    }
+};
+
+// As join_wave, with e: what lies behind this lane's run into `after` and A.
+template <bool PK, int VEC>
+__device__ __forceinline__ void join_wave_both(Moves<VEC> &m, float (&H)[VEC], float (&E)[VEC], Moves<VEC> &beside, float (&B)[VEC],
+                                               float (&A)[VEC]) {
+    beside.none();
+#pragma unroll
+    for (int e = 0; e < VEC; ++e) A[e] = B[e] = 0.f;
+    if constexpr (GlrLane<VEC>::kTG == 2) {
+        const bool second = lane_id() & 32;
+#pragma unroll
+        for (int e = 0; e < VEC; ++e) {
+            const float oP = other_half(m.P[e]), oC = other_half(m.C[e]), oH = other_half(H[e]), oE = other_half(E[e]);
+            beside.P[e] = oP;
+            beside.C[e] = oC;
+            B[e] = oH;
+            A[e] = oE;
+            const float P1 = second ? oP : m.P[e], C1 = second ? oC : m.C[e], P2 = second ? m.P[e] : oP, C2 = second ? m.C[e] : oC;
+            H[e] = move<PK>(P2, C2, second ? oH : H[e], second ? H[e] : oH);
+            E[e] = move<PK>(P1, C1, second ? E[e] : oE, second ? oE : E[e]);
+            join<PK>(P1, C1, P2, C2, m.P[e], m.C[e]);
+        }
+    }
+}
+
+// A tile's place in the workspace: [3][D], its packed move, then H and E, which the
+// second launch replaces by the states at its borders.
+__device__ __forceinline__ float *tile_at(const GlrParams &p, int b, int tile) { return p.ws + ((int64_t)b * p.segs + tile) * 3 * p.D; }
+
+template <typename IO, typename GT, int VEC, bool PK, int FORM>
+__global__ void __launch_bounds__(64 * kGbWaves) glr_tiles_kernel(GlrParams p) {
+    constexpr int L = kGbRun, NW = kGbWaves;
+    __shared__ float lds[4][NW][kGlrCols];
+    const int group = blockIdx.x % p.groups, rest = blockIdx.x / p.groups, tile = rest % p.segs, b = rest / p.segs;
+    const GlrLane<VEC> ln(group);
+    const int w = wave_id(), row = (w * ln.kTG + ln.tg) * L, t = tile * kGbTile<VEC>;
+    BackRun<IO, GT, VEC, FORM, L> run;
+    run.fetch_all(p, b, t, row, ln.c);
+    float bias[VEC], rate[VEC];
+    channel_load<VEC>(p.bias, ln.c, p.D, bias);
+    channel_load<VEC>(p.rate, ln.c, p.D, rate);
+    Span span;
+    const Marks marks = marks_of<PK, L>(p, t + row, span);
+    run.template form_all<PK>(p, b, t + row, ln.c, marks, bias, rate);
+    Moves<VEC> beside;
+    float before[VEC], after[VEC];
+    join_wave_both<PK, VEC>(run.m, run.H, run.E, beside, before, after);
+    if (ln.tg == 0) {
+#pragma unroll
+        for (int e = 0; e < VEC; ++e) {
+            lds[0][w][ln.local() + e] = run.m.P[e];
+            lds[1][w][ln.local() + e] = run.m.C[e];
+            lds[2][w][ln.local() + e] = run.H[e];
+            lds[3][w][ln.local() + e] = run.E[e];
+        }
+    }
+    __syncthreads();
+    const int l = threadIdx.x, c = group * kGlrCols + l;
+    if (l >= kGlrCols || c >= p.D) return;
+    float P = lds[0][0][l], C = lds[1][0][l], H = lds[2][0][l], E = lds[3][0][l];
+#pragma unroll
+    for (int j = 1; j < NW; ++j) {
+        const float P2 = lds[0][j][l], C2 = lds[1][j][l];
+        H = move<PK>(P2, C2, H, lds[2][j][l]);
+        E = move<PK>(P, C, lds[3][j][l], E);
+        join<PK>(P, C, P2, C2, P, C);
+    }
+    float *out = tile_at(p, b, tile) + c;
+    out[0] = pack_move<PK>(P, C);
+    out[p.D] = H;
+    out[2 * (int64_t)p.D] = E;
+}
+
+// H -> the h in front of a tile, E -> the e behind it: 64 channels and one
+// direction a workgroup.  Each of its 16 waves has a share of the tiles: its
+// move first, then, from the state at its border, its tiles'.
+template <bool PK>
+__global__ void __launch_bounds__(1024) glr_states_kernel(GlrParams p) {
+    __shared__ float lds_p[16][kGlrCols], lds_c[16][kGlrCols], lds_h[16][kGlrCols];
+    const int back = blockIdx.x & 1, rest = blockIdx.x >> 1, group = rest % p.groups, b = rest / p.groups;
+    const int w = wave_id(), l = lane_id(), c = group * kGlrCols + l;
+    const bool live = c < p.D;
+    const int share = (p.segs + 15) / 16, n0 = w * share, n1 = n0 + share < p.segs ? n0 + share : p.segs;
+    // tile i of this direction's order
+    auto at = [&](int i) { return tile_at(p, b, back ? p.segs - 1 - i : i) + (live ? c : 0); };
+    const int64_t from = (int64_t)(1 + back) * p.D;
+    float P = 1.f, C = 0.f, S = 0.f;
+#pragma unroll 4
+    for (int i = n0; i < n1; ++i) {
+        const float q = at(i)[0], H = at(i)[from];
+        const bool far = __float_as_int(q) < 0;
+        const bool cut = PK && q == -__builtin_inff();
+        S = packed_move<PK>(q, S, H);
+        join<PK>(P, C, cut ? -1.f : far ? -q : 1.f - q, cut ? 1.f : far ? 1.f + q : q, P, C);
+    }
+    lds_p[w][l] = P;
+    lds_c[w][l] = C;
+    lds_h[w][l] = S;
+    __syncthreads();
+    if (!live) return;
+    S = 0.f;
+    for (int j = 0; j < w; ++j) S = move<PK>(lds_p[j][l], lds_c[j][l], S, lds_h[j][l]);
+#pragma unroll 4
+    for (int i = n0; i < n1; ++i) {
+        float *s = at(i);
+        const float q = s[0], H = s[from];
+        s[from] = S;
+        S = packed_move<PK>(q, S, H);
+    }
+}
+
+template <typename IO, typename GT, int VEC, bool PK, int FORM>
+__global__ void __launch_bounds__(64 * kGbWaves) glr_backward_kernel(GlrParams p) {
+    constexpr int L = kGbRun, NW = kGbWaves;
+    __shared__ float lds[3][NW][kGlrCols];
+    const int group = blockIdx.x % p.groups, rest = blockIdx.x / p.groups, tile = p.segs - 1 - rest % p.segs, b = rest / p.segs;
+    const GlrLane<VEC> ln(group);
+    const int w = wave_id(), row = (w * ln.kTG + ln.tg) * L, t = tile * kGbTile<VEC>, t0 = t + row;
+    BackRun<IO, GT, VEC, FORM, L> run;
+    run.fetch_all(p, b, t, row, ln.c);
+    float bias[VEC], rate[VEC], h[VEC], d[VEC];
+    channel_load<VEC>(p.bias, ln.c, p.D, bias);
+    channel_load<VEC>(p.rate, ln.c, p.D, rate);
+    const float *states = p.segs > 1 ? tile_at(p, b, tile) : nullptr;
+    channel_load<VEC>(states ? states + p.D : nullptr, ln.c, p.D, h);
+    channel_load<VEC>(states ? states + 2 * (int64_t)p.D : nullptr, ln.c, p.D, d);
+    if (tile == 0) pass_empty(p, PK, b, group * kGlrCols, p.dhT, p.dh0);
+    Span span;
+    const Marks marks = marks_of<PK, L>(p, t0, span);
+    run.template form_all<PK>(p, b, t0, ln.c, marks, bias, rate);
+    Moves<VEC> beside;
+    float before[VEC], after[VEC];
+    join_wave_both<PK, VEC>(run.m, run.H, run.E, beside, before, after);
+    if (ln.tg == 0) {
+#pragma unroll
+        for (int e = 0; e < VEC; ++e) {
+            lds[0][w][ln.local() + e] = pack_move<PK>(run.m.P[e], run.m.C[e]);
+            lds[1][w][ln.local() + e] = run.H[e];
+            lds[2][w][ln.local() + e] = run.E[e];
+        }
+    }
+    lds_barrier();
+#pragma unroll
+    for (int j = 0; j < NW - 1; ++j) {
+        const int k = NW - 1 - j;
+#pragma unroll
+        for (int e = 0; e < VEC; ++e) {
+            if (j < w) h[e] = packed_move<PK>(lds[0][j][ln.local() + e], h[e], lds[1][j][ln.local() + e]);
+            if (k > w) d[e] = packed_move<PK>(lds[0][k][ln.local() + e], d[e], lds[2][k][ln.local() + e]);
+        }
+    }
+    if constexpr (ln.kTG == 2) {
+#pragma unroll
+        for (int e = 0; e < VEC; ++e) {
+            const float hn = move<PK>(beside.P[e], beside.C[e], h[e], before[e]), dn = move<PK>(beside.P[e], beside.C[e], d[e], after[e]);
+            h[e] = ln.tg ? hn : h[e];
+            d[e] = ln.tg ? d[e] : dn;
+        }
+    }
+    // the state in front of every token
+    float prev[L][VEC];
+#pragma unroll
+    for (int i = 0; i < L; ++i)
+#pragma unroll
+        for (int e = 0; e < VEC; ++e) {
+            prev[i][e] = h[e];
+            h[e] = PK && (marks.first >> i & 1) ? run.u[i][e] : fmaf(run.a[i][e], h[e], run.u[i][e]);
+        }
+    const bool odd = __ballot(marks.valid != (1u << L) - 1 || marks.first != 0) != 0;
+    if (odd) {
+#pragma unroll
+        for (int i = 0; i < L; ++i)
+            if (marks.first >> i & 1) state_load<VEC>(p, p.h0, state_of<PK>(p, b, t0 + i), ln.c, prev[i]);
+    }
+    const TileRows<IO, VEC> rx(p.dx, b * p.dxb + (int64_t)t * p.dxt, p.dxt, row, ln.c, p.D);
+    const TileRows<GT, VEC> rg(p.dg, b * p.dgb + (int64_t)t * p.dgt, p.dgt, row, ln.c, p.D);
+    float sb[VEC], sr[VEC];
+#pragma unroll
+    for (int e = 0; e < VEC; ++e) sb[e] = sr[e] = 0.f;
+#pragma unroll
+    for (int i = L - 1; i >= 0; --i) {
+        float x[VEC], g[VEC], dx[VEC], dg[VEC];
+        run.x[i].get(x);
+        run.g[i].get(g);
+        const bool ok = marks.valid >> i & 1;
+#pragma unroll
+        for (int e = 0; e < VEC; ++e) {
+            float a, c, slope, sig;
+            gate_of<FORM>(g[e] + bias[e], rate[e], a, c, slope, sig);
+            const float k = input_scale(p.scale, a, c), dh = run.dy[i][e] + d[e], out = run.a[i][e] * dh;
+            const float da = fmaf(out, prev[i][e], dh * x[e] * input_slope(p.scale, a, k));
+            dx[e] = dh * k;
+            dg[e] = da * slope;
+            // (a token of no sequence may hold anything)
+            sb[e] += ok ? dg[e] : 0.f;
+            sr[e] -= ok ? da * sig : 0.f;
+            d[e] = out;
+        }
+        rx.store(dx, i, ok);
+        rg.store(dg, i, ok);
+        if (odd && (marks.first >> i & 1)) {
+            if (p.dh0) state_store<VEC>(p, p.dh0, state_of<PK>(p, b, t0 + i), ln.c, true, d);
+            if (PK) {
+#pragma unroll
+                for (int e = 0; e < VEC; ++e) d[e] = 0.f;
+            }
+        }
+    }
+    if (!p.grads) return;
+    // the tile's sums, in a fixed order
+    __syncthreads();
+#pragma unroll
+    for (int e = 0; e < VEC; ++e) {
+        if constexpr (ln.kTG == 2) {
+            sb[e] += other_half(sb[e]);
+            sr[e] += other_half(sr[e]);
+        }
+        if (ln.tg == 0) {
+            lds[0][w][ln.local() + e] = sb[e];
+            lds[1][w][ln.local() + e] = sr[e];
+        }
+    }
+    __syncthreads();
+    const int which = threadIdx.x >> 6, l = lane_id(), c = group * kGlrCols + l;
+    if (which > 1 || c >= p.D) return;
+    float s = 0.f;
+#pragma unroll
+    for (int j = 0; j < NW; ++j) s += lds[which][j][l];
+    p.part[(((int64_t)b * p.segs + tile) * 2 + which) * p.D + c] = s;
+}
+
+namespace {
+
+int64_t glr_tiles(const gdn_glr_problem *pr, bool pairs) {
+    const int64_t per = pairs ? kGbTile<2> : kGbTile<1>, n = (pr->T + per - 1) / per;
+    return n < 1 ? 1 : n;
+}
+
+// (for the smaller tiles, which need more: whether channels go in pairs depends on pointers too)
+int64_t glr_backward_bytes(const gdn_glr_problem *pr) {
+    const int64_t n = glr_tiles(pr, false);
+    return pr->B * n * (n > 1 ? 5 : 2) * pr->D * 4;
+}
+
+template <typename IO, typename GT, int VEC, bool PK>
+const void *glr_back_fn(int form, bool tiles) {
+    switch (form) {
+        case GDN_GLR_LOG:
+            return tiles ? (const void *)&glr_tiles_kernel<IO, GT, VEC, PK, 0> : (const void *)&glr_backward_kernel<IO, GT, VEC, PK, 0>;
+        case GDN_GLR_SIGMOID:
+            return tiles ? (const void *)&glr_tiles_kernel<IO, GT, VEC, PK, 1> : (const void *)&glr_backward_kernel<IO, GT, VEC, PK, 1>;
+        default:
+            return tiles ? (const void *)&glr_tiles_kernel<IO, GT, VEC, PK, 2> : (const void *)&glr_backward_kernel<IO, GT, VEC, PK, 2>;
+    }
+}
+template <bool PK>
+const void *glr_back_pick(const gdn_glr_problem *pr, bool pairs, bool tiles) {
+    if (pairs) return glr_back_fn<bf16_t, bf16_t, 2, PK>(pr->form, tiles);
+    if (pr->io_dtype == GDN_F32) return glr_back_fn<float, float, 1, PK>(pr->form, tiles);
+    return pr->g_dtype == GDN_F32 ? glr_back_fn<bf16_t, float, 1, PK>(pr->form, tiles) : glr_back_fn<bf16_t, bf16_t, 1, PK>(pr->form, tiles);
+}
+
+}  // namespace
+}  // namespace gdn
+
+using namespace gdn;
+
+extern "C" {
+
+size_t gdn_workspace_bytes_glr_backward(const gdn_glr_problem *pr) {
+    if (check_glr(pr, pr && pr->n_seqs > 0) != GDN_OK) return 0;
+    return (size_t)glr_backward_bytes(pr);
+}
+
+gdn_status gdn_glr_backward(const gdn_glr_problem *pr, const void *dy, const void *x, const void *gate, const float *bias,
+                            const float *rate, const float *h0, const int32_t *cu_seqlens, const float *dhT, void *dx,
+                            void *dgate, float *dbias, float *drate, float *dh0, void *workspace, size_t workspace_bytes,
+                            void *stream) {
+    gdn_status st = check_glr(pr, cu_seqlens != nullptr);
+    if (st != GDN_OK) return st;
+    if ((pr->form == GDN_GLR_RATE) != (rate != nullptr)) return rate ? GDN_ERR_UNSUPPORTED : GDN_ERR_NULL_ARG;
+    if (drate && !rate) return GDN_ERR_UNSUPPORTED;
+    if (pr->T > 0 && (!dy || !x || !gate || !dx || !dgate)) return GDN_ERR_NULL_ARG;
+    if (!glr_aligned(pr, {dy, x, dx}, {gate, dgate}, {bias, rate, h0, cu_seqlens, dhT, dbias, drate, dh0})) return GDN_ERR_ALIGNMENT;
+    const size_t need = (size_t)glr_backward_bytes(pr);
+    if (need && (!workspace || workspace_bytes < need)) return GDN_ERR_WORKSPACE;
+    if (!aligned_to(workspace, 16)) return GDN_ERR_ALIGNMENT;
+    GlrParams gp;
+    fill_glr(pr, gp, cu_seqlens);
+    const bool pairs = glr_pairs(pr, {dy, x, dx}, {gate, dgate},
+                                 {pr->x_stride_b, pr->x_stride_t, pr->g_stride_b, pr->g_stride_t, pr->dy_stride_b, pr->dy_stride_t,
+                                  pr->dx_stride_b, pr->dx_stride_t, pr->dg_stride_b, pr->dg_stride_t});
+    const int64_t tiles = glr_tiles(pr, pairs);
+    if (!grid_ok(tiles * pr->B, (int64_t)gp.groups * 64 * kGbWaves)) return GDN_ERR_UNSUPPORTED;
+    gp.dy = dy;
+    gp.x = x;
+    gp.g = gate;
+    gp.bias = bias;
+    gp.rate = rate;
+    gp.h0 = h0;
+    gp.dhT = dhT;
+    gp.dx = dx;
+    gp.dg = dgate;
+    gp.dh0 = dh0;
+    gp.segs = (int)tiles;
+    gp.grads = dbias || drate;
+    gp.part = (float *)workspace;
+    gp.ws = gp.part + pr->B * tiles * 2 * pr->D;
+    const int grid = (int)(pr->B * tiles * gp.groups);
+    hipStream_t s = (hipStream_t)stream;
+    if (tiles > 1) {
+        st = launch_kernel(cu_seqlens ? glr_back_pick<true>(pr, pairs, true) : glr_back_pick<false>(pr, pairs, true), grid, &gp, s, 64 * kGbWaves);
+        if (st != GDN_OK) return st;
+        st = launch_kernel(cu_seqlens ? (const void *)&glr_states_kernel<true> : (const void *)&glr_states_kernel<false>,
+                           (int)(2 * pr->B * gp.groups), &gp, s, 1024);
+        if (st != GDN_OK) return st;
+    }
+    st = launch_kernel(cu_seqlens ? glr_back_pick<true>(pr, pairs, false) : glr_back_pick<false>(pr, pairs, false), grid, &gp, s, 64 * kGbWaves);
+    if (st != GDN_OK || !gp.grads) return st;
+    return enqueue_norm_sums(gp.part, dbias, drate, pr->D, pr->B * tiles, 1, s);
+}
+
+}  // extern "C"

@@ -6,6 +6,8 @@
 // 8-byte words in a row (the compiler would join them into a wider store).
 #pragma once
 
+#include <type_traits>
+
 #include "../../include/libgdn_layer.h"
 #include "gdn_buffer.h"
 #include "gdn_internal.h"
@@ -49,6 +51,35 @@ __device__ __forceinline__ void row_load(rsrc_t r, uint32_t e, float (&x)[VEC]) 
         for (int i = 0; i < 4; ++i) x[i] = __uint_as_float(v[i]);
     }
 }
+
+// The same as loaded, for rows that are in flight while others are worked on:
+// turned into floats where they are used.  Offsets in bytes: the lane's, and a
+// uniform one.
+template <typename T, int VEC>
+struct RawRow {
+    static constexpr int kB = sizeof(T);
+    uint32_t u[VEC * kB < 4 ? 1 : VEC * kB / 4];
+    __device__ __forceinline__ void load(rsrc_t r, uint32_t off, uint32_t soff) {
+        if constexpr (VEC * kB == 2) {
+            u[0] = bload16(r, off, soff);
+        } else if constexpr (VEC * kB == 4) {
+            u[0] = bload32(r, off, soff);
+        } else if constexpr (VEC * kB == 8) {
+            const u32x2 v = __builtin_amdgcn_raw_buffer_load_b64(r, off, soff, 0);
+            u[0] = v[0];
+            u[1] = v[1];
+        } else {
+            const u32x4 v = bload128(r, off, soff);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) u[i] = v[i];
+        }
+    }
+    __device__ __forceinline__ void get(float (&x)[VEC]) const {
+#pragma unroll
+        for (int i = 0; i < VEC; ++i)
+            x[i] = __uint_as_float(kB == 4 ? u[i] : i & 1 ? u[i / 2] & 0xffff0000u : u[i / 2] << 16);
+    }
+};
 
 // two floats as bf16, in one instruction
 __device__ __forceinline__ uint32_t pack_bf16(float a, float b) {
@@ -103,6 +134,25 @@ __device__ __forceinline__ void lds_barrier() {
     asm volatile("" ::: "memory");
 }
 
+// e^x for fp32's sake: the argument's product with log2(e) rounds by up to |x| 2^-24,
+// which would be an error of that size in the result; it is put back.
+// (Below -150 the result is zero anyway, and -inf would leave nothing to put back.)
+__device__ __forceinline__ float exact_exp(float x) {
+    x = x < -150.f ? -150.f : x;
+    const float t = x * kLog2e, lo = fmaf(x, kLog2e, -t) + x * 1.92596299e-8f;
+    return fast_exp2(t) * fmaf(lo, 0.693147181f, 1.f);
+}
+
+// 1 / (1 + e^-v) and what it lacks to 1, each good to its own last digits.
+struct Sigmoid {
+    float s, o;
+    __device__ __forceinline__ explicit Sigmoid(float v) {
+        const float e = exact_exp(-fabsf(v)), r = __builtin_amdgcn_rcpf(1.f + e), n = e * r;
+        s = v >= 0.f ? r : n;
+        o = v >= 0.f ? n : r;
+    }
+};
+
 // ---------------------------------------------------------------------------
 // Sums and maxima over the lanes of a wave; every lane gets the result.  The
 // order of the additions does not depend on anything but the lane numbers.
@@ -113,11 +163,43 @@ __device__ __forceinline__ float wave_sum(float x) {
     return x;
 }
 
+// The same with vector instructions only (no LDS): over the LANES (16, 32 or 64)
+// adjacent lanes that a lane is among, in every one of them.
+template <int LANES>
+__device__ __forceinline__ float lanes_sum(float x) {
+    auto dpp = [](float v, auto ctrl) {
+        return __int_as_float(__builtin_amdgcn_update_dpp(0, __float_as_int(v), decltype(ctrl)::value, 0xf, 0xf, false));
+    };
+    x += dpp(x, std::integral_constant<int, 0xB1>());       // lane ^ 1
+    x += dpp(x, std::integral_constant<int, 0x4E>());       // lane ^ 2
+    x += dpp(x, std::integral_constant<int, 0x141>());      // the other half of 8 lanes, mirrored
+    x += dpp(x, std::integral_constant<int, 0x140>());      // the other half of 16
+    if constexpr (LANES >= 32) {
+        const auto h = __builtin_amdgcn_permlane16_swap(__float_as_uint(x), __float_as_uint(x), false, false);
+        x = __uint_as_float(h[0]) + __uint_as_float(h[1]);
+    }
+    if constexpr (LANES >= 64) {
+        const auto h = __builtin_amdgcn_permlane32_swap(__float_as_uint(x), __float_as_uint(x), false, false);
+        x = __uint_as_float(h[0]) + __uint_as_float(h[1]);
+    }
+    return x;
+}
+
 template <int LANES>
 __device__ __forceinline__ float lanes_max(float x) {
 #pragma unroll
     for (int m = 1; m < LANES; m <<= 1) x = fmaxf(x, __shfl_xor(x, m, 64));
     return x;
+}
+
+// Whether row b has slot s to itself or is the first to name it.
+__device__ __forceinline__ bool first_with_slot(const int32_t *slots, int b, int s) {
+    bool seen = false;
+    for (int i = 0; i < b; i += 64) {
+        const int k = i + lane_id();
+        seen |= k < b && slots[k] == s;
+    }
+    return __ballot(seen) == 0;
 }
 
 }  // namespace gdn

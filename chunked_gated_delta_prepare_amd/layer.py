@@ -1,6 +1,7 @@
 """Binding of libgdn's layer operators (include/libgdn_layer.h): the
-root-mean-square norm, the short causal convolution and the selective state
-space scan around the recurrence.  As in the package itself every step runs in
+root-mean-square norm, layer norm, the short causal convolution, the selective
+state space scan and the gated linear recurrence around the recurrence, and the
+gated norm behind its heads.  As in the package itself every step runs in
 libgdn's HIP kernels; this module checks tensors, allocates outputs and
 workspaces with torch and passes raw pointers and a stream.
 
@@ -13,6 +14,13 @@ workspaces with torch and passes raw pointers and a stream.
     ssm_backward(dy, x, dt, A, B, C, D, dt_bias, h0)
                         -> (dx, ddt, dA, dB, dC, dD, ddt_bias, dh0)
     ssm_step(x, dt, A, B, C, state, D, dt_bias)   -> y, the state in place
+    layer_norm_forward(x, weight, bias, residual) -> (y, s, scales)
+    layer_norm_backward(dy, s, weight, bias, dres) -> (ds, dx, dweight, dbias)
+    gate_norm_forward(x, z, weight, bias=None)    -> y
+    gate_norm_backward(dy, x, z, weight, bias=None) -> (dx, dz, dweight, dbias)
+    glr_forward(x, gate, h0=None)                 -> (y, hT)
+    glr_backward(dy, x, gate, h0, dhT)            -> (dx, dgate, dbias, drate, dh0)
+    glr_step(x, gate, state)                      -> y, the state in place
 
 The work goes to ``stream``, or to the current stream of the tensors' device;
 outputs and workspaces are allocated on that stream.
@@ -24,8 +32,8 @@ import functools
 
 import torch
 
-from .layer_abi import (GDN_E4M3, LAYER_EXPORTS, ConvProblem, NormProblem,  # noqa: F401
-                        SsmProblem, declare)
+from .layer_abi import (GDN_E4M3, LAYER_EXPORTS, ConvProblem, GateNormProblem, GlrProblem,  # noqa: F401
+                        NormProblem, SsmProblem, declare)
 
 _FP8 = torch.float8_e4m3fn
 _CODE = {torch.float32: 0, torch.bfloat16: 1, _FP8: GDN_E4M3}
@@ -610,4 +618,397 @@ def _ssm_step(handle, dev, code, x, dt, A, B, C, state, D, dt_bias, softplus, sl
                          0, 0, 0, code, _CODE[dt.dtype], softplus)
         _call("gdn_ssm_step", pr, x.data_ptr(), dt.data_ptr(), A.data_ptr(), B.data_ptr(), C.data_ptr(), _ptr(D), _ptr(dt_bias), state.data_ptr(),
               _ptr(slots), state.shape[0], y.data_ptr(), handle)
+    return y
+
+
+# ---------------------------------------------------------------------------
+# layer norm
+# ---------------------------------------------------------------------------
+
+def layer_norm_forward(x, weight, bias=None, residual=None, *, eps=1e-5, out_dtype=None, group=0, y=None, s=None,
+                       scales=None, stream=None):
+    """s = x + residual (in the residual's type), y = (s - m) r w + b with m =
+    mean(s) and r = 1 / sqrt(mean((s - m)^2) + eps) over the last dimension.
+
+    Arguments and results as norm_forward's; bias [D] in the weight's type, or
+    None (zero)."""
+    dev = _device(x, "x")
+    shape, dt = x.shape, x.dtype
+    if x.dim() < 1 or shape[-1] < 1:
+        raise ValueError("x must have a last dimension of at least 1, got %s" % (tuple(shape),))
+    code = _io_code(x, "x")
+    _check(weight, "weight", dev, shape[-1:], dt, torch.float32)
+    if bias is not None:
+        _check(bias, "bias", dev, shape[-1:], weight.dtype)
+    if residual is not None:
+        _check(residual, "residual", dev, shape, dt, torch.float32)
+    if out_dtype not in (None, dt, _FP8):
+        raise TypeError("out_dtype must be %s or %s, got %s" % (dt, _FP8, out_dtype))
+    if group not in (0, 128):
+        raise ValueError("group must be 0 (a scale per row) or 128, got %r" % (group,))
+    return _on(dev, stream, _layer_norm_forward, dev, code, x, weight, bias, residual, eps, out_dtype or dt, group, y, s, scales)
+
+
+def _layer_norm_forward(handle, dev, code, x, weight, bias, residual, eps, od, group, y, s, scales):
+    shape, D = x.shape, x.shape[-1]
+    if x.is_contiguous():
+        rows, stride = x.numel() // D, D
+    else:
+        merged = _rows(x)
+        if merged is None:
+            raise ValueError("x's rows must be contiguous and lie at one stride")
+        rows, stride = merged
+    y = _out(y, "y", dev, shape, od, (x, weight, bias, residual), x)
+    scode = code
+    if residual is not None:
+        scode = _CODE[residual.dtype]
+        if s is not None and s.data_ptr() == residual.data_ptr():
+            _check(s, "s", dev, shape, residual.dtype)
+            _apart(s, "s", x, weight, bias, y)
+        else:
+            s = _out(s, "s", dev, shape, residual.dtype, (x, weight, bias, residual, y), residual)
+    else:
+        _unwritten(s, "s", "a residual")
+    if od is _FP8:
+        scales = _out(scales, "scales", dev, shape[:-1] + ((D + group - 1) // group if group else 1,), torch.float32,
+                      (x, weight, bias, residual, y, s))
+    else:
+        _unwritten(scales, "scales", "an 8-bit output")
+    pr, _ = _problem(NormProblem, None, rows, D, stride, code, scode, _CODE[weight.dtype], _CODE[od], group, eps)
+    _call("gdn_layer_norm_forward", pr, x.data_ptr(), _ptr(residual), weight.data_ptr(), _ptr(bias), y.data_ptr(), _ptr(s), _ptr(scales),
+          handle)
+    return y, s, scales
+
+
+def layer_norm_backward(dy, s, weight, bias=None, dres=None, *, eps=1e-5, x_dtype=None, ds=None, dx=None, dweight=None,
+                        dbias=None, workspace=None, stream=None):
+    """Layer norm's gradients: arguments as norm_backward's, and the forward's
+    bias, whose values are not read.  Returns (ds, dx, dweight, dbias): dbias [D]
+    fp32, None without a bias."""
+    dev = _device(dy, "dy")
+    shape, dt = dy.shape, dy.dtype
+    if dy.dim() < 1 or shape[-1] < 1:
+        raise ValueError("dy must have a last dimension of at least 1, got %s" % (tuple(shape),))
+    code = _io_code(dy, "dy")
+    if x_dtype not in (None, dt):
+        raise TypeError("dy has x's type: got %s for x of %s" % (dt, x_dtype))
+    if not dy.is_contiguous():
+        raise ValueError("dy must be contiguous")
+    _check(s, "s", dev, shape, dt, torch.float32)
+    _check(weight, "weight", dev, shape[-1:], dt, torch.float32)
+    if bias is None:
+        _unwritten(dbias, "dbias", "a bias")
+    else:
+        _check(bias, "bias", dev, shape[-1:], weight.dtype)
+    if dres is not None:
+        _check(dres, "dres", dev, shape, s.dtype)
+    return _on(dev, stream, _layer_norm_backward, dev, code, dy, s, weight, bias, dres, eps, ds, dx, dweight, dbias, workspace)
+
+
+def _layer_norm_backward(handle, dev, code, dy, s, weight, bias, dres, eps, ds, dx, dweight, dbias, workspace):
+    shape, D = dy.shape, dy.shape[-1]
+    ins = (dy, s, weight, bias)
+    if dres is not None and ds is not None and ds.data_ptr() == dres.data_ptr():
+        _check(ds, "ds", dev, shape, s.dtype)
+        _apart(ds, "ds", *ins)
+    else:
+        ds = _out(ds, "ds", dev, shape, s.dtype, ins + (dres,), s)
+    if s.dtype is dy.dtype:
+        if dx is not None and dx is not ds:
+            raise ValueError("dx is ds where x and s have one type")
+        dx = None
+    else:
+        dx = _out(dx, "dx", dev, shape, dy.dtype, ins + (dres, ds), dy)
+    dweight = _out(dweight, "dweight", dev, shape[-1:], torch.float32, ins + (dres, ds, dx))
+    dbias = None if bias is None else _out(dbias, "dbias", dev, shape[-1:], torch.float32, ins + (dres, ds, dx, dweight))
+    pr, need = _problem(NormProblem, "gdn_workspace_bytes_layer_norm_backward", dy.numel() // D, D, D, code, _CODE[s.dtype],
+                        _CODE[weight.dtype], code, 0, eps)
+    workspace, size = _workspace(need, dev, workspace)
+    _call("gdn_layer_norm_backward", pr, dy.data_ptr(), s.data_ptr(), weight.data_ptr(), _ptr(dres), ds.data_ptr(), _ptr(dx), dweight.data_ptr(),
+          _ptr(dbias), _ptr(workspace), size, handle)
+    return ds, ds if dx is None else dx, dweight, dbias
+
+
+# ---------------------------------------------------------------------------
+# gated norm
+# ---------------------------------------------------------------------------
+
+_ACT = {"silu": 0, "sigmoid": 1}
+
+
+def _head_strides(t, name):
+    """[..., H, D] as T tokens of H rows: (T, H, token stride, head stride).  Two
+    dimensions are tokens of one row."""
+    shape, strides = t.shape, t.stride()
+    D = shape[-1]
+    H, sh = (shape[-2], strides[-2]) if len(shape) > 2 else (1, D)
+    T = 1
+    for n in (shape[:-2] if len(shape) > 2 else shape[:-1]):
+        T *= n
+    if t.is_contiguous():
+        return T, H, H * D, D
+    if not t.numel():
+        return T, H, H * D, D
+    if D > 1 and strides[-1] != 1:
+        raise ValueError("%s's rows must be contiguous" % name)
+    st, want = None, None
+    for n, s in zip(reversed(shape[:-2] if len(shape) > 2 else shape[:-1]), reversed(strides[:-2] if len(shape) > 2 else strides[:-1])):
+        if n == 1:
+            continue
+        if st is None:
+            st = s
+        elif s != want:
+            raise ValueError("%s's tokens must lie at one stride" % name)
+        want = s * n
+    return T, H, H * D if st is None else st, sh if H > 1 else D
+
+
+def _apart_rows(T, H, D, st, sh, name):
+    """Rows of an output at two strides do not overlap."""
+    if T * H < 2:
+        return
+    if H > 1 and sh < D or T > 1 and st < D:
+        raise ValueError("%s's rows must not overlap" % name)
+    if T > 1 and H > 1 and not (st >= (H - 1) * sh + D or sh >= (T - 1) * st + D):
+        raise ValueError("%s's rows must not overlap" % name)
+
+
+def _gate_norm_checks(x, z, weight, bias, activation, center):
+    dev = _device(x, "x")
+    code = _io_code(x, "x")
+    if x.dim() < 1 or x.shape[-1] < 1:
+        raise ValueError("x must have a last dimension of at least 1, got %s" % (tuple(x.shape),))
+    _check(z, "z", dev, x.shape, x.dtype, dense=False)
+    if not isinstance(weight, torch.Tensor):
+        raise TypeError("weight must be a torch.Tensor")
+    each = weight.dim() == 2
+    if each and x.dim() < 3:
+        raise ValueError("a weight of its own for every head needs x of [..., H, D]")
+    _check(weight, "weight", dev, x.shape[-2:] if each else x.shape[-1:], x.dtype, torch.float32)
+    if bias is not None:
+        if not center:
+            raise ValueError("a bias needs center=True")
+        _check(bias, "bias", dev, weight.shape, weight.dtype)
+    if activation not in _ACT:
+        raise ValueError("activation must be 'silu' or 'sigmoid', got %r" % (activation,))
+    return dev, code, each
+
+
+def _gate_norm_problem(size_of, x, z, dz, weight, code, each, first, center, act, eps):
+    D = x.shape[-1]
+    T, H, xt, xh = _head_strides(x, "x")
+    _, _, zt, zh = _head_strides(z, "z")
+    dt, dh = (0, 0)
+    if dz is not None:
+        _, _, dt, dh = _head_strides(dz, "dz")
+        _apart_rows(T, H, D, dt, dh, "dz")
+    return _problem(GateNormProblem, size_of, T, H, D, xt, xh, zt, zh, dt, dh, code, _CODE[weight.dtype], int(each), int(first),
+                    int(center), act, eps)
+
+
+def gate_norm_forward(x, z, weight, bias=None, *, eps=1e-5, activation="silu", gate_first=False, center=False, y=None,
+                      stream=None):
+    """The norm behind a recurrence's heads: y = n(x) act(z), or with gate_first
+    y = n(x act(z)); n(v) = v r w with r = 1 / sqrt(mean(v^2) + eps) over the last
+    dimension, and centred (v - m) r w + b.
+
+    x and z [..., H, D] (or [..., D]) bf16 or fp32, whose tokens and heads may each
+    lie at a stride; weight [D], or [H, D] for weights of each head, in x's type or
+    fp32; bias like it (with center), or None.  activation: "silu" or "sigmoid".
+    Returns y, dense."""
+    dev, code, each = _gate_norm_checks(x, z, weight, bias, activation, center)
+    return _on(dev, stream, _gate_norm_forward, dev, code, x, z, weight, bias, each, gate_first, center, _ACT[activation], eps, y)
+
+
+def _gate_norm_forward(handle, dev, code, x, z, weight, bias, each, first, center, act, eps, y):
+    y = _out(y, "y", dev, x.shape, x.dtype, (x, z, weight, bias), x)
+    pr, _ = _gate_norm_problem(None, x, z, None, weight, code, each, first, center, act, eps)
+    _call("gdn_gate_norm_forward", pr, x.data_ptr(), z.data_ptr(), weight.data_ptr(), _ptr(bias), y.data_ptr(), handle)
+    return y
+
+
+def gate_norm_backward(dy, x, z, weight, bias=None, *, eps=1e-5, activation="silu", gate_first=False, center=False, dx=None,
+                       dz=None, dweight=None, dbias=None, workspace=None, stream=None):
+    """The gated norm's gradients for dy (dense, like x).  Returns (dx, dz, dweight,
+    dbias): dx dense; dz may be given as a part of a wider buffer, as z is of a
+    projection's rows; dweight and dbias fp32 like the weight and the bias (None
+    without one)."""
+    dev, code, each = _gate_norm_checks(x, z, weight, bias, activation, center)
+    _check(dy, "dy", dev, x.shape, x.dtype)
+    if bias is None:
+        _unwritten(dbias, "dbias", "a bias")
+    return _on(dev, stream, _gate_norm_backward, dev, code, dy, x, z, weight, bias, each, gate_first, center, _ACT[activation], eps,
+               dx, dz, dweight, dbias, workspace)
+
+
+def _gate_norm_backward(handle, dev, code, dy, x, z, weight, bias, each, first, center, act, eps, dx, dz, dweight, dbias, workspace):
+    ins = (dy, x, z, weight, bias)
+    dx = _out(dx, "dx", dev, x.shape, x.dtype, ins, x)
+    if dz is None:
+        dz = torch.empty(x.shape, device=dev, dtype=x.dtype)
+    else:
+        _check(dz, "dz", dev, x.shape, x.dtype, dense=False)
+        _apart(dz, "dz", *ins, dx)
+    dweight = _out(dweight, "dweight", dev, weight.shape, torch.float32, ins + (dx, dz), weight)
+    dbias = None if bias is None else _out(dbias, "dbias", dev, bias.shape, torch.float32, ins + (dx, dz, dweight), bias)
+    pr, need = _gate_norm_problem("gdn_workspace_bytes_gate_norm_backward", x, z, dz, weight, code, each, first, center, act, eps)
+    workspace, size = _workspace(need, dev, workspace)
+    _call("gdn_gate_norm_backward", pr, dy.data_ptr(), x.data_ptr(), z.data_ptr(), weight.data_ptr(), _ptr(bias), dx.data_ptr(), dz.data_ptr(),
+          dweight.data_ptr(), _ptr(dbias), _ptr(workspace), size, handle)
+    return dx, dz, dweight, dbias
+
+
+# ---------------------------------------------------------------------------
+# gated linear recurrence
+# ---------------------------------------------------------------------------
+
+_FORM = {"log": 0, "sigmoid": 1, "rate": 2}
+_SCALE = {None: 0, "complement": 1, "norm": 2}
+
+
+def _glr_checks(x, gate, gate_bias, rate, form, scale, dims):
+    dev = _device(x, "x")
+    code = _io_code(x, "x")
+    if x.dim() != dims or x.shape[-1] < 1:
+        raise ValueError("x must be %s, got %s" % ("[B, T, D]" if dims == 3 else "[B, D]", tuple(x.shape)))
+    _check(gate, "gate", dev, x.shape, x.dtype, torch.float32, dense=False)
+    if form not in _FORM:
+        raise ValueError("form must be 'log', 'sigmoid' or 'rate', got %r" % (form,))
+    if scale not in _SCALE:
+        raise ValueError("scale must be None, 'complement' or 'norm', got %r" % (scale,))
+    if (form == "rate") != (rate is not None):
+        raise ValueError("a rate is needed for form 'rate'" if rate is None else "a rate is for form 'rate' only")
+    for t, name in ((gate_bias, "gate_bias"), (rate, "rate")):
+        if t is not None:
+            _check(t, name, dev, x.shape[-1:], torch.float32)
+    return dev, code
+
+
+def glr_forward(x, gate, h0=None, *, gate_bias=None, rate=None, form="log", scale=None, cu_seqlens=None, y=None, hT=None,
+                output_final_state=True, workspace=None, stream=None):
+    """Gated linear recurrence per channel: h_t = a_t h_{t-1} + c_t x_t, y_t = h_t.
+
+    form: with v = gate + gate_bias, "log": log a = v; "sigmoid": a = sigmoid(v);
+    "rate": log a = -rate sigmoid(v).  scale: c = 1 (None), 1 - a ("complement") or
+    sqrt(1 - a^2) ("norm").  x [B, T, D] bf16 or fp32, gate like it in x's type or
+    fp32 (tokens of each may be strided); gate_bias, rate [D] fp32; h0 [B, D] fp32, or
+    [n, D] with cu_seqlens (as in conv_forward).  Returns (y [B, T, D], hT like h0
+    or None)."""
+    dev, code = _glr_checks(x, gate, gate_bias, rate, form, scale, 3)
+    n = _packed(cu_seqlens, dev, x.shape[0])
+    if h0 is not None:
+        _check(h0, "h0", dev, (n or x.shape[0], x.shape[2]), torch.float32)
+    return _on(dev, stream, _glr_forward, dev, code, x, gate, h0, gate_bias, rate, _FORM[form], _SCALE[scale], cu_seqlens, n, y, hT,
+               output_final_state, workspace)
+
+
+def _glr_forward(handle, dev, code, x, gate, h0, gate_bias, rate, form, scale, cu_seqlens, n, y, hT, want, workspace):
+    B, T, D = x.shape
+    ins = (x, gate, h0, gate_bias, rate, cu_seqlens)
+    y = _out(y, "y", dev, x.shape, x.dtype, ins, x)
+    if hT is not None or want:
+        hT = _out(hT, "hT", dev, (n or B, D), torch.float32, ins + (y,), h0)
+    pr, need = _problem(GlrProblem, "gdn_workspace_bytes_glr", B, T, D, *_strides(x, "x"), *_strides(gate, "gate"), 0, 0, 0, 0, 0, 0, n,
+                        code, _CODE[gate.dtype], form, scale)
+    workspace, size = _workspace(need, dev, workspace)
+    _call("gdn_glr_forward", pr, x.data_ptr(), gate.data_ptr(), _ptr(gate_bias), _ptr(rate), _ptr(h0), _ptr(cu_seqlens), y.data_ptr(),
+          _ptr(hT), _ptr(workspace), size, handle)
+    return y, hT
+
+
+def glr_backward(dy, x, gate, h0=None, dhT=None, *, gate_bias=None, rate=None, form="log", scale=None, cu_seqlens=None,
+                 dx=None, dgate=None, dbias=None, drate=None, dh0=None, workspace=None, stream=None):
+    """The recurrence's gradients for dy [B, T, D] (tokens may be strided) and dhT
+    (of the final states, or None); the states are formed again from the inputs.
+    Returns (dx, dgate, dbias, drate, dh0): dx in x's type, dgate in the gate's, dbias
+    (of gate_bias), drate and dh0 fp32, None where gate_bias, rate and h0 are.  dx and
+    dgate may be given as parts of one buffer, as the gradient of the projection
+    that x and the gate come from."""
+    dev, code = _glr_checks(x, gate, gate_bias, rate, form, scale, 3)
+    n = _packed(cu_seqlens, dev, x.shape[0])
+    _check(dy, "dy", dev, x.shape, x.dtype, dense=False)
+    for t, name, of, what in ((dbias, "dbias", gate_bias, "gate_bias"), (drate, "drate", rate, "rate"), (dh0, "dh0", h0, "h0")):
+        if of is None:
+            _unwritten(t, name, what)
+    for t, name in ((h0, "h0"), (dhT, "dhT")):
+        if t is not None:
+            _check(t, name, dev, (n or x.shape[0], x.shape[2]), torch.float32)
+    return _on(dev, stream, _glr_backward, dev, code, dy, x, gate, h0, dhT, gate_bias, rate, _FORM[form], _SCALE[scale], cu_seqlens, n,
+               dx, dgate, dbias, drate, dh0, workspace)
+
+
+def _token_rows_apart(dx, dgate):
+    """dx and dgate, each [B, T, D] at strides of its own, hold no element twice."""
+    B, T, D = dx.shape
+    if not dx.numel():
+        return
+    (xb, xt), (gb, gt) = _strides(dx, "dx"), _strides(dgate, "dgate")
+    for (sb, st), name in (((xb, xt), "dx"), ((gb, gt), "dgate")):
+        if T > 1 and st < D or B > 1 and sb < (T - 1) * st + D:
+            raise ValueError("%s's rows must not overlap" % name)
+    (a, a1), (b, b1) = _span(dx), _span(dgate)
+    if a1 <= b or b1 <= a:
+        return
+    # rows side by side in one buffer
+    size = dx.element_size()
+    apart = abs(b - a) // size
+    first = a if a < b else b
+    end = max(a, b) - first + D * size
+    if dx.dtype is dgate.dtype and (T == 1 or xt == gt) and (B == 1 or xb == gb) and apart >= D and (T == 1 or end <= xt * size) \
+            and (B == 1 or end + (T - 1) * xt * size <= xb * size):
+        return
+    raise ValueError("dx and dgate must not share memory")
+
+
+def _glr_backward(handle, dev, code, dy, x, gate, h0, dhT, gate_bias, rate, form, scale, cu_seqlens, n, dx, dgate, dbias, drate, dh0,
+                  workspace):
+    B, T, D = x.shape
+    ins = (dy, x, gate, h0, dhT, gate_bias, rate, cu_seqlens)
+    for t, name, like in ((dx, "dx", x), (dgate, "dgate", gate)):
+        if t is not None:
+            _check(t, name, dev, x.shape, like.dtype, dense=False)
+            _apart(t, name, *ins)
+    if dx is None and dgate is None and x.dtype is gate.dtype:
+        # side by side, as a projection lays x and the gate out
+        both = torch.empty(B, T, 2 * D, device=dev, dtype=x.dtype)
+        dx, dgate = both[..., :D], both[..., D:]
+    else:
+        dx = torch.empty(B, T, D, device=dev, dtype=x.dtype) if dx is None else dx
+        dgate = torch.empty(B, T, D, device=dev, dtype=gate.dtype) if dgate is None else dgate
+        _token_rows_apart(dx, dgate)
+    ins += (dx, dgate)
+    dbias = None if gate_bias is None else _out(dbias, "dbias", dev, (D,), torch.float32, ins, gate_bias)
+    drate = None if rate is None else _out(drate, "drate", dev, (D,), torch.float32, ins + (dbias,), rate)
+    dh0 = None if h0 is None else _out(dh0, "dh0", dev, h0.shape, torch.float32, ins + (dbias, drate), h0)
+    pr, need = _problem(GlrProblem, "gdn_workspace_bytes_glr_backward", B, T, D, *_strides(x, "x"), *_strides(gate, "gate"),
+                        *_strides(dy, "dy"), *_strides(dx, "dx"), *_strides(dgate, "dgate"), n, code, _CODE[gate.dtype], form, scale)
+    workspace, size = _workspace(need, dev, workspace)
+    _call("gdn_glr_backward", pr, dy.data_ptr(), x.data_ptr(), gate.data_ptr(), _ptr(gate_bias), _ptr(rate), _ptr(h0), _ptr(cu_seqlens),
+          _ptr(dhT), dx.data_ptr(), dgate.data_ptr(), _ptr(dbias), _ptr(drate), _ptr(dh0), _ptr(workspace), size, handle)
+    return dx, dgate, dbias, drate, dh0
+
+
+def glr_step(x, gate, state, *, gate_bias=None, rate=None, form="log", scale=None, slots=None, y=None, stream=None):
+    """One token for each of B sequences: x and gate [B, D] (rows may be strided);
+    state [S, D] fp32, moved on in place; slots as in conv_step; the rest as in
+    glr_forward.  Returns y [B, D]."""
+    dev, code = _glr_checks(x, gate, gate_bias, rate, form, scale, 2)
+    if not isinstance(state, torch.Tensor) or state.dim() != 2:
+        raise ValueError("state must be [S, D]")
+    B, D = x.shape
+    _check(state, "state", dev, (state.shape[0], D), torch.float32)
+    if slots is not None:
+        _check(slots, "slots", dev, (B,), torch.int32)
+    _apart(state, "state", x, gate, gate_bias, rate, slots)
+    return _on(dev, stream, _glr_step, dev, code, x, gate, state, gate_bias, rate, _FORM[form], _SCALE[scale], slots, y)
+
+
+def _glr_step(handle, dev, code, x, gate, state, gate_bias, rate, form, scale, slots, y):
+    B, D = x.shape
+    y = _out(y, "y", dev, x.shape, x.dtype, (x, gate, gate_bias, rate, slots, state), x)
+    if B:
+        pr, _ = _problem(GlrProblem, None, B, 1, D, _row_stride(x, "x"), D, _row_stride(gate, "gate"), D, 0, 0, 0, 0, 0, 0, 0, code,
+                         _CODE[gate.dtype], form, scale)
+        _call("gdn_glr_step", pr, x.data_ptr(), gate.data_ptr(), _ptr(gate_bias), _ptr(rate), state.data_ptr(), _ptr(slots), state.shape[0],
+              y.data_ptr(), handle)
     return y

@@ -80,7 +80,7 @@
 extern "C" {
 #endif
 
-#define GDN_ABI_VERSION 11
+#define GDN_ABI_VERSION 12
 
 typedef enum gdn_status {
     GDN_OK = 0,

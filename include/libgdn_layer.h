@@ -1,9 +1,10 @@
 /*
  * libgdn, the operators of a layer around the recurrence -- the
- * root-mean-square norm in front of it, the short causal convolution behind
- * its projections, and the selective state space scan (the recurrence without
- * the delta rule's erase term) -- for prompts, single tokens and training, on
- * AMD Instinct MI355X (gfx950).  They are part of libgdn.so and keep the
+ * root-mean-square norm or layer norm in front of it, the short causal
+ * convolution behind its projections, the selective state space scan (the
+ * recurrence without the delta rule's erase term), the gated linear recurrence
+ * of single channels, and the gated norm behind the heads -- for prompts, single
+ * tokens and training, on AMD Instinct MI355X (gfx950).  They are part of libgdn.so and keep the
  * conventions of libgdn.h:
  *   - the caller allocates every buffer (device memory of the current device)
  *     and owns it; a call only enqueues work on `stream`, never allocates,
@@ -94,6 +95,80 @@ gdn_status gdn_norm_backward(const gdn_norm_problem *problem, const void *dy, co
                              float *dweight, void *workspace, size_t workspace_bytes,
                              void *stream);
 size_t gdn_workspace_bytes_norm_backward(const gdn_norm_problem *problem);
+
+/* ------------------------------------------------------------------------
+ * Layer norm of x plus a residual: the same problem, with the row's mean taken
+ * out and a bias.
+ *   s = x + residual, rounded to the residual's type (s = x without one)
+ *   m = mean(s),  r = 1 / sqrt(mean((s - m)^2) + eps),  y = (s - m) r weight + bias
+ * The mean is taken before the squares, so a row far from zero keeps its digits.
+ *
+ * gdn_layer_norm_forward -- as gdn_norm_forward, with bias [D] in the weight's
+ *   type, or NULL (zero).
+ */
+gdn_status gdn_layer_norm_forward(const gdn_norm_problem *problem, const void *x, const void *residual,
+                                  const void *weight, const void *bias, void *y, void *s,
+                                  float *scales, void *stream);
+
+/*
+ * gdn_layer_norm_backward -- as gdn_norm_backward, and dbias [D] fp32, or NULL:
+ *   with h = (s - m) r and u = dy w
+ *   ds = dres + r (u - mean(u) - h mean(u h)),
+ *   dweight = sum over rows dy h,  dbias = sum over rows dy
+ * Workspace: gdn_workspace_bytes_layer_norm_backward(problem) bytes, 16-byte
+ * aligned.  Two launches.
+ */
+gdn_status gdn_layer_norm_backward(const gdn_norm_problem *problem, const void *dy, const void *s,
+                                   const void *weight, const void *dres, void *ds, void *dx,
+                                   float *dweight, float *dbias, void *workspace,
+                                   size_t workspace_bytes, void *stream);
+size_t gdn_workspace_bytes_layer_norm_backward(const gdn_norm_problem *problem);
+
+/* ------------------------------------------------------------------------
+ * Gated norm, the norm behind a recurrence's heads: T tokens of H rows of D
+ * elements, each row on its own.
+ *   y = n(x) act(z),  or with the gate first  y = n(x act(z))
+ *   n(v) = v r weight,  r = 1 / sqrt(mean(v^2) + eps);  centred:
+ *   n(v) = (v - m) r weight + bias,  m = mean(v), r of v - m
+ *   act(z) = z / (1 + e^-z) or 1 / (1 + e^-z)
+ * Everything between the loads and the stores is fp32.
+ */
+#define GDN_ACT_SILU 0
+#define GDN_ACT_SIGMOID 1
+
+typedef struct gdn_gate_norm_problem {
+    int64_t T, H, D;          /* T >= 0, H >= 1, 1 <= D <= 8192; T H < 2^31 */
+    int64_t x_stride_t, x_stride_h;    /* x [T, H, D]: between tokens, rows of a token */
+    int64_t z_stride_t, z_stride_h;    /* z [T, H, D] */
+    int64_t dz_stride_t, dz_stride_h;  /* dz (backward only): rows must not overlap */
+    int32_t io_dtype;         /* of x, z, y and their gradients */
+    int32_t w_dtype;          /* of weight and bias: io_dtype or GDN_F32 */
+    int32_t each;             /* 0: weight and bias are [D]; 1: [H, D] */
+    int32_t gate_first, center, act;
+    float eps;                /* >= 0 */
+} gdn_gate_norm_problem;
+
+/*
+ * gdn_gate_norm_forward -- y [T, H, D] (dense).  weight [D] or [H, D]; bias
+ * like it, or NULL (zero; without center it must be NULL).  One launch (for
+ * every 2^22 rows).
+ */
+gdn_status gdn_gate_norm_forward(const gdn_gate_norm_problem *problem, const void *x, const void *z,
+                                 const void *weight, const void *bias, void *y, void *stream);
+
+/*
+ * gdn_gate_norm_backward -- the gradients for dy [T, H, D] (dense): dx (dense)
+ * and dz in the io type, dweight fp32 like the weight, dbias fp32 like the bias
+ * (or NULL; without center it must be NULL).  The norm is formed again from x and
+ * z.  bias: as in the forward pass (dz reads it).  Workspace:
+ * gdn_workspace_bytes_gate_norm_backward(problem) bytes, 16-byte aligned.  Two
+ * launches.
+ */
+gdn_status gdn_gate_norm_backward(const gdn_gate_norm_problem *problem, const void *dy, const void *x,
+                                  const void *z, const void *weight, const void *bias, void *dx,
+                                  void *dz, float *dweight, float *dbias, void *workspace,
+                                  size_t workspace_bytes, void *stream);
+size_t gdn_workspace_bytes_gate_norm_backward(const gdn_gate_norm_problem *problem);
 
 /* ------------------------------------------------------------------------
  * Short causal convolution, one filter of W taps per channel.
@@ -232,6 +307,87 @@ size_t gdn_workspace_bytes_ssm_backward(const gdn_ssm_problem *problem);
 gdn_status gdn_ssm_step(const gdn_ssm_problem *problem, const void *x, const void *dt,
                         const float *A, const void *Bm, const void *Cm, const float *D,
                         const float *dt_bias, float *state, const int32_t *slots,
+                        int64_t n_slots, void *y, void *stream);
+
+/* ------------------------------------------------------------------------
+ * Gated linear recurrence of single channels.  Per sequence and channel
+ *   h_t = a_t h_{t-1} + c_t x_t,    y_t = h_t
+ * where a_t comes from a gate, with v_t = gate_t + bias:
+ *   GDN_GLR_LOG      log a = v                      (v <= 0 for a memory that fades)
+ *   GDN_GLR_SIGMOID  a = 1 / (1 + e^-v)
+ *   GDN_GLR_RATE     log a = -rate / (1 + e^-v)     (rate >= 0, per channel)
+ * and c_t from a_t:
+ *   GDN_GLR_PLAIN       c = 1
+ *   GDN_GLR_COMPLEMENT  c = 1 - a
+ *   GDN_GLR_NORM        c = sqrt(1 - a^2)
+ * The state is fp32 and 1 - a is taken from log a, not from a rounded a: over
+ * segments of the sequence the state moves as h - (1 - a) h, so that memories of
+ * thousands of tokens keep their digits (final states of bf16 or fp32 inputs within 1e-6 of the
+ * recurrence in 64 bits, of the vectors' norms).  A NaN or an infinity in a
+ * token reaches the tokens behind it in its sequence and channel, no other.
+ * In the gradients c = sqrt(1 - a^2) has the derivative 0 by log a where a is 1.
+ */
+#define GDN_GLR_LOG 0
+#define GDN_GLR_SIGMOID 1
+#define GDN_GLR_RATE 2
+#define GDN_GLR_PLAIN 0
+#define GDN_GLR_COMPLEMENT 1
+#define GDN_GLR_NORM 2
+
+typedef struct gdn_glr_problem {
+    int64_t B, T, D;          /* B >= 1, T >= 0, D >= 1 */
+    int64_t x_stride_b, x_stride_t;    /* x [B, T, D]: between batches, tokens */
+    int64_t g_stride_b, g_stride_t;    /* gate [B, T, D] */
+    int64_t dy_stride_b, dy_stride_t;  /* dy (backward only) */
+    int64_t dx_stride_b, dx_stride_t;  /* dx (backward only): rows must not overlap */
+    int64_t dg_stride_b, dg_stride_t;  /* dgate (backward only): rows must not overlap */
+    int64_t n_seqs;           /* packed sequences (with cu_seqlens); else 0 */
+    int32_t io_dtype;         /* of x, y and their gradients */
+    int32_t g_dtype;          /* of the gate and its gradient: io_dtype or GDN_F32 */
+    int32_t form;             /* GDN_GLR_LOG, _SIGMOID, _RATE */
+    int32_t scale;            /* GDN_GLR_PLAIN, _COMPLEMENT, _NORM */
+} gdn_glr_problem;
+
+/*
+ * gdn_glr_forward -- y [B, T, D] (dense) and the final states.
+ *   bias [D] fp32 or NULL (zero); rate [D] fp32 (GDN_GLR_RATE only, else NULL);
+ *   h0, hT [B, D] fp32 ([n_seqs, D] with cu_seqlens) or NULL.
+ *   cu_seqlens as in gdn_conv_forward; rows of y that belong to no sequence
+ *   are left as they were.
+ * Strides between tokens are at most 2^20; states have fewer than 2^29 values in all.
+ * Workspace: gdn_workspace_bytes_glr(problem) bytes (may be 0), 16-byte aligned.
+ * One or two launches.
+ */
+gdn_status gdn_glr_forward(const gdn_glr_problem *problem, const void *x, const void *gate,
+                           const float *bias, const float *rate, const float *h0,
+                           const int32_t *cu_seqlens, void *y, float *hT, void *workspace,
+                           size_t workspace_bytes, void *stream);
+size_t gdn_workspace_bytes_glr(const gdn_glr_problem *problem);
+
+/*
+ * gdn_glr_backward -- the gradients for dy [B, T, D] and dhT (the final states'
+ * gradient, or NULL): dx in the io type, dgate in the gate's, dbias and drate
+ * [D] fp32, dh0 fp32 like h0; dbias, drate (GDN_GLR_RATE only) and dh0 may be
+ * NULL.  The states are formed again from the inputs.  With cu_seqlens, dx and
+ * dgate of rows that belong to no sequence are left as they were.  Workspace:
+ * gdn_workspace_bytes_glr_backward(problem) bytes, 16-byte aligned.  Up to four
+ * launches.
+ */
+gdn_status gdn_glr_backward(const gdn_glr_problem *problem, const void *dy, const void *x,
+                            const void *gate, const float *bias, const float *rate, const float *h0,
+                            const int32_t *cu_seqlens, const float *dhT, void *dx, void *dgate,
+                            float *dbias, float *drate, float *dh0, void *workspace,
+                            size_t workspace_bytes, void *stream);
+size_t gdn_workspace_bytes_glr_backward(const gdn_glr_problem *problem);
+
+/*
+ * gdn_glr_step -- one token for each of B sequences (T = 1): y [B, D], and the
+ * states [n_slots, D] fp32 move on in place; slots, padding and repeated slots
+ * as in gdn_conv_step.  x and the gate have x_stride_b and g_stride_b between
+ * rows.  One launch.
+ */
+gdn_status gdn_glr_step(const gdn_glr_problem *problem, const void *x, const void *gate,
+                        const float *bias, const float *rate, float *state, const int32_t *slots,
                         int64_t n_slots, void *y, void *stream);
 
 #ifdef __cplusplus
