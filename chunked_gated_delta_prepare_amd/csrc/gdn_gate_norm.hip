@@ -22,31 +22,35 @@ struct GateNormParams {
     float *part;
     int64_t rows;                                    // of one class: rows that share their weights
     int64_t xt, xh, zt, zh, dzt, dzh;
-    uint32_t H, classes;
-    int D, parts, w_f32, first, center, silu;
+    uint32_t H, inv_h, classes;                      // inv_h: 2^32 / H, rounded down
+    int D, parts, w_f32, silu;
     int64_t row0;                                    // of this launch (forward)
     float eps, inv_d;
 };
 
-// VEC elements of a row at its element e, zero where the row has none.
+// VEC elements of a row at its element e, or at its first where it has none there
+// (so that no branch stands around a load): keep() makes those zero.
 template <typename T, int VEC>
-__device__ __forceinline__ void fetch_row(RawRow<T, VEC> &r, const T *row, uint32_t e, bool ok) {
-#pragma unroll
-    for (auto &v : r.u) v = 0;
-    if (!ok) return;
+__device__ __forceinline__ void fetch_row(RawRow<T, VEC> &r, const T *row, uint32_t e, uint32_t D) {
+    row += e < D ? e : 0;
     if constexpr (VEC * sizeof(T) == 2) {
-        r.u[0] = *(const uint16_t *)(row + e);
+        r.u[0] = *(const uint16_t *)row;
     } else if constexpr (VEC * sizeof(T) == 4) {
-        r.u[0] = *(const uint32_t *)(row + e);
+        r.u[0] = *(const uint32_t *)row;
     } else if constexpr (VEC * sizeof(T) == 8) {
-        const u32x2 v = *(const u32x2 *)(row + e);
+        const u32x2 v = *(const u32x2 *)row;
         r.u[0] = v[0];
         r.u[1] = v[1];
     } else {
-        const u32x4 v = *(const u32x4 *)(row + e);
+        const u32x4 v = *(const u32x4 *)row;
 #pragma unroll
         for (int i = 0; i < 4; ++i) r.u[i] = v[i];
     }
+}
+template <typename T, int VEC>
+__device__ __forceinline__ void keep(RawRow<T, VEC> &r, bool ok) {
+#pragma unroll
+    for (auto &v : r.u) v = ok ? v : 0;
 }
 
 // VEC values to a row's element e, where e < end (the row's length, or 0).  All
@@ -66,16 +70,29 @@ __device__ __forceinline__ void put_row(T *row, uint32_t e, uint32_t end, const 
     }
 }
 
-// act(z) and act'(z)
+// Row `at` of all as token t and head h.
+__device__ __forceinline__ void token_head(const GateNormParams &p, uint32_t at, uint32_t &t, uint32_t &h) {
+    // (the product falls short of the quotient by less than 2)
+    t = __umulhi(at, p.inv_h);
+    h = at - t * p.H;
+    if (h >= p.H) {
+        ++t;
+        h -= p.H;
+    }
+}
+
+// act(z) and act'(z); for bf16 the exponential's last digits do not matter.
+template <typename IO>
 struct Act {
     float a, d;
     __device__ __forceinline__ Act(float z, int silu) {
-        const Sigmoid g(z);
+        const Sigmoid<sizeof(IO) == 4> g(z);
         a = silu ? z * g.s : g.s;
         d = silu ? fmaf(z * g.s, g.o, g.s) : g.s * g.o;
     }
 };
 
+// Sums over the TPR threads of a slot, in every one of them; red has N TPR / 64 places.
 template <int TPR, int N>
 __device__ __forceinline__ void slot_total(float (&v)[N], float *red) {
 #pragma unroll
@@ -100,29 +117,34 @@ __device__ __forceinline__ void slot_total(float (&v)[N], float *red) {
 template <int TPR>
 constexpr int kGateThreads = TPR < 256 ? 256 : TPR;
 
-// v -> v - mean v where the row has elements
-template <int VEC, int TPR, int K>
-__device__ __forceinline__ void slot_mean(float (&v)[K][VEC], uint32_t D, int tid, float inv_d, float *red) {
-    float t[1] = {0.f};
+// v -> v - mean v of each of R rows, where it has elements
+template <int VEC, int TPR, int K, int R>
+__device__ __forceinline__ void slot_mean(float (&v)[R][K][VEC], uint32_t D, int tid, float inv_d, float *red) {
+    float t[R];
 #pragma unroll
-    for (int k = 0; k < K; ++k)
+    for (int j = 0; j < R; ++j) {
+        t[j] = 0.f;
 #pragma unroll
-        for (int i = 0; i < VEC; ++i) t[0] += v[k][i];
+        for (int k = 0; k < K; ++k)
+#pragma unroll
+            for (int i = 0; i < VEC; ++i) t[j] += v[j][k][i];
+    }
     slot_total<TPR>(t, red);
-    const float m = t[0] * inv_d;
 #pragma unroll
-    for (int k = 0; k < K; ++k)
+    for (int j = 0; j < R; ++j)
 #pragma unroll
-        for (int i = 0; i < VEC; ++i) v[k][i] = (uint32_t)((k * TPR + tid) * VEC) < D ? v[k][i] - m : 0.f;
+        for (int k = 0; k < K; ++k)
+#pragma unroll
+            for (int i = 0; i < VEC; ++i) v[j][k][i] = (uint32_t)((k * TPR + tid) * VEC) < D ? v[j][k][i] - t[j] * inv_d : 0.f;
 }
 
 __device__ __forceinline__ float inverse_root(float ms, float eps) { return 1.f / sqrtf((ms < 0.f ? 0.f : ms) + eps); }
 
-// R rows of a slot's are loaded before the first is worked on.
-template <typename IO, int VEC, int TPR, int K, int R>
+// A slot (TPR threads) has R rows in flight and works on them together.
+template <typename IO, int VEC, int TPR, int K, int R, bool FIRST, bool CENTER>
 __global__ void __launch_bounds__(kGateThreads<TPR>) gate_norm_forward_kernel(GateNormParams p) {
     constexpr int kSlots = kGateThreads<TPR> / TPR;
-    __shared__ float red[2][2][TPR < 64 ? 1 : TPR / 64];
+    __shared__ float red[3 * R * (TPR < 64 ? 1 : TPR / 64)];
     const int slot = threadIdx.x / TPR, tid = threadIdx.x % TPR;
     const uint32_t D = p.D;
     RawRow<IO, VEC> xr[R][K], zr[R][K];
@@ -132,45 +154,54 @@ __global__ void __launch_bounds__(kGateThreads<TPR>) gate_norm_forward_kernel(Ga
     for (int j = 0; j < R; ++j) {
         const int64_t row = row0 + j * kSlots;
         const bool live = row < p.rows;
-        const uint32_t at = live ? (uint32_t)row : 0, t = at / p.H;
-        head[j] = at - t * p.H;
+        const uint32_t at = live ? (uint32_t)row : 0;
+        uint32_t t;
+        token_head(p, at, t, head[j]);
         const IO *xp = (const IO *)p.x + t * p.xt + head[j] * p.xh, *zp = (const IO *)p.z + t * p.zt + head[j] * p.zh;
 #pragma unroll
         for (int k = 0; k < K; ++k) {
             const uint32_t e = (k * TPR + tid) * VEC;
-            fetch_row(xr[j][k], xp, e, live && e < D);
-            fetch_row(zr[j][k], zp, e, live && e < D);
+            fetch_row(xr[j][k], xp, e, D);
+            fetch_row(zr[j][k], zp, e, D);
         }
     }
     const uint32_t wb = p.w_f32 ? 4 : (uint32_t)sizeof(IO), nw = D * (p.classes > 1 ? p.H : 1);
     const rsrc_t rw = make_rsrc(p.w, nw * wb), rb = make_rsrc(p.b, p.b ? nw * wb : 0);
+    float v[R][K][VEC], g[R][K][VEC], t[2 * R];
 #pragma unroll
-    for (int j = 0; j < R; ++j) {
-        const int64_t row = row0 + j * kSlots;
-        float v[K][VEC], g[K][VEC];
+    for (int j = 0; j < R; ++j)
 #pragma unroll
         for (int k = 0; k < K; ++k) {
-            xr[j][k].get(v[k]);
-            zr[j][k].get(g[k]);
+            // (a row past the end is the first one again, and is not stored)
+            keep(xr[j][k], (uint32_t)((k * TPR + tid) * VEC) < D);
+            keep(zr[j][k], (uint32_t)((k * TPR + tid) * VEC) < D);
+            xr[j][k].get(v[j][k]);
+            zr[j][k].get(g[j][k]);
 #pragma unroll
             for (int i = 0; i < VEC; ++i) {
-                const float a = Act(g[k][i], p.silu).a;
-                if (p.first) v[k][i] *= a;
-                g[k][i] = p.first ? 1.f : a;
+                const float a = Act<IO>(g[j][k][i], p.silu).a;
+                if (FIRST) v[j][k][i] *= a;
+                g[j][k][i] = FIRST ? 1.f : a;
             }
         }
-        if (p.center) slot_mean<VEC, TPR, K>(v, D, tid, p.inv_d, red[0][0]);
-        float t[2] = {0.f, 0.f};
+    if (CENTER) slot_mean<VEC, TPR, K, R>(v, D, tid, p.inv_d, red);
+#pragma unroll
+    for (int j = 0; j < R; ++j) {
+        t[2 * j] = t[2 * j + 1] = 0.f;
 #pragma unroll
         for (int k = 0; k < K; ++k)
 #pragma unroll
             for (int i = 0; i < VEC; ++i) {
-                t[0] += v[k][i] * v[k][i];
-                t[1] += v[k][i];
+                t[2 * j] += v[j][k][i] * v[j][k][i];
+                t[2 * j + 1] += v[j][k][i];
             }
-        slot_total<TPR>(t, red[1][0]);
-        const float m = p.center ? t[1] * p.inv_d : 0.f;
-        const float r = inverse_root(t[0] * p.inv_d - m * m, p.eps);
+    }
+    slot_total<TPR>(t, red + R * (TPR < 64 ? 1 : TPR / 64));
+#pragma unroll
+    for (int j = 0; j < R; ++j) {
+        const int64_t row = row0 + j * kSlots;
+        const float m = CENTER ? t[2 * j + 1] * p.inv_d : 0.f;
+        const float r = inverse_root(t[2 * j] * p.inv_d - m * m, p.eps);
         const uint32_t own = p.classes > 1 ? head[j] * D : 0, end = row < p.rows ? D : 0;
 #pragma unroll
         for (int k = 0; k < K; ++k) {
@@ -180,8 +211,8 @@ __global__ void __launch_bounds__(kGateThreads<TPR>) gate_norm_forward_kernel(Ga
             row_load_either<IO, VEC>(rw, p.w_f32, own + e, w);
             row_load_either<IO, VEC>(rb, p.w_f32, own + e, b);
 #pragma unroll
-            for (int i = 0; i < VEC; ++i) v[k][i] = fmaf((v[k][i] - m) * r, w[i], b[i]) * g[k][i];
-            put_row<IO, VEC>((IO *)p.y + row * D, e, end, v[k]);
+            for (int i = 0; i < VEC; ++i) v[j][k][i] = fmaf((v[j][k][i] - m) * r, w[i], b[i]) * g[j][k][i];
+            put_row<IO, VEC>((IO *)p.y + row * D, e, end, v[j][k]);
         }
     }
 }
@@ -189,99 +220,167 @@ __global__ void __launch_bounds__(kGateThreads<TPR>) gate_norm_forward_kernel(Ga
 // A class is the rows that share their weights: all, or one head's.  Its rows
 // go to its workgroups' slots in turn; the slots' shares of dw and db stay in
 // registers and meet in LDS, and every workgroup leaves one row of D sums of
-// each in the workspace.  The next row is in flight while one is worked on (not
-// in the workgroups of 1024 threads, which have 128 registers each).
-template <typename IO, int VEC, int TPR, int K>
+// each in the workspace.  The next R rows are in flight while R are worked on
+// (not where rows of more than 4096 elements fill the registers).
+template <typename IO, int VEC, int TPR, int K, int R, bool FIRST, bool CENTER>
 __global__ void __launch_bounds__(kGateThreads<TPR>) gate_norm_backward_kernel(GateNormParams p) {
     constexpr int kSlots = kGateThreads<TPR> / TPR;
     constexpr int kW = TPR < 64 ? 1 : TPR / 64;
-    constexpr bool kAhead = TPR < 1024;
-    __shared__ float red[2][5][kW];
+    constexpr bool kAhead = K * VEC * R <= 8;
+    __shared__ float red[2][5 * R * kW];
     __shared__ float sums[TPR < 256 ? 4 : 1][TPR < 256 ? 2 : 1][TPR < 256 ? TPR * K * VEC : 1];
-    const int slot = threadIdx.x / TPR, tid = threadIdx.x % TPR;
+    const int slot = threadIdx.x / TPR, tid0 = threadIdx.x % TPR;
+    int tid = tid0;
     const uint32_t D = p.D, cls = blockIdx.x % p.classes, part = blockIdx.x / p.classes;
     const uint32_t wb = p.w_f32 ? 4 : (uint32_t)sizeof(IO);
     const rsrc_t rw = make_rsrc((const char *)p.w + (int64_t)cls * D * wb, D * wb),
                  rb = make_rsrc((const char *)p.b + (p.b ? (int64_t)cls * D * wb : 0), p.b ? D * wb : 0);
-    float w[K][VEC], b[K][VEC], dw[K][VEC], db[K][VEC];
+    // a vector of the weights: kept, or loaded again where it is used
+    float kw[kAhead ? K : 1][VEC], kb[kAhead ? K : 1][VEC], dw[K][VEC], db[K][VEC];
+    auto load_weights = [&](int k, float (&w)[VEC], float (&b)[VEC]) {
+        row_load_either<IO, VEC>(rw, p.w_f32, (k * TPR + tid) * VEC, w);
+        row_load_either<IO, VEC>(rb, p.w_f32, (k * TPR + tid) * VEC, b);
+    };
+    // The same without a branch: of the two types' descriptors one is empty, and reads zeros.
+    const rsrc_t rw4 = make_rsrc((const char *)p.w + (int64_t)cls * D * wb, wb == 4 ? D * 4 : 0),
+                 rw2 = make_rsrc((const char *)p.w + (int64_t)cls * D * wb, wb == 2 ? D * 2 : 0),
+                 rb4 = make_rsrc((const char *)p.b + (p.b ? (int64_t)cls * D * wb : 0), p.b && wb == 4 ? D * 4 : 0),
+                 rb2 = make_rsrc((const char *)p.b + (p.b ? (int64_t)cls * D * wb : 0), p.b && wb == 2 ? D * 2 : 0);
+    auto load_both = [&](rsrc_t r4, rsrc_t r2, int k, float (&w)[VEC]) {
+        RawRow<float, VEC> a4;
+        RawRow<bf16_t, VEC> a2;
+        float w2[VEC];
+        a4.load(r4, tid0 * VEC * 4, k * TPR * VEC * 4);
+        a2.load(r2, tid0 * VEC * 2, k * TPR * VEC * 2);
+        a4.get(w);
+        a2.get(w2);
+#pragma unroll
+        for (int i = 0; i < VEC; ++i) w[i] = __uint_as_float(__float_as_uint(w[i]) | __float_as_uint(w2[i]));
+    };
+    auto weights = [&](int k, float (&w)[VEC], float (&b)[VEC]) {
+        if constexpr (kAhead) {
+#pragma unroll
+            for (int i = 0; i < VEC; ++i) {
+                w[i] = kw[k][i];
+                b[i] = kb[k][i];
+            }
+        } else {
+            __builtin_amdgcn_sched_barrier(0);      // no loads ahead
+            load_both(rw4, rw2, k, w);
+            load_both(rb4, rb2, k, b);
+        }
+    };
 #pragma unroll
     for (int k = 0; k < K; ++k) {
-        row_load_either<IO, VEC>(rw, p.w_f32, (k * TPR + tid) * VEC, w[k]);
-        row_load_either<IO, VEC>(rb, p.w_f32, (k * TPR + tid) * VEC, b[k]);
+        if constexpr (kAhead) load_weights(k, kw[k], kb[k]);
 #pragma unroll
         for (int i = 0; i < VEC; ++i) dw[k][i] = db[k][i] = 0.f;
     }
-    RawRow<IO, VEC> xn[K], zn[K], dn[K];
-    // row i of this class: row i classes + cls of all
+    RawRow<IO, VEC> xn[R][K], zn[R][K], dn[R][K];
+    // rows i + j kSlots of this class: row i classes + cls of all
     auto fetch = [&](int64_t i) {
-        const bool live = i < p.rows;
-        const uint32_t at = live ? (uint32_t)(i * p.classes + cls) : 0, t = at / p.H, h = at - t * p.H;
-        const IO *xp = (const IO *)p.x + t * p.xt + h * p.xh, *zp = (const IO *)p.z + t * p.zt + h * p.zh,
-                 *dp = (const IO *)p.dy + (int64_t)at * D;
 #pragma unroll
-        for (int k = 0; k < K; ++k) {
-            const uint32_t e = (k * TPR + tid) * VEC;
-            fetch_row(xn[k], xp, e, live && e < D);
-            fetch_row(zn[k], zp, e, live && e < D);
-            fetch_row(dn[k], dp, e, live && e < D);
+        for (int j = 0; j < R; ++j) {
+            const bool live = i + j * kSlots < p.rows;
+            const uint32_t at = live ? (uint32_t)((i + j * kSlots) * p.classes + cls) : 0;
+            uint32_t t, h;
+            token_head(p, at, t, h);
+            const IO *xp = (const IO *)p.x + t * p.xt + h * p.xh, *zp = (const IO *)p.z + t * p.zt + h * p.zh,
+                     *dp = (const IO *)p.dy + (int64_t)at * D;
+#pragma unroll
+            for (int k = 0; k < K; ++k) {
+                const uint32_t e = (k * TPR + tid) * VEC;
+                fetch_row(xn[j][k], xp, e, D);
+                fetch_row(zn[j][k], zp, e, D);
+                fetch_row(dn[j][k], dp, e, D);
+            }
         }
     };
     // (all slots of a workgroup make the same number of turns: rows of several waves meet at barriers)
-    const int64_t step = (int64_t)p.parts * kSlots;
-    int64_t i0 = (int64_t)part * kSlots;
+    const int64_t step = (int64_t)p.parts * (kSlots * R);
+    int64_t i0 = (int64_t)part * (kSlots * R);
     if (kAhead) fetch(i0 + slot);
     int turn = 0;
     for (; i0 < p.rows; i0 += step) {
-        if (!kAhead) fetch(i0 + slot);
-        const bool live = i0 + slot < p.rows;
-        const uint32_t at = live ? (uint32_t)((i0 + slot) * p.classes + cls) : 0, t0 = at / p.H, hd = at - t0 * p.H;
-        float x[K][VEC], z[K][VEC], d[K][VEC], v[K][VEC];
-#pragma unroll
-        for (int k = 0; k < K; ++k) {
-            xn[k].get(x[k]);
-            zn[k].get(z[k]);
-            dn[k].get(d[k]);
+        if constexpr (!kAhead) {
+            // (offsets formed in the loop: kept, they would fill the registers)
+            asm volatile("" : "+v"(tid));
+            fetch(i0 + slot);
         }
+        // v: the row that is normed; d: dy; act(z) and act'(z)
+        float x[R][K][VEC], v[R][K][VEC], d[R][K][VEC], ga[R][K][VEC], gd[R][K][VEC], t[4 * R];
+#pragma unroll
+        for (int j = 0; j < R; ++j)
+#pragma unroll
+            for (int k = 0; k < K; ++k) {
+                float z[VEC];
+                // (nor does a row past the end enter the sums)
+                const bool ok = i0 + slot + j * kSlots < p.rows && (uint32_t)((k * TPR + tid) * VEC) < D;
+                keep(xn[j][k], ok);
+                keep(zn[j][k], ok);
+                keep(dn[j][k], ok);
+                xn[j][k].get(x[j][k]);
+                zn[j][k].get(z);
+                dn[j][k].get(d[j][k]);
+#pragma unroll
+                for (int i = 0; i < VEC; ++i) {
+                    const Act<IO> g(z[i], p.silu);
+                    ga[j][k][i] = g.a;
+                    gd[j][k][i] = g.d;
+                    v[j][k][i] = FIRST ? x[j][k][i] * g.a : x[j][k][i];
+                }
+            }
         if (kAhead) fetch(i0 + step + slot);
+        if (CENTER) slot_mean<VEC, TPR, K, R>(v, D, tid, p.inv_d, red[turn]);
 #pragma unroll
-        for (int k = 0; k < K; ++k)
+        for (int j = 0; j < R; ++j) {
 #pragma unroll
-            for (int i = 0; i < VEC; ++i) v[k][i] = p.first ? x[k][i] * Act(z[k][i], p.silu).a : x[k][i];
-        if (p.center) slot_mean<VEC, TPR, K>(v, D, tid, p.inv_d, red[turn][0]);
-        float t[4] = {0.f, 0.f, 0.f, 0.f};
+            for (int q = 0; q < 4; ++q) t[4 * j + q] = 0.f;
 #pragma unroll
-        for (int k = 0; k < K; ++k)
+            for (int k = 0; k < K; ++k) {
+                float w[VEC], b[VEC];
+                weights(k, w, b);
 #pragma unroll
-            for (int i = 0; i < VEC; ++i) {
-                const float u = (p.first ? d[k][i] : d[k][i] * Act(z[k][i], p.silu).a) * w[k][i];
-                t[0] += v[k][i] * v[k][i];
-                t[1] += u * v[k][i];
-                t[2] += v[k][i];
-                t[3] += u;
+                for (int i = 0; i < VEC; ++i) {
+                    const float u = (FIRST ? d[j][k][i] : d[j][k][i] * ga[j][k][i]) * w[i];
+                    t[4 * j] += v[j][k][i] * v[j][k][i];
+                    t[4 * j + 1] += u * v[j][k][i];
+                    t[4 * j + 2] += v[j][k][i];
+                    t[4 * j + 3] += u;
+                }
             }
-        slot_total<TPR>(t, red[turn][1]);
+        }
+        slot_total<TPR>(t, red[turn] + R * kW);
         turn ^= 1;
-        const float m = p.center ? t[2] * p.inv_d : 0.f, mu = p.center ? t[3] * p.inv_d : 0.f;
-        const float r = inverse_root(t[0] * p.inv_d - m * m, p.eps);
-        const float c = r * (t[1] * p.inv_d - m * (t[3] * p.inv_d));
-        IO *xo = (IO *)p.dx + (int64_t)at * D, *zo = (IO *)p.dz + t0 * p.dzt + hd * p.dzh;
-        const uint32_t end = live ? D : 0;
 #pragma unroll
-        for (int k = 0; k < K; ++k) {
-            const uint32_t e = (k * TPR + tid) * VEC;
-            float dx[VEC], dz[VEC];
+        for (int j = 0; j < R; ++j) {
+            const int64_t i1 = i0 + slot + j * kSlots;
+            const bool live = i1 < p.rows;
+            const uint32_t at = live ? (uint32_t)(i1 * p.classes + cls) : 0;
+            uint32_t t0, hd;
+            token_head(p, at, t0, hd);
+            const float m = CENTER ? t[4 * j + 2] * p.inv_d : 0.f, mu = CENTER ? t[4 * j + 3] * p.inv_d : 0.f;
+            const float r = inverse_root(t[4 * j] * p.inv_d - m * m, p.eps);
+            const float c = r * (t[4 * j + 1] * p.inv_d - m * (t[4 * j + 3] * p.inv_d));
+            IO *xo = (IO *)p.dx + (int64_t)at * D, *zo = (IO *)p.dz + t0 * p.dzt + hd * p.dzh;
+            const uint32_t end = live ? D : 0;
 #pragma unroll
-            for (int i = 0; i < VEC; ++i) {
-                const Act g(z[k][i], p.silu);
-                const float h = (v[k][i] - m) * r, dd = p.first ? d[k][i] : d[k][i] * g.a;
-                const float dv = r * (dd * w[k][i] - mu - h * c);
-                dw[k][i] += dd * h;
-                db[k][i] += dd;
-                dx[i] = p.first ? dv * g.a : dv;
-                dz[i] = (p.first ? dv * x[k][i] : d[k][i] * fmaf(h, w[k][i], b[k][i])) * g.d;
+            for (int k = 0; k < K; ++k) {
+                const uint32_t e = (k * TPR + tid) * VEC;
+                float dx[VEC], dz[VEC], w[VEC], b[VEC];
+                weights(k, w, b);
+#pragma unroll
+                for (int i = 0; i < VEC; ++i) {
+                    const float h = (v[j][k][i] - m) * r, dd = FIRST ? d[j][k][i] : d[j][k][i] * ga[j][k][i];
+                    const float dv = r * (dd * w[i] - mu - h * c);
+                    dw[k][i] += dd * h;
+                    db[k][i] += dd;
+                    dx[i] = FIRST ? dv * ga[j][k][i] : dv;
+                    dz[i] = (FIRST ? dv * x[j][k][i] : d[j][k][i] * fmaf(h, w[i], b[i])) * gd[j][k][i];
+                }
+                put_row<IO, VEC>(xo, e, end, dx);
+                put_row<IO, VEC>(zo, e, end, dz);
             }
-            put_row<IO, VEC>(xo, e, end, dx);
-            put_row<IO, VEC>(zo, e, end, dz);
         }
     }
     float *out = p.part + ((int64_t)cls * p.parts + part) * 2 * D;
@@ -337,8 +436,11 @@ gdn_status check_gate_norm(const gdn_gate_norm_problem *pr) {
 }
 
 int64_t gate_classes(const gdn_gate_norm_problem *pr) { return pr->each ? pr->H : 1; }
-int gate_tpr(int64_t D) { return D <= 64 ? 16 : D <= 128 ? 32 : D <= 512 ? 64 : D <= 2048 ? 256 : D <= 4096 ? 512 : 1024; }
-int gate_slots(int64_t D) { return gate_tpr(D) < 256 ? 256 / gate_tpr(D) : 1; }
+int gate_tpr(int64_t D) { return D <= 64 ? 16 : D <= 128 ? 32 : D <= 512 ? 64 : D <= 2048 ? 256 : 512; }
+// rows that a workgroup of the backward pass works on at a time (see gate_d)
+int gate_slots(int64_t D) {
+    return (gate_tpr(D) < 256 ? 256 / gate_tpr(D) : 1) * (D <= 256 || (D > 512 && D <= 1024) ? 2 : 1);
+}
 
 // Workgroups of a class in the backward pass.
 int64_t gate_parts(const gdn_gate_norm_problem *pr) {
@@ -349,35 +451,51 @@ int64_t gate_parts(const gdn_gate_norm_problem *pr) {
     return turns ? (n + turns - 1) / turns : 0;
 }
 
-template <bool BWD, typename IO, int VEC, int TPR, int K, int R>
+struct GateForm {
+    bool first, center;
+};
+
+template <bool BWD, typename IO, int VEC, int TPR, int K, int R, bool FIRST, bool CENTER>
 gdn_status run_gate(GateNormParams &np, int64_t rows, hipStream_t s) {
     if constexpr (BWD) {
-        return launch_kernel((const void *)&gate_norm_backward_kernel<IO, VEC, TPR, K>, (int)rows, &np, s, kGateThreads<TPR>);
+        return launch_kernel((const void *)&gate_norm_backward_kernel<IO, VEC, TPR, K, R, FIRST, CENTER>, (int)rows, &np, s, kGateThreads<TPR>);
     } else {
         constexpr int kPer = kGateThreads<TPR> / TPR * R;
-        return launch_kernel((const void *)&gate_norm_forward_kernel<IO, VEC, TPR, K, R>, (int)((rows + kPer - 1) / kPer), &np, s,
+        return launch_kernel((const void *)&gate_norm_forward_kernel<IO, VEC, TPR, K, R, FIRST, CENTER>, (int)((rows + kPer - 1) / kPer), &np, s,
                              kGateThreads<TPR>);
     }
 }
 
+template <bool BWD, typename IO, int VEC, int TPR, int K, int R>
+gdn_status gate_form(GateNormParams &np, GateForm f, int64_t rows, hipStream_t s) {
+    if (f.first) return f.center ? run_gate<BWD, IO, VEC, TPR, K, R, true, true>(np, rows, s) : run_gate<BWD, IO, VEC, TPR, K, R, true, false>(np, rows, s);
+    return f.center ? run_gate<BWD, IO, VEC, TPR, K, R, false, true>(np, rows, s) : run_gate<BWD, IO, VEC, TPR, K, R, false, false>(np, rows, s);
+}
+
+// Rows of a slot at a time: forward 16 elements a thread in flight, backward 8 (of three
+// tensors; 16 take 280 registers).
 template <bool BWD, typename IO, int VEC>
-gdn_status gate_d(GateNormParams &np, int64_t rows, hipStream_t s) {
+gdn_status gate_d(GateNormParams &np, GateForm f, int64_t rows, hipStream_t s) {
     const int D = np.D;
-    constexpr int M = 4 / VEC;
-    if (D <= 64) return run_gate<BWD, IO, VEC, 16, M, 4>(np, rows, s);
-    if (D <= 128) return run_gate<BWD, IO, VEC, 32, M, 4>(np, rows, s);
-    if (D <= 256) return run_gate<BWD, IO, VEC, 64, M, 4>(np, rows, s);
-    if (D <= 512) return run_gate<BWD, IO, VEC, 64, 2 * M, 2>(np, rows, s);
-    if (D <= 1024) return run_gate<BWD, IO, VEC, 256, M, 1>(np, rows, s);
-    if (D <= 2048) return run_gate<BWD, IO, VEC, 256, 2 * M, 1>(np, rows, s);
-    if (D <= 4096) return run_gate<BWD, IO, VEC, 512, 2 * M, 1>(np, rows, s);
-    return run_gate<BWD, IO, VEC, 1024, 2 * M, 1>(np, rows, s);
+    constexpr int M = 4 / VEC, R = BWD ? 2 : 4;
+    if (D <= 64) return gate_form<BWD, IO, VEC, 16, M, R>(np, f, rows, s);
+    if (D <= 128) return gate_form<BWD, IO, VEC, 32, M, R>(np, f, rows, s);
+    if (D <= 256) return gate_form<BWD, IO, VEC, 64, M, R>(np, f, rows, s);
+    if (D <= 512) return gate_form<BWD, IO, VEC, 64, 2 * M, R / 2>(np, f, rows, s);
+    if (D <= 1024) return gate_form<BWD, IO, VEC, 256, M, R>(np, f, rows, s);
+    if (D <= 2048) return gate_form<BWD, IO, VEC, 256, 2 * M, R / 2>(np, f, rows, s);
+    if (D <= 4096) return gate_form<BWD, IO, VEC, 512, 2 * M, R / 2>(np, f, rows, s);
+    if constexpr (BWD)
+        return gate_form<BWD, IO, VEC, 512, 4 * M, 1>(np, f, rows, s);
+    else
+        return gate_form<BWD, IO, VEC, 1024, 2 * M, 1>(np, f, rows, s);
 }
 
 template <bool BWD>
 gdn_status gate_types(const gdn_gate_norm_problem *pr, GateNormParams &np, bool vec, int64_t rows, hipStream_t s) {
-    if (pr->io_dtype == GDN_F32) return vec ? gate_d<BWD, float, 4>(np, rows, s) : gate_d<BWD, float, 1>(np, rows, s);
-    return vec ? gate_d<BWD, bf16_t, 4>(np, rows, s) : gate_d<BWD, bf16_t, 1>(np, rows, s);
+    const GateForm f{pr->gate_first != 0, pr->center != 0};
+    if (pr->io_dtype == GDN_F32) return vec ? gate_d<BWD, float, 4>(np, f, rows, s) : gate_d<BWD, float, 1>(np, f, rows, s);
+    return vec ? gate_d<BWD, bf16_t, 4>(np, f, rows, s) : gate_d<BWD, bf16_t, 1>(np, f, rows, s);
 }
 
 void fill_gate(const gdn_gate_norm_problem *pr, GateNormParams &np) {
@@ -389,11 +507,10 @@ void fill_gate(const gdn_gate_norm_problem *pr, GateNormParams &np) {
     np.dzt = pr->dz_stride_t;
     np.dzh = pr->dz_stride_h;
     np.H = (uint32_t)pr->H;
+    np.inv_h = pr->H == 1 ? 0xffffffffu : (uint32_t)(((uint64_t)1 << 32) / pr->H);
     np.classes = (uint32_t)gate_classes(pr);
     np.D = (int)pr->D;
     np.w_f32 = pr->w_dtype == GDN_F32;
-    np.first = pr->gate_first != 0;
-    np.center = pr->center != 0;
     np.silu = pr->act == GDN_ACT_SILU;
     np.eps = pr->eps;
     np.inv_d = 1.f / (float)pr->D;

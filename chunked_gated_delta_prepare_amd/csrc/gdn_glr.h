@@ -44,55 +44,119 @@ struct GlrParams {
 // gates
 // ---------------------------------------------------------------------------
 
-// 1 - e^z, and e^z.  |z| < 1/2: the series -z (1 + z/2 + ... + z^7/8!), whose next term is
-// below 2^-26 of it; else 1 - e^z is at least 0.39 and loses a bit.
-__device__ __forceinline__ void decay_of_log(float z, float &a, float &c) {
-    float s = fmaf(z, 1.f / 40320.f, 1.f / 5040.f);
-    s = fmaf(z, s, 1.f / 720.f);
-    s = fmaf(z, s, 1.f / 120.f);
-    s = fmaf(z, s, 1.f / 24.f);
-    s = fmaf(z, s, 1.f / 6.f);
-    s = fmaf(z, s, 0.5f);
-    s = fmaf(z, s, 1.f) * -z;
-    const float e = exact_exp(z);
-    const bool small = fabsf(z) < 0.5f;
-    c = small ? s : 1.f - e;
-    a = small ? 1.f - s : e;
+// 1 - e^-y, and e^-y.  |y| < 1/2: the series y (1 - y/2 + ... - y^7/8!), whose next term is
+// below 2^-26 of it; else 1 - e^-y is at least 0.39 and loses a bit.  NEAR: |y| < 1/8
+// is known, where five terms do (y^5/720 < 2^-24).
+template <bool NEAR>
+__device__ __forceinline__ void decay_of(float y, float &a, float &c) {
+    float s = 1.f / 120.f;
+    if constexpr (!NEAR) {
+        s = fmaf(y, -1.f / 40320.f, 1.f / 5040.f);
+        s = fmaf(y, s, -1.f / 720.f);
+        s = fmaf(y, s, 1.f / 120.f);
+    }
+    s = fmaf(y, s, -1.f / 24.f);
+    s = fmaf(y, s, 1.f / 6.f);
+    s = fmaf(y, s, -0.5f);
+    s = fmaf(y, s, 1.f) * y;
+    if constexpr (NEAR) {
+        c = s;
+        a = 1.f - s;
+    } else {
+        const float e = fast_exp2(y * -kLog2e);
+        const bool small = fabsf(y) < 0.5f;
+        c = small ? s : 1.f - e;
+        a = small ? 1.f - s : e;
+    }
+}
+
+// How a gate becomes a decay: its form, and whether |log a| < 1/8 is known (a rate
+// below 1/8 in all channels of a wave, as gates of long memories have it).
+enum { kLog = GDN_GLR_LOG, kSigmoid = GDN_GLR_SIGMOID, kRate = GDN_GLR_RATE };
+
+// The bias as gate_of takes it: for a sigmoid's exponent.
+template <int FORM, int VEC>
+__device__ __forceinline__ void scale_bias(float (&bias)[VEC]) {
+    if constexpr (FORM != kLog) {
+#pragma unroll
+        for (int e = 0; e < VEC; ++e) bias[e] *= -kLog2e;
+    }
 }
 
 // A token's decay a, c = 1 - a, and for the gradients d(log a)/d(gate) (slope) and the
-// gate's sigmoid (GDN_GLR_RATE).
-template <int FORM>
-__device__ __forceinline__ void gate_of(float v, float rate, float &a, float &c, float &slope, float &sig) {
-    if constexpr (FORM == GDN_GLR_LOG) {
-        decay_of_log(v, a, c);
+// gate's sigmoid (kRate).  The sigmoid s = 1 / (1 + e^-v) is good to its own last digits and |v| / 2
+// units more, o = 1 - s too: e^-v s where e^-v is below 1.
+template <int FORM, bool NEAR = false>
+__device__ __forceinline__ void gate_of(float g, float bias, float rate, float &a, float &c, float &slope, float &sig) {
+    if constexpr (FORM == kLog) {
+        decay_of<false>(-(g + bias), a, c);
         slope = 1.f;
         sig = 0.f;
     } else {
-        const Sigmoid g(v);
-        if constexpr (FORM == GDN_GLR_SIGMOID) {
-            a = g.s;
-            c = g.o;
-            slope = g.o;
+        const float e = fast_exp2(fmaf(g, -kLog2e, bias)), s = __builtin_amdgcn_rcpf(1.f + e), o = e < 1.f ? e * s : 1.f - s;
+        if constexpr (FORM == kSigmoid) {
+            a = s;
+            c = o;
+            slope = o;
             sig = 0.f;
         } else {
-            const float la = -rate * g.s;
-            decay_of_log(la, a, c);
-            slope = la * g.o;
-            sig = g.s;
+            const float y = rate * s;
+            decay_of<NEAR>(y, a, c);
+            slope = -y * o;
+            sig = s;
         }
     }
 }
 
-// The input's factor.
-__device__ __forceinline__ float input_scale(int scale, float a, float c) {
-    return scale == GDN_GLR_PLAIN ? 1.f : scale == GDN_GLR_COMPLEMENT ? c : __builtin_amdgcn_sqrtf(c * (1.f + a));
+// Whether a wave's rates are all below 1/8.
+template <int FORM, int VEC>
+__device__ __forceinline__ bool near_rates(const float (&rate)[VEC]) {
+    if constexpr (FORM != kRate) return false;
+    bool far = false;
+#pragma unroll
+    for (int e = 0; e < VEC; ++e) far |= !(fabsf(rate[e]) < 0.125f);
+    return __ballot(far) == 0;
 }
-// Its derivative by log a, for the factor k.
-__device__ __forceinline__ float input_slope(int scale, float a, float k) {
-    if (scale == GDN_GLR_PLAIN) return 0.f;
-    if (scale == GDN_GLR_COMPLEMENT) return -a;
-    return k > 0.f ? -a * a * __builtin_amdgcn_rcpf(k) : k == 0.f ? 0.f : k;      // (a NaN stays one)
+
+// The input's factor.
+template <int SCALE>
+__device__ __forceinline__ float input_scale(float a, float c) {
+    return SCALE == GDN_GLR_PLAIN ? 1.f : SCALE == GDN_GLR_COMPLEMENT ? c : __builtin_amdgcn_sqrtf(fmaf(c, a, c));
+}
+// The factor k and its derivative by log a, which is taken as 0 where a is 1.
+template <int SCALE>
+__device__ __forceinline__ void input_slope(float a, float c, float &k, float &dk) {
+    k = 1.f;
+    dk = 0.f;
+    if constexpr (SCALE == GDN_GLR_COMPLEMENT) {
+        k = c;
+        dk = -a;
+    }
+    if constexpr (SCALE == GDN_GLR_NORM) {
+        const float q = fmaf(c, a, c), r = q == 0.f ? 0.f : __builtin_amdgcn_rsqf(q);
+        k = q * r;
+        dk = -a * a * r;
+    }
+}
+
+// f(scale, near) with both as constants.
+template <int FORM, typename F>
+__device__ __forceinline__ void with_scale(int scale, bool near, F f) {
+    auto by_scale = [&](auto n) {
+        if (scale == GDN_GLR_PLAIN)
+            f(std::integral_constant<int, GDN_GLR_PLAIN>(), n);
+        else if (scale == GDN_GLR_COMPLEMENT)
+            f(std::integral_constant<int, GDN_GLR_COMPLEMENT>(), n);
+        else
+            f(std::integral_constant<int, GDN_GLR_NORM>(), n);
+    };
+    if constexpr (FORM == kRate) {
+        if (near) {
+            by_scale(std::true_type());
+            return;
+        }
+    }
+    by_scale(std::false_type());
 }
 
 // ---------------------------------------------------------------------------
@@ -177,15 +241,30 @@ struct Marks {
 // A packed sequence's rows, kept from run to run.
 struct Span {
     int n = 0, begin = 0, end = 0;
-    __device__ __forceinline__ void at(const GlrParams &p, int t) {
-        if (t >= begin && t < end) return;
-        n = seq_of(p, t);
+    __device__ __forceinline__ void set(const GlrParams &p, int seq) {
+        n = seq;
         begin = cu_at(p, n);
         end = cu_at(p, n + 1);
     }
+    __device__ __forceinline__ void at(const GlrParams &p, int t) {
+        if (t < begin || t >= end) set(p, seq_of(p, t));
+    }
+    // The same for a token that the wave has in common: 64 offsets at a time.
+    __device__ __forceinline__ void at_wave(const GlrParams &p, int t) {
+        if (t >= begin && t < end) return;
+        int lo = 0, hi = p.n_seqs;
+        while (hi - lo > 1) {
+            const int step = (hi - lo + 63) / 64, i = lo + lane_id() * step;
+            const int k = __popcll(__ballot(i < hi && cu_at(p, i < hi ? i : lo) <= t));
+            lo += (k ? k - 1 : 0) * step;
+            hi = hi < lo + step ? hi : lo + step;
+        }
+        set(p, lo);
+    }
 };
+// t_wave: the first token of the wave's runs, `tokens` in all; s: the wave's.
 template <bool PK, int L>
-__device__ __forceinline__ Marks marks_of(const GlrParams &p, int t0, Span &s) {
+__device__ __forceinline__ Marks marks_of(const GlrParams &p, int t_wave, int tokens, int t0, Span &s) {
     constexpr uint32_t kAll = (1u << L) - 1;
     const int n = p.T - t0;
     const uint32_t exist = n >= L ? kAll : n <= 0 ? 0 : (1u << n) - 1;
@@ -193,19 +272,20 @@ __device__ __forceinline__ Marks marks_of(const GlrParams &p, int t0, Span &s) {
     if constexpr (!PK) {
         m.first = t0 == 0 ? 1 & exist : 0;
         m.last = n >= 1 && n <= L ? 1u << (n - 1) : 0;
-    } else if (exist) {
-        s.at(p, t0);
-        if (!(s.begin < t0 && t0 + L < s.end)) {
-            m.valid = 0;
+    } else if (t_wave < p.T) {
+        s.at_wave(p, t_wave);
+        if (s.begin < t_wave && t_wave + tokens < s.end) return m;
+        // a sequence begins or ends here, or there is none
+        Span own = s;
+        m.valid = 0;
 #pragma unroll 1
-            for (int i = 0; i < L && t0 + i < p.T; ++i) {
-                const int t = t0 + i;
-                s.at(p, t);
-                const uint32_t in = t >= s.begin && t < s.end ? 1u << i : 0;
-                m.valid |= in;
-                if (t == s.begin) m.first |= in;
-                if (t == s.end - 1) m.last |= in;
-            }
+        for (int i = 0; i < L && t0 + i < p.T; ++i) {
+            const int t = t0 + i;
+            own.at(p, t);
+            const uint32_t in = t >= own.begin && t < own.end ? 1u << i : 0;
+            m.valid |= in;
+            if (t == own.begin) m.first |= in;
+            if (t == own.end - 1) m.last |= in;
         }
     }
     return m;
@@ -286,18 +366,23 @@ __device__ __forceinline__ void channel_load(const float *w, int c, int D, float
     row_load<float, VEC>(make_rsrc(w, w ? (uint32_t)D * 4 : 0), c, x);
 }
 
-// A thread's run: a and u = c x of its L tokens, and where they move a state.
-template <typename IO, typename GT, int VEC, int FORM, int L>
-struct Run {
+// A thread's rows of L tokens.
+template <typename IO, typename GT, int VEC, int L>
+struct RunRows {
     RawRow<IO, VEC> x[L];
     RawRow<GT, VEC> g[L];
-    float a[L][VEC], u[L][VEC], H[VEC];
-    Moves<VEC> m;
-
-    // rows of the run's first token on; `exist` of them do
-    __device__ __forceinline__ void fetch(const GlrParams &p, int b, int t_base, int row, int c) {
+    // full: all rows of the workgroup exist
+    __device__ __forceinline__ void fetch(const GlrParams &p, int b, int t_base, int row, int c, bool full) {
         const TileRows<IO, VEC> rx(p.x, b * p.xb + (int64_t)t_base * p.xt, p.xt, row, c, p.D);
         const TileRows<GT, VEC> rg(p.g, b * p.gb + (int64_t)t_base * p.gt, p.gt, row, c, p.D);
+        if (full) {
+#pragma unroll
+            for (int i = 0; i < L; ++i) {
+                rx.load(x[i], i, true);
+                rg.load(g[i], i, true);
+            }
+            return;
+        }
         const int n = p.T - t_base - row;
 #pragma unroll
         for (int i = 0; i < L; ++i) {
@@ -305,64 +390,29 @@ struct Run {
             rg.load(g[i], i, i < n);
         }
     }
-    template <int SCALE>
-    __device__ __forceinline__ void form_as(const float (&bias)[VEC], const float (&rate)[VEC]) {
-        m.none();
-#pragma unroll
-        for (int e = 0; e < VEC; ++e) H[e] = 0.f;
-#pragma unroll
-        for (int i = 0; i < L; ++i) {
-            float xv[VEC], gv[VEC];
-            x[i].get(xv);
-            g[i].get(gv);
-#pragma unroll
-            for (int e = 0; e < VEC; ++e) {
-                float c, slope, sig;
-                gate_of<FORM>(gv[e] + bias[e], rate[e], a[i][e], c, slope, sig);
-                u[i][e] = xv[e] * input_scale(SCALE, a[i][e], c);
-                H[e] = fmaf(a[i][e], H[e], u[i][e]);
-                m.P[e] *= a[i][e];
-                m.C[e] = fmaf(c, 1.f - m.C[e], m.C[e]);
-            }
-        }
-    }
-    __device__ __forceinline__ void form(int scale, const float (&bias)[VEC], const float (&rate)[VEC]) {
-        if (scale == GDN_GLR_PLAIN)
-            form_as<GDN_GLR_PLAIN>(bias, rate);
-        else if (scale == GDN_GLR_COMPLEMENT)
-            form_as<GDN_GLR_COMPLEMENT>(bias, rate);
-        else
-            form_as<GDN_GLR_NORM>(bias, rate);
-    }
-    // The first tokens of sequences take their initial state; in packed rows
-    // nothing passes them.
-    template <bool PK>
-    __device__ __forceinline__ void begin(const GlrParams &p, int b, int t0, int c, uint32_t first) {
-        if (__ballot(first != 0) == 0) return;
-        float h[VEC];
-#pragma unroll
-        for (int e = 0; e < VEC; ++e) h[e] = 0.f;
-#pragma unroll
-        for (int i = 0; i < L; ++i) {
-            const bool f = first >> i & 1;
-            if (f && p.h0) {
-                float h0[VEC];
-                state_load<VEC>(p, p.h0, state_of<PK>(p, b, t0 + i), c, h0);
-#pragma unroll
-                for (int e = 0; e < VEC; ++e) u[i][e] = fmaf(a[i][e], h0[e], u[i][e]);
-            }
-#pragma unroll
-            for (int e = 0; e < VEC; ++e) h[e] = f ? u[i][e] : fmaf(a[i][e], h[e], u[i][e]);
-        }
-        if (first) {
-#pragma unroll
-            for (int e = 0; e < VEC; ++e) {
-                H[e] = h[e];
-                if (PK) m.P[e] = -1.f;
-            }
-        }
-    }
 };
+
+// One channel of a state, by lane.
+__device__ __forceinline__ float state_at(const GlrParams &p, const float *s, int n, int c) {
+    float x[1];
+    state_load<1>(p, s, n, c, x);
+    return x[0];
+}
+
+// Where a run moves a state: H from zero, and its P and C, a token at a time.  In packed
+// rows (ODD: some lane's run has one) a first token takes its sequence's initial
+// state, and nothing passes it.
+template <bool ODD>
+__device__ __forceinline__ void move_on(bool first, float h0, float a, float c, float u, float &H, float &P, float &C) {
+    if constexpr (ODD) {
+        H = first ? fmaf(a, h0, u) : fmaf(a, H, u);
+        P = first || P < 0.f ? -1.f : P * a;
+    } else {
+        H = fmaf(a, H, u);
+        P *= a;
+    }
+    C = fmaf(c, 1.f - C, C);
+}
 
 // The move of a wave's whole run into (P, C, H), of what lies in it before this lane's
 // into `before` and E.

@@ -14,20 +14,22 @@ constexpr int kGlrTile = kGlrWaves * GlrLane<VEC>::kTG * kGlrRun;      // tokens
 // workspace.  One read of x and the gate and one write of y; the next tile's
 // rows are in flight while one is worked on.
 template <typename IO, typename GT, int VEC, bool PK, int FORM>
-__global__ void __launch_bounds__(64 * kGlrWaves) glr_forward_kernel(GlrParams p) {
+__global__ void __launch_bounds__(64 * kGlrWaves, 2) glr_forward_kernel(GlrParams p) {
     constexpr int L = kGlrRun, NW = kGlrWaves;
     __shared__ float lds_q[2][NW][kGlrCols], lds_h[2][NW][kGlrCols];
     const int group = blockIdx.x % p.groups, rest = blockIdx.x / p.groups, seg = rest % p.segs, b = rest / p.segs;
     const GlrLane<VEC> ln(group);
     const int w = wave_id(), row = (w * ln.kTG + ln.tg) * L;
     const int t_begin = seg * p.seg_len, t_end = t_begin + p.seg_len < p.T ? t_begin + p.seg_len : p.T;
-    Run<IO, GT, VEC, FORM, L> run;
-    if (t_begin < t_end) run.fetch(p, b, t_begin, row, ln.c);
+    RunRows<IO, GT, VEC, L> rows;
+    if (t_begin < t_end) rows.fetch(p, b, t_begin, row, ln.c, t_begin + kGlrTile<VEC> <= p.T);
     float bias[VEC], rate[VEC], h[VEC];
     channel_load<VEC>(p.bias, ln.c, p.D, bias);
     channel_load<VEC>(p.rate, ln.c, p.D, rate);
-#pragma unroll
-    for (int e = 0; e < VEC; ++e) h[e] = 0.f;
+    scale_bias<FORM, VEC>(bias);
+    const bool near = near_rates<FORM, VEC>(rate);
+    // (packed rows take initial states at their sequences' first tokens)
+    state_load<VEC>(p, PK ? nullptr : p.h0, b, ln.c, h);
     for (int j = 0; j < seg; ++j) {
         const float *s = p.ws + ((int64_t)b * (p.segs - 1) + j) * 2 * p.D;
         float q[VEC], H[VEC];
@@ -40,18 +42,63 @@ __global__ void __launch_bounds__(64 * kGlrWaves) glr_forward_kernel(GlrParams p
     Span span;
     int turn = 0;
     for (int t = t_begin; t < t_end; t += kGlrTile<VEC>, turn ^= 1) {
-        run.form(p.scale, bias, rate);
-        if (t + kGlrTile<VEC> < t_end) run.fetch(p, b, t + kGlrTile<VEC>, row, ln.c);
-        const Marks marks = marks_of<PK, L>(p, t + row, span);
-        run.template begin<PK>(p, b, t + row, ln.c, marks.first);
+        const int t0 = t + row;
+        const Marks marks = marks_of<PK, L>(p, t + w * ln.kTG * L, ln.kTG * L, t0, span);
+        const bool odd = PK && __ballot(marks.first != 0) != 0;
+        float a[L][VEC], u[L][VEC], H[VEC];
+        Moves<VEC> m;
+        m.none();
+#pragma unroll
+        for (int e = 0; e < VEC; ++e) H[e] = 0.f;
+        with_scale<FORM>(p.scale, near, [&](auto sc, auto nr) {
+#pragma unroll
+            for (int i = 0; i < L; ++i) {
+                float xv[VEC], gv[VEC];
+                rows.x[i].get(xv);
+                rows.g[i].get(gv);
+#pragma unroll
+                for (int e = 0; e < VEC; ++e) {
+                    float c, slope, sig;
+                    gate_of<FORM, nr.value>(gv[e], bias[e], rate[e], a[i][e], c, slope, sig);
+                    u[i][e] = xv[e] * input_scale<sc.value>(a[i][e], c);
+                    move_on<false>(false, 0.f, a[i][e], c, u[i][e], H[e], m.P[e], m.C[e]);
+                }
+            }
+        });
+        if (t + kGlrTile<VEC> < t_end) rows.fetch(p, b, t + kGlrTile<VEC>, row, ln.c, t + 2 * kGlrTile<VEC> <= p.T);
+        if (odd) {
+            // u of a first token holds its sequence's initial state
+            float n[VEC];
+#pragma unroll
+            for (int e = 0; e < VEC; ++e) n[e] = 0.f;
+#pragma unroll
+            for (int i = 0; i < L; ++i) {
+                const bool f = marks.first >> i & 1;
+                if (f) {
+                    float h0[VEC];
+                    state_load<VEC>(p, p.h0, seq_of(p, t0 + i), ln.c, h0);
+#pragma unroll
+                    for (int e = 0; e < VEC; ++e) u[i][e] = fmaf(a[i][e], h0[e], u[i][e]);
+                }
+#pragma unroll
+                for (int e = 0; e < VEC; ++e) n[e] = f ? u[i][e] : fmaf(a[i][e], n[e], u[i][e]);
+            }
+            if (marks.first) {
+#pragma unroll
+                for (int e = 0; e < VEC; ++e) {
+                    H[e] = n[e];
+                    m.P[e] = -1.f;
+                }
+            }
+        }
         Moves<VEC> before;
         float E[VEC];
-        join_wave<PK, VEC>(run.m, run.H, before, E);
+        join_wave<PK, VEC>(m, H, before, E);
         if (ln.tg == 0) {
 #pragma unroll
             for (int e = 0; e < VEC; ++e) {
-                lds_q[turn][w][ln.local() + e] = pack_move<PK>(run.m.P[e], run.m.C[e]);
-                lds_h[turn][w][ln.local() + e] = run.H[e];
+                lds_q[turn][w][ln.local() + e] = pack_move<PK>(m.P[e], m.C[e]);
+                lds_h[turn][w][ln.local() + e] = H[e];
             }
         }
         // (one barrier a tile: the other half of LDS is next, and its readers are behind the next barrier)
@@ -69,22 +116,21 @@ __global__ void __launch_bounds__(64 * kGlrWaves) glr_forward_kernel(GlrParams p
         for (int e = 0; e < VEC; ++e)
             if (ln.tg > 0) mine[e] = move<PK>(before.P[e], before.C[e], mine[e], E[e]);
         const TileRows<IO, VEC> ry(p.y, ((int64_t)b * p.T + t) * p.D, p.D, row, ln.c, p.D);
-        if (__ballot(marks.valid != (1u << L) - 1 || (marks.first | marks.last) != 0) == 0) {
+        if (!odd && __ballot(marks.valid != (1u << L) - 1 || marks.last != 0) == 0) {
 #pragma unroll
             for (int i = 0; i < L; ++i) {
 #pragma unroll
-                for (int e = 0; e < VEC; ++e) mine[e] = fmaf(run.a[i][e], mine[e], run.u[i][e]);
+                for (int e = 0; e < VEC; ++e) mine[e] = fmaf(a[i][e], mine[e], u[i][e]);
                 ry.store(mine, i, true);
             }
         } else {
 #pragma unroll
             for (int i = 0; i < L; ++i) {
-                // (u of a first token holds its sequence's initial state)
                 const bool f = PK && (marks.first >> i & 1);
 #pragma unroll
-                for (int e = 0; e < VEC; ++e) mine[e] = f ? run.u[i][e] : fmaf(run.a[i][e], mine[e], run.u[i][e]);
+                for (int e = 0; e < VEC; ++e) mine[e] = f ? u[i][e] : fmaf(a[i][e], mine[e], u[i][e]);
                 ry.store(mine, i, marks.valid >> i & 1);
-                if (p.hT && (marks.last >> i & 1)) state_store<VEC>(p, p.hT, state_of<PK>(p, b, t + row + i), ln.c, true, mine);
+                if (p.hT && (marks.last >> i & 1)) state_store<VEC>(p, p.hT, state_of<PK>(p, b, t0 + i), ln.c, true, mine);
             }
         }
     }
@@ -93,37 +139,65 @@ __global__ void __launch_bounds__(64 * kGlrWaves) glr_forward_kernel(GlrParams p
 // The moves of all segments but the last: a wave walks its share of the segment
 // backwards, so that what it reads last is what the next launch reads first.
 template <typename IO, typename GT, int VEC, bool PK, int FORM>
-__global__ void __launch_bounds__(64 * kGlrWaves) glr_moves_kernel(GlrParams p) {
+__global__ void __launch_bounds__(64 * kGlrWaves, 2) glr_moves_kernel(GlrParams p) {
     constexpr int L = kGlrRun, NW = kGlrWaves, kStep = GlrLane<VEC>::kTG * L;
     __shared__ float lds_p[NW][kGlrCols], lds_c[NW][kGlrCols], lds_h[NW][kGlrCols];
     const int segs = p.segs - 1;
     const int group = blockIdx.x % p.groups, rest = blockIdx.x / p.groups, seg = rest % segs, b = rest / segs;
     const GlrLane<VEC> ln(group);
     const int w = wave_id(), row = ln.tg * L, share = p.seg_len / NW;
-    const int t0 = seg * p.seg_len + w * share;
+    const int t_first = seg * p.seg_len + w * share;
     float bias[VEC], rate[VEC];
     channel_load<VEC>(p.bias, ln.c, p.D, bias);
     channel_load<VEC>(p.rate, ln.c, p.D, rate);
+    scale_bias<FORM, VEC>(bias);
+    const bool near = near_rates<FORM, VEC>(rate);
     Moves<VEC> all;
-    float H[VEC];
+    float S[VEC];
     all.none();
 #pragma unroll
-    for (int e = 0; e < VEC; ++e) H[e] = 0.f;
-    Run<IO, GT, VEC, FORM, L> run;
-    run.fetch(p, b, t0 + share - kStep, row, ln.c);
+    for (int e = 0; e < VEC; ++e) S[e] = 0.f;
+    RunRows<IO, GT, VEC, L> rows;
+    rows.fetch(p, b, t_first + share - kStep, row, ln.c, true);
     Span span;
-    for (int t = t0 + share - kStep; t >= t0; t -= kStep) {
-        run.form(p.scale, bias, rate);
-        if (t > t0) run.fetch(p, b, t - kStep, row, ln.c);
-        const Marks marks = marks_of<PK, L>(p, t + row, span);
-        run.template begin<PK>(p, b, t + row, ln.c, marks.first);
+    for (int t = t_first + share - kStep; t >= t_first; t -= kStep) {
+        const int t0 = t + row;
+        const Marks marks = PK ? marks_of<PK, L>(p, t, kStep, t0, span) : Marks{};
+        Moves<VEC> m;
+        float H[VEC];
+        m.none();
+#pragma unroll
+        for (int e = 0; e < VEC; ++e) H[e] = 0.f;
+        auto walk = [&](auto odd) {
+            with_scale<FORM>(p.scale, near, [&](auto sc, auto nr) {
+#pragma unroll
+                for (int i = 0; i < L; ++i) {
+                    float xv[VEC], gv[VEC];
+                    rows.x[i].get(xv);
+                    rows.g[i].get(gv);
+                    const bool f = odd.value && (marks.first >> i & 1);
+                    const int n = f ? seq_of(p, t0 + i) : 0;
+#pragma unroll
+                    for (int e = 0; e < VEC; ++e) {
+                        float a, c, slope, sig;
+                        gate_of<FORM, nr.value>(gv[e], bias[e], rate[e], a, c, slope, sig);
+                        move_on<odd.value>(f, f ? state_at(p, p.h0, n, ln.c + e) : 0.f, a, c, xv[e] * input_scale<sc.value>(a, c), H[e], m.P[e], m.C[e]);
+                    }
+                }
+            });
+        };
+        if (PK && __ballot(marks.first != 0) != 0)
+            walk(std::bool_constant<PK>());
+        else
+            walk(std::false_type());
+        if (t > t_first) rows.fetch(p, b, t - kStep, row, ln.c, true);
         Moves<VEC> before;
         float E[VEC];
-        join_wave<PK, VEC>(run.m, run.H, before, E);
+        join_wave<PK, VEC>(m, H, before, E);
 #pragma unroll
         for (int e = 0; e < VEC; ++e) {
-            H[e] = move<PK>(all.P[e], all.C[e], run.H[e], H[e]);
-            join<PK>(run.m.P[e], run.m.C[e], all.P[e], all.C[e], all.P[e], all.C[e]);
+            S[e] = move<PK>(all.P[e], all.C[e], H[e], S[e]);
+            join<PK>(m.P[e], m.C[e], all.P[e], all.C[e], all.P[e], all.C[e]);
         }
     }
     if (ln.tg == 0) {
@@ -131,21 +205,21 @@ __global__ void __launch_bounds__(64 * kGlrWaves) glr_moves_kernel(GlrParams p) 
         for (int e = 0; e < VEC; ++e) {
             lds_p[w][ln.local() + e] = all.P[e];
             lds_c[w][ln.local() + e] = all.C[e];
-            lds_h[w][ln.local() + e] = H[e];
+            lds_h[w][ln.local() + e] = S[e];
         }
     }
     __syncthreads();
     const int l = threadIdx.x, c = group * kGlrCols + l;
     if (l >= kGlrCols || c >= p.D) return;
-    float P = lds_p[0][l], C = lds_c[0][l], S = lds_h[0][l];
+    float P = lds_p[0][l], C = lds_c[0][l], H = lds_h[0][l];
 #pragma unroll
     for (int j = 1; j < NW; ++j) {
-        S = move<PK>(lds_p[j][l], lds_c[j][l], S, lds_h[j][l]);
+        H = move<PK>(lds_p[j][l], lds_c[j][l], H, lds_h[j][l]);
         join<PK>(P, C, lds_p[j][l], lds_c[j][l], P, C);
     }
     float *out = p.ws + ((int64_t)b * segs + seg) * 2 * p.D + c;
     out[0] = pack_move<PK>(P, C);
-    out[p.D] = S;
+    out[p.D] = H;
 }
 
 // One token for each of B rows, 256 channels a workgroup.
@@ -162,8 +236,10 @@ __global__ void __launch_bounds__(256) glr_step_kernel(GlrParams p) {
     float *h = p.state + s * p.D + c;
     const float x = io_traits<IO>::load((const IO *)p.x + b * p.xb + c), g = io_traits<GT>::load((const GT *)p.g + b * p.gb + c);
     float a, k, slope, sig;
-    gate_of<FORM>(g + (p.bias ? p.bias[c] : 0.f), p.rate ? p.rate[c] : 0.f, a, k, slope, sig);
-    const float v = fmaf(a, *h, x * input_scale(p.scale, a, k));
+    float bias[1] = {p.bias ? p.bias[c] : 0.f};
+    scale_bias<FORM, 1>(bias);
+    gate_of<FORM>(g, bias[0], p.rate ? p.rate[c] : 0.f, a, k, slope, sig);
+    const float v = fmaf(a, *h, x * (p.scale == GDN_GLR_PLAIN ? 1.f : p.scale == GDN_GLR_COMPLEMENT ? k : input_scale<GDN_GLR_NORM>(a, k)));
     *h = v;
     io_traits<IO>::store(y, v);
 }
@@ -224,12 +300,12 @@ struct GlrPlan {
     int64_t segs, seg_len;
 };
 
-// Segments for about 512 workgroups of 64 channels, two a CU, of four tiles at least
+// Segments for about 256 workgroups of 64 channels, one a CU, of four tiles at least
 // (a segment's rows are read once more for its move).
 GlrPlan glr_plan(const gdn_glr_problem *pr) {
     constexpr int64_t kTile = kGlrTile<2>;         // (a multiple of the tile of single channels)
     const int64_t streams = pr->B * ((pr->D + kGlrCols - 1) / kGlrCols), tiles = (pr->T + kTile - 1) / kTile;
-    int64_t segs = (512 + streams - 1) / streams;
+    int64_t segs = (256 + streams - 1) / streams;
     segs = segs < tiles / 4 ? segs : tiles / 4;
     segs = segs < 1 ? 1 : segs;
     GlrPlan s;

@@ -14,82 +14,11 @@
 
 namespace gdn {
 
-constexpr int kGbWaves = 8;
-constexpr int kGbRun = 8;              // tokens of a thread
-
+constexpr int kGbWaves = 4;
 template <int VEC>
-constexpr int kGbTile = kGbWaves * GlrLane<VEC>::kTG * kGbRun;
-
-// A thread's run with dy: the run's moves of h (m, H) and of e (m, E).
-template <typename IO, typename GT, int VEC, int FORM, int L>
-struct BackRun : Run<IO, GT, VEC, FORM, L> {
-    RawRow<IO, VEC> dyr[L];
-    float dy[L][VEC], E[VEC];
-
-    __device__ __forceinline__ void fetch_all(const GlrParams &p, int b, int t_base, int row, int c) {
-        this->fetch(p, b, t_base, row, c);
-        const TileRows<IO, VEC> rd(p.dy, b * p.yb + (int64_t)t_base * p.yt, p.yt, row, c, p.D);
-        const int n = p.T - t_base - row;
-#pragma unroll
-        for (int i = 0; i < L; ++i) rd.load(dyr[i], i, i < n);
-    }
-    // (tokens of no sequence move nothing; the last of a sequence takes dhT, and e does not
-    // pass the first)
-    template <bool PK>
-    __device__ __forceinline__ void form_all(const GlrParams &p, int b, int t0, int c, const Marks &marks, const float (&bias)[VEC],
-                                             const float (&rate)[VEC]) {
-        this->form(p.scale, bias, rate);
-#pragma unroll
-        for (int i = 0; i < L; ++i) dyr[i].get(dy[i]);
-        const bool odd = marks.valid != (1u << L) - 1 || (marks.first | marks.last) != 0;
-        if (__ballot(odd) != 0) {
-#pragma unroll
-            for (int i = 0; i < L; ++i) {
-                if (!(marks.valid >> i & 1)) {
-#pragma unroll
-                    for (int e = 0; e < VEC; ++e) {
-                        this->a[i][e] = 1.f;
-                        this->u[i][e] = dy[i][e] = 0.f;
-                    }
-                }
-                if (p.dhT && (marks.last >> i & 1)) {
-                    float d[VEC];
-                    state_load<VEC>(p, p.dhT, state_of<PK>(p, b, t0 + i), c, d);
-#pragma unroll
-                    for (int e = 0; e < VEC; ++e) dy[i][e] += d[e];
-                }
-            }
-            if (marks.valid != (1u << L) - 1) {
-                // the run's move without them (they are at its ends, or it is all of them)
-#pragma unroll
-                for (int e = 0; e < VEC; ++e) {
-                    this->H[e] = 0.f;
-                    this->m.P[e] = 1.f;
-#pragma unroll
-                    for (int i = 0; i < L; ++i) {
-                        this->H[e] = fmaf(this->a[i][e], this->H[e], this->u[i][e]);
-                        this->m.P[e] *= this->a[i][e];
-                    }
-                    this->m.C[e] = 1.f - this->m.P[e];
-                }
-            }
-        }
-        this->template begin<PK>(p, b, t0, c, marks.first);
-#pragma unroll
-        for (int e = 0; e < VEC; ++e) E[e] = 0.f;
-        if (PK && __ballot(marks.first != 0) != 0) {
-#pragma unroll
-            for (int i = L - 1; i >= 0; --i)
-#pragma unroll
-                for (int e = 0; e < VEC; ++e) E[e] = marks.first >> i & 1 ? 0.f : this->a[i][e] * (dy[i][e] + E[e]);
-        } else {
-#pragma unroll
-            for (int i = L - 1; i >= 0; --i)
-#pragma unroll
-                for (int e = 0; e < VEC; ++e) E[e] = this->a[i][e] * (dy[i][e] + E[e]);
-        }
-    }
-};
+constexpr int kGbRun = VEC == 2 ? 4 : 8;      // tokens of a thread
+template <int VEC>
+constexpr int kGbTile = kGbWaves * GlrLane<VEC>::kTG * kGbRun<VEC>;      // 32 either way
 
 // As join_wave, with e: what lies behind this lane's run into `after` and A.
 template <bool PK, int VEC>
@@ -115,52 +44,105 @@ __device__ __forceinline__ void join_wave_both(Moves<VEC> &m, float (&H)[VEC], f
     }
 }
 
+template <typename IO, int VEC, int L>
+__device__ __forceinline__ void fetch_dy(const GlrParams &p, RawRow<IO, VEC> (&dy)[L], int b, int t_base, int row, int c, bool full) {
+    const TileRows<IO, VEC> rd(p.dy, b * p.yb + (int64_t)t_base * p.yt, p.yt, row, c, p.D);
+    const int n = p.T - t_base - row;
+#pragma unroll
+    for (int i = 0; i < L; ++i) rd.load(dy[i], i, full || i < n);
+}
+
 // A tile's place in the workspace: [3][D], its packed move, then H and E, which the
 // second launch replaces by the states at its borders.
 __device__ __forceinline__ float *tile_at(const GlrParams &p, int b, int tile) { return p.ws + ((int64_t)b * p.segs + tile) * 3 * p.D; }
 
+// dhT of the sequence that ends with token t, one channel.
+__device__ __forceinline__ float last_gradient(const GlrParams &p, int t, int c) { return state_at(p, p.dhT, seq_of(p, t), c); }
+
 template <typename IO, typename GT, int VEC, bool PK, int FORM>
 __global__ void __launch_bounds__(64 * kGbWaves) glr_tiles_kernel(GlrParams p) {
-    constexpr int L = kGbRun, NW = kGbWaves;
+    constexpr int L = kGbRun<VEC>, NW = kGbWaves;
     __shared__ float lds[4][NW][kGlrCols];
     const int group = blockIdx.x % p.groups, rest = blockIdx.x / p.groups, tile = rest % p.segs, b = rest / p.segs;
     const GlrLane<VEC> ln(group);
-    const int w = wave_id(), row = (w * ln.kTG + ln.tg) * L, t = tile * kGbTile<VEC>;
-    BackRun<IO, GT, VEC, FORM, L> run;
-    run.fetch_all(p, b, t, row, ln.c);
+    const int w = wave_id(), row = (w * ln.kTG + ln.tg) * L, t = tile * kGbTile<VEC>, t0 = t + row;
+    RunRows<IO, GT, VEC, L> rows;
+    RawRow<IO, VEC> dyr[L];
+    const bool full = t + kGbTile<VEC> <= p.T;
+    rows.fetch(p, b, t, row, ln.c, full);
+    fetch_dy<IO, VEC, L>(p, dyr, b, t, row, ln.c, full);
     float bias[VEC], rate[VEC];
     channel_load<VEC>(p.bias, ln.c, p.D, bias);
     channel_load<VEC>(p.rate, ln.c, p.D, rate);
+    scale_bias<FORM, VEC>(bias);
+    const bool near = near_rates<FORM, VEC>(rate);
     Span span;
-    const Marks marks = marks_of<PK, L>(p, t + row, span);
-    run.template form_all<PK>(p, b, t + row, ln.c, marks, bias, rate);
+    const Marks marks = marks_of<PK, L>(p, t + w * ln.kTG * L, ln.kTG * L, t0, span);
+    Moves<VEC> m;
+    float H[VEC], E[VEC];
+    m.none();
+#pragma unroll
+    for (int e = 0; e < VEC; ++e) H[e] = E[e] = 0.f;
+    // E as a sum over the run: what its tokens' dy leave behind the run's front
+    auto walk = [&](auto odd) {
+        with_scale<FORM>(p.scale, near, [&](auto sc, auto nr) {
+#pragma unroll
+            for (int i = 0; i < L; ++i) {
+                float xv[VEC], gv[VEC], dv[VEC];
+                rows.x[i].get(xv);
+                rows.g[i].get(gv);
+                dyr[i].get(dv);
+                const bool ok = !odd.value || (marks.valid >> i & 1), f = PK && odd.value && (marks.first >> i & 1);
+                const bool end = PK && odd.value && (marks.last >> i & 1);
+#pragma unroll
+                for (int e = 0; e < VEC; ++e) {
+                    float a, c, slope, sig;
+                    gate_of<FORM, nr.value>(gv[e], bias[e], rate[e], a, c, slope, sig);
+                    float u = xv[e] * input_scale<sc.value>(a, c);
+                    if (odd.value && !ok) {
+                        // a token of no sequence moves nothing
+                        a = 1.f;
+                        c = u = dv[e] = 0.f;
+                    }
+                    if (end) dv[e] += last_gradient(p, t0 + i, ln.c + e);
+                    move_on<PK && odd.value>(f, f ? state_at(p, p.h0, seq_of(p, t0 + i), ln.c + e) : 0.f, a, c, u, H[e], m.P[e], m.C[e]);
+                    // (behind a first token P is marked, and e does not pass it)
+                    E[e] = PK && m.P[e] < 0.f ? E[e] : fmaf(m.P[e], dv[e], E[e]);
+                }
+            }
+        });
+    };
+    if (__ballot(marks.valid != (1u << L) - 1 || (PK && (marks.first | marks.last) != 0)) != 0)
+        walk(std::true_type());
+    else
+        walk(std::false_type());
     Moves<VEC> beside;
     float before[VEC], after[VEC];
-    join_wave_both<PK, VEC>(run.m, run.H, run.E, beside, before, after);
+    join_wave_both<PK, VEC>(m, H, E, beside, before, after);
     if (ln.tg == 0) {
 #pragma unroll
         for (int e = 0; e < VEC; ++e) {
-            lds[0][w][ln.local() + e] = run.m.P[e];
-            lds[1][w][ln.local() + e] = run.m.C[e];
-            lds[2][w][ln.local() + e] = run.H[e];
-            lds[3][w][ln.local() + e] = run.E[e];
+            lds[0][w][ln.local() + e] = m.P[e];
+            lds[1][w][ln.local() + e] = m.C[e];
+            lds[2][w][ln.local() + e] = H[e];
+            lds[3][w][ln.local() + e] = E[e];
         }
     }
     __syncthreads();
     const int l = threadIdx.x, c = group * kGlrCols + l;
     if (l >= kGlrCols || c >= p.D) return;
-    float P = lds[0][0][l], C = lds[1][0][l], H = lds[2][0][l], E = lds[3][0][l];
+    float P = lds[0][0][l], C = lds[1][0][l], hh = lds[2][0][l], ee = lds[3][0][l];
 #pragma unroll
     for (int j = 1; j < NW; ++j) {
         const float P2 = lds[0][j][l], C2 = lds[1][j][l];
-        H = move<PK>(P2, C2, H, lds[2][j][l]);
-        E = move<PK>(P, C, lds[3][j][l], E);
+        hh = move<PK>(P2, C2, hh, lds[2][j][l]);
+        ee = move<PK>(P, C, lds[3][j][l], ee);
         join<PK>(P, C, P2, C2, P, C);
     }
     float *out = tile_at(p, b, tile) + c;
     out[0] = pack_move<PK>(P, C);
-    out[p.D] = H;
-    out[2 * (int64_t)p.D] = E;
+    out[p.D] = hh;
+    out[2 * (int64_t)p.D] = ee;
 }
 
 // H -> the h in front of a tile, E -> the e behind it: 64 channels and one
@@ -190,7 +172,9 @@ __global__ void __launch_bounds__(1024) glr_states_kernel(GlrParams p) {
     lds_h[w][l] = S;
     __syncthreads();
     if (!live) return;
-    S = 0.f;
+    // (packed rows take them at their sequences' first and last tokens)
+    const float *s0 = PK ? nullptr : back ? p.dhT : p.h0;
+    S = s0 ? s0[(int64_t)b * p.D + c] : 0.f;
     for (int j = 0; j < w; ++j) S = move<PK>(lds_p[j][l], lds_c[j][l], S, lds_h[j][l]);
 #pragma unroll 4
     for (int i = n0; i < n1; ++i) {
@@ -202,43 +186,107 @@ __global__ void __launch_bounds__(1024) glr_states_kernel(GlrParams p) {
 }
 
 template <typename IO, typename GT, int VEC, bool PK, int FORM>
-__global__ void __launch_bounds__(64 * kGbWaves) glr_backward_kernel(GlrParams p) {
-    constexpr int L = kGbRun, NW = kGbWaves;
+__global__ void __launch_bounds__(64 * kGbWaves, 4) glr_backward_kernel(GlrParams p) {
+    constexpr int L = kGbRun<VEC>, NW = kGbWaves;
     __shared__ float lds[3][NW][kGlrCols];
     const int group = blockIdx.x % p.groups, rest = blockIdx.x / p.groups, tile = p.segs - 1 - rest % p.segs, b = rest / p.segs;
     const GlrLane<VEC> ln(group);
     const int w = wave_id(), row = (w * ln.kTG + ln.tg) * L, t = tile * kGbTile<VEC>, t0 = t + row;
-    BackRun<IO, GT, VEC, FORM, L> run;
-    run.fetch_all(p, b, t, row, ln.c);
+    RunRows<IO, GT, VEC, L> rows;
+    RawRow<IO, VEC> dyr[L];
+    const bool full = t + kGbTile<VEC> <= p.T;
+    rows.fetch(p, b, t, row, ln.c, full);
+    fetch_dy<IO, VEC, L>(p, dyr, b, t, row, ln.c, full);
     float bias[VEC], rate[VEC], h[VEC], d[VEC];
     channel_load<VEC>(p.bias, ln.c, p.D, bias);
     channel_load<VEC>(p.rate, ln.c, p.D, rate);
-    const float *states = p.segs > 1 ? tile_at(p, b, tile) : nullptr;
-    channel_load<VEC>(states ? states + p.D : nullptr, ln.c, p.D, h);
-    channel_load<VEC>(states ? states + 2 * (int64_t)p.D : nullptr, ln.c, p.D, d);
+    scale_bias<FORM, VEC>(bias);
+    const bool near = near_rates<FORM, VEC>(rate);
+    if (p.segs > 1) {
+        channel_load<VEC>(tile_at(p, b, tile) + p.D, ln.c, p.D, h);
+        channel_load<VEC>(tile_at(p, b, tile) + 2 * (int64_t)p.D, ln.c, p.D, d);
+    } else {
+        state_load<VEC>(p, PK ? nullptr : p.h0, b, ln.c, h);
+        state_load<VEC>(p, PK ? nullptr : p.dhT, b, ln.c, d);
+    }
     if (tile == 0) pass_empty(p, PK, b, group * kGlrCols, p.dhT, p.dh0);
     Span span;
-    const Marks marks = marks_of<PK, L>(p, t0, span);
-    run.template form_all<PK>(p, b, t0, ln.c, marks, bias, rate);
+    const Marks marks = marks_of<PK, L>(p, t + w * ln.kTG * L, ln.kTG * L, t0, span);
+    const bool odd = __ballot(marks.valid != (1u << L) - 1 || marks.first != 0 || (PK && marks.last != 0)) != 0;
+    // what the walk back needs of a token: a, the input's factor k and its slope, the gate's slope and sigmoid
+    float a[L][VEC], k[L][VEC], dk[L][VEC], slope[L][VEC], sig[L][VEC], x[L][VEC], dy[L][VEC], H[VEC], E[VEC];
+    Moves<VEC> m;
+    m.none();
+#pragma unroll
+    for (int e = 0; e < VEC; ++e) H[e] = E[e] = 0.f;
+    with_scale<FORM>(p.scale, near, [&](auto sc, auto nr) {
+#pragma unroll
+        for (int i = 0; i < L; ++i) {
+            float gv[VEC];
+            rows.x[i].get(x[i]);
+            rows.g[i].get(gv);
+            dyr[i].get(dy[i]);
+#pragma unroll
+            for (int e = 0; e < VEC; ++e) {
+                float c;
+                gate_of<FORM, nr.value>(gv[e], bias[e], rate[e], a[i][e], c, slope[i][e], sig[i][e]);
+                input_slope<sc.value>(a[i][e], c, k[i][e], dk[i][e]);
+                move_on<false>(false, 0.f, a[i][e], c, k[i][e] * x[i][e], H[e], m.P[e], m.C[e]);
+                E[e] = fmaf(m.P[e], dy[i][e], E[e]);
+            }
+        }
+    });
+    if (odd) {
+        // the run again, token by token
+        float n[VEC];
+#pragma unroll
+        for (int e = 0; e < VEC; ++e) {
+            n[e] = E[e] = 0.f;
+            m.P[e] = 1.f;
+        }
+#pragma unroll
+        for (int i = 0; i < L; ++i) {
+            const bool ok = marks.valid >> i & 1, f = PK && (marks.first >> i & 1), end = PK && (marks.last >> i & 1);
+#pragma unroll
+            for (int e = 0; e < VEC; ++e) {
+                if (!ok) {
+                    // a token of no sequence moves nothing, and may hold anything
+                    a[i][e] = 1.f;
+                    k[i][e] = dk[i][e] = slope[i][e] = sig[i][e] = x[i][e] = dy[i][e] = 0.f;
+                }
+                if (end) dy[i][e] += last_gradient(p, t0 + i, ln.c + e);
+                const float h0 = f ? state_at(p, p.h0, seq_of(p, t0 + i), ln.c + e) : n[e];
+                n[e] = fmaf(a[i][e], h0, k[i][e] * x[i][e]);
+                m.P[e] = f || m.P[e] < 0.f ? -1.f : m.P[e] * a[i][e];
+                E[e] = m.P[e] < 0.f ? E[e] : fmaf(m.P[e], dy[i][e], E[e]);
+            }
+        }
+        if (marks.valid != (1u << L) - 1) {
+#pragma unroll
+            for (int e = 0; e < VEC; ++e) m.C[e] = 1.f - m.P[e];
+        }
+#pragma unroll
+        for (int e = 0; e < VEC; ++e) H[e] = n[e];
+    }
     Moves<VEC> beside;
     float before[VEC], after[VEC];
-    join_wave_both<PK, VEC>(run.m, run.H, run.E, beside, before, after);
+    join_wave_both<PK, VEC>(m, H, E, beside, before, after);
     if (ln.tg == 0) {
 #pragma unroll
         for (int e = 0; e < VEC; ++e) {
-            lds[0][w][ln.local() + e] = pack_move<PK>(run.m.P[e], run.m.C[e]);
-            lds[1][w][ln.local() + e] = run.H[e];
-            lds[2][w][ln.local() + e] = run.E[e];
+            lds[0][w][ln.local() + e] = pack_move<PK>(m.P[e], m.C[e]);
+            lds[1][w][ln.local() + e] = H[e];
+            lds[2][w][ln.local() + e] = E[e];
         }
     }
     lds_barrier();
 #pragma unroll
     for (int j = 0; j < NW - 1; ++j) {
-        const int k = NW - 1 - j;
+        const int q = NW - 1 - j;
 #pragma unroll
         for (int e = 0; e < VEC; ++e) {
             if (j < w) h[e] = packed_move<PK>(lds[0][j][ln.local() + e], h[e], lds[1][j][ln.local() + e]);
-            if (k > w) d[e] = packed_move<PK>(lds[0][k][ln.local() + e], d[e], lds[2][k][ln.local() + e]);
+            if (q > w) d[e] = packed_move<PK>(lds[0][q][ln.local() + e], d[e], lds[2][q][ln.local() + e]);
         }
     }
     if constexpr (ln.kTG == 2) {
@@ -252,17 +300,13 @@ __global__ void __launch_bounds__(64 * kGbWaves) glr_backward_kernel(GlrParams p
     // the state in front of every token
     float prev[L][VEC];
 #pragma unroll
-    for (int i = 0; i < L; ++i)
+    for (int i = 0; i < L; ++i) {
+        if (PK && odd && (marks.first >> i & 1)) state_load<VEC>(p, p.h0, seq_of(p, t0 + i), ln.c, h);
 #pragma unroll
         for (int e = 0; e < VEC; ++e) {
             prev[i][e] = h[e];
-            h[e] = PK && (marks.first >> i & 1) ? run.u[i][e] : fmaf(run.a[i][e], h[e], run.u[i][e]);
+            h[e] = fmaf(a[i][e], h[e], k[i][e] * x[i][e]);
         }
-    const bool odd = __ballot(marks.valid != (1u << L) - 1 || marks.first != 0) != 0;
-    if (odd) {
-#pragma unroll
-        for (int i = 0; i < L; ++i)
-            if (marks.first >> i & 1) state_load<VEC>(p, p.h0, state_of<PK>(p, b, t0 + i), ln.c, prev[i]);
     }
     const TileRows<IO, VEC> rx(p.dx, b * p.dxb + (int64_t)t * p.dxt, p.dxt, row, ln.c, p.D);
     const TileRows<GT, VEC> rg(p.dg, b * p.dgb + (int64_t)t * p.dgt, p.dgt, row, ln.c, p.D);
@@ -271,21 +315,17 @@ __global__ void __launch_bounds__(64 * kGbWaves) glr_backward_kernel(GlrParams p
     for (int e = 0; e < VEC; ++e) sb[e] = sr[e] = 0.f;
 #pragma unroll
     for (int i = L - 1; i >= 0; --i) {
-        float x[VEC], g[VEC], dx[VEC], dg[VEC];
-        run.x[i].get(x);
-        run.g[i].get(g);
-        const bool ok = marks.valid >> i & 1;
+        float dx[VEC], dg[VEC];
+        const bool ok = !odd || (marks.valid >> i & 1);       // (uniformly true in most tiles)
 #pragma unroll
         for (int e = 0; e < VEC; ++e) {
-            float a, c, slope, sig;
-            gate_of<FORM>(g[e] + bias[e], rate[e], a, c, slope, sig);
-            const float k = input_scale(p.scale, a, c), dh = run.dy[i][e] + d[e], out = run.a[i][e] * dh;
-            const float da = fmaf(out, prev[i][e], dh * x[e] * input_slope(p.scale, a, k));
-            dx[e] = dh * k;
-            dg[e] = da * slope;
-            // (a token of no sequence may hold anything)
+            const float dh = dy[i][e] + d[e], out = a[i][e] * dh;
+            const float da = fmaf(out, prev[i][e], dh * x[i][e] * dk[i][e]);
+            dx[e] = dh * k[i][e];
+            dg[e] = da * slope[i][e];
+            // (what a token of no sequence has in front of it may be no number)
             sb[e] += ok ? dg[e] : 0.f;
-            sr[e] -= ok ? da * sig : 0.f;
+            sr[e] -= ok ? da * sig[i][e] : 0.f;
             d[e] = out;
         }
         rx.store(dx, i, ok);

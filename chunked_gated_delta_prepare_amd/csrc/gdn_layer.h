@@ -143,11 +143,14 @@ __device__ __forceinline__ float exact_exp(float x) {
     return fast_exp2(t) * fmaf(lo, 0.693147181f, 1.f);
 }
 
-// 1 / (1 + e^-v) and what it lacks to 1, each good to its own last digits.
+// 1 / (1 + e^-v) and what it lacks to 1, each good to its own last digits (EXACT) or
+// to |v| / 2 units of them.
+template <bool EXACT>
 struct Sigmoid {
     float s, o;
     __device__ __forceinline__ explicit Sigmoid(float v) {
-        const float e = exact_exp(-fabsf(v)), r = __builtin_amdgcn_rcpf(1.f + e), n = e * r;
+        const float e = EXACT ? exact_exp(-fabsf(v)) : fast_exp2(fabsf(v) * -kLog2e);
+        const float r = __builtin_amdgcn_rcpf(1.f + e), n = e * r;
         s = v >= 0.f ? r : n;
         o = v >= 0.f ? n : r;
     }

@@ -18,7 +18,7 @@ struct LayerNormParams {
     void *y, *s, *ds, *dx;
     float *scales, *dw, *db, *part;
     int64_t rows, x_stride;
-    int D, nwg, w_f32, fp8, group;
+    int D, nwg, turns, w_f32, fp8, group;
     float eps, inv_d;
 };
 
@@ -63,73 +63,122 @@ __device__ __forceinline__ void take_mean(float (&s)[K][VEC], uint32_t D, int ti
         for (int i = 0; i < VEC; ++i) s[k][i] = (uint32_t)((k * TPR + tid) * VEC) < D ? s[k][i] - m : 0.f;
 }
 
+// A workgroup takes `turns` rows (or four times as many, one a wave), with the
+// weights in registers and the next row in flight (not where a thread holds 32
+// elements of a row): the weights of one row after the other would be half of
+// what comes through the second cache.
 template <typename IO, typename RS, int VEC, int TPR, int K>
 __global__ void __launch_bounds__(TPR < 256 ? 256 : TPR) layer_norm_forward_kernel(LayerNormParams p) {
     constexpr int kRows = TPR < 256 ? 256 / TPR : 1;
-    __shared__ float red[3][TPR / 64];
+    constexpr bool kAhead = K * VEC <= 16;
+    __shared__ float red[4][TPR / 64];
     __shared__ uint32_t gmax[kRows][kRowGroups<VEC, TPR, K>];
     const int sub = TPR < 256 ? wave_id() : 0;
     const int tid = TPR < 256 ? lane_id() : threadIdx.x;
-    const int64_t row = (int64_t)blockIdx.x * kRows + sub;
-    const bool live = row < p.rows;
-    const uint32_t D = p.D, dm = live ? D : 0;       // a row past the end reads and stores nothing
-    const int64_t at = live ? row : 0;
-    const rsrc_t rx = make_rsrc((const IO *)p.x + at * p.x_stride, dm * sizeof(IO));
-    float s[K][VEC];
+    const uint32_t D = p.D;
+    RawRow<IO, VEC> xn[kAhead ? K : 1];
+    RawRow<RS, VEC> rn[kAhead ? K : 1];
+    // (a row past the end reads zeros and stores nothing)
+    auto fetch = [&](int64_t row) {
+        if constexpr (!kAhead) return;
+        const bool live = row < p.rows;
+        const int64_t at = live ? row : 0;
+        const rsrc_t rx = make_rsrc((const IO *)p.x + at * p.x_stride, live ? D * sizeof(IO) : 0);
+        const rsrc_t rr = make_rsrc((const RS *)p.res + (p.res ? at * D : 0), live && p.res ? D * sizeof(RS) : 0);
 #pragma unroll
-    for (int k = 0; k < K; ++k) row_load<IO, VEC>(rx, (k * TPR + tid) * VEC, s[k]);
-    if (p.res) {
-        const rsrc_t rr = make_rsrc((const RS *)p.res + at * D, dm * sizeof(RS));
-        const rsrc_t ro = make_rsrc((RS *)p.s + at * D, dm * sizeof(RS));
-        float t[K][VEC];
+        for (int k = 0; k < (kAhead ? K : 1); ++k) {
+            xn[k].load(rx, tid * VEC * sizeof(IO), k * TPR * VEC * sizeof(IO));
+            rn[k].load(rr, tid * VEC * sizeof(RS), k * TPR * VEC * sizeof(RS));
+        }
+    };
+    const int turns = kAhead ? p.turns : 1;
+    int64_t row = (int64_t)blockIdx.x * turns * kRows + sub;
+    if (kAhead) fetch(row);
+    const uint32_t wb = p.w_f32 ? 4 : (uint32_t)sizeof(IO);
+    const rsrc_t rw = make_rsrc(p.w, D * wb), rb = make_rsrc(p.b, p.b ? D * wb : 0);
+    float w[kAhead ? K : 1][VEC], b[kAhead ? K : 1][VEC];
+    auto weights = [&](int k, float (&wk)[VEC], float (&bk)[VEC]) {
+        row_load_either<IO, VEC>(rw, p.w_f32, (k * TPR + tid) * VEC, wk);
+        row_load_either<IO, VEC>(rb, p.w_f32, (k * TPR + tid) * VEC, bk);
+    };
+    if constexpr (kAhead) {
 #pragma unroll
-        for (int k = 0; k < K; ++k) row_load<RS, VEC>(rr, (k * TPR + tid) * VEC, t[k]);
-#pragma unroll
-        for (int k = 0; k < K; ++k) {
+        for (int k = 0; k < K; ++k) weights(k, w[k], b[k]);
+    }
+    for (int turn = 0; turn < turns; ++turn, row += kRows) {
+        const bool live = row < p.rows;
+        const uint32_t dm = live ? D : 0;
+        const int64_t at = live ? row : 0;
+        float s[K][VEC];
+        auto keep = [&](int k, const float (&r)[VEC]) {
 #pragma unroll
             for (int i = 0; i < VEC; ++i) {
-                s[k][i] += t[k][i];
+                s[k][i] += r[i];
                 // the norm is taken of the row as it is kept, which the
                 // backward pass reads
                 if constexpr (sizeof(RS) == 2) s[k][i] = bf16_bits_to_f32(f32_to_bf16_bits(s[k][i]));
             }
-            row_store<RS, VEC>(ro, (k * TPR + tid) * VEC, s[k]);
+        };
+        if constexpr (kAhead) {
+#pragma unroll
+            for (int k = 0; k < K; ++k) {
+                float r[VEC];
+                xn[k].get(s[k]);
+                rn[k].get(r);
+                if (p.res) keep(k, r);
+            }
+        } else {
+            const rsrc_t rx = make_rsrc((const IO *)p.x + at * p.x_stride, dm * sizeof(IO));
+#pragma unroll
+            for (int k = 0; k < K; ++k) row_load<IO, VEC>(rx, (k * TPR + tid) * VEC, s[k]);
+            if (p.res) {
+                const rsrc_t rr = make_rsrc((const RS *)p.res + at * D, dm * sizeof(RS));
+#pragma unroll
+                for (int k = 0; k < K; ++k) {
+                    float r[VEC];
+                    row_load<RS, VEC>(rr, (k * TPR + tid) * VEC, r);
+                    keep(k, r);
+                }
+            }
+        }
+        if (kAhead && turn + 1 < turns) fetch(row + kRows);
+        if (p.res) {
+            const rsrc_t ro = make_rsrc((RS *)p.s + at * D, dm * sizeof(RS));
+#pragma unroll
+            for (int k = 0; k < K; ++k) row_store<RS, VEC>(ro, (k * TPR + tid) * VEC, s[k]);
+        }
+        take_mean<VEC, TPR, K>(s, D, tid, p.inv_d, red[0]);
+        float t[2] = {0.f, 0.f};
+#pragma unroll
+        for (int k = 0; k < K; ++k)
+#pragma unroll
+            for (int i = 0; i < VEC; ++i) {
+                t[0] += s[k][i];
+                t[1] += s[k][i] * s[k][i];
+            }
+        row_total<TPR>(t, red[1]);
+        const float m = t[0] * p.inv_d;
+        const float r = inverse_deviation(t[1] * p.inv_d - m * m, p.eps);
+        float amax = 0.f;
+#pragma unroll
+        for (int k = 0; k < K; ++k) {
+            constexpr int kLast = kAhead ? K - 1 : 0;
+            if constexpr (!kAhead) weights(k, w[0], b[0]);
+#pragma unroll
+            for (int i = 0; i < VEC; ++i) {
+                s[k][i] = fmaf((s[k][i] - m) * r, w[k < kLast ? k : kLast][i], b[k < kLast ? k : kLast][i]);
+                amax = fmaxf(amax, fabsf(s[k][i]));
+            }
+        }
+        if (!p.fp8) {
+            const rsrc_t ry = make_rsrc((IO *)p.y + at * D, dm * sizeof(IO));
+#pragma unroll
+            for (int k = 0; k < K; ++k) row_store<IO, VEC>(ry, (k * TPR + tid) * VEC, s[k]);
+        } else {
+            store_row_e4m3<VEC, TPR, K>(make_rsrc((uint8_t *)p.y + at * D, dm), p.scales + at * (p.group ? (D + 127) >> 7 : 1), live, D,
+                                        p.group, amax, s, tid, red[3], gmax[sub]);
         }
     }
-    take_mean<VEC, TPR, K>(s, D, tid, p.inv_d, red[0]);
-    float t[2] = {0.f, 0.f};
-#pragma unroll
-    for (int k = 0; k < K; ++k)
-#pragma unroll
-        for (int i = 0; i < VEC; ++i) {
-            t[0] += s[k][i];
-            t[1] += s[k][i] * s[k][i];
-        }
-    row_total<TPR>(t, red[1]);
-    const float m = t[0] * p.inv_d;
-    const float r = inverse_deviation(t[1] * p.inv_d - m * m, p.eps);
-    const uint32_t wb = p.w_f32 ? 4 : (uint32_t)sizeof(IO);
-    const rsrc_t rw = make_rsrc(p.w, D * wb), rb = make_rsrc(p.b, p.b ? D * wb : 0);
-    float amax = 0.f;
-#pragma unroll
-    for (int k = 0; k < K; ++k) {
-        float w[VEC], b[VEC];
-        row_load_either<IO, VEC>(rw, p.w_f32, (k * TPR + tid) * VEC, w);
-        row_load_either<IO, VEC>(rb, p.w_f32, (k * TPR + tid) * VEC, b);
-#pragma unroll
-        for (int i = 0; i < VEC; ++i) {
-            s[k][i] = fmaf((s[k][i] - m) * r, w[i], b[i]);
-            amax = fmaxf(amax, fabsf(s[k][i]));
-        }
-    }
-    if (!p.fp8) {
-        const rsrc_t ry = make_rsrc((IO *)p.y + at * D, dm * sizeof(IO));
-#pragma unroll
-        for (int k = 0; k < K; ++k) row_store<IO, VEC>(ry, (k * TPR + tid) * VEC, s[k]);
-        return;
-    }
-    store_row_e4m3<VEC, TPR, K>(make_rsrc((uint8_t *)p.y + at * D, dm), p.scales + at * (p.group ? (D + 127) >> 7 : 1), live, D, p.group,
-                                amax, s, tid, red[0], gmax[sub]);
 }
 
 // Rows go to the workgroups in turn; each keeps its shares of dw and db in
@@ -286,6 +335,8 @@ namespace {
 constexpr int64_t kLnRows = 1 << 22;      // a forward launch's: a multiple of 4, under 2^32 threads
 constexpr int kLnWgs = 512;               // workgroups of the backward pass, at most
 
+constexpr int kLnTurns = 4, kLnMany = 1024;      // rows of a forward workgroup, where that leaves kLnMany of them
+
 int ln_rows_per_wg(int64_t D) { return D <= 256 ? 4 : 1; }
 
 // Workgroups of the backward pass: as many as need the same number of turns as kLnWgs.
@@ -378,7 +429,9 @@ gdn_status gdn_layer_norm_forward(const gdn_norm_problem *pr, const void *x, con
         np.y = (char *)y + r * pr->D * (int64_t)ob;
         np.s = s ? (char *)s + r * pr->D * (int64_t)sb : nullptr;
         np.scales = scales ? scales + r * ng : nullptr;
-        const gdn_status at = ln_types<false>(pr, np, vec, (np.rows + k - 1) / k, (hipStream_t)stream);
+        const int64_t groups = (np.rows + k - 1) / k;
+        np.turns = np.D <= 8192 && groups >= kLnTurns * kLnMany ? kLnTurns : 1;
+        const gdn_status at = ln_types<false>(pr, np, vec, (groups + np.turns - 1) / np.turns, (hipStream_t)stream);
         if (at != GDN_OK) return at;
     }
     return GDN_OK;

@@ -118,7 +118,10 @@ def _span(t):
     lo = t.data_ptr()
     if t.is_contiguous():
         return lo, lo + t.nbytes
-    return lo, lo + t.element_size() * (1 + sum((n - 1) * s for n, s in zip(t.shape, t.stride())))
+    last = 1
+    for n, s in zip(t.shape, t.stride()):
+        last += (n - 1) * s
+    return lo, lo + t.element_size() * last
 
 
 def _apart(out, name, *inputs):
@@ -598,6 +601,12 @@ def _row_stride(t, name):
     """Between the rows of a step's input [b, ...] whose rows are dense."""
     if t.is_contiguous():
         return t.numel() // t.shape[0]
+    if len(t.shape) == 2:
+        n, D = t.shape
+        s, one = t.stride()
+        if one != 1 and D != 1:
+            raise ValueError("%s's rows must be contiguous" % name)
+        return s if n != 1 else D
     want = 1
     for n, s in zip(reversed(t.shape[1:]), reversed(t.stride()[1:])):
         if n != 1 and s != want:
@@ -739,28 +748,26 @@ _ACT = {"silu": 0, "sigmoid": 1}
 def _head_strides(t, name):
     """[..., H, D] as T tokens of H rows: (T, H, token stride, head stride).  Two
     dimensions are tokens of one row."""
-    shape, strides = t.shape, t.stride()
-    D = shape[-1]
-    H, sh = (shape[-2], strides[-2]) if len(shape) > 2 else (1, D)
+    shape, D = t.shape, t.shape[-1]
+    lead, H = (shape[:-2], shape[-2]) if len(shape) > 2 else (shape[:-1], 1)
     T = 1
-    for n in (shape[:-2] if len(shape) > 2 else shape[:-1]):
+    for n in lead:
         T *= n
-    if t.is_contiguous():
+    if t.is_contiguous() or not t.numel():
         return T, H, H * D, D
-    if not t.numel():
-        return T, H, H * D, D
+    strides = t.stride()
     if D > 1 and strides[-1] != 1:
         raise ValueError("%s's rows must be contiguous" % name)
-    st, want = None, None
-    for n, s in zip(reversed(shape[:-2] if len(shape) > 2 else shape[:-1]), reversed(strides[:-2] if len(shape) > 2 else strides[:-1])):
+    st, want = H * D, None
+    for n, s in zip(lead[::-1], strides[len(lead) - 1::-1]):
         if n == 1:
             continue
-        if st is None:
+        if want is None:
             st = s
         elif s != want:
             raise ValueError("%s's tokens must lie at one stride" % name)
         want = s * n
-    return T, H, H * D if st is None else st, sh if H > 1 else D
+    return T, H, st, strides[-2] if H > 1 else D
 
 
 def _apart_rows(T, H, D, st, sh, name):
@@ -795,14 +802,13 @@ def _gate_norm_checks(x, z, weight, bias, activation, center):
 
 
 def _gate_norm_problem(size_of, x, z, dz, weight, code, each, first, center, act, eps):
-    D = x.shape[-1]
     T, H, xt, xh = _head_strides(x, "x")
     _, _, zt, zh = _head_strides(z, "z")
-    dt, dh = (0, 0)
+    dt, dh = 0, 0
     if dz is not None:
         _, _, dt, dh = _head_strides(dz, "dz")
-        _apart_rows(T, H, D, dt, dh, "dz")
-    return _problem(GateNormProblem, size_of, T, H, D, xt, xh, zt, zh, dt, dh, code, _CODE[weight.dtype], int(each), int(first),
+        _apart_rows(T, H, x.shape[-1], dt, dh, "dz")
+    return _problem(GateNormProblem, size_of, T, H, x.shape[-1], xt, xh, zt, zh, dt, dh, code, _CODE[weight.dtype], int(each), int(first),
                     int(center), act, eps)
 
 
@@ -878,9 +884,10 @@ def _glr_checks(x, gate, gate_bias, rate, form, scale, dims):
         raise ValueError("scale must be None, 'complement' or 'norm', got %r" % (scale,))
     if (form == "rate") != (rate is not None):
         raise ValueError("a rate is needed for form 'rate'" if rate is None else "a rate is for form 'rate' only")
-    for t, name in ((gate_bias, "gate_bias"), (rate, "rate")):
-        if t is not None:
-            _check(t, name, dev, x.shape[-1:], torch.float32)
+    if gate_bias is not None:
+        _check(gate_bias, "gate_bias", dev, x.shape[-1:], torch.float32)
+    if rate is not None:
+        _check(rate, "rate", dev, x.shape[-1:], torch.float32)
     return dev, code
 
 
@@ -1003,12 +1010,16 @@ def glr_step(x, gate, state, *, gate_bias=None, rate=None, form="log", scale=Non
     return _on(dev, stream, _glr_step, dev, code, x, gate, state, gate_bias, rate, _FORM[form], _SCALE[scale], slots, y)
 
 
+@functools.lru_cache(maxsize=4096)
+def _glr_step_problem(B, D, xs, gs, code, gcode, form, scale):
+    return ctypes.byref(GlrProblem(B, 1, D, xs, D, gs, D, 0, 0, 0, 0, 0, 0, 0, code, gcode, form, scale))
+
+
 def _glr_step(handle, dev, code, x, gate, state, gate_bias, rate, form, scale, slots, y):
     B, D = x.shape
     y = _out(y, "y", dev, x.shape, x.dtype, (x, gate, gate_bias, rate, slots, state), x)
     if B:
-        pr, _ = _problem(GlrProblem, None, B, 1, D, _row_stride(x, "x"), D, _row_stride(gate, "gate"), D, 0, 0, 0, 0, 0, 0, 0, code,
-                         _CODE[gate.dtype], form, scale)
+        pr = _glr_step_problem(B, D, _row_stride(x, "x"), _row_stride(gate, "gate"), code, _CODE[gate.dtype], form, scale)
         _call("gdn_glr_step", pr, x.data_ptr(), gate.data_ptr(), _ptr(gate_bias), _ptr(rate), state.data_ptr(), _ptr(slots), state.shape[0],
               y.data_ptr(), handle)
     return y
