@@ -420,7 +420,7 @@ __global__ void __launch_bounds__(kGateThreads<TPR>) gate_norm_backward_kernel(G
 
 namespace {
 
-constexpr int64_t kGateRows = 1 << 22;     // a forward launch's, under 2^32 threads
+constexpr int64_t kGateRows = 1 << 21;     // a forward launch's, under 2^32 threads
 constexpr int kGateWgs = 1024;             // workgroups of the backward pass, about
 
 gdn_status check_gate_norm(const gdn_gate_norm_problem *pr) {

@@ -6,23 +6,24 @@ namespace gdn {
 constexpr int kGlrWaves = 8;
 constexpr int kGlrRun = 16;            // tokens of a thread at a time
 
-template <int VEC>
-constexpr int kGlrTile = kGlrWaves * GlrLane<VEC>::kTG * kGlrRun;      // tokens of a workgroup at a time
+template <int VEC, int NW = kGlrWaves>
+constexpr int kGlrTile = NW * GlrLane<VEC>::kTG * kGlrRun;      // tokens of a workgroup at a time
 
 // y and the final states: a workgroup walks one segment of 64 channels, tile by
 // tile; the state at a segment's start comes from the segments' moves in the
 // workspace.  One read of x and the gate and one write of y; the next tile's
-// rows are in flight while one is worked on.
-template <typename IO, typename GT, int VEC, bool PK, int FORM>
-__global__ void __launch_bounds__(64 * kGlrWaves, 2) glr_forward_kernel(GlrParams p) {
-    constexpr int L = kGlrRun, NW = kGlrWaves;
+// rows are in flight while one is worked on.  NW waves: eight, or one for many
+// short sequences.
+template <typename IO, typename GT, int VEC, bool PK, int FORM, int NW>
+__global__ void __launch_bounds__(64 * NW, 2) glr_forward_kernel(GlrParams p) {
+    constexpr int L = kGlrRun, kTile = kGlrTile<VEC, NW>;
     __shared__ float lds_q[2][NW][kGlrCols], lds_h[2][NW][kGlrCols];
     const int group = blockIdx.x % p.groups, rest = blockIdx.x / p.groups, seg = rest % p.segs, b = rest / p.segs;
     const GlrLane<VEC> ln(group);
     const int w = wave_id(), row = (w * ln.kTG + ln.tg) * L;
     const int t_begin = seg * p.seg_len, t_end = t_begin + p.seg_len < p.T ? t_begin + p.seg_len : p.T;
     RunRows<IO, GT, VEC, L> rows;
-    if (t_begin < t_end) rows.fetch(p, b, t_begin, row, ln.c, t_begin + kGlrTile<VEC> <= p.T);
+    if (t_begin < t_end) rows.fetch(p, b, t_begin, row, ln.c, t_begin + kTile <= p.T);
     float bias[VEC], rate[VEC], h[VEC];
     channel_load<VEC>(p.bias, ln.c, p.D, bias);
     channel_load<VEC>(p.rate, ln.c, p.D, rate);
@@ -41,7 +42,7 @@ __global__ void __launch_bounds__(64 * kGlrWaves, 2) glr_forward_kernel(GlrParam
     if (seg == 0) pass_empty(p, PK, b, group * kGlrCols, p.h0, p.hT);
     Span span;
     int turn = 0;
-    for (int t = t_begin; t < t_end; t += kGlrTile<VEC>, turn ^= 1) {
+    for (int t = t_begin; t < t_end; t += kTile, turn ^= 1) {
         const int t0 = t + row;
         const Marks marks = marks_of<PK, L>(p, t + w * ln.kTG * L, ln.kTG * L, t0, span);
         const bool odd = PK && __ballot(marks.first != 0) != 0;
@@ -65,7 +66,7 @@ __global__ void __launch_bounds__(64 * kGlrWaves, 2) glr_forward_kernel(GlrParam
                 }
             }
         });
-        if (t + kGlrTile<VEC> < t_end) rows.fetch(p, b, t + kGlrTile<VEC>, row, ln.c, t + 2 * kGlrTile<VEC> <= p.T);
+        if (t + kTile < t_end) rows.fetch(p, b, t + kTile, row, ln.c, t + 2 * kTile <= p.T);
         if (odd) {
             // u of a first token holds its sequence's initial state
             float n[VEC];
@@ -316,22 +317,23 @@ GlrPlan glr_plan(const gdn_glr_problem *pr) {
     return s;
 }
 
+enum { kMoves, kForward, kShort };
+template <typename IO, typename GT, int VEC, bool PK, int FORM>
+const void *glr_form_fn(int which) {
+    if constexpr (!PK)
+        if (which == kShort) return (const void *)&glr_forward_kernel<IO, GT, VEC, PK, FORM, 1>;
+    return which == kMoves ? (const void *)&glr_moves_kernel<IO, GT, VEC, PK, FORM> : (const void *)&glr_forward_kernel<IO, GT, VEC, PK, FORM, kGlrWaves>;
+}
 template <typename IO, typename GT, int VEC, bool PK>
-const void *glr_fn(int form, bool moves) {
-    switch (form) {
-        case GDN_GLR_LOG:
-            return moves ? (const void *)&glr_moves_kernel<IO, GT, VEC, PK, 0> : (const void *)&glr_forward_kernel<IO, GT, VEC, PK, 0>;
-        case GDN_GLR_SIGMOID:
-            return moves ? (const void *)&glr_moves_kernel<IO, GT, VEC, PK, 1> : (const void *)&glr_forward_kernel<IO, GT, VEC, PK, 1>;
-        default:
-            return moves ? (const void *)&glr_moves_kernel<IO, GT, VEC, PK, 2> : (const void *)&glr_forward_kernel<IO, GT, VEC, PK, 2>;
-    }
+const void *glr_fn(int form, int which) {
+    return form == GDN_GLR_LOG ? glr_form_fn<IO, GT, VEC, PK, 0>(which)
+           : form == GDN_GLR_SIGMOID ? glr_form_fn<IO, GT, VEC, PK, 1>(which) : glr_form_fn<IO, GT, VEC, PK, 2>(which);
 }
 template <bool PK>
-const void *glr_pick(const gdn_glr_problem *pr, bool pairs, bool moves) {
-    if (pairs) return glr_fn<bf16_t, bf16_t, 2, PK>(pr->form, moves);
-    if (pr->io_dtype == GDN_F32) return glr_fn<float, float, 1, PK>(pr->form, moves);
-    return pr->g_dtype == GDN_F32 ? glr_fn<bf16_t, float, 1, PK>(pr->form, moves) : glr_fn<bf16_t, bf16_t, 1, PK>(pr->form, moves);
+const void *glr_pick(const gdn_glr_problem *pr, bool pairs, int which) {
+    if (pairs) return glr_fn<bf16_t, bf16_t, 2, PK>(pr->form, which);
+    if (pr->io_dtype == GDN_F32) return glr_fn<float, float, 1, PK>(pr->form, which);
+    return pr->g_dtype == GDN_F32 ? glr_fn<bf16_t, float, 1, PK>(pr->form, which) : glr_fn<bf16_t, bf16_t, 1, PK>(pr->form, which);
 }
 
 template <typename IO, typename GT>
@@ -393,12 +395,14 @@ gdn_status gdn_glr_forward(const gdn_glr_problem *pr, const void *x, const void 
     const bool pairs = glr_pairs(pr, {x, y}, {gate}, {pr->x_stride_b, pr->x_stride_t, pr->g_stride_b, pr->g_stride_t});
     const int64_t wgs = pr->B * gp.groups;
     if (s.segs > 1) {
-        st = launch_kernel(cu_seqlens ? glr_pick<true>(pr, pairs, true) : glr_pick<false>(pr, pairs, true), (int)(wgs * (s.segs - 1)), &gp,
+        st = launch_kernel(cu_seqlens ? glr_pick<true>(pr, pairs, kMoves) : glr_pick<false>(pr, pairs, kMoves), (int)(wgs * (s.segs - 1)), &gp,
                            (hipStream_t)stream, 64 * kGlrWaves);
         if (st != GDN_OK) return st;
     }
-    return launch_kernel(cu_seqlens ? glr_pick<true>(pr, pairs, false) : glr_pick<false>(pr, pairs, false), (int)(wgs * s.segs), &gp,
-                         (hipStream_t)stream, 64 * kGlrWaves);
+    // many sequences of a few tokens: a wave each (SHORTFIG)
+    const bool few = !cu_seqlens && pr->T <= 64 && wgs >= 1024;
+    return launch_kernel(cu_seqlens ? glr_pick<true>(pr, pairs, kForward) : glr_pick<false>(pr, pairs, few ? kShort : kForward),
+                         (int)(wgs * s.segs), &gp, (hipStream_t)stream, few ? 64 : 64 * kGlrWaves);
 }
 
 gdn_status gdn_glr_step(const gdn_glr_problem *pr, const void *x, const void *gate, const float *bias, const float *rate,

@@ -151,7 +151,7 @@ typedef struct gdn_gate_norm_problem {
 /*
  * gdn_gate_norm_forward -- y [T, H, D] (dense).  weight [D] or [H, D]; bias
  * like it, or NULL (zero; without center it must be NULL).  One launch (for
- * every 2^22 rows).
+ * every 2^21 rows).
  */
 gdn_status gdn_gate_norm_forward(const gdn_gate_norm_problem *problem, const void *x, const void *z,
                                  const void *weight, const void *bias, void *y, void *stream);

@@ -269,7 +269,7 @@ def glr(x, gate, bias, rate, h0, lens, form, scale, dy=None, dhT=None):
         for t in reversed(range(at - lens[n], at)):
             d, s = d + dy[t], s + dy[t].abs()
             e = e + UNIT * 2 * s
-            dx[t], ex[t] = d * k[t], k[t] * (e + UNIT * 16 * s)
+            dx[t], ex[t] = d * k[t], k[t].abs() * (e + UNIT * 16 * s)
             size = a[t] * s * sprev[t] + s * (x[t] * dk[t]).abs()
             da[t], dasize[t] = a[t] * d * prev[t] + d * x[t] * dk[t], size
             eda[t] = a[t] * (e * sprev[t] + s * eprev[t]) + e * (x[t] * dk[t]).abs() + 32 * UNIT * size

@@ -95,6 +95,22 @@ def test_lengths(T, D, dt):
         check(inputs(1, T, D, dt, dt, form, h0=h0), [T], form, scale)
 
 
+@pytest.mark.parametrize("T", [1, 5, 16, 33, 64])
+@pytest.mark.parametrize("D,dt", [(66, BF), (65, BF), (64, F32)])
+def test_many_short_sequences(T, D, dt):
+    """A wave each: over a thousand of them."""
+    B = 700
+    check(inputs(B, T, D, dt, dt, "rate"), [T] * B, "rate", "norm")
+
+
+def test_growing_states():
+    """Gates above zero: the state grows, by a tenth a token at most here."""
+    d = inputs(1, 200, 64, F32, F32, "log")
+    d["gate"] = d["gate"].abs().clamp(max=0.1) * torch.where(rnd(1, 200, 64, seed=3) > 0, 1.0, -1.0)
+    for scale in (None, "complement"):
+        check(d, [200], "log", scale)
+
+
 @pytest.mark.parametrize("D", [1, 2, 3, 62, 64, 65, 128, 200])
 @pytest.mark.parametrize("dt", [BF, F32])
 def test_widths(D, dt):
