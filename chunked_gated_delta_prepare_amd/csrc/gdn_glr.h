@@ -233,11 +233,6 @@ __device__ __forceinline__ int seq_of(const GlrParams &p, int t) {
     return lo;
 }
 
-// Of a thread's L tokens from t0: which exist and are in a sequence, which are the
-// first and the last of one.
-struct Marks {
-    uint32_t valid, first, last;
-};
 // A packed sequence's rows, kept from run to run.
 struct Span {
     int n = 0, begin = 0, end = 0;
@@ -247,6 +242,9 @@ struct Span {
         end = cu_at(p, n + 1);
     }
     __device__ __forceinline__ void at(const GlrParams &p, int t) {
+        if (t >= begin && t < end) return;
+        // mostly the next one
+        if (n + 2 <= p.n_seqs) set(p, n + 1);
         if (t < begin || t >= end) set(p, seq_of(p, t));
     }
     // The same for a token that the wave has in common: 64 offsets at a time.
@@ -262,13 +260,20 @@ struct Span {
         set(p, lo);
     }
 };
+// Of a thread's L tokens from t0: which exist and are in a sequence, which are the
+// first and the last of one; and, in packed rows with a first or a last, the
+// sequence of the first of them.
+struct Marks {
+    uint32_t valid, first, last;
+    Span start;
+};
 // t_wave: the first token of the wave's runs, `tokens` in all; s: the wave's.
 template <bool PK, int L>
 __device__ __forceinline__ Marks marks_of(const GlrParams &p, int t_wave, int tokens, int t0, Span &s) {
     constexpr uint32_t kAll = (1u << L) - 1;
     const int n = p.T - t0;
     const uint32_t exist = n >= L ? kAll : n <= 0 ? 0 : (1u << n) - 1;
-    Marks m{exist, 0, 0};
+    Marks m{exist, 0, 0, {}};
     if constexpr (!PK) {
         m.first = t0 == 0 ? 1 & exist : 0;
         m.last = n >= 1 && n <= L ? 1u << (n - 1) : 0;
@@ -282,6 +287,7 @@ __device__ __forceinline__ Marks marks_of(const GlrParams &p, int t_wave, int to
         for (int i = 0; i < L && t0 + i < p.T; ++i) {
             const int t = t0 + i;
             own.at(p, t);
+            if (i == 0) m.start = own;
             const uint32_t in = t >= own.begin && t < own.end ? 1u << i : 0;
             m.valid |= in;
             if (t == own.begin) m.first |= in;
@@ -290,20 +296,22 @@ __device__ __forceinline__ Marks marks_of(const GlrParams &p, int t_wave, int to
     }
     return m;
 }
-// The sequence of token t: its number (packed), else the batch.
-template <bool PK>
-__device__ __forceinline__ int state_of(const GlrParams &p, int b, int t) {
-    return PK ? seq_of(p, t) : b;
-}
-
-// Sequences without a token hand their state through: out[n] = in[n] (or zero).
+// Sequences without a token hand their state through: out[n] = in[n] (or zero).  A wave
+// looks at 64 of them at a time.
 __device__ __forceinline__ void pass_empty(const GlrParams &p, bool packed, int b, int c0, const float *in, float *out) {
     if (!out) return;
-    const int n0 = packed ? 0 : b, n1 = packed ? p.n_seqs : b + 1;
-    const int c = c0 + (int)(threadIdx.x & 63);
-    for (int n = n0 + (int)(threadIdx.x >> 6); n < n1; n += (int)(blockDim.x >> 6)) {
-        const bool empty = packed ? cu_at(p, n) >= cu_at(p, n + 1) : p.T == 0;
-        if (empty && c < p.D) out[(int64_t)n * p.D + c] = in ? in[(int64_t)n * p.D + c] : 0.f;
+    const int c = c0 + lane_id();
+    auto pass = [&](int n) {
+        if (c < p.D) out[(int64_t)n * p.D + c] = in ? in[(int64_t)n * p.D + c] : 0.f;
+    };
+    if (!packed) {
+        if (p.T == 0 && wave_id() == 0) pass(b);
+        return;
+    }
+    for (int n0 = wave_id() * 64; n0 < p.n_seqs; n0 += (int)blockDim.x) {
+        const int n = n0 + lane_id();
+        uint64_t empty = __ballot(n < p.n_seqs && cu_at(p, n < p.n_seqs ? n : 0) >= cu_at(p, n < p.n_seqs ? n + 1 : 0));
+        for (; empty; empty &= empty - 1) pass(n0 + __builtin_ctzll(empty));
     }
 }
 

@@ -1,4 +1,14 @@
 // Gated linear recurrence, forward and step (see gdn_glr.h for the mathematics).
+//
+// Bound by memory where channels and sequences fill the chip (8 sequences of 8192
+// tokens, 4096 channels of bf16: 341 us, 4.7 TB/s, a copy's rate); a single long
+// sequence is cut into segments and its rows are read once more for their moves
+// (65536 tokens: 208 us, then 325).  Vector instructions come next: with the gate's
+// exponential, reciprocal, series and square root some 36 an element (rate, norm) or 24 (sigmoid,
+// complement), which keep the units busy for 0.75 and 0.5 of the time.  16384 packed
+// tokens of 4096 channels, rate and norm: 71 us the moves, 101 us y.  Eight waves of 16
+// tokens a thread and one workgroup a CU; four waves and 512 workgroups 556 against 536 us
+// (65536 tokens), 8 tokens a thread 580, 16 waves 619.
 #include "gdn_glr.h"
 
 namespace gdn {
@@ -12,8 +22,8 @@ constexpr int kGlrTile = NW * GlrLane<VEC>::kTG * kGlrRun;      // tokens of a w
 // y and the final states: a workgroup walks one segment of 64 channels, tile by
 // tile; the state at a segment's start comes from the segments' moves in the
 // workspace.  One read of x and the gate and one write of y; the next tile's
-// rows are in flight while one is worked on.  NW waves: eight, or one for many
-// short sequences.
+// rows are in flight while one is worked on.  NW waves: eight, or four or one for
+// many short sequences.
 template <typename IO, typename GT, int VEC, bool PK, int FORM, int NW>
 __global__ void __launch_bounds__(64 * NW, 2) glr_forward_kernel(GlrParams p) {
     constexpr int L = kGlrRun, kTile = kGlrTile<VEC, NW>;
@@ -70,6 +80,7 @@ __global__ void __launch_bounds__(64 * NW, 2) glr_forward_kernel(GlrParams p) {
         if (odd) {
             // u of a first token holds its sequence's initial state
             float n[VEC];
+            Span q = marks.start;
 #pragma unroll
             for (int e = 0; e < VEC; ++e) n[e] = 0.f;
 #pragma unroll
@@ -77,7 +88,8 @@ __global__ void __launch_bounds__(64 * NW, 2) glr_forward_kernel(GlrParams p) {
                 const bool f = marks.first >> i & 1;
                 if (f) {
                     float h0[VEC];
-                    state_load<VEC>(p, p.h0, seq_of(p, t0 + i), ln.c, h0);
+                    q.at(p, t0 + i);
+                    state_load<VEC>(p, p.h0, q.n, ln.c, h0);
 #pragma unroll
                     for (int e = 0; e < VEC; ++e) u[i][e] = fmaf(a[i][e], h0[e], u[i][e]);
                 }
@@ -125,13 +137,17 @@ __global__ void __launch_bounds__(64 * NW, 2) glr_forward_kernel(GlrParams p) {
                 ry.store(mine, i, true);
             }
         } else {
+            Span q = marks.start;
 #pragma unroll
             for (int i = 0; i < L; ++i) {
                 const bool f = PK && (marks.first >> i & 1);
 #pragma unroll
                 for (int e = 0; e < VEC; ++e) mine[e] = f ? u[i][e] : fmaf(a[i][e], mine[e], u[i][e]);
                 ry.store(mine, i, marks.valid >> i & 1);
-                if (p.hT && (marks.last >> i & 1)) state_store<VEC>(p, p.hT, state_of<PK>(p, b, t0 + i), ln.c, true, mine);
+                if (p.hT && (marks.last >> i & 1)) {
+                    if (PK) q.at(p, t0 + i);
+                    state_store<VEC>(p, p.hT, PK ? q.n : b, ln.c, true, mine);
+                }
             }
         }
     }
@@ -171,18 +187,19 @@ __global__ void __launch_bounds__(64 * kGlrWaves, 2) glr_moves_kernel(GlrParams 
         for (int e = 0; e < VEC; ++e) H[e] = 0.f;
         auto walk = [&](auto odd) {
             with_scale<FORM>(p.scale, near, [&](auto sc, auto nr) {
+                Span q = marks.start;
 #pragma unroll
                 for (int i = 0; i < L; ++i) {
                     float xv[VEC], gv[VEC];
                     rows.x[i].get(xv);
                     rows.g[i].get(gv);
                     const bool f = odd.value && (marks.first >> i & 1);
-                    const int n = f ? seq_of(p, t0 + i) : 0;
+                    if (f) q.at(p, t0 + i);
 #pragma unroll
                     for (int e = 0; e < VEC; ++e) {
                         float a, c, slope, sig;
                         gate_of<FORM, nr.value>(gv[e], bias[e], rate[e], a, c, slope, sig);
-                        move_on<odd.value>(f, f ? state_at(p, p.h0, n, ln.c + e) : 0.f, a, c, xv[e] * input_scale<sc.value>(a, c), H[e], m.P[e], m.C[e]);
+                        move_on<odd.value>(f, f ? state_at(p, p.h0, q.n, ln.c + e) : 0.f, a, c, xv[e] * input_scale<sc.value>(a, c), H[e], m.P[e], m.C[e]);
                     }
                 }
             });
@@ -317,11 +334,13 @@ GlrPlan glr_plan(const gdn_glr_problem *pr) {
     return s;
 }
 
-enum { kMoves, kForward, kShort };
+enum { kMoves, kForward, kMany, kShort };
 template <typename IO, typename GT, int VEC, bool PK, int FORM>
 const void *glr_form_fn(int which) {
-    if constexpr (!PK)
+    if constexpr (!PK) {
         if (which == kShort) return (const void *)&glr_forward_kernel<IO, GT, VEC, PK, FORM, 1>;
+        if (which == kMany) return (const void *)&glr_forward_kernel<IO, GT, VEC, PK, FORM, 4>;
+    }
     return which == kMoves ? (const void *)&glr_moves_kernel<IO, GT, VEC, PK, FORM> : (const void *)&glr_forward_kernel<IO, GT, VEC, PK, FORM, kGlrWaves>;
 }
 template <typename IO, typename GT, int VEC, bool PK>
@@ -399,10 +418,18 @@ gdn_status gdn_glr_forward(const gdn_glr_problem *pr, const void *x, const void 
                            (hipStream_t)stream, 64 * kGlrWaves);
         if (st != GDN_OK) return st;
     }
-    // many sequences of a few tokens: a wave each (SHORTFIG)
-    const bool few = !cu_seqlens && pr->T <= 64 && wgs >= 1024;
-    return launch_kernel(cu_seqlens ? glr_pick<true>(pr, pairs, kForward) : glr_pick<false>(pr, pairs, few ? kShort : kForward),
-                         (int)(wgs * s.segs), &gp, (hipStream_t)stream, few ? 64 : 64 * kGlrWaves);
+    // A workgroup of eight waves fills a CU, so sequences that do not fill its tile are waited
+    // for one after the other: one wave for up to 64 tokens (or a single run of each thread), four
+    // for up to 512, where there are workgroups enough.  4096 channels of bf16: 256 sequences of 16 tokens
+    // 338 us with eight waves, 35 with one; 64 of 4 tokens 85 and 11; 64 of 100 tokens 90 with eight, 35 with
+    // four, of 512 tokens (32 sequences) 95 and 90.
+    const int which = cu_seqlens                                                         ? kForward
+                      : pr->T <= (pairs ? kGlrTile<2, 1> : kGlrTile<1, 1>) || (pr->T <= 64 && wgs >= 512) ? kShort
+                      : pr->T <= 512 && wgs >= 1024                                      ? kMany
+                                                                                         : kForward;
+    const int waves = which == kShort ? 1 : which == kMany ? 4 : kGlrWaves;
+    return launch_kernel(cu_seqlens ? glr_pick<true>(pr, pairs, which) : glr_pick<false>(pr, pairs, which), (int)(wgs * s.segs), &gp,
+                         (hipStream_t)stream, 64 * waves);
 }
 
 gdn_status gdn_glr_step(const gdn_glr_problem *pr, const void *x, const void *gate, const float *bias, const float *rate,

@@ -61,6 +61,31 @@ __device__ __forceinline__ void store_e4m3(rsrc_t r, uint32_t e, const float (&v
     }
 }
 
+// Weights and biases of a row's K vectors, `step` elements apart from e on, in the io
+// type or fp32: all loads first, then their conversions (a choice of type at every
+// vector would wait for each of them).
+template <typename T, int VEC, int K>
+__device__ __forceinline__ void load_affine_as(rsrc_t rw, rsrc_t rb, uint32_t e, uint32_t step, float (&w)[K][VEC], float (&b)[K][VEC]) {
+    RawRow<T, VEC> x[K], y[K];
+#pragma unroll
+    for (int k = 0; k < K; ++k) {
+        x[k].load(rw, e * sizeof(T), k * step * sizeof(T));
+        y[k].load(rb, e * sizeof(T), k * step * sizeof(T));
+    }
+#pragma unroll
+    for (int k = 0; k < K; ++k) {
+        x[k].get(w[k]);
+        y[k].get(b[k]);
+    }
+}
+template <typename IO, int VEC, int K>
+__device__ __forceinline__ void load_affine(rsrc_t rw, rsrc_t rb, bool f32, uint32_t e, uint32_t step, float (&w)[K][VEC], float (&b)[K][VEC]) {
+    if (sizeof(IO) == 4 || f32)
+        load_affine_as<float, VEC, K>(rw, rb, e, step, w, b);
+    else
+        load_affine_as<IO, VEC, K>(rw, rb, e, step, w, b);
+}
+
 // Scales that a row of K vectors of VEC elements for each of TPR threads may have.
 template <int VEC, int TPR, int K>
 constexpr int kRowGroups = (TPR * VEC * K + 127) / 128;

@@ -103,6 +103,13 @@ def test_many_short_sequences(T, D, dt):
     check(inputs(B, T, D, dt, dt, "rate"), [T] * B, "rate", "norm")
 
 
+@pytest.mark.parametrize("T,D,dt", [(70, 66, BF), (130, 65, BF), (65, 130, F32)])
+def test_many_sequences_of_some_tiles(T, D, dt):
+    """Four waves each."""
+    B = 520
+    check(inputs(B, T, D, dt, dt, "sigmoid"), [T] * B, "sigmoid", "complement", grads=False)
+
+
 def test_growing_states():
     """Gates above zero: the state grows, by a tenth a token at most here."""
     d = inputs(1, 200, 64, F32, F32, "log")
