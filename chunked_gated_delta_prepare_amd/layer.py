@@ -745,21 +745,20 @@ def _layer_norm_backward(handle, dev, code, dy, s, weight, bias, dres, eps, ds, 
 _ACT = {"silu": 0, "sigmoid": 1}
 
 
-def _head_strides(t, name):
+def _head_strides(shape, strides, name):
     """[..., H, D] as T tokens of H rows: (T, H, token stride, head stride).  Two
     dimensions are tokens of one row."""
-    shape, D = t.shape, t.shape[-1]
+    D = shape[-1]
     lead, H = (shape[:-2], shape[-2]) if len(shape) > 2 else (shape[:-1], 1)
     T = 1
     for n in lead:
         T *= n
-    if t.is_contiguous() or not t.numel():
+    if T * H * D == 0:
         return T, H, H * D, D
-    strides = t.stride()
     if D > 1 and strides[-1] != 1:
         raise ValueError("%s's rows must be contiguous" % name)
     st, want = H * D, None
-    for n, s in zip(lead[::-1], strides[len(lead) - 1::-1]):
+    for n, s in zip(lead[::-1], strides[len(lead) - 1::-1] if lead else ()):
         if n == 1:
             continue
         if want is None:
@@ -801,15 +800,16 @@ def _gate_norm_checks(x, z, weight, bias, activation, center):
     return dev, code, each
 
 
-def _gate_norm_problem(size_of, x, z, dz, weight, code, each, first, center, act, eps):
-    T, H, xt, xh = _head_strides(x, "x")
-    _, _, zt, zh = _head_strides(z, "z")
+@functools.lru_cache(maxsize=4096)
+def _gate_norm_problem(size_of, shape, xs, zs, dzs, code, wcode, each, first, center, act, eps):
+    T, H, xt, xh = _head_strides(shape, xs, "x")
+    _, _, zt, zh = _head_strides(shape, zs, "z")
     dt, dh = 0, 0
-    if dz is not None:
-        _, _, dt, dh = _head_strides(dz, "dz")
-        _apart_rows(T, H, x.shape[-1], dt, dh, "dz")
-    return _problem(GateNormProblem, size_of, T, H, x.shape[-1], xt, xh, zt, zh, dt, dh, code, _CODE[weight.dtype], int(each), int(first),
-                    int(center), act, eps)
+    if dzs is not None:
+        _, _, dt, dh = _head_strides(shape, dzs, "dz")
+        _apart_rows(T, H, shape[-1], dt, dh, "dz")
+    return _problem(GateNormProblem, size_of, T, H, shape[-1], xt, xh, zt, zh, dt, dh, code, wcode, int(each), int(first), int(center),
+                    act, eps)
 
 
 def gate_norm_forward(x, z, weight, bias=None, *, eps=1e-5, activation="silu", gate_first=False, center=False, y=None,
@@ -828,7 +828,7 @@ def gate_norm_forward(x, z, weight, bias=None, *, eps=1e-5, activation="silu", g
 
 def _gate_norm_forward(handle, dev, code, x, z, weight, bias, each, first, center, act, eps, y):
     y = _out(y, "y", dev, x.shape, x.dtype, (x, z, weight, bias), x)
-    pr, _ = _gate_norm_problem(None, x, z, None, weight, code, each, first, center, act, eps)
+    pr, _ = _gate_norm_problem(None, x.shape, x.stride(), z.stride(), None, code, _CODE[weight.dtype], each, first, center, act, eps)
     _call("gdn_gate_norm_forward", pr, x.data_ptr(), z.data_ptr(), weight.data_ptr(), _ptr(bias), y.data_ptr(), handle)
     return y
 
@@ -851,13 +851,14 @@ def _gate_norm_backward(handle, dev, code, dy, x, z, weight, bias, each, first, 
     ins = (dy, x, z, weight, bias)
     dx = _out(dx, "dx", dev, x.shape, x.dtype, ins, x)
     if dz is None:
-        dz = torch.empty(x.shape, device=dev, dtype=x.dtype)
+        dz = _out(None, "dz", dev, x.shape, x.dtype, ins, x)
     else:
         _check(dz, "dz", dev, x.shape, x.dtype, dense=False)
         _apart(dz, "dz", *ins, dx)
     dweight = _out(dweight, "dweight", dev, weight.shape, torch.float32, ins + (dx, dz), weight)
     dbias = None if bias is None else _out(dbias, "dbias", dev, bias.shape, torch.float32, ins + (dx, dz, dweight), bias)
-    pr, need = _gate_norm_problem("gdn_workspace_bytes_gate_norm_backward", x, z, dz, weight, code, each, first, center, act, eps)
+    pr, need = _gate_norm_problem("gdn_workspace_bytes_gate_norm_backward", x.shape, x.stride(), z.stride(), dz.stride(), code,
+                                  _CODE[weight.dtype], each, first, center, act, eps)
     workspace, size = _workspace(need, dev, workspace)
     _call("gdn_gate_norm_backward", pr, dy.data_ptr(), x.data_ptr(), z.data_ptr(), weight.data_ptr(), _ptr(bias), dx.data_ptr(), dz.data_ptr(),
           dweight.data_ptr(), _ptr(dbias), _ptr(workspace), size, handle)
@@ -891,6 +892,24 @@ def _glr_checks(x, gate, gate_bias, rate, form, scale, dims):
     return dev, code
 
 
+def _token_strides(shape, strides, name):
+    """(batch, token) strides of [B, T, D] whose rows are dense (see _strides)."""
+    B, T, D = shape
+    if strides[2] != 1 and D != 1 and B * T * D:
+        raise ValueError("%s must be contiguous behind its token dimension" % name)
+    return (strides[0] if B != 1 else 0), (strides[1] if T != 1 else D)
+
+
+@functools.lru_cache(maxsize=4096)
+def _glr_problem(size_of, shape, xs, gs, grads, n, code, gcode, form, scale):
+    """grads: the strides of dy, dx and dgate, or None."""
+    at = _token_strides(shape, xs, "x") + _token_strides(shape, gs, "gate")
+    for name, strides in zip(("dy", "dx", "dgate"), grads or ()):
+        at += _token_strides(shape, strides, name)
+    at += (0, 0) * (0 if grads else 3)
+    return _problem(GlrProblem, size_of, *shape, *at, n, code, gcode, form, scale)
+
+
 def glr_forward(x, gate, h0=None, *, gate_bias=None, rate=None, form="log", scale=None, cu_seqlens=None, y=None, hT=None,
                 output_final_state=True, workspace=None, stream=None):
     """Gated linear recurrence per channel: h_t = a_t h_{t-1} + c_t x_t, y_t = h_t.
@@ -915,8 +934,7 @@ def _glr_forward(handle, dev, code, x, gate, h0, gate_bias, rate, form, scale, c
     y = _out(y, "y", dev, x.shape, x.dtype, ins, x)
     if hT is not None or want:
         hT = _out(hT, "hT", dev, (n or B, D), torch.float32, ins + (y,), h0)
-    pr, need = _problem(GlrProblem, "gdn_workspace_bytes_glr", B, T, D, *_strides(x, "x"), *_strides(gate, "gate"), 0, 0, 0, 0, 0, 0, n,
-                        code, _CODE[gate.dtype], form, scale)
+    pr, need = _glr_problem("gdn_workspace_bytes_glr", x.shape, x.stride(), gate.stride(), None, n, code, _CODE[gate.dtype], form, scale)
     workspace, size = _workspace(need, dev, workspace)
     _call("gdn_glr_forward", pr, x.data_ptr(), gate.data_ptr(), _ptr(gate_bias), _ptr(rate), _ptr(h0), _ptr(cu_seqlens), y.data_ptr(),
           _ptr(hT), _ptr(workspace), size, handle)
@@ -934,9 +952,12 @@ def glr_backward(dy, x, gate, h0=None, dhT=None, *, gate_bias=None, rate=None, f
     dev, code = _glr_checks(x, gate, gate_bias, rate, form, scale, 3)
     n = _packed(cu_seqlens, dev, x.shape[0])
     _check(dy, "dy", dev, x.shape, x.dtype, dense=False)
-    for t, name, of, what in ((dbias, "dbias", gate_bias, "gate_bias"), (drate, "drate", rate, "rate"), (dh0, "dh0", h0, "h0")):
-        if of is None:
-            _unwritten(t, name, what)
+    if gate_bias is None:
+        _unwritten(dbias, "dbias", "a gate_bias")
+    if rate is None:
+        _unwritten(drate, "drate", "a rate")
+    if h0 is None:
+        _unwritten(dh0, "dh0", "an h0")
     for t, name in ((h0, "h0"), (dhT, "dhT")):
         if t is not None:
             _check(t, name, dev, (n or x.shape[0], x.shape[2]), torch.float32)
@@ -971,15 +992,14 @@ def _glr_backward(handle, dev, code, dy, x, gate, h0, dhT, gate_bias, rate, form
                   workspace):
     B, T, D = x.shape
     ins = (dy, x, gate, h0, dhT, gate_bias, rate, cu_seqlens)
-    for t, name, like in ((dx, "dx", x), (dgate, "dgate", gate)):
-        if t is not None:
-            _check(t, name, dev, x.shape, like.dtype, dense=False)
-            _apart(t, name, *ins)
-    if dx is None and dgate is None and x.dtype is gate.dtype:
-        # side by side, as a projection lays x and the gate out
-        both = torch.empty(B, T, 2 * D, device=dev, dtype=x.dtype)
-        dx, dgate = both[..., :D], both[..., D:]
+    if dx is None and dgate is None:
+        dx = torch.empty(B, T, D, device=dev, dtype=x.dtype)
+        dgate = torch.empty(B, T, D, device=dev, dtype=gate.dtype)
     else:
+        for t, name, like in ((dx, "dx", x), (dgate, "dgate", gate)):
+            if t is not None:
+                _check(t, name, dev, x.shape, like.dtype, dense=False)
+                _apart(t, name, *ins)
         dx = torch.empty(B, T, D, device=dev, dtype=x.dtype) if dx is None else dx
         dgate = torch.empty(B, T, D, device=dev, dtype=gate.dtype) if dgate is None else dgate
         _token_rows_apart(dx, dgate)
@@ -987,8 +1007,8 @@ def _glr_backward(handle, dev, code, dy, x, gate, h0, dhT, gate_bias, rate, form
     dbias = None if gate_bias is None else _out(dbias, "dbias", dev, (D,), torch.float32, ins, gate_bias)
     drate = None if rate is None else _out(drate, "drate", dev, (D,), torch.float32, ins + (dbias,), rate)
     dh0 = None if h0 is None else _out(dh0, "dh0", dev, h0.shape, torch.float32, ins + (dbias, drate), h0)
-    pr, need = _problem(GlrProblem, "gdn_workspace_bytes_glr_backward", B, T, D, *_strides(x, "x"), *_strides(gate, "gate"),
-                        *_strides(dy, "dy"), *_strides(dx, "dx"), *_strides(dgate, "dgate"), n, code, _CODE[gate.dtype], form, scale)
+    pr, need = _glr_problem("gdn_workspace_bytes_glr_backward", x.shape, x.stride(), gate.stride(), (dy.stride(), dx.stride(), dgate.stride()),
+                            n, code, _CODE[gate.dtype], form, scale)
     workspace, size = _workspace(need, dev, workspace)
     _call("gdn_glr_backward", pr, dy.data_ptr(), x.data_ptr(), gate.data_ptr(), _ptr(gate_bias), _ptr(rate), _ptr(h0), _ptr(cu_seqlens),
           _ptr(dhT), dx.data_ptr(), dgate.data_ptr(), _ptr(dbias), _ptr(drate), _ptr(dh0), _ptr(workspace), size, handle)
