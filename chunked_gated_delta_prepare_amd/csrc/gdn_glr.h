@@ -16,7 +16,10 @@
 // Layout of a wave: 64 channels innermost, 4 bytes a lane where rows allow it
 // (VEC = 2 channels of bf16 in CL = 32 lanes; else VEC = 1, CL = 64), and TG =
 // 64 / CL groups of lanes behind each other that take runs of L consecutive
-// tokens.  (8 bytes a lane would make four groups, and twice the joining.)
+// tokens.  (8 bytes a lane would make four groups, and twice the joining.)  Runs are put
+// together with one channel a lane: a swap of the wave's halves brings both groups'
+// runs of one channel into a lane, and the states at their fronts back (both channels of
+// both lanes: 402 us for 2 x 8192 tokens of 4096 channels forward and backward, so 368).
 #pragma once
 
 #include <initializer_list>
@@ -36,7 +39,7 @@ struct GlrParams {
     int64_t xb, xt, gb, gt, yb, yt, dxb, dxt, dgb, dgt;      // strides (y: dy)
     int64_t n_slots, n_states;                               // states: B or n_seqs
     int B, T, D, n_seqs, scale;
-    int groups, segs, seg_len;                               // channels / 64; segments (backward: tiles)
+    int groups, segs, seg_len, pieces;                       // channels / 64; segments (backward: tiles) and their pieces
     int grads;                                               // whether dbias or drate is wanted
 };
 
@@ -205,10 +208,12 @@ __device__ __forceinline__ float packed_move(float q, float h, float H) {
     return PK && q == -__builtin_inff() ? H : r;
 }
 
-// The value of the lane with the other token of lane bit 5 (lane ^ 32).
-__device__ __forceinline__ float other_half(float x) {
-    const auto h = __builtin_amdgcn_permlane32_swap(__float_as_uint(x), __float_as_uint(x), false, false);
-    return __uint_as_float(lane_id() & 32 ? h[0] : h[1]);
+// Two groups of lanes with two channels each, or, after a swap of halves, both groups'
+// values of one channel: {x[0], x[1]} of a lane to {the first group's, the second's}, and back.
+__device__ __forceinline__ void swap_halves(float &x, float &y) {
+    const auto h = __builtin_amdgcn_permlane32_swap(__float_as_uint(x), __float_as_uint(y), false, false);
+    x = __uint_as_float(h[0]);
+    y = __uint_as_float(h[1]);
 }
 
 // ---------------------------------------------------------------------------
@@ -324,7 +329,8 @@ struct GlrLane {
         c = group * kGlrCols + (lane_id() % kCL) * VEC;
         tg = lane_id() / kCL;
     }
-    __device__ __forceinline__ int local() const { return (lane_id() % kCL) * VEC; }      // among the workgroup's channels
+    // the lane's one channel, among the workgroup's, behind swap_halves
+    __device__ __forceinline__ int one() const { return VEC == 2 ? (lane_id() & 31) * 2 + (lane_id() >> 5) : lane_id(); }
 };
 
 // An offset past every descriptor here (rows' offsets are below 2^30 bytes).
@@ -422,27 +428,52 @@ __device__ __forceinline__ void move_on(bool first, float h0, float a, float c, 
     C = fmaf(c, 1.f - C, C);
 }
 
-// The move of a wave's whole run into (P, C, H), of what lies in it before this lane's
-// into `before` and E.
-template <bool PK, int VEC>
-__device__ __forceinline__ void join_wave(Moves<VEC> &m, float (&H)[VEC], Moves<VEC> &before, float (&E)[VEC]) {
-    before.none();
-#pragma unroll
-    for (int e = 0; e < VEC; ++e) E[e] = 0.f;
-    if constexpr (GlrLane<VEC>::kTG == 2) {
-        const bool second = lane_id() & 32;
-#pragma unroll
-        for (int e = 0; e < VEC; ++e) {
-            const float oP = other_half(m.P[e]), oC = other_half(m.C[e]), oH = other_half(H[e]);
-            if (second) {
-                before.P[e] = oP;
-                before.C[e] = oC;
-                E[e] = oH;
-            }
-            const float P2 = second ? m.P[e] : oP, C2 = second ? m.C[e] : oC;
-            H[e] = move<PK>(P2, C2, second ? oH : H[e], second ? H[e] : oH);
-            join<PK>(second ? oP : m.P[e], second ? oC : m.C[e], P2, C2, m.P[e], m.C[e]);
+// A wave's run, of one channel a lane: its move, its H and (backward) E, and those of its
+// two groups of lanes, whose runs lie behind each other.
+struct WaveRun {
+    float P, C, H, E, P0, C0, H0, E0, P1, C1, H1, E1;
+};
+template <bool PK, int VEC, bool BOTH>
+__device__ __forceinline__ WaveRun join_wave(const Moves<VEC> &m, const float (&H)[VEC], const float (&E)[VEC]) {
+    WaveRun r;
+    r.P = r.P0 = m.P[0];
+    r.C = r.C0 = m.C[0];
+    r.H = r.H0 = H[0];
+    r.E = r.E0 = E[0];
+    if constexpr (VEC == 2) {
+        r.P1 = m.P[1];
+        r.C1 = m.C[1];
+        r.H1 = H[1];
+        swap_halves(r.P0, r.P1);
+        swap_halves(r.C0, r.C1);
+        swap_halves(r.H0, r.H1);
+        r.H = move<PK>(r.P1, r.C1, r.H0, r.H1);
+        if constexpr (BOTH) {
+            r.E1 = E[1];
+            swap_halves(r.E0, r.E1);
+            r.E = move<PK>(r.P0, r.C0, r.E1, r.E0);
         }
+        join<PK>(r.P0, r.C0, r.P1, r.C1, r.P, r.C);
+    }
+    return r;
+}
+// The state in front of the wave's run -> in front of the lane's, of its VEC channels.
+template <bool PK, int VEC>
+__device__ __forceinline__ void spread_state(const WaveRun &r, float h, float (&x)[VEC]) {
+    x[0] = h;
+    if constexpr (VEC == 2) {
+        x[1] = move<PK>(r.P0, r.C0, h, r.H0);
+        swap_halves(x[0], x[1]);
+    }
+}
+// The same backwards, with what lies behind.
+template <bool PK, int VEC>
+__device__ __forceinline__ void spread_behind(const WaveRun &r, float d, float (&x)[VEC]) {
+    x[0] = d;
+    if constexpr (VEC == 2) {
+        x[1] = d;
+        x[0] = move<PK>(r.P1, r.C1, d, r.E1);
+        swap_halves(x[0], x[1]);
     }
 }
 

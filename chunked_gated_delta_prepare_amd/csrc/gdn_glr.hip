@@ -9,12 +9,15 @@
 // tokens of 4096 channels, rate and norm: 71 us the moves, 101 us y.  Eight waves of 16
 // tokens a thread and one workgroup a CU; four waves and 512 workgroups 556 against 536 us
 // (65536 tokens), 8 tokens a thread 580, 16 waves 619.
+#include <algorithm>
+
 #include "gdn_glr.h"
 
 namespace gdn {
 
 constexpr int kGlrWaves = 8;
 constexpr int kGlrRun = 16;            // tokens of a thread at a time
+constexpr int kGlrAhead = 4;           // moves that a workgroup of the forward pass reads at a time
 
 template <int VEC, int NW = kGlrWaves>
 constexpr int kGlrTile = NW * GlrLane<VEC>::kTG * kGlrRun;      // tokens of a workgroup at a time
@@ -34,20 +37,29 @@ __global__ void __launch_bounds__(64 * NW, 2) glr_forward_kernel(GlrParams p) {
     const int t_begin = seg * p.seg_len, t_end = t_begin + p.seg_len < p.T ? t_begin + p.seg_len : p.T;
     RunRows<IO, GT, VEC, L> rows;
     if (t_begin < t_end) rows.fetch(p, b, t_begin, row, ln.c, t_begin + kTile <= p.T);
-    float bias[VEC], rate[VEC], h[VEC];
+    // (states and moves between runs are of one channel a lane)
+    const int l = lane_id(), c1 = group * kGlrCols + ln.one();
+    float bias[VEC], rate[VEC];
     channel_load<VEC>(p.bias, ln.c, p.D, bias);
     channel_load<VEC>(p.rate, ln.c, p.D, rate);
     scale_bias<FORM, VEC>(bias);
     const bool near = near_rates<FORM, VEC>(rate);
     // (packed rows take initial states at their sequences' first tokens)
-    state_load<VEC>(p, PK ? nullptr : p.h0, b, ln.c, h);
-    for (int j = 0; j < seg; ++j) {
-        const float *s = p.ws + ((int64_t)b * (p.segs - 1) + j) * 2 * p.D;
-        float q[VEC], H[VEC];
-        channel_load<VEC>(s, ln.c, p.D, q);
-        channel_load<VEC>(s + p.D, ln.c, p.D, H);
+    float h = state_at(p, PK ? nullptr : p.h0, b, c1);
+    // the moves of what lies in front, whose loads go out kGlrAhead at a time
+    const int moves = seg * p.pieces;
+    const float *ws = p.ws + (int64_t)b * (p.segs - 1) * p.pieces * 2 * p.D;
+    for (int j0 = 0; j0 < moves; j0 += kGlrAhead) {
+        float q[kGlrAhead][1], H[kGlrAhead][1];
 #pragma unroll
-        for (int e = 0; e < VEC; ++e) h[e] = packed_move<PK>(q[e], h[e], H[e]);
+        for (int j = 0; j < kGlrAhead; ++j) {
+            const float *s = ws + (int64_t)(j0 + j < moves ? j0 + j : j0) * 2 * p.D;
+            channel_load<1>(s, c1, p.D, q[j]);
+            channel_load<1>(s + p.D, c1, p.D, H[j]);
+        }
+#pragma unroll
+        for (int j = 0; j < kGlrAhead; ++j)
+            if (j0 + j < moves) h = packed_move<PK>(q[j][0], h, H[j][0]);
     }
     if (seg == 0) pass_empty(p, PK, b, group * kGlrCols, p.h0, p.hT);
     Span span;
@@ -104,30 +116,18 @@ __global__ void __launch_bounds__(64 * NW, 2) glr_forward_kernel(GlrParams p) {
                 }
             }
         }
-        Moves<VEC> before;
-        float E[VEC];
-        join_wave<PK, VEC>(m, H, before, E);
-        if (ln.tg == 0) {
-#pragma unroll
-            for (int e = 0; e < VEC; ++e) {
-                lds_q[turn][w][ln.local() + e] = pack_move<PK>(m.P[e], m.C[e]);
-                lds_h[turn][w][ln.local() + e] = H[e];
-            }
-        }
+        const WaveRun run = join_wave<PK, VEC, false>(m, H, H);
+        lds_q[turn][w][l] = pack_move<PK>(run.P, run.C);
+        lds_h[turn][w][l] = run.H;
         // (one barrier a tile: the other half of LDS is next, and its readers are behind the next barrier)
         lds_barrier();
-        float mine[VEC];
+        float front, mine[VEC];
 #pragma unroll
         for (int j = 0; j < NW; ++j) {
-#pragma unroll
-            for (int e = 0; e < VEC; ++e) {
-                if (j == w) mine[e] = h[e];
-                h[e] = packed_move<PK>(lds_q[turn][j][ln.local() + e], h[e], lds_h[turn][j][ln.local() + e]);
-            }
+            if (j == w) front = h;
+            h = packed_move<PK>(lds_q[turn][j][l], h, lds_h[turn][j][l]);
         }
-#pragma unroll
-        for (int e = 0; e < VEC; ++e)
-            if (ln.tg > 0) mine[e] = move<PK>(before.P[e], before.C[e], mine[e], E[e]);
+        spread_state<PK, VEC>(run, front, mine);
         const TileRows<IO, VEC> ry(p.y, ((int64_t)b * p.T + t) * p.D, p.D, row, ln.c, p.D);
         if (!odd && __ballot(marks.valid != (1u << L) - 1 || marks.last != 0) == 0) {
 #pragma unroll
@@ -153,27 +153,26 @@ __global__ void __launch_bounds__(64 * NW, 2) glr_forward_kernel(GlrParams p) {
     }
 }
 
-// The moves of all segments but the last: a wave walks its share of the segment
-// backwards, so that what it reads last is what the next launch reads first.
+// The moves of all segments but the last, each in pieces of its tiles so that there
+// are workgroups for the whole chip.  A wave walks its share of a piece backwards,
+// and a segment's first pieces come last, so that what is read last is what the
+// next launch reads first.
 template <typename IO, typename GT, int VEC, bool PK, int FORM>
 __global__ void __launch_bounds__(64 * kGlrWaves, 2) glr_moves_kernel(GlrParams p) {
     constexpr int L = kGlrRun, NW = kGlrWaves, kStep = GlrLane<VEC>::kTG * L;
     __shared__ float lds_p[NW][kGlrCols], lds_c[NW][kGlrCols], lds_h[NW][kGlrCols];
-    const int segs = p.segs - 1;
-    const int group = blockIdx.x % p.groups, rest = blockIdx.x / p.groups, seg = rest % segs, b = rest / segs;
+    const int segs = p.segs - 1, K = p.pieces, tiles = p.seg_len / kGlrTile<2>;
+    const int group = blockIdx.x % p.groups, rest = blockIdx.x / p.groups, seg = rest % segs, b = rest / segs % p.B;
+    const int piece = K - 1 - rest / segs / p.B, tile = piece * tiles / K, share = ((piece + 1) * tiles / K - tile) * (kGlrTile<2> / NW);
     const GlrLane<VEC> ln(group);
-    const int w = wave_id(), row = ln.tg * L, share = p.seg_len / NW;
-    const int t_first = seg * p.seg_len + w * share;
+    const int w = wave_id(), row = ln.tg * L;
+    const int t_first = seg * p.seg_len + tile * kGlrTile<2> + w * share;
     float bias[VEC], rate[VEC];
     channel_load<VEC>(p.bias, ln.c, p.D, bias);
     channel_load<VEC>(p.rate, ln.c, p.D, rate);
     scale_bias<FORM, VEC>(bias);
     const bool near = near_rates<FORM, VEC>(rate);
-    Moves<VEC> all;
-    float S[VEC];
-    all.none();
-#pragma unroll
-    for (int e = 0; e < VEC; ++e) S[e] = 0.f;
+    float P = 1.f, C = 0.f, S = 0.f;      // of one channel a lane
     RunRows<IO, GT, VEC, L> rows;
     rows.fetch(p, b, t_first + share - kStep, row, ln.c, true);
     Span span;
@@ -209,33 +208,25 @@ __global__ void __launch_bounds__(64 * kGlrWaves, 2) glr_moves_kernel(GlrParams 
         else
             walk(std::false_type());
         if (t > t_first) rows.fetch(p, b, t - kStep, row, ln.c, true);
-        Moves<VEC> before;
-        float E[VEC];
-        join_wave<PK, VEC>(m, H, before, E);
-#pragma unroll
-        for (int e = 0; e < VEC; ++e) {
-            S[e] = move<PK>(all.P[e], all.C[e], H[e], S[e]);
-            join<PK>(m.P[e], m.C[e], all.P[e], all.C[e], all.P[e], all.C[e]);
-        }
+        const WaveRun run = join_wave<PK, VEC, false>(m, H, H);
+        S = move<PK>(P, C, run.H, S);
+        join<PK>(run.P, run.C, P, C, P, C);
     }
-    if (ln.tg == 0) {
-#pragma unroll
-        for (int e = 0; e < VEC; ++e) {
-            lds_p[w][ln.local() + e] = all.P[e];
-            lds_c[w][ln.local() + e] = all.C[e];
-            lds_h[w][ln.local() + e] = S[e];
-        }
-    }
+    const int l = lane_id(), c = group * kGlrCols + ln.one();
+    lds_p[w][l] = P;
+    lds_c[w][l] = C;
+    lds_h[w][l] = S;
     __syncthreads();
-    const int l = threadIdx.x, c = group * kGlrCols + l;
-    if (l >= kGlrCols || c >= p.D) return;
-    float P = lds_p[0][l], C = lds_c[0][l], H = lds_h[0][l];
+    if (w != 0 || c >= p.D) return;
+    P = lds_p[0][l];
+    C = lds_c[0][l];
+    float H = lds_h[0][l];
 #pragma unroll
     for (int j = 1; j < NW; ++j) {
         H = move<PK>(lds_p[j][l], lds_c[j][l], H, lds_h[j][l]);
         join<PK>(P, C, lds_p[j][l], lds_c[j][l], P, C);
     }
-    float *out = p.ws + ((int64_t)b * segs + seg) * 2 * p.D + c;
+    float *out = p.ws + (((int64_t)b * segs + seg) * K + piece) * 2 * p.D + c;
     out[0] = pack_move<PK>(P, C);
     out[p.D] = H;
 }
@@ -315,11 +306,12 @@ void fill_glr(const gdn_glr_problem *pr, GlrParams &gp, const int32_t *cu) {
 namespace {
 
 struct GlrPlan {
-    int64_t segs, seg_len;
+    int64_t segs, seg_len, pieces;
 };
 
 // Segments for about 256 workgroups of 64 channels, one a CU, of four tiles at least
-// (a segment's rows are read once more for its move).
+// (a segment's rows are read once more for its move).  Their pieces for the moves: for 256
+// workgroups however short, for 1024 if they keep four tiles.
 GlrPlan glr_plan(const gdn_glr_problem *pr) {
     constexpr int64_t kTile = kGlrTile<2>;         // (a multiple of the tile of single channels)
     const int64_t streams = pr->B * ((pr->D + kGlrCols - 1) / kGlrCols), tiles = (pr->T + kTile - 1) / kTile;
@@ -331,8 +323,13 @@ GlrPlan glr_plan(const gdn_glr_problem *pr) {
     s.seg_len = s.seg_len < kTile ? kTile : s.seg_len;
     s.segs = (pr->T + s.seg_len - 1) / s.seg_len;
     s.segs = s.segs < 1 ? 1 : s.segs;
+    const int64_t wgs = streams * s.segs, n = s.seg_len / kTile;
+    const int64_t fill = std::min((255 + wgs) / wgs, n), more = std::min((1023 + wgs) / wgs, n / 4);
+    s.pieces = std::max(fill, more);
     return s;
 }
+
+int64_t glr_bytes(const gdn_glr_problem *pr, const GlrPlan &s) { return pr->B * (s.segs - 1) * s.pieces * 2 * pr->D * 4; }
 
 enum { kMoves, kForward, kMany, kShort };
 template <typename IO, typename GT, int VEC, bool PK, int FORM>
@@ -382,7 +379,7 @@ extern "C" {
 
 size_t gdn_workspace_bytes_glr(const gdn_glr_problem *pr) {
     if (check_glr(pr, pr && pr->n_seqs > 0) != GDN_OK) return 0;
-    return (size_t)(pr->B * (glr_plan(pr).segs - 1)) * 2 * pr->D * 4;
+    return (size_t)glr_bytes(pr, glr_plan(pr));
 }
 
 gdn_status gdn_glr_forward(const gdn_glr_problem *pr, const void *x, const void *gate, const float *bias, const float *rate,
@@ -397,8 +394,8 @@ gdn_status gdn_glr_forward(const gdn_glr_problem *pr, const void *x, const void 
     const GlrPlan s = glr_plan(pr);
     GlrParams gp;
     fill_glr(pr, gp, cu_seqlens);
-    if (!grid_ok(s.segs * pr->B, (int64_t)gp.groups * 64 * kGlrWaves)) return GDN_ERR_UNSUPPORTED;
-    const size_t need = (size_t)(pr->B * (s.segs - 1)) * 2 * pr->D * 4;
+    if (!grid_ok(s.segs * s.pieces * pr->B, (int64_t)gp.groups * 64 * kGlrWaves)) return GDN_ERR_UNSUPPORTED;
+    const size_t need = (size_t)glr_bytes(pr, s);
     if (need && (!workspace || workspace_bytes < need)) return GDN_ERR_WORKSPACE;
     if (!aligned_to(workspace, 16)) return GDN_ERR_ALIGNMENT;
     gp.x = x;
@@ -411,10 +408,11 @@ gdn_status gdn_glr_forward(const gdn_glr_problem *pr, const void *x, const void 
     gp.ws = (float *)workspace;
     gp.segs = (int)s.segs;
     gp.seg_len = (int)s.seg_len;
+    gp.pieces = (int)s.pieces;
     const bool pairs = glr_pairs(pr, {x, y}, {gate}, {pr->x_stride_b, pr->x_stride_t, pr->g_stride_b, pr->g_stride_t});
     const int64_t wgs = pr->B * gp.groups;
     if (s.segs > 1) {
-        st = launch_kernel(cu_seqlens ? glr_pick<true>(pr, pairs, kMoves) : glr_pick<false>(pr, pairs, kMoves), (int)(wgs * (s.segs - 1)), &gp,
+        st = launch_kernel(cu_seqlens ? glr_pick<true>(pr, pairs, kMoves) : glr_pick<false>(pr, pairs, kMoves), (int)(wgs * (s.segs - 1) * s.pieces), &gp,
                            (hipStream_t)stream, 64 * kGlrWaves);
         if (st != GDN_OK) return st;
     }

@@ -24,30 +24,6 @@ constexpr int kGbRun = VEC == 2 ? 4 : 8;      // tokens of a thread
 template <int VEC>
 constexpr int kGbTile = kGbWaves * GlrLane<VEC>::kTG * kGbRun<VEC>;      // 32 either way
 
-// As join_wave, with e: what lies behind this lane's run into `after` and A.
-template <bool PK, int VEC>
-__device__ __forceinline__ void join_wave_both(Moves<VEC> &m, float (&H)[VEC], float (&E)[VEC], Moves<VEC> &beside, float (&B)[VEC],
-                                               float (&A)[VEC]) {
-    beside.none();
-#pragma unroll
-    for (int e = 0; e < VEC; ++e) A[e] = B[e] = 0.f;
-    if constexpr (GlrLane<VEC>::kTG == 2) {
-        const bool second = lane_id() & 32;
-#pragma unroll
-        for (int e = 0; e < VEC; ++e) {
-            const float oP = other_half(m.P[e]), oC = other_half(m.C[e]), oH = other_half(H[e]), oE = other_half(E[e]);
-            beside.P[e] = oP;
-            beside.C[e] = oC;
-            B[e] = oH;
-            A[e] = oE;
-            const float P1 = second ? oP : m.P[e], C1 = second ? oC : m.C[e], P2 = second ? m.P[e] : oP, C2 = second ? m.C[e] : oC;
-            H[e] = move<PK>(P2, C2, second ? oH : H[e], second ? H[e] : oH);
-            E[e] = move<PK>(P1, C1, second ? E[e] : oE, second ? oE : E[e]);
-            join<PK>(P1, C1, P2, C2, m.P[e], m.C[e]);
-        }
-    }
-}
-
 template <typename IO, int VEC, int L>
 __device__ __forceinline__ void fetch_dy(const GlrParams &p, RawRow<IO, VEC> (&dy)[L], int b, int t_base, int row, int c, bool full) {
     const TileRows<IO, VEC> rd(p.dy, b * p.yb + (int64_t)t_base * p.yt, p.yt, row, c, p.D);
@@ -119,21 +95,14 @@ __global__ void __launch_bounds__(64 * kGbWaves) glr_tiles_kernel(GlrParams p) {
         walk(std::true_type());
     else
         walk(std::false_type());
-    Moves<VEC> beside;
-    float before[VEC], after[VEC];
-    join_wave_both<PK, VEC>(m, H, E, beside, before, after);
-    if (ln.tg == 0) {
-#pragma unroll
-        for (int e = 0; e < VEC; ++e) {
-            lds[0][w][ln.local() + e] = m.P[e];
-            lds[1][w][ln.local() + e] = m.C[e];
-            lds[2][w][ln.local() + e] = H[e];
-            lds[3][w][ln.local() + e] = E[e];
-        }
-    }
+    const WaveRun run = join_wave<PK, VEC, true>(m, H, E);
+    const int l = lane_id(), c = group * kGlrCols + ln.one();
+    lds[0][w][l] = run.P;
+    lds[1][w][l] = run.C;
+    lds[2][w][l] = run.H;
+    lds[3][w][l] = run.E;
     __syncthreads();
-    const int l = threadIdx.x, c = group * kGlrCols + l;
-    if (l >= kGlrCols || c >= p.D) return;
+    if (w != 0 || c >= p.D) return;
     float P = lds[0][0][l], C = lds[1][0][l], hh = lds[2][0][l], ee = lds[3][0][l];
 #pragma unroll
     for (int j = 1; j < NW; ++j) {
@@ -200,17 +169,19 @@ __global__ void __launch_bounds__(64 * kGbWaves, 4) glr_backward_kernel(GlrParam
     const bool full = t + kGbTile<VEC> <= p.T;
     rows.fetch(p, b, t, row, ln.c, full);
     fetch_dy<IO, VEC, L>(p, dyr, b, t, row, ln.c, full);
-    float bias[VEC], rate[VEC], h[VEC], d[VEC];
+    // (states and moves between runs are of one channel a lane)
+    const int l = lane_id(), c1 = group * kGlrCols + ln.one();
+    float bias[VEC], rate[VEC], h1[1], d1[1];
     channel_load<VEC>(p.bias, ln.c, p.D, bias);
     channel_load<VEC>(p.rate, ln.c, p.D, rate);
     scale_bias<FORM, VEC>(bias);
     const bool near = near_rates<FORM, VEC>(rate);
     if (p.segs > 1) {
-        channel_load<VEC>(tile_at(p, b, tile) + p.D, ln.c, p.D, h);
-        channel_load<VEC>(tile_at(p, b, tile) + 2 * (int64_t)p.D, ln.c, p.D, d);
+        channel_load<1>(tile_at(p, b, tile) + p.D, c1, p.D, h1);
+        channel_load<1>(tile_at(p, b, tile) + 2 * (int64_t)p.D, c1, p.D, d1);
     } else {
-        state_load<VEC>(p, PK ? nullptr : p.h0, b, ln.c, h);
-        state_load<VEC>(p, PK ? nullptr : p.dhT, b, ln.c, d);
+        state_load<1>(p, PK ? nullptr : p.h0, b, c1, h1);
+        state_load<1>(p, PK ? nullptr : p.dhT, b, c1, d1);
     }
     if (tile == 0) pass_empty(p, PK, b, group * kGlrCols, p.dhT, p.dh0);
     Span span;
@@ -279,35 +250,20 @@ __global__ void __launch_bounds__(64 * kGbWaves, 4) glr_backward_kernel(GlrParam
 #pragma unroll
         for (int e = 0; e < VEC; ++e) H[e] = n[e];
     }
-    Moves<VEC> beside;
-    float before[VEC], after[VEC];
-    join_wave_both<PK, VEC>(m, H, E, beside, before, after);
-    if (ln.tg == 0) {
-#pragma unroll
-        for (int e = 0; e < VEC; ++e) {
-            lds[0][w][ln.local() + e] = pack_move<PK>(m.P[e], m.C[e]);
-            lds[1][w][ln.local() + e] = H[e];
-            lds[2][w][ln.local() + e] = E[e];
-        }
-    }
+    const WaveRun run = join_wave<PK, VEC, true>(m, H, E);
+    lds[0][w][l] = pack_move<PK>(run.P, run.C);
+    lds[1][w][l] = run.H;
+    lds[2][w][l] = run.E;
     lds_barrier();
 #pragma unroll
     for (int j = 0; j < NW - 1; ++j) {
         const int q = NW - 1 - j;
-#pragma unroll
-        for (int e = 0; e < VEC; ++e) {
-            if (j < w) h[e] = packed_move<PK>(lds[0][j][ln.local() + e], h[e], lds[1][j][ln.local() + e]);
-            if (q > w) d[e] = packed_move<PK>(lds[0][q][ln.local() + e], d[e], lds[2][q][ln.local() + e]);
-        }
+        if (j < w) h1[0] = packed_move<PK>(lds[0][j][l], h1[0], lds[1][j][l]);
+        if (q > w) d1[0] = packed_move<PK>(lds[0][q][l], d1[0], lds[2][q][l]);
     }
-    if constexpr (ln.kTG == 2) {
-#pragma unroll
-        for (int e = 0; e < VEC; ++e) {
-            const float hn = move<PK>(beside.P[e], beside.C[e], h[e], before[e]), dn = move<PK>(beside.P[e], beside.C[e], d[e], after[e]);
-            h[e] = ln.tg ? hn : h[e];
-            d[e] = ln.tg ? d[e] : dn;
-        }
-    }
+    float h[VEC], d[VEC];
+    spread_state<PK, VEC>(run, h1[0], h);
+    spread_behind<PK, VEC>(run, d1[0], d);
     // the state in front of every token
     float prev[L][VEC];
 #pragma unroll
@@ -324,52 +280,54 @@ __global__ void __launch_bounds__(64 * kGbWaves, 4) glr_backward_kernel(GlrParam
     float sb[VEC], sr[VEC];
 #pragma unroll
     for (int e = 0; e < VEC; ++e) sb[e] = sr[e] = 0.f;
+    auto walk = [&](auto some) {
 #pragma unroll
-    for (int i = L - 1; i >= 0; --i) {
-        float dx[VEC], dg[VEC];
-        const bool ok = !odd || (marks.valid >> i & 1);       // (uniformly true in most tiles)
+        for (int i = L - 1; i >= 0; --i) {
+            float dx[VEC], dg[VEC];
+            const bool ok = !some.value || (marks.valid >> i & 1);
 #pragma unroll
-        for (int e = 0; e < VEC; ++e) {
-            const float dh = dy[i][e] + d[e], out = a[i][e] * dh;
-            const float da = fmaf(out, prev[i][e], dh * x[i][e] * dk[i][e]);
-            dx[e] = dh * k[i][e];
-            dg[e] = da * slope[i][e];
-            // (what a token of no sequence has in front of it may be no number)
-            sb[e] += ok ? dg[e] : 0.f;
-            sr[e] -= ok ? da * sig[i][e] : 0.f;
-            d[e] = out;
-        }
-        rx.store(dx, i, ok);
-        rg.store(dg, i, ok);
-        if (odd && (marks.first >> i & 1)) {
-            if (p.dh0) state_store<VEC>(p, p.dh0, seq[i], ln.c, true, d);
-            if (PK) {
+            for (int e = 0; e < VEC; ++e) {
+                const float dh = dy[i][e] + d[e], out = a[i][e] * dh;
+                const float da = fmaf(out, prev[i][e], dh * x[i][e] * dk[i][e]);
+                dx[e] = dh * k[i][e];
+                dg[e] = da * slope[i][e];
+                // (what a token of no sequence has in front of it may be no number)
+                sb[e] += ok ? dg[e] : 0.f;
+                sr[e] -= ok ? da * sig[i][e] : 0.f;
+                d[e] = out;
+            }
+            rx.store(dx, i, ok);
+            rg.store(dg, i, ok);
+            if (some.value && (marks.first >> i & 1)) {
+                if (p.dh0) state_store<VEC>(p, p.dh0, seq[i], ln.c, true, d);
+                if (PK) {
 #pragma unroll
-                for (int e = 0; e < VEC; ++e) d[e] = 0.f;
+                    for (int e = 0; e < VEC; ++e) d[e] = 0.f;
+                }
             }
         }
-    }
+    };
+    if (odd)
+        walk(std::true_type());
+    else
+        walk(std::false_type());
     if (!p.grads) return;
     // the tile's sums, in a fixed order
     __syncthreads();
-#pragma unroll
-    for (int e = 0; e < VEC; ++e) {
-        if constexpr (ln.kTG == 2) {
-            sb[e] += other_half(sb[e]);
-            sr[e] += other_half(sr[e]);
-        }
-        if (ln.tg == 0) {
-            lds[0][w][ln.local() + e] = sb[e];
-            lds[1][w][ln.local() + e] = sr[e];
-        }
+    if constexpr (VEC == 2) {
+        swap_halves(sb[0], sb[1]);
+        swap_halves(sr[0], sr[1]);
+        sb[0] += sb[1];
+        sr[0] += sr[1];
     }
+    lds[0][w][l] = sb[0];
+    lds[1][w][l] = sr[0];
     __syncthreads();
-    const int which = threadIdx.x >> 6, l = lane_id(), c = group * kGlrCols + l;
-    if (which > 1 || c >= p.D) return;
+    if (w > 1 || c1 >= p.D) return;
     float s = 0.f;
 #pragma unroll
-    for (int j = 0; j < NW; ++j) s += lds[which][j][l];
-    p.part[(((int64_t)b * p.segs + tile) * 2 + which) * p.D + c] = s;
+    for (int j = 0; j < NW; ++j) s += lds[w][j][l];
+    p.part[(((int64_t)b * p.segs + tile) * 2 + w) * p.D + c1] = s;
 }
 
 namespace {

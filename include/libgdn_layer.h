@@ -324,7 +324,10 @@ gdn_status gdn_ssm_step(const gdn_ssm_problem *problem, const void *x, const voi
  * segments of the sequence the state moves as h - (1 - a) h, so that memories of
  * thousands of tokens keep their digits (final states of bf16 or fp32 inputs within 1e-6 of the
  * recurrence in 64 bits, of the vectors' norms).  A NaN or an infinity in a
- * token reaches the tokens behind it in its sequence and channel, no other.
+ * token reaches the tokens behind it in its sequence and channel, no other (an
+ * infinity as one or as a NaN: it may meet its own negative in the state's move).
+ * Gates above zero let the state grow; the products of a run's decays must stay
+ * finite too.
  * In the gradients c = sqrt(1 - a^2) has the derivative 0 by log a where a is 1.
  */
 #define GDN_GLR_LOG 0

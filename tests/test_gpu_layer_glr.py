@@ -136,6 +136,22 @@ def test_segments_and_long_memories(dt, gt, form, scale, memory):
         assert (hT.cpu().double() - ref).norm() <= 1e-6 * ref.norm()
 
 
+@pytest.mark.parametrize("lens,packed", [([9100], False), ([9100, 9100], False), ([3000, 0, 4100, 1, 1999], True)])
+@pytest.mark.parametrize("dt", [BF, F32])
+def test_segments_in_uneven_pieces(lens, packed, dt):
+    """Wide enough that a segment's move is put together from a few pieces of some tiles; the
+    recurrence of single channels is compared in some of them, the first and the last among them."""
+    B = 1 if packed else len(lens)
+    D = 4100 // B
+    d = inputs(B, sum(lens) if packed else lens[0], D, dt, dt, "sigmoid", n=len(lens), memory=500.0)
+    cu = torch.tensor([0] + lens).cumsum(0).to(torch.int32).to(DEV) if packed else None
+    y, hT = gdn.glr_forward(d["x"], d["gate"], d["h0"], gate_bias=d["gate_bias"], form="sigmoid", scale="complement", cu_seqlens=cu)
+    cols = [0, 1, 63, 64, 1027, D - 1]
+    ref = reference({k: v if v is None else v[..., cols] for k, v in d.items()}, lens, "sigmoid", "complement", grads=False)
+    close(y.flatten(0, 1)[:, cols], ref["y"], ref["y_err"], "y")
+    close(hT[:, cols], ref["hT"], ref["hT_err"], "hT")
+
+
 @pytest.mark.parametrize("lens", [[1], [0, 5], [5, 0, 0, 70, 1, 0, 300, 16, 2], [3] * 70, [0, 0, 0], [600, 1, 1, 1, 700, 0], [256, 256, 256, 128],
                                   [1300, 0, 2200]])
 @pytest.mark.parametrize("dt", [BF, F32])
