@@ -1,14 +1,14 @@
 // Gated linear recurrence, forward and step (see gdn_glr.h for the mathematics).
 //
 // Bound by memory where channels and sequences fill the chip (8 sequences of 8192
-// tokens, 4096 channels of bf16: 341 us, 4.7 TB/s, a copy's rate); a single long
+// tokens, 4096 channels of bf16: 346 us, 4.7 TB/s, near a copy's rate); a single long
 // sequence is cut into segments and its rows are read once more for their moves
-// (65536 tokens: 208 us, then 325).  Vector instructions come next: with the gate's
-// exponential, reciprocal, series and square root some 36 an element (rate, norm) or 24 (sigmoid,
-// complement), which keep the units busy for 0.75 and 0.5 of the time.  16384 packed
-// tokens of 4096 channels, rate and norm: 71 us the moves, 101 us y.  Eight waves of 16
-// tokens a thread and one workgroup a CU; four waves and 512 workgroups 556 against 536 us
-// (65536 tokens), 8 tokens a thread 580, 16 waves 619.
+// (65536 tokens: 173 us, 4.6 TB/s, then 323, 5.0 TB/s).  Vector instructions come next: with the
+// gate's exponential, reciprocal, series and square root some 24 an element (rate, norm) or
+// 19 (sigmoid, complement), which keep the units busy for half of the time.  16384 packed
+// tokens of 4096 channels, rate and norm: 64 us the moves, 93 us y.  Eight waves of 16
+// tokens a thread and one workgroup a CU (before the moves had pieces: four waves and 512
+// workgroups 556 against 536 us for 65536 tokens, 8 tokens a thread 580, 16 waves 619).
 #include <algorithm>
 
 #include "gdn_glr.h"
