@@ -323,8 +323,17 @@ __global__ void __launch_bounds__(1024) norm_sums_kernel(SumsParams p) {
 }
 
 gdn_status enqueue_norm_sums(const float *part, float *dw, float *db, int64_t D, int64_t rows, int64_t classes, hipStream_t s) {
-    SumsParams sp{part, dw, db, D, rows, (D + kSumCols - 1) / kSumCols};
-    return launch_kernel((const void *)&norm_sums_kernel, (int)(classes * sp.cols * ((dw != nullptr) + (db != nullptr))), &sp, s, 1024);
+    const int64_t cols = (D + kSumCols - 1) / kSumCols, both = (dw != nullptr) + (db != nullptr);
+    if (!both) return GDN_OK;
+    // (as many launches as classes need, of under 2^32 threads)
+    const int64_t step = (((int64_t)1 << 32) - 1) / 1024 / (cols * both);
+    for (int64_t c = 0; c < classes; c += step) {
+        const int64_t n = classes - c < step ? classes - c : step;
+        SumsParams sp{part + c * rows * 2 * D, dw ? dw + c * D : nullptr, db ? db + c * D : nullptr, D, rows, cols};
+        const gdn_status st = launch_kernel((const void *)&norm_sums_kernel, (int)(n * cols * both), &sp, s, 1024);
+        if (st != GDN_OK) return st;
+    }
+    return GDN_OK;
 }
 
 namespace {

@@ -162,7 +162,7 @@ inline gdn_status check_norm(const gdn_norm_problem *pr) {
 }
 
 // dw[c][j] and db[c][j] (either may be NULL) = the sums over the rows i of part [classes][rows][2][D], in
-// a fixed order.  One launch.
+// a fixed order.  One launch (for every 2^22 workgroups: D columns in sixteens, of each class and of dw and db).
 gdn_status enqueue_norm_sums(const float *part, float *dw, float *db, int64_t D, int64_t rows, int64_t classes, hipStream_t s);
 
 }  // namespace gdn

@@ -162,7 +162,7 @@ gdn_status gdn_gate_norm_forward(const gdn_gate_norm_problem *problem, const voi
  * (or NULL; without center it must be NULL).  The norm is formed again from x and
  * z.  bias: as in the forward pass (dz reads it).  Workspace:
  * gdn_workspace_bytes_gate_norm_backward(problem) bytes, 16-byte aligned.  Two
- * launches.
+ * launches (more from H D = 2^25 on, with weights of each head).
  */
 gdn_status gdn_gate_norm_backward(const gdn_gate_norm_problem *problem, const void *dy, const void *x,
                                   const void *z, const void *weight, const void *bias, void *dx,

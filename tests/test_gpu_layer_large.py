@@ -1,0 +1,41 @@
+"""The layer norm, gated norm and gated linear recurrence at sizes whose launches, rows or
+offsets pass 32 bits, against the definitions in 64 bits at some places of them."""
+import pytest
+
+torch = pytest.importorskip("torch")
+
+import chunked_gated_delta_prepare_amd as gdn
+from oracle import layer as L
+
+pytestmark = pytest.mark.gpu
+DEV = "cuda:0"
+BF, F32 = torch.bfloat16, torch.float32
+HALF = {BF: 2.0 ** -8, F32: 2.0 ** -24}
+ARITH = 2.0 ** -18          # of a row's terms, as in test_gpu_layer_norms.py
+
+
+def normal(*shape, seed, dtype=BF):
+    return torch.empty(*shape, device=DEV, dtype=dtype).normal_(generator=torch.Generator(device=DEV).manual_seed(seed))
+
+
+def close(got, ref, tol, what):
+    d = (got.detach().cpu().double() - ref).abs()
+    bad = ~(d <= tol)
+    assert not bad.any(), "%s: %d of %d off, worst %.3e over its tolerance" % (what, int(bad.sum()), bad.numel(),
+                                                                               float((d - tol).max()))
+
+
+def test_gate_norm_sums_of_many_wide_heads():
+    """2^25 weights and as many biases: the sums take two launches, whose border is among
+    the heads compared (each is summed on its own: two rows, so one addition)."""
+    T, H, D = 2, 4096, 8192
+    x, z, dy = (normal(T, H, D, seed=i) for i in range(3))
+    w, b = normal(H, D, seed=4), normal(H, D, seed=5)
+    dx, dz, dw, db = gdn.gate_norm_backward(dy, x, z, w, b, center=True)
+    at = [0, 1, 2047, H - 3, H - 2, H - 1]
+    ref = L.gate_norm(x[:, at], z[:, at], w[at], b[at], 1e-5, "silu", False, True, dy[:, at])
+    close(dx[:, at], ref["dx"], ref["dx"].abs() * HALF[BF] + ref["dxsize"] * ARITH, "dx")
+    close(dz[:, at], ref["dz"], ref["dz"].abs() * HALF[BF] + ref["dzsize"] * ARITH, "dz")
+    close(dw[at], ref["dw"], ref["dwsize"] * ARITH, "dw")
+    close(db[at], ref["db"], ref["dbsize"] * ARITH, "db")
+    assert db[:, ::97].any(1).all() and dw[:, ::97].any(1).all()
