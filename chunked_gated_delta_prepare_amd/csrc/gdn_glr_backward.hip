@@ -118,15 +118,17 @@ __global__ void __launch_bounds__(64 * kGbWaves) glr_tiles_kernel(GlrParams p) {
 }
 
 // H -> the h in front of a tile, E -> the e behind it: 64 channels and one
-// direction a workgroup.  Each of its 16 waves has a share of the tiles: its
-// move first, then, from the state at its border, its tiles'.
+// direction a workgroup.  Each of its waves (16, or one a tile if they are fewer: many short
+// sequences need many workgroups) has a share of the tiles: its move first, then, from the
+// state at its border, its tiles'.
+constexpr int kGsWaves = 16;
 template <bool PK>
-__global__ void __launch_bounds__(1024) glr_states_kernel(GlrParams p) {
-    __shared__ float lds_p[16][kGlrCols], lds_c[16][kGlrCols], lds_h[16][kGlrCols];
+__global__ void __launch_bounds__(64 * kGsWaves) glr_states_kernel(GlrParams p) {
+    __shared__ float lds_p[kGsWaves][kGlrCols], lds_c[kGsWaves][kGlrCols], lds_h[kGsWaves][kGlrCols];
     const int back = blockIdx.x & 1, rest = blockIdx.x >> 1, group = rest % p.groups, b = rest / p.groups;
     const int w = wave_id(), l = lane_id(), c = group * kGlrCols + l;
     const bool live = c < p.D;
-    const int share = (p.segs + 15) / 16, n0 = w * share, n1 = n0 + share < p.segs ? n0 + share : p.segs;
+    const int waves = blockDim.x / 64, share = (p.segs + waves - 1) / waves, n0 = w * share, n1 = n0 + share < p.segs ? n0 + share : p.segs;
     // tile i of this direction's order
     auto at = [&](int i) { return tile_at(p, b, back ? p.segs - 1 - i : i) + (live ? c : 0); };
     const int64_t from = (int64_t)(1 + back) * p.D;
@@ -392,6 +394,7 @@ gdn_status gdn_glr_backward(const gdn_glr_problem *pr, const void *dy, const voi
                                  {pr->x_stride_b, pr->x_stride_t, pr->g_stride_b, pr->g_stride_t, pr->dy_stride_b, pr->dy_stride_t,
                                   pr->dx_stride_b, pr->dx_stride_t, pr->dg_stride_b, pr->dg_stride_t});
     const int64_t tiles = glr_tiles(pr, pairs);
+    // (the states' launch, of two waves or fewer for every tile, is the smaller one)
     if (!grid_ok(tiles * pr->B, (int64_t)gp.groups * 64 * kGbWaves)) return GDN_ERR_UNSUPPORTED;
     gp.dy = dy;
     gp.x = x;
@@ -413,7 +416,7 @@ gdn_status gdn_glr_backward(const gdn_glr_problem *pr, const void *dy, const voi
         st = launch_kernel(cu_seqlens ? glr_back_pick<true>(pr, pairs, true) : glr_back_pick<false>(pr, pairs, true), grid, &gp, s, 64 * kGbWaves);
         if (st != GDN_OK) return st;
         st = launch_kernel(cu_seqlens ? (const void *)&glr_states_kernel<true> : (const void *)&glr_states_kernel<false>,
-                           (int)(2 * pr->B * gp.groups), &gp, s, 1024);
+                           (int)(2 * pr->B * gp.groups), &gp, s, 64 * (int)(tiles < kGsWaves ? tiles : kGsWaves));
         if (st != GDN_OK) return st;
     }
     st = launch_kernel(cu_seqlens ? glr_back_pick<true>(pr, pairs, false) : glr_back_pick<false>(pr, pairs, false), grid, &gp, s, 64 * kGbWaves);

@@ -39,3 +39,22 @@ def test_gate_norm_sums_of_many_wide_heads():
     close(dw[at], ref["dw"], ref["dwsize"] * ARITH, "dw")
     close(db[at], ref["db"], ref["dbsize"] * ARITH, "db")
     assert db[:, ::97].any(1).all() and dw[:, ::97].any(1).all()
+
+
+def test_gradients_of_very_many_short_sequences():
+    """2^21 sequences of 33 tokens of one channel: each is what it is in a batch of few (the same
+    tiles and runs, so the same bits)."""
+    B, T, D = 1 << 21, 33, 1
+    x, dy = normal(B, T, D, seed=1), normal(B, T, D, seed=2)
+    gate, h0 = normal(B, T, D, seed=3), normal(B, D, seed=4, dtype=F32)
+    kw = dict(rate=torch.full((D,), 0.1, device=DEV), form="rate", scale="norm")
+    dhT = normal(B, D, seed=5, dtype=F32)
+    dx, dg, _, _, dh0 = gdn.glr_backward(dy, x, gate, h0, dhT, **kw)
+    for at in (slice(0, 5), slice(B // 2 - 3, B // 2 + 3), slice(B - 5, B)):
+        dx1, dg1, _, _, dh1 = gdn.glr_backward(dy[at], x[at], gate[at], h0[at], dhT[at], **kw)
+        for a, b in ((dx, dx1), (dg, dg1), (dh0, dh1)):
+            assert torch.equal(a[at], b)
+    n = 5
+    ref = L.glr(x[-n:].flatten(0, 1), gate[-n:].flatten(0, 1), None, kw["rate"], h0[-n:], [T] * n, "rate", "norm", dy[-n:].flatten(0, 1), dhT[-n:])
+    for v, name in ((dx[-n:].flatten(0, 1), "dx"), (dg[-n:].flatten(0, 1), "dgate"), (dh0[-n:], "dh0")):
+        close(v, ref[name], ref[name + "_err"] + ref[name].abs() * HALF[v.dtype] + 2.0 ** -120, name)

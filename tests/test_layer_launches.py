@@ -96,3 +96,32 @@ def test_sums_of_the_weights_gradients(launches):
             done += classes
         assert done == H
     assert len(found[-1][1]) == 2
+
+
+def glr(name, B, T, D, io=1, grads=True):
+    pr = dict(B=B, T=T, D=D, n_seqs=0, io_dtype=io, g_dtype=io, form=2, scale=2)
+    for k in ("x", "g", "dy", "dx", "dg"):
+        pr[k + "_stride_b"], pr[k + "_stride_t"] = T * D, D
+    if name == "gdn_glr_forward":
+        args = [FAKE] * 5 + [None, FAKE, FAKE, FAKE, BIG]
+    else:
+        args = [FAKE] * 6 + [None] + [FAKE] * 3 + [FAKE if grads else None] * 2 + [FAKE, FAKE, BIG]
+    return name, "GlrProblem", pr, args
+
+
+def test_gradients_of_very_many_short_sequences(launches):
+    """Two to seven tiles of 32 tokens a sequence: the launch of the states at the tiles' borders
+    has no more threads than the tiles'."""
+    sizes = [(1 << 21, 33, 1), (1 << 22, 33, 64), ((1 << 23) - 1, 33, 64), (1 << 21, 224, 64), (1 << 15, 513, 640), (2, 8192, 4096)]
+    found = launches([glr("gdn_glr_backward", *s) for s in sizes])
+    assert small(found)
+    for (B, T, D), (status, calls) in zip(sizes, found):
+        tiles, groups = -(-T // 32), -(-D // 64)
+        if B * D >= 1 << 29 or tiles * B * groups * 256 >= 1 << 32:
+            assert status == 3 and not calls
+            continue
+        assert status == 0 and [c[:2] for c in calls[:3]] == [[tiles * B * groups, 256], [2 * B * groups, 64 * min(tiles, 16)],
+                                                              [tiles * B * groups, 256]]
+    # whatever is enqueued is enqueued whole
+    found = launches([glr("gdn_glr_backward", 1 << k, T, 1) for k in range(19, 25) for T in (1, 32, 33, 64, 65, 97, 225, 481, 513)])
+    assert small(found) and all((status == 0) == bool(calls) for status, calls in found)
