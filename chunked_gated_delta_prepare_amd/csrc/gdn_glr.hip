@@ -398,7 +398,19 @@ gdn_status gdn_glr_forward(const gdn_glr_problem *pr, const void *x, const void 
     const GlrPlan s = glr_plan(pr);
     GlrParams gp;
     fill_glr(pr, gp, cu_seqlens);
-    if (!grid_ok(s.segs * s.pieces * pr->B, (int64_t)gp.groups * 64 * kGlrWaves)) return GDN_ERR_UNSUPPORTED;
+    const bool pairs = glr_pairs(pr, {x, y}, {gate}, {pr->x_stride_b, pr->x_stride_t, pr->g_stride_b, pr->g_stride_t});
+    const int64_t wgs = pr->B * gp.groups;
+    // A workgroup of eight waves fills a CU, so sequences that do not fill its tile are waited
+    // for one after the other: one wave for up to 64 tokens (or a single run of each thread), four
+    // for up to 512, where there are workgroups enough.  4096 channels of bf16: 256 sequences of 16 tokens
+    // 338 us with eight waves, 35 with one; 64 of 4 tokens 85 and 11; 64 of 100 tokens 90 with eight, 35 with
+    // four, of 512 tokens (32 sequences) 95 and 90.
+    const int which = cu_seqlens                                                         ? kForward
+                      : pr->T <= (pairs ? kGlrTile<2, 1> : kGlrTile<1, 1>) || (pr->T <= 64 && wgs >= 512) ? kShort
+                      : pr->T <= 512 && wgs >= 1024                                      ? kMany
+                                                                                         : kForward;
+    const int waves = which == kShort ? 1 : which == kMany ? 4 : kGlrWaves;
+    if (!grid_ok(s.segs * s.pieces * pr->B, (int64_t)gp.groups * 64 * waves)) return GDN_ERR_UNSUPPORTED;
     const size_t need = (size_t)glr_bytes(pr, s);
     if (need && (!workspace || workspace_bytes < need)) return GDN_ERR_WORKSPACE;
     if (!aligned_to(workspace, 16)) return GDN_ERR_ALIGNMENT;
@@ -413,23 +425,11 @@ gdn_status gdn_glr_forward(const gdn_glr_problem *pr, const void *x, const void 
     gp.segs = (int)s.segs;
     gp.seg_len = (int)s.seg_len;
     gp.pieces = (int)s.pieces;
-    const bool pairs = glr_pairs(pr, {x, y}, {gate}, {pr->x_stride_b, pr->x_stride_t, pr->g_stride_b, pr->g_stride_t});
-    const int64_t wgs = pr->B * gp.groups;
     if (s.segs > 1) {
         st = launch_kernel(cu_seqlens ? glr_pick<true>(pr, pairs, kMoves) : glr_pick<false>(pr, pairs, kMoves), (int)(wgs * (s.segs - 1) * s.pieces), &gp,
                            (hipStream_t)stream, 64 * kGlrWaves);
         if (st != GDN_OK) return st;
     }
-    // A workgroup of eight waves fills a CU, so sequences that do not fill its tile are waited
-    // for one after the other: one wave for up to 64 tokens (or a single run of each thread), four
-    // for up to 512, where there are workgroups enough.  4096 channels of bf16: 256 sequences of 16 tokens
-    // 338 us with eight waves, 35 with one; 64 of 4 tokens 85 and 11; 64 of 100 tokens 90 with eight, 35 with
-    // four, of 512 tokens (32 sequences) 95 and 90.
-    const int which = cu_seqlens                                                         ? kForward
-                      : pr->T <= (pairs ? kGlrTile<2, 1> : kGlrTile<1, 1>) || (pr->T <= 64 && wgs >= 512) ? kShort
-                      : pr->T <= 512 && wgs >= 1024                                      ? kMany
-                                                                                         : kForward;
-    const int waves = which == kShort ? 1 : which == kMany ? 4 : kGlrWaves;
     return launch_kernel(cu_seqlens ? glr_pick<true>(pr, pairs, which) : glr_pick<false>(pr, pairs, which), (int)(wgs * s.segs), &gp,
                          (hipStream_t)stream, 64 * waves);
 }

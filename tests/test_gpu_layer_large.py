@@ -58,3 +58,19 @@ def test_gradients_of_very_many_short_sequences():
     ref = L.glr(x[-n:].flatten(0, 1), gate[-n:].flatten(0, 1), None, kw["rate"], h0[-n:], [T] * n, "rate", "norm", dy[-n:].flatten(0, 1), dhT[-n:])
     for v, name in ((dx[-n:].flatten(0, 1), "dx"), (dg[-n:].flatten(0, 1), "dgate"), (dh0[-n:], "dh0")):
         close(v, ref[name], ref[name + "_err"] + ref[name].abs() * HALF[v.dtype] + 2.0 ** -120, name)
+
+
+def test_very_many_short_prompts():
+    """2^23 prompts of two tokens, a wave each: each is what it is among few (the same runs, so the
+    same bits), and the recurrence in 64 bits."""
+    B, T, D = 1 << 23, 2, 3
+    x, gate, h0 = normal(B, T, D, seed=1), normal(B, T, D, seed=3), normal(B, D, seed=4, dtype=F32)
+    kw = dict(form="sigmoid", scale="complement")
+    y, hT = gdn.glr_forward(x, gate, h0, **kw)
+    n = 5
+    for at in (slice(0, n), slice(B // 2 - n, B // 2), slice(B - n, B)):
+        y1, h1 = gdn.glr_forward(x[at], gate[at], h0[at], **kw)
+        assert torch.equal(y[at], y1) and torch.equal(hT[at], h1)
+        ref = L.glr(x[at].flatten(0, 1), gate[at].flatten(0, 1), None, None, h0[at], [T] * n, "sigmoid", "complement")
+        close(y1.flatten(0, 1), ref["y"], ref["y_err"] + ref["y"].abs() * HALF[BF] + 2.0 ** -120, "y")
+        close(h1, ref["hT"], ref["hT_err"] + ref["hT"].abs() * HALF[F32] + 2.0 ** -120, "hT")

@@ -125,3 +125,16 @@ def test_gradients_of_very_many_short_sequences(launches):
     # whatever is enqueued is enqueued whole
     found = launches([glr("gdn_glr_backward", 1 << k, T, 1) for k in range(19, 25) for T in (1, 32, 33, 64, 65, 97, 225, 481, 513)])
     assert small(found) and all((status == 0) == bool(calls) for status, calls in found)
+
+
+def test_very_many_short_prompts(launches):
+    """A wave for each of 2^24 prompts of some tokens, four waves for 2^23 of some more; with
+    eight waves each the launch would be too large, and is refused."""
+    sizes = [(1 << 24, 16, 1, 64), (1 << 23, 64, 63, 64), (1 << 23, 200, 1, 256), (1 << 23, 513, 1, 0), ((1 << 23) - 1, 513, 1, 512), (1, 37, 1030, 512)]
+    found = launches([glr("gdn_glr_forward", B, T, D) for B, T, D, _ in sizes])
+    assert small(found)
+    for (B, T, D, threads), (status, calls) in zip(sizes, found):
+        if not threads:
+            assert status == 3 and not calls
+        else:
+            assert status == 0 and [c[:2] for c in calls] == [[B * -(-D // 64), threads]]
