@@ -134,7 +134,8 @@ __device__ __forceinline__ void store_row_e4m3(rsrc_t ry, float *scales, bool li
         __syncthreads();
 #pragma unroll
         for (int k = 0; k < K; ++k) {
-            const float m = lanes_max<64>(fabsf(y[k][0]));
+            // (the larger with zero: a wave of NaN alone has none to leave out)
+            const float m = fmaxf(lanes_max<64>(fabsf(y[k][0])), 0.f);
             const int gi = (k * TPR + tid) >> 7;
             if (lane_id() == 0) atomicMax(&gmax[gi], __float_as_uint(m));
         }
