@@ -126,7 +126,10 @@ template <int SCALE>
 __device__ __forceinline__ float input_scale(float a, float c) {
     return SCALE == GDN_GLR_PLAIN ? 1.f : SCALE == GDN_GLR_COMPLEMENT ? c : __builtin_amdgcn_sqrtf(fmaf(c, a, c));
 }
-// The factor k and its derivative by log a, which is taken as 0 where a is 1.
+// The factor k and its derivative by log a.  Both are 0 where 1 - a^2 is below fp32's
+// normal numbers: the root's instruction, and its reciprocal's, take those for zero, and the
+// reciprocal would be infinite.  (Scaled by 2^64 and back they are right down to the
+// least denormal number, for 3 % of the time of the packed rows' forward pass.)
 template <int SCALE>
 __device__ __forceinline__ void input_slope(float a, float c, float &k, float &dk) {
     k = 1.f;
@@ -136,7 +139,7 @@ __device__ __forceinline__ void input_slope(float a, float c, float &k, float &d
         dk = -a;
     }
     if constexpr (SCALE == GDN_GLR_NORM) {
-        const float q = fmaf(c, a, c), r = q == 0.f ? 0.f : __builtin_amdgcn_rsqf(q);
+        const float q = fmaf(c, a, c), r = fabsf(q) < 0x1p-126f ? 0.f : __builtin_amdgcn_rsqf(q);
         k = q * r;
         dk = -a * a * r;
     }

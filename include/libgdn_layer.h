@@ -328,7 +328,8 @@ gdn_status gdn_ssm_step(const gdn_ssm_problem *problem, const void *x, const voi
  * infinity as one or as a NaN: it may meet its own negative in the state's move).
  * Gates above zero let the state grow; the products of a run's decays must stay
  * finite too.
- * In the gradients c = sqrt(1 - a^2) has the derivative 0 by log a where a is 1.
+ * A sigmoid below 2^-126 is taken as 0, and so is c = sqrt(1 - a^2) where 1 - a^2 is below 2^-126;
+ * its derivative by log a is 0 there.
  */
 #define GDN_GLR_LOG 0
 #define GDN_GLR_SIGMOID 1

@@ -56,3 +56,74 @@ def test_a_nan_does_not_enter_the_scale(D, first, n, centered, group):
     u = ref / full
     # half a step of e4m3, whose subnormals are 2^-9 apart
     close(got, u, u.abs() * (2.0 ** -4 + ARITH) + 2.0 ** -10 + size / full, "q")
+
+
+# ---------------------------------------------------------------------------
+# gated linear recurrence
+# ---------------------------------------------------------------------------
+
+HALF = {BF: 2.0 ** -8, F32: 2.0 ** -24}
+TINY = 2.0 ** -120
+
+
+def glr_close(got, ref, names):
+    for name, v in zip(names, got):
+        if v is not None:
+            r = ref[name]
+            close(v.reshape(r.shape), r, ref[name + "_err"] + r.abs() * HALF[v.dtype] + TINY, name)
+
+
+@pytest.mark.parametrize("dt,gt", [(BF, BF), (BF, F32), (F32, F32)])
+@pytest.mark.parametrize("D", [64, 65])
+@pytest.mark.parametrize("scale", [None, "complement", "norm"])
+def test_decays_next_to_one(dt, gt, D, scale):
+    """Log decays down to the least denormal number (log sigmoid of 88 and more is one): 1 - a is
+    the gate itself, sqrt(1 - a^2) = sqrt(-2 gate), its derivative -1 / sqrt(-2 gate); from
+    1 - a^2 < 2^-126 on both are 0, as for a gate of 0.  Each tolerance is the oracle's, relative
+    errors of fp32."""
+    T = 40
+    sizes = [0.0, 1e-36, 1e-37, 2.0 ** -126, 2.0 ** -127, 1e-38, 1e-39, 8e-40, 2.0 ** -133, 0.0]
+    gate = -torch.tensor([[sizes[(t + c) % 10] if t % 13 else 0.1 for c in range(D)] for t in range(T)]).to(gt).to(DEV)[None]
+    if gt == F32:
+        gate[0, 7] = -2.0 ** -149
+    taken = gate if scale != "norm" else torch.where(gate > -2.0 ** -127, torch.zeros_like(gate), gate)
+    x, dy = rnd(1, T, D, seed=1, dtype=dt), rnd(1, T, D, seed=2, dtype=dt)
+    for h0 in (rnd(1, D, seed=3), None):
+        dhT = None if h0 is None else rnd(1, D, seed=4)
+        y, hT = gdn.glr_forward(x, gate, h0, scale=scale)
+        grads = gdn.glr_backward(dy, x, gate, h0, dhT, scale=scale)
+        ref = L.glr(x[0], taken[0], None, None, h0, [T], "log", scale, dy[0], dhT)
+        glr_close((y, hT, *grads), ref, ("y", "hT", "dx", "dgate", "dbias", "drate", "dh0"))
+    # from nothing: the inputs alone, whose factors are as small as 2^-63
+    first = gate[0, 1:11].contiguous()
+    state, one = torch.zeros(10, D, device=DEV), x[0, 1:11]
+    y = gdn.glr_step(one, first, state, scale=scale)
+    ref = L.glr(one, taken[0, 1:11], None, None, None, [1] * 10, "log", scale)
+    glr_close((y, state), ref, ("y", "hT"))
+
+
+def test_rates_of_far_gates():
+    """log a = -rate sigmoid(v) with v as far as -82, rate sigmoid(v) >= 2^-125: one token from
+    nothing.  The sigmoid is good to 2 |v| units of 2^-24; the factor takes half of that, the
+    gates' gradients no more than all of it: 2^-16, and 2^-15 with every other rounding."""
+    D, V = 64, [-60.0, -70.0, -80.0, -81.0, -82.0]
+    B = len(V)
+    gate = torch.tensor(V, device=DEV)[:, None, None].expand(B, 1, D).contiguous()
+    rate = torch.linspace(0.02, 0.1, D, device=DEV)
+    x, dy = rnd(B, 1, D, seed=1), rnd(B, 1, D, seed=2)
+    s = torch.sigmoid(gate.cpu().double())
+    r, xd, d = rate.cpu().double(), x.cpu().double(), dy.cpu().double()
+    assert float((r * s).min()) >= 2.0 ** -125
+    c = -torch.expm1(-r * s)
+    k = torch.sqrt(c * (2 - c))
+    y, hT = gdn.glr_forward(x, gate, rate=rate, form="rate", scale="norm")
+    dx, dg, _, dr, _ = gdn.glr_backward(dy, x, gate, rate=rate, form="rate", scale="norm")
+    da = -d * xd * (1 - c).square() / k
+    for v, want, what in ((y, k * xd, "y"), (hT, (k * xd)[:, 0], "hT"), (dx, k * d, "dx"), (dg, -da * r * s * (1 - s), "dgate")):
+        close(v, want, want.abs() * 2.0 ** -15, what)
+    close(dr, -(da * s).sum((0, 1)), (da * s).abs().sum((0, 1)) * 2.0 ** -15, "drate")
+    # farther: rate sigmoid(v) is a denormal number or 0, every result smaller than the root of 2^-126 times |x| or |dy| < 8
+    gate = torch.tensor([-85.0, -86.0, -87.0, -88.0, -200.0], device=DEV)[:, None, None].expand(B, 1, D).contiguous()
+    y, hT = gdn.glr_forward(x, gate, rate=rate, form="rate", scale="norm")
+    for t in (y, hT, *gdn.glr_backward(dy, x, gate, rate=rate, form="rate", scale="norm")):
+        assert t is None or (t.abs() < 2.0 ** -54).all()
