@@ -43,6 +43,12 @@ struct GlrParams {
     int grads;                                               // whether dbias or drate is wanted
 };
 
+// A lane's VEC channel weights (fp32), zero without any.
+template <int VEC>
+__device__ __forceinline__ void channel_load(const float *w, int c, int D, float (&x)[VEC]) {
+    row_load<float, VEC>(make_rsrc(w, w ? (uint32_t)D * 4 : 0), c, x);
+}
+
 // ---------------------------------------------------------------------------
 // gates
 // ---------------------------------------------------------------------------
@@ -77,26 +83,37 @@ __device__ __forceinline__ void decay_of(float y, float &a, float &c) {
 // below 1/8 in all channels of a wave, as gates of long memories have it).
 enum { kLog = GDN_GLR_LOG, kSigmoid = GDN_GLR_SIGMOID, kRate = GDN_GLR_RATE };
 
-// The bias as gate_of takes it: for a sigmoid's exponent.
+// A channel's bias, for a sigmoid as its exponent takes it: in units of it, rounded, and
+// what 2^-(that rounding) is.  Without it the sigmoid would be off by |bias| units where
+// gate and bias cancel.
+struct GateBias {
+    float b, fix;
+};
 template <int FORM, int VEC>
-__device__ __forceinline__ void scale_bias(float (&bias)[VEC]) {
-    if constexpr (FORM != kLog) {
+__device__ __forceinline__ void load_bias(const float *w, int c, int D, GateBias (&bias)[VEC]) {
+    float b[VEC];
+    channel_load<VEC>(w, c, D, b);
 #pragma unroll
-        for (int e = 0; e < VEC; ++e) bias[e] *= -kLog2e;
+    for (int e = 0; e < VEC; ++e) {
+        const float t = b[e] * -kLog2e;
+        bias[e].b = FORM == kLog ? b[e] : t;
+        // (nothing to put back for an infinite one)
+        bias[e].fix = fabsf(t) < 0x1p100f ? fmaf(fmaf(b[e], -kLog2e, -t), 0.693147181f, 1.f) : 1.f;
     }
 }
 
 // A token's decay a, c = 1 - a, and for the gradients d(log a)/d(gate) (slope) and the
-// gate's sigmoid (kRate).  The sigmoid s = 1 / (1 + e^-v) is good to its own last digits and |v| / 2
-// units more, o = 1 - s too: e^-v s where e^-v is below 1.
+// gate's sigmoid (kRate).  The sigmoid s = 1 / (1 + e^-v), v = gate + bias, and o = 1 - s are good to their
+// own last digits and |v| units of 2^-24 more, o as e^-v s where e^-v is below 1.
 template <int FORM, bool NEAR = false>
-__device__ __forceinline__ void gate_of(float g, float bias, float rate, float &a, float &c, float &slope, float &sig) {
+__device__ __forceinline__ void gate_of(float g, GateBias bias, float rate, float &a, float &c, float &slope, float &sig) {
     if constexpr (FORM == kLog) {
-        decay_of<false>(-(g + bias), a, c);
+        decay_of<false>(-(g + bias.b), a, c);
         slope = 1.f;
         sig = 0.f;
     } else {
-        const float e = fast_exp2(fmaf(g, -kLog2e, bias)), s = __builtin_amdgcn_rcpf(1.f + e), o = e < 1.f ? e * s : 1.f - s;
+        const float x = fast_exp2(fmaf(g, -kLog2e, bias.b)), e = x * bias.fix, s = __builtin_amdgcn_rcpf(fmaf(x, bias.fix, 1.f));
+        const float o = e < 1.f ? e * s : 1.f - s;
         if constexpr (FORM == kSigmoid) {
             a = s;
             c = o;
@@ -375,12 +392,6 @@ __device__ __forceinline__ void state_store(const GlrParams &p, float *s, int n,
 #pragma unroll
     for (int i = 0; i < VEC; ++i)
         bstore32(__float_as_uint(x[i]), r, ok && c + i < p.D ? ((uint32_t)n * p.D + c + i) * 4 : kNowhere, 0);
-}
-
-// A lane's VEC channel weights (fp32), zero without any.
-template <int VEC>
-__device__ __forceinline__ void channel_load(const float *w, int c, int D, float (&x)[VEC]) {
-    row_load<float, VEC>(make_rsrc(w, w ? (uint32_t)D * 4 : 0), c, x);
 }
 
 // A thread's rows of L tokens.

@@ -39,10 +39,10 @@ __global__ void __launch_bounds__(64 * NW, 2) glr_forward_kernel(GlrParams p) {
     if (t_begin < t_end) rows.fetch(p, b, t_begin, row, ln.c, t_begin + kTile <= p.T);
     // (states and moves between runs are of one channel a lane)
     const int l = lane_id(), c1 = group * kGlrCols + ln.one();
-    float bias[VEC], rate[VEC];
-    channel_load<VEC>(p.bias, ln.c, p.D, bias);
+    GateBias bias[VEC];
+    float rate[VEC];
+    load_bias<FORM, VEC>(p.bias, ln.c, p.D, bias);
     channel_load<VEC>(p.rate, ln.c, p.D, rate);
-    scale_bias<FORM, VEC>(bias);
     const bool near = near_rates<FORM, VEC>(rate);
     // (packed rows take initial states at their sequences' first tokens)
     float h = state_at(p, PK ? nullptr : p.h0, b, c1);
@@ -167,10 +167,10 @@ __global__ void __launch_bounds__(64 * kGlrWaves, 2) glr_moves_kernel(GlrParams 
     const GlrLane<VEC> ln(group);
     const int w = wave_id(), row = ln.tg * L;
     const int t_first = seg * p.seg_len + tile * kGlrTile<2> + w * share;
-    float bias[VEC], rate[VEC];
-    channel_load<VEC>(p.bias, ln.c, p.D, bias);
+    GateBias bias[VEC];
+    float rate[VEC];
+    load_bias<FORM, VEC>(p.bias, ln.c, p.D, bias);
     channel_load<VEC>(p.rate, ln.c, p.D, rate);
-    scale_bias<FORM, VEC>(bias);
     const bool near = near_rates<FORM, VEC>(rate);
     float P = 1.f, C = 0.f, S = 0.f;      // of one channel a lane
     RunRows<IO, GT, VEC, L> rows;
@@ -245,8 +245,8 @@ __global__ void __launch_bounds__(256) glr_step_kernel(GlrParams p) {
     float *h = p.state + s * p.D + c;
     const float x = io_traits<IO>::load((const IO *)p.x + b * p.xb + c), g = io_traits<GT>::load((const GT *)p.g + b * p.gb + c);
     float a, k, slope, sig;
-    float bias[1] = {p.bias ? p.bias[c] : 0.f};
-    scale_bias<FORM, 1>(bias);
+    GateBias bias[1];
+    load_bias<FORM, 1>(p.bias, c, p.D, bias);
     gate_of<FORM>(g, bias[0], p.rate ? p.rate[c] : 0.f, a, k, slope, sig);
     const float v = fmaf(a, *h, x * (p.scale == GDN_GLR_PLAIN ? 1.f : p.scale == GDN_GLR_COMPLEMENT ? k : input_scale<GDN_GLR_NORM>(a, k)));
     *h = v;

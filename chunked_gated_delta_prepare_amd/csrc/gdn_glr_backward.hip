@@ -48,10 +48,10 @@ __global__ void __launch_bounds__(64 * kGbWaves) glr_tiles_kernel(GlrParams p) {
     const bool full = t + kGbTile<VEC> <= p.T;
     rows.fetch(p, b, t, row, ln.c, full);
     fetch_dy<IO, VEC, L>(p, dyr, b, t, row, ln.c, full);
-    float bias[VEC], rate[VEC];
-    channel_load<VEC>(p.bias, ln.c, p.D, bias);
+    GateBias bias[VEC];
+    float rate[VEC];
+    load_bias<FORM, VEC>(p.bias, ln.c, p.D, bias);
     channel_load<VEC>(p.rate, ln.c, p.D, rate);
-    scale_bias<FORM, VEC>(bias);
     const bool near = near_rates<FORM, VEC>(rate);
     Span span;
     const Marks marks = marks_of<PK, L>(p, t + w * ln.kTG * L, ln.kTG * L, t0, span);
@@ -173,10 +173,10 @@ __global__ void __launch_bounds__(64 * kGbWaves, 4) glr_backward_kernel(GlrParam
     fetch_dy<IO, VEC, L>(p, dyr, b, t, row, ln.c, full);
     // (states and moves between runs are of one channel a lane)
     const int l = lane_id(), c1 = group * kGlrCols + ln.one();
-    float bias[VEC], rate[VEC], h1[1], d1[1];
-    channel_load<VEC>(p.bias, ln.c, p.D, bias);
+    GateBias bias[VEC];
+    float rate[VEC], h1[1], d1[1];
+    load_bias<FORM, VEC>(p.bias, ln.c, p.D, bias);
     channel_load<VEC>(p.rate, ln.c, p.D, rate);
-    scale_bias<FORM, VEC>(bias);
     const bool near = near_rates<FORM, VEC>(rate);
     if (p.segs > 1) {
         channel_load<1>(tile_at(p, b, tile) + p.D, c1, p.D, h1);
