@@ -970,21 +970,19 @@ def _token_rows_apart(dx, dgate):
     B, T, D = dx.shape
     if not dx.numel():
         return
-    (xb, xt), (gb, gt) = _strides(dx, "dx"), _strides(dgate, "dgate")
-    for (sb, st), name in (((xb, xt), "dx"), ((gb, gt), "dgate")):
-        if T > 1 and st < D or B > 1 and sb < (T - 1) * st + D:
-            raise ValueError("%s's rows must not overlap" % name)
+    at, to = _strides(dx, "dx"), _strides(dgate, "dgate")
+    _apart_rows(T, B, D, at[1], at[0], "dx")
+    _apart_rows(T, B, D, to[1], to[0], "dgate")
     (a, a1), (b, b1) = _span(dx), _span(dgate)
     if a1 <= b or b1 <= a:
         return
-    # rows side by side in one buffer
-    size = dx.element_size()
-    apart = abs(b - a) // size
-    first = a if a < b else b
-    end = max(a, b) - first + D * size
-    if dx.dtype is dgate.dtype and (T == 1 or xt == gt) and (B == 1 or xb == gb) and apart >= D and (T == 1 or end <= xt * size) \
-            and (B == 1 or end + (T - 1) * xt * size <= xb * size):
-        return
+    # parts of one buffer: rows at the same strides, of which no two are nearer than D
+    apart, off = divmod(b - a, dx.element_size())
+    if dx.dtype is dgate.dtype and at == to and not off:
+        (so, no), (si, ni) = sorted(((at[0], B), (at[1], T)), reverse=True)
+        near = lambda d, s, n: {max(1 - n, min(n - 1, -d // s + k)) for k in (-1, 0, 1, 2)} if n > 1 else {0}  # noqa: E731
+        if all(abs(apart + o * so + i * si) >= D for o in near(apart, so, no) for i in near(apart + o * so, si, ni)):
+            return
     raise ValueError("dx and dgate must not share memory")
 
 

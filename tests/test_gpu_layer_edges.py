@@ -155,3 +155,15 @@ def test_gates_that_their_bias_cancels(bias, form, gt):
         gdn.glr_step(x[:, t], gate[:, t], state, **kw)
     ref = L.glr(x[0, :3], gate[0, :3], b, rate, None, [3], form, "complement")
     glr_close((state,), ref, ("hT",))
+
+
+def test_gradients_in_any_layout():
+    """The same bits wherever they go: time-major, halves of a batch, side by side in either."""
+    B, T, D = 3, 77, 64
+    x, gate, dy = (rnd(B, T, D, seed=i, dtype=BF) for i in range(3))
+    kw = dict(rate=torch.full((D,), 0.1, device=DEV), form="rate", scale="norm")
+    want = gdn.glr_backward(dy, x, gate, **kw)
+    halves, tokens = torch.empty(B, 2, T, D, device=DEV, dtype=BF), torch.empty(T, B, 2 * D, device=DEV, dtype=BF)
+    for dx, dg in ((halves[:, 0], halves[:, 1]), (tokens[..., D:].transpose(0, 1), tokens[..., :D].transpose(0, 1))):
+        got = gdn.glr_backward(dy, x, gate, dx=dx, dgate=dg, **kw)
+        assert got[0] is dx and got[1] is dg and torch.equal(dx, want[0]) and torch.equal(dg, want[1]) and torch.equal(got[3], want[3])
