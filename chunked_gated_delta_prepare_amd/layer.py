@@ -57,7 +57,8 @@ def _call(name, *args):
 
 
 # What a problem's sizes, strides and types alone decide: its structure and
-# the bytes of workspace it needs.
+# the bytes of workspace it needs.  (Fields are plain numbers: anything else would be
+# found again by its identity, whatever it holds by then.)
 @functools.lru_cache(maxsize=4096)
 def _problem(kind, size_of, *fields):
     ref = ctypes.byref(kind(*fields))
@@ -211,7 +212,7 @@ def norm_forward(x, weight, residual=None, *, eps=1e-6, out_dtype=None, group=0,
         raise TypeError("out_dtype must be %s or %s, got %s" % (dt, _FP8, out_dtype))
     if group not in (0, 128):
         raise ValueError("group must be 0 (a scale per row) or 128, got %r" % (group,))
-    return _on(dev, stream, _norm_forward, dev, code, x, weight, residual, eps, out_dtype or dt, group, y, s, scales)
+    return _on(dev, stream, _norm_forward, dev, code, x, weight, residual, float(eps), out_dtype or dt, int(group), y, s, scales)
 
 
 def _norm_forward(handle, dev, code, x, weight, residual, eps, od, group, y, s, scales):
@@ -265,7 +266,7 @@ def norm_backward(dy, s, weight, dres=None, *, eps=1e-6, x_dtype=None, ds=None, 
     _check(weight, "weight", dev, shape[-1:], dt, torch.float32)
     if dres is not None:
         _check(dres, "dres", dev, shape, s.dtype)
-    return _on(dev, stream, _norm_backward, dev, code, dy, s, weight, dres, eps, ds, dx, dweight, workspace)
+    return _on(dev, stream, _norm_backward, dev, code, dy, s, weight, dres, float(eps), ds, dx, dweight, workspace)
 
 
 def _norm_backward(handle, dev, code, dy, s, weight, dres, eps, ds, dx, dweight, workspace):
@@ -655,7 +656,7 @@ def layer_norm_forward(x, weight, bias=None, residual=None, *, eps=1e-5, out_dty
         raise TypeError("out_dtype must be %s or %s, got %s" % (dt, _FP8, out_dtype))
     if group not in (0, 128):
         raise ValueError("group must be 0 (a scale per row) or 128, got %r" % (group,))
-    return _on(dev, stream, _layer_norm_forward, dev, code, x, weight, bias, residual, eps, out_dtype or dt, group, y, s, scales)
+    return _on(dev, stream, _layer_norm_forward, dev, code, x, weight, bias, residual, float(eps), out_dtype or dt, int(group), y, s, scales)
 
 
 def _layer_norm_forward(handle, dev, code, x, weight, bias, residual, eps, od, group, y, s, scales):
@@ -711,7 +712,7 @@ def layer_norm_backward(dy, s, weight, bias=None, dres=None, *, eps=1e-5, x_dtyp
         _check(bias, "bias", dev, shape[-1:], weight.dtype)
     if dres is not None:
         _check(dres, "dres", dev, shape, s.dtype)
-    return _on(dev, stream, _layer_norm_backward, dev, code, dy, s, weight, bias, dres, eps, ds, dx, dweight, dbias, workspace)
+    return _on(dev, stream, _layer_norm_backward, dev, code, dy, s, weight, bias, dres, float(eps), ds, dx, dweight, dbias, workspace)
 
 
 def _layer_norm_backward(handle, dev, code, dy, s, weight, bias, dres, eps, ds, dx, dweight, dbias, workspace):
@@ -823,7 +824,8 @@ def gate_norm_forward(x, z, weight, bias=None, *, eps=1e-5, activation="silu", g
     fp32; bias like it (with center), or None.  activation: "silu" or "sigmoid".
     Returns y, dense."""
     dev, code, each = _gate_norm_checks(x, z, weight, bias, activation, center)
-    return _on(dev, stream, _gate_norm_forward, dev, code, x, z, weight, bias, each, gate_first, center, _ACT[activation], eps, y)
+    return _on(dev, stream, _gate_norm_forward, dev, code, x, z, weight, bias, each, bool(gate_first), bool(center), _ACT[activation],
+               float(eps), y)
 
 
 def _gate_norm_forward(handle, dev, code, x, z, weight, bias, each, first, center, act, eps, y):
@@ -843,8 +845,8 @@ def gate_norm_backward(dy, x, z, weight, bias=None, *, eps=1e-5, activation="sil
     _check(dy, "dy", dev, x.shape, x.dtype)
     if bias is None:
         _unwritten(dbias, "dbias", "a bias")
-    return _on(dev, stream, _gate_norm_backward, dev, code, dy, x, z, weight, bias, each, gate_first, center, _ACT[activation], eps,
-               dx, dz, dweight, dbias, workspace)
+    return _on(dev, stream, _gate_norm_backward, dev, code, dy, x, z, weight, bias, each, bool(gate_first), bool(center), _ACT[activation],
+               float(eps), dx, dz, dweight, dbias, workspace)
 
 
 def _gate_norm_backward(handle, dev, code, dy, x, z, weight, bias, each, first, center, act, eps, dx, dz, dweight, dbias, workspace):
