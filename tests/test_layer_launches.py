@@ -138,3 +138,15 @@ def test_very_many_short_prompts(launches):
             assert status == 3 and not calls
         else:
             assert status == 0 and [c[:2] for c in calls] == [[B * -(-D // 64), threads]]
+
+
+def test_pieces_of_the_moves(launches):
+    """(sequences, tokens, channels, fp32, workgroups of the moves and of y): fp32 rows are not
+    cut in two or three pieces."""
+    sizes = [(1, 8192, 4096, 0, 3 * 64 * 2, 256), (1, 8192, 4096, 1, 3 * 64, 256), (1, 12288, 4096, 0, 3 * 64 * 3, 256),
+             (1, 12288, 4096, 1, 3 * 64, 256), (1, 65536, 4096, 0, 3 * 64 * 4, 256), (1, 65536, 4096, 1, 3 * 64 * 4, 256),
+             (2, 8192, 4096, 1, 128 * 4, 256), (1, 2048, 1024, 1, 16 * 4, 32), (1, 2048, 1024, 0, 16 * 4, 32)]
+    found = launches([glr("gdn_glr_forward", B, T, D, 0 if f else 1) for B, T, D, f, _, _ in sizes])
+    assert small(found)
+    for (*size, moves, y), (status, calls) in zip(sizes, found):
+        assert status == 0 and [c[:2] for c in calls] == [[moves, 512], [y, 512]], (size, calls)
