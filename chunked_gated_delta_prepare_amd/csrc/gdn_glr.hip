@@ -260,11 +260,11 @@ gdn_status check_glr(const gdn_glr_problem *pr, bool packed) {
     if (!io_dtype_ok(pr->io_dtype) || (pr->g_dtype != pr->io_dtype && pr->g_dtype != GDN_F32)) return GDN_ERR_UNSUPPORTED;
     if (pr->form < GDN_GLR_LOG || pr->form > GDN_GLR_RATE || pr->scale < GDN_GLR_PLAIN || pr->scale > GDN_GLR_NORM)
         return GDN_ERR_UNSUPPORTED;
-    if (pr->T > (1 << 30) || pr->B > (1 << 24) || pr->D > (1 << 23)) return GDN_ERR_UNSUPPORTED;
+    if (pr->T > (1 << 30) || pr->B > (1 << 24) || pr->D > (1 << 20)) return GDN_ERR_UNSUPPORTED;
     // a tile's rows and the states are addressed with 32-bit byte offsets
     for (int64_t v : {pr->x_stride_t, pr->g_stride_t, pr->dy_stride_t, pr->dx_stride_t, pr->dg_stride_t})
         if (v < 0 || v > (1 << 20)) return GDN_ERR_UNSUPPORTED;
-    if (pr->D > (1 << 20) || (packed ? pr->n_seqs : pr->B) * pr->D >= (1 << 29)) return GDN_ERR_UNSUPPORTED;
+    if ((packed ? pr->n_seqs : pr->B) * pr->D >= (1 << 29)) return GDN_ERR_UNSUPPORTED;
     return GDN_OK;
 }
 

@@ -22,7 +22,8 @@ constexpr int kGbWaves = 4;
 template <int VEC>
 constexpr int kGbRun = VEC == 2 ? 4 : 8;      // tokens of a thread
 template <int VEC>
-constexpr int kGbTile = kGbWaves * GlrLane<VEC>::kTG * kGbRun<VEC>;      // 32 either way
+constexpr int kGbTile = kGbWaves * GlrLane<VEC>::kTG * kGbRun<VEC>;
+static_assert(kGbTile<1> == 32 && kGbTile<2> == 32, "whether channels go in pairs depends on pointers, a workspace's size does not");
 
 template <typename IO, int VEC, int L>
 __device__ __forceinline__ void fetch_dy(const GlrParams &p, RawRow<IO, VEC> (&dy)[L], int b, int t_base, int row, int c, bool full) {
@@ -334,14 +335,14 @@ __global__ void __launch_bounds__(64 * kGbWaves, 4) glr_backward_kernel(GlrParam
 
 namespace {
 
-int64_t glr_tiles(const gdn_glr_problem *pr, bool pairs) {
-    const int64_t per = pairs ? kGbTile<2> : kGbTile<1>, n = (pr->T + per - 1) / per;
+int64_t glr_tiles(const gdn_glr_problem *pr) {
+    const int64_t n = (pr->T + kGbTile<2> - 1) / kGbTile<2>;
     return n < 1 ? 1 : n;
 }
 
-// (for the smaller tiles, which need more: whether channels go in pairs depends on pointers too)
+// Two sums a tile and channel, and where tiles meet its move, H and E.
 int64_t glr_backward_bytes(const gdn_glr_problem *pr) {
-    const int64_t n = glr_tiles(pr, false);
+    const int64_t n = glr_tiles(pr);
     return pr->B * n * (n > 1 ? 5 : 2) * pr->D * 4;
 }
 
@@ -393,7 +394,7 @@ gdn_status gdn_glr_backward(const gdn_glr_problem *pr, const void *dy, const voi
     const bool pairs = glr_pairs(pr, {dy, x, dx}, {gate, dgate},
                                  {pr->x_stride_b, pr->x_stride_t, pr->g_stride_b, pr->g_stride_t, pr->dy_stride_b, pr->dy_stride_t,
                                   pr->dx_stride_b, pr->dx_stride_t, pr->dg_stride_b, pr->dg_stride_t});
-    const int64_t tiles = glr_tiles(pr, pairs);
+    const int64_t tiles = glr_tiles(pr);
     // (the states' launch, of two waves or fewer for every tile, is the smaller one)
     if (!grid_ok(tiles * pr->B, (int64_t)gp.groups * 64 * kGbWaves)) return GDN_ERR_UNSUPPORTED;
     gp.dy = dy;

@@ -339,13 +339,13 @@ gdn_status gdn_ssm_step(const gdn_ssm_problem *problem, const void *x, const voi
 #define GDN_GLR_NORM 2
 
 typedef struct gdn_glr_problem {
-    int64_t B, T, D;          /* B >= 1, T >= 0, D >= 1 */
+    int64_t B, T, D;          /* 1 <= B <= 2^24, 0 <= T <= 2^30, 1 <= D <= 2^20 */
     int64_t x_stride_b, x_stride_t;    /* x [B, T, D]: between batches, tokens */
     int64_t g_stride_b, g_stride_t;    /* gate [B, T, D] */
     int64_t dy_stride_b, dy_stride_t;  /* dy (backward only) */
     int64_t dx_stride_b, dx_stride_t;  /* dx (backward only): rows must not overlap */
     int64_t dg_stride_b, dg_stride_t;  /* dgate (backward only): rows must not overlap */
-    int64_t n_seqs;           /* packed sequences (with cu_seqlens); else 0 */
+    int64_t n_seqs;           /* packed sequences (with cu_seqlens), at most 2^24; else 0 */
     int32_t io_dtype;         /* of x, y and their gradients */
     int32_t g_dtype;          /* of the gate and its gradient: io_dtype or GDN_F32 */
     int32_t form;             /* GDN_GLR_LOG, _SIGMOID, _RATE */
