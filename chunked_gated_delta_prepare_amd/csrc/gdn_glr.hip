@@ -311,12 +311,15 @@ struct GlrPlan {
 
 // Segments for about 256 workgroups of 64 channels, one a CU, of four tiles at least
 // (a segment's rows are read once more for its move).  Their pieces for the moves: for 256
-// workgroups however short, for 1024 if they keep four tiles (fp32: and are four at least).
-// Whole segments against pieces, forward: 65536 tokens of 4096 channels of bf16 524 and 494 us, 2048 of 1024
-// 36 and 28; two pieces, 4096 of 8192 65.8 and 55.9 (a gate of fp32 80.8 and 69.5), 8192 of 4096 66.2 and 64.5;
-// fp32, 2 x 8192 of 4096 (four pieces) 219 and 204, but two, 8192 of 4096 104.7 and 111.3 (4096 of 8192 105.4 and
-// 103.5), and three, 12288 of 4096 173 and 179.  Pieces for 512 or 768 workgroups 538 and 530 us (65536
-// tokens), for 2048 496; of one tile, for 1024 workgroups, 80 against 75 us (16384 tokens of 1030 channels).
+// workgroups however short, for 1024 if they keep four tiles (fp32: and are four at least, or
+// the moves are of one segment, for half of the chip), for 2048, as two run on a CU, if they keep eight
+// (packed rows, of which one does: not).
+// Whole segments against pieces, forward: 65536 tokens of 4096 channels of bf16 530 and 494 us, 2048 of 1024
+// 33.5 and 25.7; two pieces, 4096 of 8192 65.8 and 55.9 (a gate of fp32 80.8 and 69.5), 8192 of 4096 66.2 and 64.5;
+// fp32, 2 x 8192 of 4096 (four pieces) 219 and 205, 4096 of 8192 (two, of one segment) 105.4 and 103.5, but
+// two of each of three segments, 8192 of 4096, 104.7 and 111.3, and three, 12288 of 4096, 173 and 179.  Pieces of one tile, for 1024 workgroups, 76 against 69 us (16384
+// tokens of 1030 channels); for 512 or 768 workgroups 544 and 530 us (65536 tokens), for 1024 504; for 2048 of four
+// tiles 251 against 247 (32768 tokens), and packed, 65536 tokens, 551 against 539.
 GlrPlan glr_plan(const gdn_glr_problem *pr) {
     constexpr int64_t kTile = kGlrTile<2>;         // (a multiple of the tile of single channels)
     const int64_t streams = pr->B * ((pr->D + kGlrCols - 1) / kGlrCols), tiles = (pr->T + kTile - 1) / kTile;
@@ -329,8 +332,9 @@ GlrPlan glr_plan(const gdn_glr_problem *pr) {
     s.segs = (pr->T + s.seg_len - 1) / s.seg_len;
     s.segs = s.segs < 1 ? 1 : s.segs;
     const int64_t wgs = streams * s.segs, n = s.seg_len / kTile;
-    const int64_t fill = std::min((255 + wgs) / wgs, n), more = std::min((1023 + wgs) / wgs, n / 4);
-    s.pieces = std::max(fill, pr->io_dtype == GDN_F32 && more < 4 ? 1 : more);
+    const int64_t fill = std::min((255 + wgs) / wgs, n), many = pr->n_seqs > 0 ? 0 : std::min((2047 + wgs) / wgs, n / 8);
+    const int64_t more = std::max(std::min((1023 + wgs) / wgs, n / 4), many);
+    s.pieces = std::max(fill, pr->io_dtype == GDN_F32 && s.segs > 2 && more < 4 ? 1 : more);
     return s;
 }
 

@@ -141,12 +141,16 @@ def test_very_many_short_prompts(launches):
 
 
 def test_pieces_of_the_moves(launches):
-    """(sequences, tokens, channels, fp32, workgroups of the moves and of y): fp32 rows are not
-    cut in two or three pieces."""
+    """(sequences, tokens, channels, fp32, workgroups of the moves and of y): fp32 rows of
+    several segments before the last are not cut in two or three pieces; long ones in twice as many of eight tiles, unless they are packed."""
     sizes = [(1, 8192, 4096, 0, 3 * 64 * 2, 256), (1, 8192, 4096, 1, 3 * 64, 256), (1, 12288, 4096, 0, 3 * 64 * 3, 256),
-             (1, 12288, 4096, 1, 3 * 64, 256), (1, 65536, 4096, 0, 3 * 64 * 4, 256), (1, 65536, 4096, 1, 3 * 64 * 4, 256),
-             (2, 8192, 4096, 1, 128 * 4, 256), (1, 2048, 1024, 1, 16 * 4, 32), (1, 2048, 1024, 0, 16 * 4, 32)]
+             (1, 12288, 4096, 1, 3 * 64, 256), (1, 65536, 4096, 0, 3 * 64 * 8, 256), (1, 32768, 4096, 1, 3 * 64 * 4, 256),
+             (2, 8192, 4096, 1, 128 * 4, 256), (2, 4096, 4096, 1, 128 * 2, 256), (1, 2048, 1024, 1, 16 * 4, 32), (1, 2048, 1024, 0, 16 * 4, 32)]
     found = launches([glr("gdn_glr_forward", B, T, D, 0 if f else 1) for B, T, D, f, _, _ in sizes])
     assert small(found)
     for (*size, moves, y), (status, calls) in zip(sizes, found):
         assert status == 0 and [c[:2] for c in calls] == [[moves, 512], [y, 512]], (size, calls)
+    packed = glr("gdn_glr_forward", 1, 65536, 4096)
+    packed[2]["n_seqs"], packed[3][5] = 9, FAKE
+    status, calls = launches([packed])[0]
+    assert status == 0 and [c[:2] for c in calls] == [[3 * 64 * 4, 512], [256, 512]]
