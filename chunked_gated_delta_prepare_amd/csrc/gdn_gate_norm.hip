@@ -8,8 +8,9 @@
 //   dw = sum dn h,  db = sum dn over the rows that share w
 //
 // Bound by memory: every tensor is read or written once (16384 tokens of 64 rows of 128 in
-// bf16 forward 161 us, 5.0 TB/s; 16384 of 4 rows of 1024, gate first, forward 92 us, 4.4
-// TB/s, backward 154 us, 4.4 TB/s, and 4.7 us the sums; 4096 rows of 128 3.9 us, a launch's own time).  TPR threads hold a
+// bf16 forward 160 us, 5.0 TB/s; 16384 of 4 rows of 1024, gate first, forward 91 us, 4.4
+// TB/s, backward 152 us, 4.4 TB/s, and 4.8 us the sums; 4096 rows of 128 4 us, a launch's own time; rows of
+// single elements as fast as of four: 16384 of 1030 26.0 us forward, of 1028 26.5).  TPR threads hold a
 // row (K vectors of VEC elements each), from 16 lanes for the 64 elements of a
 // small head to a workgroup; rows of one wave or less need no barrier.  Where
 // a head's rows lie is a stride between tokens and one between heads, so the

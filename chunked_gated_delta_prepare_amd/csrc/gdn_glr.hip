@@ -1,13 +1,16 @@
 // Gated linear recurrence, forward and step (see gdn_glr.h for the mathematics).
 //
 // Bound by memory where channels and sequences fill the chip (8 sequences of 8192
-// tokens, 4096 channels of bf16: 346 us, 4.7 TB/s, near a copy's rate); a single long
+// tokens, 4096 channels of bf16: 343 us, 4.7 TB/s, near a copy's rate); a single long
 // sequence is cut into segments and its rows are read once more for their moves
-// (65536 tokens: 173 us, 4.6 TB/s, then 323, 5.0 TB/s).  Vector instructions come next: with the
+// (65536 tokens: 167 us, 4.8 TB/s, then 325, 5.0 TB/s).  Vector instructions come next: with the
 // gate's exponential, reciprocal, series and square root some 24 an element (rate, norm) or
-// 19 (sigmoid, complement), which keep the units busy for half of the time.  16384 packed
-// tokens of 4096 channels, rate and norm: 64 us the moves, 93 us y.  Eight waves of 16
-// tokens a thread and one workgroup a CU (before the moves had pieces: four waves and 512
+// 20 (sigmoid, complement), which keep the units busy for half of the time (long moves,
+// two workgroups a CU: 0.74).  16384 packed tokens of 4096 channels, rate and norm, are short of
+// waves, with one workgroup a CU (165 to 191 registers): 64 us the moves (3.1 TB/s), 94 us y (4.3 TB/s),
+// vector instructions for half of either.  Prompts of some thousand tokens fill few CUs: 2048 of
+// 1024 channels 7 us the moves and 20 us y, of 32 workgroups.  Eight waves of 16
+// tokens a thread and one workgroup a CU for y (before the moves had pieces: four waves and 512
 // workgroups 556 against 536 us for 65536 tokens, 8 tokens a thread 580, 16 waves 619).
 #include <algorithm>
 
@@ -314,8 +317,8 @@ struct GlrPlan {
 // workgroups however short, for 1024 if they keep four tiles (fp32: and are four at least, or
 // the moves are of one segment, for half of the chip), for 2048, as two run on a CU, if they keep eight
 // (packed rows, of which one does: not).
-// Whole segments against pieces, forward: 65536 tokens of 4096 channels of bf16 530 and 494 us, 2048 of 1024
-// 33.5 and 25.7; two pieces, 4096 of 8192 65.8 and 55.9 (a gate of fp32 80.8 and 69.5), 8192 of 4096 66.2 and 64.5;
+// Whole segments against pieces, forward: 65536 tokens of 4096 channels of bf16 530 and 492 us, 2048 of 1024
+// 33.5 and 25.5; two pieces, 4096 of 8192 65.8 and 55.9 (a gate of fp32 80.8 and 69.5), 8192 of 4096 66.2 and 64.5;
 // fp32, 2 x 8192 of 4096 (four pieces) 219 and 205, 4096 of 8192 (two, of one segment) 105.4 and 103.5, but
 // two of each of three segments, 8192 of 4096, 104.7 and 111.3, and three, 12288 of 4096, 173 and 179.  Pieces of one tile, for 1024 workgroups, 76 against 69 us (16384
 // tokens of 1030 channels); for 512 or 768 workgroups 544 and 530 us (65536 tokens), for 1024 504; for 2048 of four

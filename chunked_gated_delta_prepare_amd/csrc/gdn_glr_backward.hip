@@ -9,9 +9,9 @@
 // moves in the workspace, a second turns them into those states, and the third
 // reads its tile again and writes the gradients.  It takes the tiles in the
 // other order, so that the last ones come out of the last cache.
-// 2 x 8192 tokens of 4096 channels, rate and norm: 91 us the moves (403 MB, 4.4 TB/s), 13 the
-// states, 152 the gradients (700 MB, 4.6 TB/s; some 60 vector instructions an element keep the
-// units busy for 0.75 of it), 8 the sums.  Tiles of 32 tokens, 4 a thread, in 104
+// 2 x 8192 tokens of 4096 channels, rate and norm: 87 us the moves (403 MB, 4.6 TB/s), 13 the
+// states, 156 the gradients (700 MB, 4.5 TB/s; some 60 vector instructions an element keep the
+// units busy for 0.77 of it), 8 the sums.  Tiles of 32 tokens, 4 a thread, in 104
 // registers: 8 a thread do not fit the 128 of four waves a SIMD.
 #include "gdn_glr.h"
 #include "gdn_norm_rows.h"

@@ -9,11 +9,12 @@
 // VEC elements each): the mean is taken first and the squares of what is left
 // after it, so rows far from zero keep their digits; what rounding left of the
 // mean (the mean of s - m) is taken out in the same sums.
-// Measured: 16384 rows of 8192 in bf16 with a residual to e4m3 199 us, 4.7 TB/s (249 with a
+// Measured (the kernels alone): 16384 rows of 8192 in bf16 with a residual to e4m3 200 us, 4.7 TB/s (249 with a
 // row a workgroup, 242 with 256 threads a row); 16384 rows of 4096 in bf16 with a residual
-// forward 90 us (6.0 TB/s, part of it out of the last cache), backward 110 us (4.9 TB/s), the
-// sums 7; 1003 rows of 2050 with an fp32 residual 29 us in all, three launches that wait
-// for each other; 32 rows 4.3 us, a launch's own time and two reductions.
+// forward 90 us (6.0 TB/s, part of it out of the last cache), backward 114 to 118 us (4.6 TB/s), the
+// sums 7; 1003 rows of 2050 with an fp32 residual 9, 12 and 6 us, three launches that wait for each
+// other, the sums' rows of two rows each 8.2 MB written and read again beside 33 MB of data;
+// 32 rows 4 us, a launch's own time and two reductions.
 #include "gdn_norm_rows.h"
 
 namespace gdn {
