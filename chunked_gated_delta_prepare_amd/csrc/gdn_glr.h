@@ -83,9 +83,9 @@ __device__ __forceinline__ void decay_of(float y, float &a, float &c) {
 // below 1/8 in all channels of a wave, as gates of long memories have it).
 enum { kLog = GDN_GLR_LOG, kSigmoid = GDN_GLR_SIGMOID, kRate = GDN_GLR_RATE };
 
-// A channel's bias, for a sigmoid as its exponent takes it: in units of it, rounded, and
-// what 2^-(that rounding) is.  Without it the sigmoid would be off by |bias| units where
-// gate and bias cancel.
+// A channel's bias, for a sigmoid as its exponent takes it: in units of it, rounded, and 2 to
+// the power of what the rounding left out.  Without that the sigmoid would be off by |bias| units
+// where gate and bias cancel.
 struct GateBias {
     float b, fix;
 };
@@ -97,8 +97,8 @@ __device__ __forceinline__ void load_bias(const float *w, int c, int D, GateBias
     for (int e = 0; e < VEC; ++e) {
         const float t = b[e] * -kLog2e;
         bias[e].b = FORM == kLog ? b[e] : t;
-        // (nothing to put back for an infinite one)
-        bias[e].fix = fabsf(t) < 0x1p100f ? fmaf(fmaf(b[e], -kLog2e, -t), 0.693147181f, 1.f) : 1.f;
+        // (a larger one leaves gate + bias nothing behind the point; an infinite one has nothing left out)
+        bias[e].fix = fabsf(t) < 0x1p26f ? fast_exp2(fmaf(b[e], -kLog2e, -t)) : 1.f;
     }
 }
 

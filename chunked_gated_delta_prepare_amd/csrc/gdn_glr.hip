@@ -318,11 +318,12 @@ struct GlrPlan {
 // the moves are of one segment, for half of the chip), for 2048, as two run on a CU, if they keep eight
 // (packed rows, of which one does: not).
 // Whole segments against pieces, forward: 65536 tokens of 4096 channels of bf16 530 and 492 us, 2048 of 1024
-// 33.5 and 25.5; two pieces, 4096 of 8192 65.8 and 55.9 (a gate of fp32 80.8 and 69.5), 8192 of 4096 66.2 and 64.5;
-// fp32, 2 x 8192 of 4096 (four pieces) 219 and 205, 4096 of 8192 (two, of one segment) 105.4 and 103.5, but
-// two of each of three segments, 8192 of 4096, 104.7 and 111.3, and three, 12288 of 4096, 173 and 179.  Pieces of one tile, for 1024 workgroups, 76 against 69 us (16384
-// tokens of 1030 channels); for 512 or 768 workgroups 544 and 530 us (65536 tokens), for 1024 504; for 2048 of four
-// tiles 251 against 247 (32768 tokens), and packed, 65536 tokens, 551 against 539.
+// 33.5 and 25.5; two pieces, 4096 of 8192 65.8 and 55.9 (a gate of fp32 80.8 and 69.5), 8192 of 4096 66.2 and
+// 64.5; fp32, 2 x 8192 of 4096 (four pieces) 219 and 205, 4096 of 8192 (two, of one segment) 105.4 and 103.5,
+// but two of each of three segments, 8192 of 4096, 104.7 and 111.3, and three, 12288 of 4096, 173 and 179.
+// Pieces of one tile, for 1024 workgroups, 76 against 69 us (16384 tokens of 1030 channels); for 512 or 768
+// workgroups 544 and 530 us (65536 tokens), for 1024 504; for 2048 of four tiles 251 against 247 (32768
+// tokens), and packed, 65536 tokens, 551 against 539.
 GlrPlan glr_plan(const gdn_glr_problem *pr) {
     constexpr int64_t kTile = kGlrTile<2>;         // (a multiple of the tile of single channels)
     const int64_t streams = pr->B * ((pr->D + kGlrCols - 1) / kGlrCols), tiles = (pr->T + kTile - 1) / kTile;

@@ -129,7 +129,7 @@ def test_rates_of_far_gates():
         assert t is None or (t.abs() < 2.0 ** -54).all()
 
 
-@pytest.mark.parametrize("bias", [0.0, 10.0, 60.0, 300.0])
+@pytest.mark.parametrize("bias", [0.0, 10.0, 60.0, 300.0, 46080.0, 1474560.0])
 @pytest.mark.parametrize("form", ["sigmoid", "rate", "log"])
 @pytest.mark.parametrize("gt", [F32, BF])
 def test_gates_that_their_bias_cancels(bias, form, gt):
